@@ -432,6 +432,144 @@ typedef struct inkattn_qkvr_params {
  * input except conv_state_*_out == conv_state_*_in under the rule above. */
 INKATTN_API inkattn_status inkattn_qkvr_prologue(const inkattn_qkvr_params *p, void *stream);
 
+/* ------------------------------------------------------------------------------
+ * The rest of the decoder layer.  Between the attention and inkattn_output_conv sits the
+ * output projection [VV §TP sharding nhận biết sconv: o_proj output -> sconv -> residual
+ * connection -> RMSNorm]; after it comes the MoE [SG §Inkling のモデルアーキテクチャ: sigmoid
+ * scores, the 6 best of 256 routed experts, 2 shared experts that join the normalisation of
+ * the weights but not the choice], whose output goes through the layer's fourth ShortConv
+ * (inkattn_output_conv again).  inkattn_linear, inkattn_route, inkattn_grouped_linear and
+ * inkattn_expert_combine are those products and what lies between them.
+ *
+ * The two products accumulate in fp32 on the tensor cores, apply bias and activation to the
+ * fp32 sums, and round once to the output type.  With v = x w^T + bias:
+ *   NONE v   RELU max(v, 0)   GELU v (1 + erf(v / sqrt 2)) / 2   SILU v / (1 + exp(-v))
+ *   SWIGLU   w (and bias) hold 2 F rows, F gate rows first, then F up rows:
+ *            SILU(gate) * up, F values; F must be a multiple of 16.
+ * Results do not depend on the GPU's scheduling: every sum is added in a fixed order.
+ * In these four calls an array without rows (N_tok == 0, M == 0) may be NULL.
+ * ------------------------------------------------------------------------------ */
+#define INKATTN_ACT_NONE 0
+#define INKATTN_ACT_RELU 1
+#define INKATTN_ACT_GELU 2
+#define INKATTN_ACT_SILU 3
+#define INKATTN_ACT_SWIGLU 4
+
+/* out[t][f] = act( sum_k x[t][k] w[f][k] + bias[f] ) + residual[t][f] */
+typedef struct inkattn_linear_params {
+    size_t struct_size;        /* = sizeof(inkattn_linear_params)                        */
+    int32_t N_tok;             /* rows of x, >= 0                                        */
+    int32_t K;                 /* input width: a multiple of 8, 8 .. 2^20                */
+    int32_t F;                 /* output features, 1 .. 2^20                             */
+    int32_t act;               /* INKATTN_ACT_*                                          */
+    int32_t out_dtype;         /* INKATTN_DTYPE_BF16 (0) or INKATTN_DTYPE_F32 (1)        */
+    const inkattn_bf16 *x;     /* [N_tok][K]; device memory of this GPU                  */
+    const inkattn_bf16 *w;     /* [F][K] (SWIGLU: [2 F][K]); device memory of this GPU   */
+    const float *bias;         /* nullable, [F] (SWIGLU: [2 F])                          */
+    const inkattn_bf16 *residual;  /* nullable, [N_tok][F], added in fp32 before the     */
+                                   /* rounding                                           */
+    void *out;                 /* [N_tok][F], bf16 or fp32 per out_dtype                 */
+    int32_t *dev_status;       /* nullable, see the conventions above                    */
+} inkattn_linear_params;
+
+/* Runs the linear layer.  x and w are read by TMA (device memory of the current device,
+ * 16-byte aligned); residual and out must be 16-byte aligned.  out may be the residual array
+ * itself (bf16), but overlaps no other input (INKATTN_ERR_INVALID_ARG). */
+INKATTN_API inkattn_status inkattn_linear(const inkattn_linear_params *p, void *stream);
+
+/* Products grouped by expert: the rows i in [expert_offsets[e], expert_offsets[e+1]) of out are
+ *   out[i][f] = act( sum_k x[s][k] w[e][f][k] + bias[e][f] ),   s = row_token ? row_token[i] : i.
+ * expert_offsets lies on the device, so the same call (or captured graph) serves any split of
+ * the rows among the experts; an expert without rows costs nothing.  Rows at and behind
+ * expert_offsets[E] are neither read nor written.  An expert whose offsets are negative,
+ * decrease or pass M is flagged (INKATTN_ERR_DEVICE_BOUNDS) and its rows left as they were,
+ * and so is a row whose row_token lies outside [0, N_x). */
+#define INKATTN_MAX_EXPERTS 1024
+typedef struct inkattn_grouped_linear_params {
+    size_t struct_size;        /* = sizeof(inkattn_grouped_linear_params)                */
+    int32_t E;                 /* experts, 1 .. INKATTN_MAX_EXPERTS                      */
+    int32_t M;                 /* rows of out (capacity), >= 0                           */
+    int32_t N_x;               /* rows of x; >= M where row_token is NULL                */
+    int32_t K;                 /* input width: a multiple of 8, 8 .. 2^20                */
+    int32_t F;                 /* output features, 1 .. 2^20                             */
+    int32_t act;               /* INKATTN_ACT_*                                          */
+    int32_t out_dtype;         /* INKATTN_DTYPE_BF16 (0) or INKATTN_DTYPE_F32 (1)        */
+    const inkattn_bf16 *x;     /* [N_x][K]; device memory of this GPU                    */
+    const inkattn_bf16 *w;     /* [E][F][K] (SWIGLU: [E][2 F][K]); device memory of this GPU */
+    const float *bias;         /* nullable, [E][F] (SWIGLU: [E][2 F])                    */
+    const int32_t *expert_offsets;  /* [E+1], non-decreasing, expert_offsets[E] <= M     */
+    const int32_t *row_token;  /* nullable, [M]: the row of x that row i multiplies      */
+    void *out;                 /* [M][F], bf16 or fp32 per out_dtype                     */
+    int32_t *dev_status;       /* nullable                                               */
+} inkattn_grouped_linear_params;
+
+/* Runs the grouped products.  Alignment and overlap rules as inkattn_linear's. */
+INKATTN_API inkattn_status inkattn_grouped_linear(const inkattn_grouped_linear_params *p, void *stream);
+
+/* The router's choice.  Token t has E routed logits and, behind them, n_shared logits of
+ * shared experts.  Its top_k routed experts are those of the largest logits, in descending
+ * order, equal logits by the lower index first (a NaN counts as -infinity).  With
+ *   s(l) = 1 / (1 + exp(-l))  (INKATTN_SCORE_SIGMOID)   or   exp(l)  (INKATTN_SCORE_SOFTMAX)
+ * the weights of the chosen and the shared experts are scale * s(l) / (sum of their s(l)), in
+ * fp32 (all zero where that sum is zero, as when every logit is -infinity).  The N_tok * top_k
+ * (token, choice) pairs are then sorted by expert, stably in (token, choice) order:
+ *   expert_offsets[e] = first row of expert e, row_token[i] = the token of row i (the row_token
+ *   of inkattn_grouped_linear), token_rows[t][j] = the row of token t's j-th choice (the
+ *   token_rows of inkattn_expert_combine). */
+#define INKATTN_SCORE_SIGMOID 0
+#define INKATTN_SCORE_SOFTMAX 1
+#define INKATTN_MAX_TOP_K 16
+#define INKATTN_MAX_SHARED 16
+typedef struct inkattn_route_params {
+    size_t struct_size;        /* = sizeof(inkattn_route_params)                         */
+    int32_t N_tok;             /* tokens, >= 0 (0 writes expert_offsets alone); N_tok *  */
+                               /* top_k <= 2^28                                          */
+    int32_t E;                 /* routed experts, 1 .. INKATTN_MAX_EXPERTS               */
+    int32_t n_shared;          /* shared experts, 0 .. INKATTN_MAX_SHARED                */
+    int32_t top_k;             /* 1 .. min(E, INKATTN_MAX_TOP_K)                         */
+    int32_t score;             /* INKATTN_SCORE_*                                        */
+    float scale;               /* factor of the weights, finite                          */
+    const float *logits;       /* [N_tok][E + n_shared]                                  */
+    int32_t *topk_ids;         /* [N_tok][top_k]                                         */
+    float *weights;            /* [N_tok][top_k + n_shared]                              */
+    int32_t *expert_offsets;   /* [E+1]                                                  */
+    int32_t *row_token;        /* [N_tok * top_k]                                        */
+    int32_t *token_rows;       /* [N_tok][top_k]                                         */
+} inkattn_route_params;
+
+/* Bytes of workspace inkattn_route needs: 0 for small batches, or if the params are invalid. */
+INKATTN_API size_t inkattn_route_workspace_bytes(const inkattn_route_params *p);
+
+/* Runs the router.  All arrays 4-byte aligned; the outputs overlap neither each other nor the
+ * logits.  workspace: device memory, 16-byte aligned, at least inkattn_route_workspace_bytes
+ * bytes (nullable when that is 0), need not be cleared; calls whose GPU work overlaps need one
+ * each. */
+INKATTN_API inkattn_status inkattn_route(const inkattn_route_params *p, void *workspace,
+                                         size_t workspace_bytes, void *stream);
+
+/* The weighted sum of each token's expert rows, in fp32, choices in order, then the shared
+ * experts in order, rounded once to bf16:
+ *   out[t] = sum_{j<top_k} weights[t][j] y[token_rows[t][j]] + sum_s weights[t][top_k+s] shared[s][t].
+ * A choice whose token_rows entry is -1 (a dropped row) adds nothing; any other entry outside
+ * [0, M) is flagged (INKATTN_ERR_DEVICE_BOUNDS) and adds nothing either. */
+typedef struct inkattn_expert_combine_params {
+    size_t struct_size;        /* = sizeof(inkattn_expert_combine_params)                */
+    int32_t N_tok;             /* tokens, >= 0                                           */
+    int32_t M;                 /* rows of y, >= 0                                        */
+    int32_t F;                 /* width: a multiple of 8, 8 .. 2^20                      */
+    int32_t top_k;             /* 1 .. INKATTN_MAX_TOP_K                                 */
+    int32_t n_shared;          /* 0 .. INKATTN_MAX_SHARED                                */
+    const inkattn_bf16 *y;     /* [M][F]                                                 */
+    const inkattn_bf16 *shared;    /* [n_shared][N_tok][F] (nullable iff n_shared == 0)  */
+    const float *weights;      /* [N_tok][top_k + n_shared]                              */
+    const int32_t *token_rows; /* [N_tok][top_k]                                         */
+    inkattn_bf16 *out;         /* [N_tok][F]                                             */
+    int32_t *dev_status;       /* nullable                                               */
+} inkattn_expert_combine_params;
+
+/* Runs the sum.  y, shared and out must be 16-byte aligned; out overlaps no input. */
+INKATTN_API inkattn_status inkattn_expert_combine(const inkattn_expert_combine_params *p, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

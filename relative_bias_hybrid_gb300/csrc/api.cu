@@ -2,7 +2,7 @@
 // descriptor setup, the decode split heuristic, and the launches.
 //
 // Nothing here computes on the host: every step of the path runs in the kernels of
-// prologue.cu, qkvr.cu, output_conv.cu, prefill_tc.cu and decode.cu.
+// prologue.cu, qkvr.cu, output_conv.cu, prefill_tc.cu, decode.cu, linear.cu and route.cu.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -256,6 +256,131 @@ inkattn_status validate_locations(const inkattn_attn_params *p) {
     return INKATTN_OK;
 }
 
+// Device memory of the current device, as TMA reads it.
+inkattn_status validate_on_device(const void *const *ptrs, int n) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return INKATTN_ERR_INVALID_ARG;
+    }
+    for (int i = 0; i < n; ++i) {
+        cudaPointerAttributes a;
+        if (cudaPointerGetAttributes(&a, ptrs[i]) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return INKATTN_ERR_INVALID_ARG;
+        }
+        if (a.type != cudaMemoryTypeDevice || a.device != dev) return INKATTN_ERR_INVALID_ARG;
+    }
+    return INKATTN_OK;
+}
+
+struct Range {
+    const void *a;
+    size_t n;
+};
+bool overlap(const Range &x, const Range &y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.a), b = reinterpret_cast<uintptr_t>(y.a);
+    return x.a && y.a && x.n && y.n && a < b + y.n && b < a + x.n;
+}
+
+// Sizes, types and alignment that the linear layer and the grouped products share.  Arrays of
+// no rows may be NULL.
+inkattn_status validate_product(int rows, int K, int F, int act, int out_dtype, const void *x, const void *w, const void *bias,
+                                const void *residual, const void *out, const void *dev_status) {
+    if (K < 8 || K % 8 != 0 || K > (1 << 20) || F < 1 || F > (1 << 20)) return INKATTN_ERR_INVALID_ARG;
+    if (act < INKATTN_ACT_NONE || act > INKATTN_ACT_SWIGLU) return INKATTN_ERR_INVALID_ARG;
+    if (act == INKATTN_ACT_SWIGLU && F % 16 != 0) return INKATTN_ERR_INVALID_ARG;
+    if (out_dtype != INKATTN_DTYPE_BF16 && out_dtype != INKATTN_DTYPE_F32) return INKATTN_ERR_INVALID_ARG;
+    if (!w || (rows > 0 && (!x || !out)) || !aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16))
+        return INKATTN_ERR_INVALID_ARG;
+    if ((bias && !aligned(bias, 4)) || (residual && !aligned(residual, 16)) || (dev_status && !aligned(dev_status, 4)))
+        return INKATTN_ERR_INVALID_ARG;
+    return INKATTN_OK;
+}
+
+inkattn_status validate_linear(const inkattn_linear_params *p) {
+    if (!p || p->struct_size != sizeof(inkattn_linear_params) || p->N_tok < 0) return INKATTN_ERR_INVALID_ARG;
+    const inkattn_status st = validate_product(p->N_tok, p->K, p->F, p->act, p->out_dtype, p->x, p->w, p->bias,
+                                               p->residual, p->out, p->dev_status);
+    if (st != INKATTN_OK) return st;
+    const size_t elems = (size_t)p->N_tok * p->F, size = p->out_dtype == INKATTN_DTYPE_F32 ? 4 : 2;
+    const size_t wrows = (size_t)p->F * (p->act == INKATTN_ACT_SWIGLU ? 2 : 1);
+    const Range out = {p->out, elems * size};
+    const Range ins[] = {{p->x, (size_t)p->N_tok * p->K * 2}, {p->w, wrows * p->K * 2}, {p->bias, wrows * 4},
+                         {p->dev_status, 4}};
+    for (const Range &in : ins)
+        if (overlap(out, in)) return INKATTN_ERR_INVALID_ARG;
+    const bool in_place = p->residual == p->out && p->out_dtype == INKATTN_DTYPE_BF16;
+    if (!in_place && overlap(out, {p->residual, elems * 2})) return INKATTN_ERR_INVALID_ARG;
+    return INKATTN_OK;
+}
+
+inkattn_status validate_grouped_linear(const inkattn_grouped_linear_params *p) {
+    if (!p || p->struct_size != sizeof(inkattn_grouped_linear_params) || p->E < 1 || p->E > INKATTN_MAX_EXPERTS ||
+        p->M < 0 || p->N_x < 0)
+        return INKATTN_ERR_INVALID_ARG;
+    const inkattn_status st = validate_product(p->M, p->K, p->F, p->act, p->out_dtype, p->x, p->w, p->bias, nullptr,
+                                               p->out, p->dev_status);
+    if (st != INKATTN_OK) return st;
+    if (p->M > 0 && (p->row_token ? p->N_x < 1 : p->N_x < p->M)) return INKATTN_ERR_INVALID_ARG;
+    if (!p->expert_offsets || !aligned(p->expert_offsets, 4) || (p->row_token && !aligned(p->row_token, 4)))
+        return INKATTN_ERR_INVALID_ARG;
+    const size_t size = p->out_dtype == INKATTN_DTYPE_F32 ? 4 : 2;
+    const size_t wrows = (size_t)p->E * p->F * (p->act == INKATTN_ACT_SWIGLU ? 2 : 1);
+    const Range out = {p->out, (size_t)p->M * p->F * size};
+    const Range ins[] = {{p->x, (size_t)p->N_x * p->K * 2}, {p->w, wrows * p->K * 2}, {p->bias, wrows * 4},
+                         {p->expert_offsets, (size_t)(p->E + 1) * 4}, {p->row_token, (size_t)p->M * 4},
+                         {p->dev_status, 4}};
+    for (const Range &in : ins)
+        if (overlap(out, in)) return INKATTN_ERR_INVALID_ARG;
+    return INKATTN_OK;
+}
+
+inkattn_status validate_route(const inkattn_route_params *p) {
+    if (!p || p->struct_size != sizeof(inkattn_route_params) || p->N_tok < 0 || p->E < 1 ||
+        p->E > INKATTN_MAX_EXPERTS || p->n_shared < 0 || p->n_shared > INKATTN_MAX_SHARED || p->top_k < 1 ||
+        p->top_k > INKATTN_MAX_TOP_K || p->top_k > p->E || !std::isfinite(p->scale))
+        return INKATTN_ERR_INVALID_ARG;
+    if (p->score != INKATTN_SCORE_SIGMOID && p->score != INKATTN_SCORE_SOFTMAX) return INKATTN_ERR_INVALID_ARG;
+    if ((long long)p->N_tok * p->top_k > (1ll << 28)) return INKATTN_ERR_INVALID_ARG;
+    if (!p->expert_offsets || !aligned(p->expert_offsets, 4)) return INKATTN_ERR_INVALID_ARG;
+    const void *ptrs[] = {p->logits, p->topk_ids, p->weights, p->row_token, p->token_rows};
+    for (const void *ptr : ptrs)
+        if ((p->N_tok > 0 && !ptr) || !aligned(ptr, 4)) return INKATTN_ERR_INVALID_ARG;
+    const size_t T = (size_t)p->N_tok;
+    const Range r[] = {{p->logits, T * (p->E + p->n_shared) * 4}, {p->topk_ids, T * p->top_k * 4},
+                       {p->weights, T * (p->top_k + p->n_shared) * 4}, {p->expert_offsets, (size_t)(p->E + 1) * 4},
+                       {p->row_token, T * p->top_k * 4}, {p->token_rows, T * p->top_k * 4}};
+    for (int i = 0; i < 6; ++i)
+        for (int j = i + 1; j < 6; ++j)
+            if (overlap(r[i], r[j])) return INKATTN_ERR_INVALID_ARG;
+    return INKATTN_OK;
+}
+
+inkattn_status validate_expert_combine(const inkattn_expert_combine_params *p) {
+    if (!p || p->struct_size != sizeof(inkattn_expert_combine_params) || p->N_tok < 0 || p->M < 0 || p->F < 8 ||
+        p->F % 8 != 0 || p->F > (1 << 20) || p->top_k < 1 || p->top_k > INKATTN_MAX_TOP_K || p->n_shared < 0 ||
+        p->n_shared > INKATTN_MAX_SHARED)
+        return INKATTN_ERR_INVALID_ARG;
+    if ((long long)p->N_tok * ((p->F + 1023) / 1024) > INT_MAX) return INKATTN_ERR_INVALID_ARG;   // (the grid)
+    const bool some = p->N_tok > 0;
+    if ((p->M > 0 && !p->y) || (some && !p->out) || (some && p->n_shared > 0 && !p->shared) || !aligned(p->y, 16) ||
+        !aligned(p->out, 16) || !aligned(p->shared, 16))
+        return INKATTN_ERR_INVALID_ARG;
+    const void *ptrs4[] = {p->weights, p->token_rows};
+    for (const void *ptr : ptrs4)
+        if ((some && !ptr) || !aligned(ptr, 4)) return INKATTN_ERR_INVALID_ARG;
+    if (p->dev_status && !aligned(p->dev_status, 4)) return INKATTN_ERR_INVALID_ARG;
+    const size_t T = (size_t)p->N_tok, F = (size_t)p->F;
+    const Range out = {p->out, T * F * 2};
+    const Range ins[] = {{p->y, (size_t)p->M * F * 2}, {p->shared, p->n_shared * T * F * 2},
+                         {p->weights, T * (p->top_k + p->n_shared) * 4}, {p->token_rows, T * p->top_k * 4},
+                         {p->dev_status, 4}};
+    for (const Range &in : ins)
+        if (overlap(out, in)) return INKATTN_ERR_INVALID_ARG;
+    return INKATTN_OK;
+}
+
 AttnScalars scalars(const inkattn_attn_params &p) {
     AttnScalars s;
     s.scale = p.softmax_scale > 0.f ? p.softmax_scale : 1.0f / sqrtf((float)kHeadDim);
@@ -415,6 +540,30 @@ bool make_qkvr_maps(const inkattn_qkvr_params &p, CUtensorMap *xmap, CUtensorMap
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_linear_maps(const LinearArgs &a, bool gated, CUtensorMap *xmap, CUtensorMap *wmap) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t K = (cuuint64_t)a.K, F = (cuuint64_t)a.F, E = (cuuint64_t)a.E;
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    auto encode = [&](CUtensorMap *map, cuuint32_t rank, const void *base, const cuuint64_t *dims,
+                      const cuuint64_t *strides, const cuuint32_t *box) {
+        return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const cuuint64_t xdims[2] = {K, (cuuint64_t)a.N_x}, xstr[1] = {K * 2};
+    const cuuint32_t xbox[2] = {64, a.offsets ? 1u : (cuuint32_t)(a.tile_n / 2)};
+    if (!encode(xmap, 2, a.x, xdims, xstr, xbox)) return false;
+    if (gated) {
+        const cuuint64_t dims[5] = {K, 16, F / 16, 2, E}, str[4] = {K * 2, 16 * K * 2, F * K * 2, 2 * F * K * 2};
+        const cuuint32_t box[5] = {64, 16, 1, 2, 1};
+        return encode(wmap, 5, a.w, dims, str, box);
+    }
+    const cuuint64_t dims[3] = {K, F, E}, str[2] = {K * 2, F * K * 2};
+    const cuuint32_t box[3] = {64, 128, 1};
+    return encode(wmap, 3, a.w, dims, str, box);
+}
+
 bool make_q_map(CUtensorMap *map, const void *base, int n_tok, int hq, int box_rows) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
     if (!enc) return false;
@@ -487,6 +636,75 @@ inkattn_status inkattn_qkvr_prologue(const inkattn_qkvr_params *p, void *stream)
     CUtensorMap xmap, wmap;
     if (!make_qkvr_maps(*p, &xmap, &wmap)) return INKATTN_ERR_CUDA;
     return launch_status(launch_qkvr(*p, xmap, wmap, sms, static_cast<cudaStream_t>(stream)));
+}
+
+inkattn_status inkattn_linear(const inkattn_linear_params *p, void *stream) {
+    inkattn_status st = validate_linear(p);
+    if (st != INKATTN_OK) return st;
+    int sms = 0;
+    if ((st = check_device(&sms)) != INKATTN_OK) return st;
+    if (p->N_tok == 0) return INKATTN_OK;
+    const void *read[] = {p->x, p->w};
+    if ((st = validate_on_device(read, 2)) != INKATTN_OK) return st;
+    LinearArgs a = {};
+    a.x = p->x;
+    a.w = p->w;
+    a.bias = p->bias;
+    a.residual = p->residual;
+    a.out = p->out;
+    a.dev_status = p->dev_status;
+    a.E = 1;
+    a.M = a.N_x = p->N_tok;
+    a.K = p->K;
+    a.F = p->F;
+    a.out_f32 = p->out_dtype == INKATTN_DTYPE_F32;
+    return launch_status(launch_linear(a, p->act, sms, static_cast<cudaStream_t>(stream)));
+}
+
+inkattn_status inkattn_grouped_linear(const inkattn_grouped_linear_params *p, void *stream) {
+    inkattn_status st = validate_grouped_linear(p);
+    if (st != INKATTN_OK) return st;
+    int sms = 0;
+    if ((st = check_device(&sms)) != INKATTN_OK) return st;
+    if (p->M == 0) return INKATTN_OK;
+    const void *read[] = {p->x, p->w};
+    if ((st = validate_on_device(read, 2)) != INKATTN_OK) return st;
+    LinearArgs a = {};
+    a.x = p->x;
+    a.w = p->w;
+    a.bias = p->bias;
+    a.out = p->out;
+    a.offsets = p->expert_offsets;
+    a.row_token = p->row_token;
+    a.dev_status = p->dev_status;
+    a.E = p->E;
+    a.M = p->M;
+    a.N_x = p->N_x;
+    a.K = p->K;
+    a.F = p->F;
+    a.out_f32 = p->out_dtype == INKATTN_DTYPE_F32;
+    return launch_status(launch_linear(a, p->act, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t inkattn_route_workspace_bytes(const inkattn_route_params *p) {
+    return validate_route(p) == INKATTN_OK ? route_workspace_bytes(*p) : 0;
+}
+
+inkattn_status inkattn_route(const inkattn_route_params *p, void *workspace, size_t workspace_bytes, void *stream) {
+    inkattn_status st = validate_route(p);
+    if (st != INKATTN_OK) return st;
+    const size_t need = route_workspace_bytes(*p);
+    if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return INKATTN_ERR_INVALID_ARG;
+    if ((st = check_device(nullptr)) != INKATTN_OK) return st;
+    return launch_status(launch_route(*p, static_cast<uint32_t *>(workspace), static_cast<cudaStream_t>(stream)));
+}
+
+inkattn_status inkattn_expert_combine(const inkattn_expert_combine_params *p, void *stream) {
+    inkattn_status st = validate_expert_combine(p);
+    if (st != INKATTN_OK) return st;
+    if ((st = check_device(nullptr)) != INKATTN_OK) return st;
+    if (p->N_tok == 0) return INKATTN_OK;
+    return launch_status(launch_expert_combine(*p, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

@@ -67,6 +67,37 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *map, 
         : "memory");
 }
 
+// As tma_load_2d_pair, for four rows of the map named one by one (its box is one row high):
+// rows r0 .. r3 land one after another at dst.
+__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const void *map, int c0, int r0, int r1, int r2,
+                                                 int r3, uint32_t bar_pair) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3),
+           "r"(bar_pair)
+        : "memory");
+}
+
+// As tma_load_2d_pair, for maps of three and of five dimensions.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *map, int c0, int c1, int c2,
+                                                 uint32_t bar_pair) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar_pair)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const void *map, int c0, int c1, int c2, int c3,
+                                                 int c4, uint32_t bar_pair) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4),
+           "r"(bar_pair)
+        : "memory");
+}
+
 // The shared::cluster address of the object at `addr`'s offset in CTA `cta_rank`.
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t cta_rank) {
     uint32_t r;
@@ -92,13 +123,14 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 // 128-byte-swizzled K-major A and B tiles (the k steps advance the start addresses by 32
 // bytes, 2 in descriptor units), then, when `rel` is nonzero, a commit of them to the
 // mbarrier at `rel_bar`'s offset in both CTAs, and, when `done` is nonzero, a second such
-// commit to `done_bar`.  acc0 = 0 makes the first MMA overwrite D.  Warp-collective like
-// mma_bf16_ss (one elected lane issues).
+// commit to `done_bar`.  acc0 = 0 makes the first MMA overwrite D.  `pair` names the pair's
+// two CTAs within the cluster, a bit per rank.  Warp-collective like mma_bf16_ss (one
+// elected lane issues).
 __device__ __forceinline__ void mma_pair_bf16_ss_k64_commit(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
                                                             uint32_t acc0, uint32_t rel_bar, uint32_t rel,
-                                                            uint32_t done_bar, uint32_t done) {
-    asm volatile("{\n\t.reg .pred e, p0, pt, pr, pd;\n\t.reg .b64 a1, b1;\n\t.reg .b16 m;\n\t"
-                 "mov.b16 m, 3;\n\t"
+                                                            uint32_t done_bar, uint32_t done,
+                                                            uint16_t pair = 3) {
+    asm volatile("{\n\t.reg .pred e, p0, pt, pr, pd;\n\t.reg .b64 a1, b1;\n\t"
                  "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.u32 pt, 0, 0;\n\t"
                  "setp.ne.b32 pr, %6, 0;\n\tsetp.ne.b32 pd, %8, 0;\n\t"
                  "elect.sync _|e, 0xffffffff;\n\tand.pred pr, pr, e;\n\tand.pred pd, pd, e;\n\t"
@@ -110,11 +142,11 @@ __device__ __forceinline__ void mma_pair_bf16_ss_k64_commit(uint32_t d, uint64_t
                  "add.s64 a1, %1, 6;\n\tadd.s64 b1, %2, 6;\n\t"
                  "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, pt;\n\t"
                  "@pr tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-                 " [%5], m;\n\t"
+                 " [%5], %9;\n\t"
                  "@pd tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-                 " [%7], m;\n\t}"
+                 " [%7], %9;\n\t}"
                  :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc0), "r"(rel_bar), "r"(rel), "r"(done_bar),
-                    "r"(done)
+                    "r"(done), "h"(pair)
                  : "memory");
 }
 // Arrives once on the local mbarrier when every pair MMA issued so far by the elected lane

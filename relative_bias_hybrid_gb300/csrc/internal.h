@@ -77,6 +77,33 @@ cudaError_t launch_dequant_e4m3(const inkattn_attn_params &p, inkattn_bf16 *k_ou
 // qkvr projections with the prologue in their epilogue; xmap / wmap from make_qkvr_maps
 cudaError_t launch_qkvr(const inkattn_qkvr_params &p, const CUtensorMap &xmap, const CUtensorMap &wmap,
                         int num_sms, cudaStream_t stream);
+// A linear layer (offsets NULL, E = 1) or the experts' grouped products (csrc/linear.cu).
+// launch_linear sets the fields below the line.
+struct LinearArgs {
+    const inkattn_bf16 *x, *w;
+    const float *bias;
+    const inkattn_bf16 *residual;
+    void *out;
+    const int32_t *offsets, *row_token;
+    int32_t *dev_status;
+    int E, M, N_x, K, F, out_f32;
+    // ----
+    int n_fblocks;           // feature blocks of an expert
+    int tile_n;              // most rows of a token tile, a multiple of 32
+    int stages, stage_bytes; // the ring
+    int splits;              // pairs of a cluster that share an item's K range
+    uint64_t wait_ns;        // limit of every bounded wait
+};
+cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStream_t stream);
+// TMA descriptors of a launch: x rows (box 64 columns x tile_n / 2 rows; a single row where
+// the rows are gathered), the weights as [E][F][K] (box 64 x 128 rows) or, gated, as
+// [E][gate, up][F / 16][16][K] (box 64 x 16 gate and the 16 up rows); 128-byte swizzle.
+bool make_linear_maps(const LinearArgs &a, bool gated, CUtensorMap *xmap, CUtensorMap *wmap);
+
+size_t route_workspace_bytes(const inkattn_route_params &p);
+cudaError_t launch_route(const inkattn_route_params &p, uint32_t *ws, cudaStream_t stream);
+cudaError_t launch_expert_combine(const inkattn_expert_combine_params &p, cudaStream_t stream);
+
 // TMA descriptors of x as [max(N_tok, 1)][d_model] and w as [F][d_model] bf16, box 64
 // columns x 128 rows, 128-byte swizzle.  Returns false on failure.
 bool make_qkvr_maps(const inkattn_qkvr_params &p, CUtensorMap *xmap, CUtensorMap *wmap);

@@ -1,0 +1,602 @@
+// linear.cu -- linear layers and the experts' grouped products on the 5th-generation tensor
+// cores (TMA + tcgen05/TMEM): bias, activation and residual in the GEMM's epilogue.
+//
+// [vLLM hỗ trợ TML Inkling ..., §TP sharding nhận biết sconv]: the output projection in front
+//  of the attention-output conv.
+// [SGLang と Miles が Inkling を初日からサポート, §Inkling のモデルアーキテクチャ]: the MoE's
+//  routed and shared experts.
+//
+// out[i][f] = act( sum_k x[s_i][k] w[e][f][k] + bias[e][f] ) + residual[i][f] over the rows i of
+// each expert e; a linear layer is the case of one expert that owns every row.
+//
+// Orientation.  The weight rows are the MMA's M side and the tokens its N side: a work item is
+// 256 weight rows times up to 256 tokens, computed by the two CTAs of a pair as one
+// M = 256 tile (tcgen05 cta_group::2), and N is the item's own token count rounded up to 32.
+// A decode batch or an expert with few rows thus pays for the rows it has (N = 32 takes an
+// eighth of the tensor time of N = 256), while the weights, which bound such a call, stream
+// through at full width.  Each CTA holds its own 128 weight rows and half of the tokens.
+//
+// The rows of a token tile are one box of x (a linear layer), or are gathered four at a time
+// by row index (grouped products): a gather costs what the tile's rows cost, and the copy of x
+// in expert order is never written.  SWIGLU: the CTA's 128 weight rows are 16 gate rows, the
+// 16 up rows of the same features, the next 16 gate rows ...; gate and up of a feature lie 16
+// lanes apart in one warp.
+//
+// One CTA per SM, 10 warps:
+//   warp 0      producer: copies of the weight rows and the token rows into a ring of stages
+//               of K = 64; as many stages as fit 192 KB
+//   warp 1      even CTA: MMA issuer, K = 16 steps into one of two TMEM accumulators (2 x 256
+//               columns), so that an item's epilogue overlaps the next item's MMAs
+//   warps 2-9   epilogue: a warp owns 32 TMEM lanes (weight rows) and every second block of 32
+//               columns (tokens); bias and activation per lane, then a turn through a private
+//               staging buffer, so that a token's features leave as 16-byte pieces
+// Both CTAs' copies of a stage complete on the even CTA's barrier, and the pair's commits
+// release it in both, as in the qkvr kernel.
+//
+// Few items (a decode batch): the K range is split over the S pairs of one cluster.  Each CTA
+// leaves its fp32 partial tile in its own shared memory (the ring, idle by then) and the
+// CTAs then add the S partials in order through distributed shared memory, each for its
+// share of the tokens: no workspace, no atomics, one launch.
+#include <atomic>
+#include <climits>
+
+#include "common.cuh"
+#include "conv4.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+#include "cta_pair.cuh"
+
+namespace inkattn {
+
+namespace {
+
+constexpr int kRowsA = 128;                       // weight rows of a CTA
+constexpr int kMaxN = 256;                        // tokens of an item
+constexpr int kKStep = 64;                        // K per ring stage (one 128-byte row)
+constexpr int kABytes = kRowsA * 128;             // 16 KB
+constexpr int kRingBytes = 192 * 1024;
+constexpr int kMaxStages = 12;
+constexpr int kThreads = 320;
+constexpr int kEpiThreads = 256;
+constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpEpi = 2;
+constexpr int kStgPitch = 36;                     // floats of a staging row: 32 features + 4
+constexpr int kStgBytes = 16 * kStgPitch * 4;     // 16 tokens, one buffer per epilogue warp
+constexpr int kRaster = 8;                        // feature blocks per raster group
+
+constexpr int kOffStg = kRingBytes;
+constexpr int kOffTiles = kOffStg + 8 * kStgBytes;                     // int tile prefix [E + 1]
+constexpr int kOffStart = kOffTiles + (INKATTN_MAX_EXPERTS + 1) * 4;   // int first row [E + 1]
+constexpr int kOffBar = (kOffStart + (INKATTN_MAX_EXPERTS + 1) * 4 + 7) / 8 * 8;
+enum Bar {
+    B_FULL = 0,
+    B_EMPTY = B_FULL + kMaxStages,
+    B_ACC_FULL = B_EMPTY + kMaxStages,
+    B_ACC_EMPTY = B_ACC_FULL + 2,
+    B_DRAIN = B_ACC_EMPTY + 2,
+    B_COUNT = B_DRAIN + 1
+};
+constexpr int kSmem = kOffBar + B_COUNT * 8 + 16;
+static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
+static_assert(kMaxN * kRowsA * 4 <= kRingBytes, "a split's partial tile lies in the ring");
+
+struct Item {
+    int e, row0, nt, n, fb;      // expert, first row, rows, MMA N (rows rounded up to 32), feature block
+};
+
+template <int kAct>
+__device__ __forceinline__ float activate(float v) {
+    if (kAct == INKATTN_ACT_RELU) return fmaxf(v, 0.f);
+    if (kAct == INKATTN_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    if (kAct == INKATTN_ACT_SILU) return v / (1.f + __expf(-v));
+    return v;
+}
+
+__device__ __forceinline__ void store_bf16(inkattn_bf16 *p, float v) {
+    *reinterpret_cast<__nv_bfloat16 *>(p) = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ float load_bf16(const inkattn_bf16 *p) { return __uint_as_float((uint32_t)*p << 16); }
+
+__device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
+}  // namespace
+
+template <int kAct>
+__global__ void __launch_bounds__(kThreads, 1)
+k_linear(const LinearArgs A, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap) {
+    constexpr bool kGated = kAct == INKATTN_ACT_SWIGLU;
+    constexpr int kFeat = kGated ? 64 : 128;           // output features of a CTA
+    extern __shared__ __align__(1024) unsigned char smem[];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t crank = cluster_ctarank();
+    const int half = (int)(crank & 1u);                // CTA of the pair
+    const uint32_t even = crank & ~1u;                 // the pair's even CTA
+    const int split = (int)(crank >> 1);               // which part of K this pair takes
+    const int cid = (int)blockIdx.x / (2 * A.splits), nclusters = (int)gridDim.x / (2 * A.splits);
+    const uint32_t s_base = smem_u32(smem);
+    if ((s_base & 1023u) != 0u) {                      // the same in every CTA
+        if (threadIdx.x == 0) set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    auto bar = [&](int i) { return s_base + kOffBar + 8u * (uint32_t)i; };
+    int *s_tiles = reinterpret_cast<int *>(smem + kOffTiles);
+    int *s_start = reinterpret_cast<int *>(smem + kOffStart);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffBar + B_COUNT * 8);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffBar + B_COUNT * 8 + 4);
+    auto cwait = [&](uint32_t addr, uint32_t parity) -> bool {
+        const bool r = mbar_wait_cluster(addr, parity, A.dev_status, abort_flag, A.wait_ns);
+        return __all_sync(0xffffffffu, r);
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < A.stages; ++s) {
+            mbar_init(bar(B_FULL + s), 1);             // (the even CTA's counts both CTAs' copies)
+            mbar_init(bar(B_EMPTY + s), 1);            // released by the pair's MMAs
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(B_ACC_FULL + s), 1);
+            mbar_init(bar(B_ACC_EMPTY + s), 16);       // every epilogue warp of both CTAs
+        }
+        mbar_init(bar(B_DRAIN), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kWarpMma) {                            // with the peer CTA's MMA warp
+        tc::tmem_alloc_pair(smem_u32(tmem_slot), 512);
+        tc::tmem_relinquish_pair();
+    }
+    if (warp == kWarpEpi) {
+        // first row of every expert and the prefix of token tiles: s_tiles[e] = tiles of experts 0 .. e-1
+        int carry = 0;
+        if (lane == 0) s_tiles[0] = 0;
+        for (int e0 = 0; e0 < A.E; e0 += 32) {
+            const int e = e0 + lane;
+            int tiles = 0;
+            if (e < A.E) {
+                const int start = A.offsets ? A.offsets[e] : 0, end = A.offsets ? A.offsets[e + 1] : A.M;
+                if (start < 0 || end < start || end > A.M) set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+                else tiles = (end - start + A.tile_n - 1) / A.tile_n;
+                s_start[e] = start;
+                if (e == A.E - 1) s_start[A.E] = end;
+            }
+            int v = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int n = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += n;
+            }
+            if (e < A.E) s_tiles[e + 1] = carry + v;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    cluster_sync();                                    // the peers' barriers exist
+    const uint32_t tmem = *tmem_slot;
+
+    const int n_items = s_tiles[A.E] * A.n_fblocks;    // (the host checked that it fits)
+    const int nk = (A.K + kKStep - 1) / kKStep;
+    const int k_lo = (int)((long long)nk * split / A.splits), k_hi = (int)((long long)nk * (split + 1) / A.splits);
+    auto item = [&](int w) {
+        Item it;
+        const int t = w / A.n_fblocks;
+        int lo = 0, hi = A.E;                          // s_tiles[lo] <= t < s_tiles[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_tiles[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        it.e = lo;
+        // the expert's items: groups of kRaster feature blocks, inside a group the token tiles
+        // one after another, so that the group's weights stay in L2 while they stream past
+        const int mt = s_tiles[lo + 1] - s_tiles[lo];
+        const int rem = w - s_tiles[lo] * A.n_fblocks;
+        const int grp = rem / (kRaster * mt), in = rem - grp * kRaster * mt;
+        const int gsz = min(kRaster, A.n_fblocks - grp * kRaster);
+        const int m = in / gsz;
+        it.fb = grp * kRaster + (in - m * gsz);
+        // tiles of near-equal size, a multiple of 32 rows
+        const int rows = s_start[lo + 1] - s_start[lo];
+        const int per = ((rows + mt - 1) / mt + 31) & ~31;
+        it.row0 = s_start[lo] + m * per;
+        it.nt = min(per, rows - m * per);
+        it.n = (it.nt + 31) & ~31;
+        return it;
+    };
+
+    if (warp == kWarpProducer) {
+        // ================================ producer ================================
+        const bool gather = A.offsets != nullptr;
+        int L = 0;                                     // stage loads issued
+        bool ok = true;
+        if (lane == 0) {
+            tma_prefetch_desc(&xmap);
+            tma_prefetch_desc(&wmap);
+        }
+        for (int w = cid; w < n_items && ok; w += nclusters) {
+            const Item it = item(w);
+            const int hn = it.n >> 1;                  // token slots of a CTA
+            // gathers of four rows in each half of the tile; this lane's four rows
+            const int g0 = (min(it.nt, hn) + 3) >> 2, g1 = (max(it.nt - hn, 0) + 3) >> 2;
+            const int mine = half ? g1 : g0;
+            int r[4] = {0, 0, 0, 0};
+            if (gather && lane < mine) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = it.row0 + min(half * hn + 4 * lane + j, it.nt - 1);
+                    r[j] = A.row_token ? __ldg(A.row_token + i) : i;
+                    if (r[j] < 0 || r[j] >= A.N_x) r[j] = 0;   // (flagged and not stored by the epilogue)
+                }
+            }
+            const uint32_t bytes = 2 * kABytes + (gather ? (uint32_t)(g0 + g1) * 512u : (uint32_t)A.tile_n * 128u);
+            for (int k = k_lo; k < k_hi; ++k, ++L) {
+                const int s = L % A.stages;
+                if (L >= A.stages && !cwait(bar(B_EMPTY + s), ((L / A.stages) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = s_base + (uint32_t)(s * A.stage_bytes);
+                const uint32_t fb = mapa_shared(bar(B_FULL + s), even);
+                if (half == 0 && lane == 0) mbar_arrive_expect_tx(bar(B_FULL + s), bytes);
+                __syncwarp();
+                if (kGated) {
+                    if (lane < 4)
+                        tma_load_5d_pair(dst + (uint32_t)lane * 4096u, &wmap, k * kKStep, 0,
+                                         it.fb * 8 + half * 4 + lane, 0, it.e, fb);
+                } else if (lane == 0) {
+                    tma_load_3d_pair(dst, &wmap, k * kKStep, it.fb * 256 + half * kRowsA, it.e, fb);
+                }
+                if (gather) {
+                    if (lane < mine)
+                        tma_gather4_pair(dst + kABytes + (uint32_t)lane * 512u, &xmap, k * kKStep, r[0], r[1], r[2],
+                                         r[3], fb);
+                } else if (lane == 0) {
+                    tma_load_2d_pair(dst + kABytes, &xmap, k * kKStep, it.row0 + half * hn, fb);
+                }
+                __syncwarp();
+            }
+        }
+        // nothing may still be landing in shared memory when the pair tears down (see qkvr.cu)
+        if (lane == 0 && half == 0)
+            for (int l = max(0, L - A.stages); l < L; ++l)
+                mbar_drain(bar(B_FULL + l % A.stages), (l / A.stages) & 1, A.dev_status, A.wait_ns);
+    } else if (warp == kWarpMma && half != 0) {
+        // the odd CTA issues no MMAs
+    } else if (warp == kWarpMma) {
+        // ================================ even CTA: MMA issuer ================================
+        const uint64_t da0 = tc::sdesc_sw128(s_base, 16, 1024);
+        const uint64_t db0 = tc::sdesc_sw128(s_base + kABytes, 16, 1024);
+        const uint16_t pair = (uint16_t)(3u << even);
+        // the last stages are not released, so that no arrival reaches a peer that has finished
+        const int my_items = cid < n_items ? (n_items - cid + nclusters - 1) / nclusters : 0;
+        const long long total = (long long)my_items * (k_hi - k_lo);
+        long long L = 0;
+        bool ok = true;
+        int i = 0;
+        for (int w = cid; w < n_items && ok; w += nclusters, ++i) {
+            const int buf = i & 1;
+            const uint32_t id = tc::idesc(2 * kRowsA, item(w).n, tc::kFmtBF16, 0, 0);
+            // both CTAs' epilogues are done with this accumulator
+            if (i >= 2 && !cwait(bar(B_ACC_EMPTY + buf), ((i >> 1) - 1) & 1)) {
+                ok = false;
+                break;
+            }
+            tc::fence_after();
+            for (int k = k_lo; k < k_hi; ++k, ++L) {
+                const int s = (int)(L % A.stages);
+                if (!cwait(bar(B_FULL + s), (uint32_t)((L / A.stages) & 1))) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                const uint64_t off = (uint64_t)(s * (A.stage_bytes >> 4));
+                tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)(buf * kMaxN), da0 + off, db0 + off, id,
+                                                k > k_lo ? 1u : 0u, bar(B_EMPTY + s), L + A.stages < total ? 1u : 0u,
+                                                bar(B_ACC_FULL + buf), k == k_hi - 1 ? 1u : 0u, pair);
+                __syncwarp();
+            }
+        }
+        // every MMA of the pair has completed before TMEM is released
+        tc::commit_pair(bar(B_DRAIN));
+        __syncwarp();
+        (void)mbar_drain(bar(B_DRAIN), 0, A.dev_status, A.wait_ns);
+        __syncwarp();
+    } else {
+        // ================================ epilogue ================================
+        const int e8 = (warp - kWarpEpi) >> 2;                // which of every two blocks of 32 tokens
+        const int quarter = warp & 3;                         // TMEM lanes this warp may access
+        float *stg = reinterpret_cast<float *>(smem + kOffStg + (warp - kWarpEpi) * kStgBytes);
+        const size_t F = (size_t)A.F;
+        inkattn_bf16 *out16 = static_cast<inkattn_bf16 *>(A.out);
+        float *out32 = static_cast<float *>(A.out);
+        // 16-byte pieces of a row start on 16-byte boundaries
+        const bool vec = A.out_f32 ? (A.F & 3) == 0 && (A.residual == nullptr || (A.F & 7) == 0) : (A.F & 7) == 0;
+        int i = 0;
+        for (int w = cid; w < n_items; w += nclusters, ++i) {
+            const Item it = item(w);
+            const int buf = i & 1;
+            // the warp's features, this lane's weight row and its bias
+            const int f0 = it.fb * 2 * kFeat + half * kFeat + (kGated ? quarter * 16 : quarter * 32);
+            const int frow = kGated ? f0 + (lane & 15) : f0 + lane;      // feature of the lane's weight row
+            float bias = 0.f;
+            if (A.bias && frow < A.F)
+                bias = __ldg(A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + (kGated && lane >= 16 ? F : 0) + frow);
+            const bool ok = mbar_wait_cluster(bar(B_ACC_FULL + buf), (uint32_t)((i >> 1) & 1), A.dev_status,
+                                              abort_flag, A.wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc::fence_after();
+            const uint32_t taddr = tmem + (uint32_t)(buf * kMaxN) + ((uint32_t)(quarter * 32) << 16);
+            auto release = [&] {
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_remote_arrive(bar(B_ACC_EMPTY + buf), even);   // its MMA warp waits
+            };
+            const int nblocks = (it.nt + 31) >> 5;
+            if (e8 >= nblocks) release();
+            for (int c = e8; c < nblocks; c += 2) {
+                uint32_t v[32];
+                tc::ld32(taddr + (uint32_t)(c * 32), v);
+                tc::wait_ld();
+                if (c + 2 >= nblocks) release();
+                if (A.splits > 1) {                           // the partial tile [token][weight row]
+                    float *part = reinterpret_cast<float *>(smem) + (size_t)c * 32 * kRowsA + quarter * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) part[j * kRowsA] = __uint_as_float(v[j]);
+                    continue;
+                }
+                // tokens of this block that are stored
+                bool mine = c * 32 + lane < it.nt;
+                if (A.row_token && mine) {
+                    const int t = __ldg(A.row_token + it.row0 + c * 32 + lane);
+                    if (t < 0 || t >= A.N_x) {
+                        mine = false;
+                        set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+                    }
+                }
+                const uint32_t live = __ballot_sync(0xffffffffu, mine);
+                const size_t row_b = (size_t)(it.row0 + c * 32);
+                if (kGated) {
+                    // lanes 0-15 hold gates, 16-31 the ups of the same features: of two tokens the
+                    // lower lanes finish the first, the upper lanes the second
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float a = __uint_as_float(v[j]) + bias, b = __uint_as_float(v[j + 1]) + bias;
+                        const float got = __shfl_xor_sync(0xffffffffu, lane < 16 ? b : a, 16);
+                        const float gate = lane < 16 ? a : got, up = lane < 16 ? got : b;
+                        const float y = activate<INKATTN_ACT_SILU>(gate) * up;
+                        stg[(j + (lane >> 4)) * 16 + (lane & 15)] = y;
+                    }
+                    __syncwarp();
+                    if (vec && !A.out_f32) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int t = q * 16 + (lane >> 1), f = f0 + (lane & 1) * 8;
+                            float y[8];
+                            *reinterpret_cast<float4 *>(y) = *reinterpret_cast<const float4 *>(stg + t * 16 + (lane & 1) * 8);
+                            *reinterpret_cast<float4 *>(y + 4) = *reinterpret_cast<const float4 *>(stg + t * 16 + (lane & 1) * 8 + 4);
+                            if (((live >> t) & 1u) && f < A.F) {
+                                const size_t o = (row_b + t) * F + f;
+                                if (A.residual) {
+                                    float r[8];
+                                    unpack8(*reinterpret_cast<const uint4 *>(A.residual + o), r);
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) y[j] += r[j];
+                                }
+                                *reinterpret_cast<uint4 *>(out16 + o) = pack8(y);
+                            }
+                        }
+                    } else {
+                        // (F is a multiple of 16: four features a lane)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int t = q * 8 + (lane >> 2), f = f0 + (lane & 3) * 4;
+                            float4 y = *reinterpret_cast<const float4 *>(stg + t * 16 + (lane & 3) * 4);
+                            if (((live >> t) & 1u) && f < A.F) {
+                                const size_t o = (row_b + t) * F + f;
+                                if (A.residual) {
+                                    y.x += load_bf16(A.residual + o); y.y += load_bf16(A.residual + o + 1);
+                                    y.z += load_bf16(A.residual + o + 2); y.w += load_bf16(A.residual + o + 3);
+                                }
+                                *reinterpret_cast<float4 *>(out32 + o) = y;
+                            }
+                        }
+                    }
+                } else if (vec) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {             // 16 tokens at a time
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            stg[j * kStgPitch + lane] = activate<kAct>(__uint_as_float(v[16 * h + j]) + bias);
+                        __syncwarp();
+                        if (!A.out_f32) {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const int t = q * 8 + (lane >> 2), f = f0 + (lane & 3) * 8;
+                                const float *src = stg + t * kStgPitch + (lane & 3) * 8;
+                                float y[8];
+                                *reinterpret_cast<float4 *>(y) = *reinterpret_cast<const float4 *>(src);
+                                *reinterpret_cast<float4 *>(y + 4) = *reinterpret_cast<const float4 *>(src + 4);
+                                if (((live >> (16 * h + t)) & 1u) && f < A.F) {
+                                    const size_t o = (row_b + 16 * h + t) * F + f;
+                                    if (A.residual) {
+                                        float r[8];
+                                        unpack8(*reinterpret_cast<const uint4 *>(A.residual + o), r);
+#pragma unroll
+                                        for (int j = 0; j < 8; ++j) y[j] += r[j];
+                                    }
+                                    *reinterpret_cast<uint4 *>(out16 + o) = pack8(y);
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int t = q * 4 + (lane >> 3), f = f0 + (lane & 7) * 4;
+                                float4 y = *reinterpret_cast<const float4 *>(stg + t * kStgPitch + (lane & 7) * 4);
+                                if (((live >> (16 * h + t)) & 1u) && f < A.F) {
+                                    const size_t o = (row_b + 16 * h + t) * F + f;
+                                    if (A.residual) {
+                                        const uint2 r = *reinterpret_cast<const uint2 *>(A.residual + o);
+                                        y.x += bf16_lo(r.x); y.y += bf16_hi(r.x);
+                                        y.z += bf16_lo(r.y); y.w += bf16_hi(r.y);
+                                    }
+                                    *reinterpret_cast<float4 *>(out32 + o) = y;
+                                }
+                            }
+                        }
+                    }
+                } else {
+                    // rows that start anywhere: a lane stores its own feature of each token
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (((live >> j) & 1u) && frow < A.F) {
+                            const size_t o = (row_b + j) * F + frow;
+                            float y = activate<kAct>(__uint_as_float(v[j]) + bias);
+                            if (A.residual) y += load_bf16(A.residual + o);
+                            if (A.out_f32) out32[o] = y;
+                            else store_bf16(out16 + o, y);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    if (A.splits > 1) {
+        __syncwarp();
+        cluster_sync();                                // every partial tile of the cluster is complete
+        const int et = (int)threadIdx.x - kWarpEpi * 32;
+        if (et >= 0 && cid < n_items) {
+            const Item it = item(cid);
+            const size_t F = (size_t)A.F;
+            // four features of one token per step; the cluster's pairs take the tokens in turn
+            constexpr int kPer = kFeat / 4;            // steps of a token
+            for (int u = et; u < ((it.nt - split + A.splits - 1) / A.splits) * kPer; u += kEpiThreads) {
+                const int t = (u / kPer) * A.splits + split, j = u % kPer;
+                const int f = it.fb * 2 * kFeat + half * kFeat + j * 4;
+                if (f >= A.F) continue;
+                const int i = it.row0 + t;
+                if (A.row_token) {
+                    const int s = __ldg(A.row_token + i);
+                    if (s < 0 || s >= A.N_x) {
+                        if (j == 0) set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+                        continue;
+                    }
+                }
+                const int lane0 = kGated ? (j >> 2) * 32 + (j & 3) * 4 : j * 4;
+                const uint32_t src = s_base + (uint32_t)((t * kRowsA + lane0) * 4);
+                float y[4] = {0.f, 0.f, 0.f, 0.f}, up[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int s = 0; s < A.splits; ++s) {
+                    const uint32_t a = mapa_shared(src, (uint32_t)(2 * s + half));
+                    const float4 p = ld_shared_cluster_f4(a);
+                    y[0] += p.x; y[1] += p.y; y[2] += p.z; y[3] += p.w;
+                    if (kGated) {
+                        const float4 q = ld_shared_cluster_f4(a + 64u);
+                        up[0] += q.x; up[1] += q.y; up[2] += q.z; up[3] += q.w;
+                    }
+                }
+                const float *b = A.bias ? A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + f : nullptr;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    if (f + n >= A.F) break;
+                    const float v = y[n] + (b ? __ldg(b + n) : 0.f);
+                    float o = activate<kGated ? INKATTN_ACT_SILU : kAct>(v);
+                    if (kGated) o *= up[n] + (b ? __ldg(b + F + n) : 0.f);
+                    const size_t at = (size_t)i * F + f + n;
+                    if (A.residual) o += load_bf16(A.residual + at);
+                    if (A.out_f32) static_cast<float *>(A.out)[at] = o;
+                    else store_bf16(static_cast<inkattn_bf16 *>(A.out) + at, o);
+                }
+            }
+        }
+    }
+
+    tc::fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {                            // with the peer CTA's MMA warp
+        tc::fence_after();
+        tc::tmem_dealloc_pair(tmem, 512);
+    }
+    cluster_sync();                  // a CTA leaves only when no peer writes into it or reads from it
+}
+
+namespace {
+
+using Kernel = void (*)(const LinearArgs, const CUtensorMap, const CUtensorMap);
+
+Kernel kernel_of(int act) {
+    switch (act) {
+        case INKATTN_ACT_RELU: return k_linear<INKATTN_ACT_RELU>;
+        case INKATTN_ACT_GELU: return k_linear<INKATTN_ACT_GELU>;
+        case INKATTN_ACT_SILU: return k_linear<INKATTN_ACT_SILU>;
+        case INKATTN_ACT_SWIGLU: return k_linear<INKATTN_ACT_SWIGLU>;
+        default: return k_linear<INKATTN_ACT_NONE>;
+    }
+}
+
+// Clusters of `ctas` CTAs that are resident at once (one CTA per SM; every activation's kernel
+// has the same launch shape).
+int resident_clusters(int ctas, int num_sms) {
+    static std::atomic<int> known[4];
+    std::atomic<int> &slot = known[ctas == 2 ? 0 : ctas == 4 ? 1 : 2];
+    int n = slot.load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ctas * (num_sms / ctas > 0 ? num_sms / ctas : 1)), 1, 1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)ctas;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k_linear<INKATTN_ACT_NONE>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    slot.store(n, std::memory_order_relaxed);
+    return n;
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStream_t stream) {
+    LinearArgs a = args;
+    const Kernel k = kernel_of(act);
+    cudaError_t err = cudaSuccess;
+    for (Kernel f : {k, kernel_of(INKATTN_ACT_NONE)})
+        if ((err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return err;
+    const int feat = act == INKATTN_ACT_SWIGLU ? 128 : 256;
+    a.n_fblocks = (a.F + feat - 1) / feat;
+    const int avg = a.M / a.E;
+    a.tile_n = a.E == 1 ? (a.M < kMaxN ? (a.M + 31) / 32 * 32 : kMaxN) : avg > 64 ? kMaxN : 128;
+    a.stage_bytes = kABytes + a.tile_n / 2 * 128;
+    a.stages = kRingBytes / a.stage_bytes < kMaxStages ? kRingBytes / a.stage_bytes : kMaxStages;
+    a.wait_ns = kernel_debug().wait_ns;
+    // at most this many items: full tiles, and one more for every expert that has rows
+    const long long items = ((long long)a.M / a.tile_n + (a.E < a.M ? a.E : a.M)) * a.n_fblocks;
+    if (items > INT_MAX / 2) return cudaErrorInvalidConfiguration;
+    const int nk = (a.K + kKStep - 1) / kKStep;
+    a.splits = 1;
+    for (int s = 2; s <= 4; s *= 2)
+        if (nk >= 4 * s && items <= resident_clusters(2 * s, num_sms)) a.splits = s;
+    const int most = resident_clusters(2 * a.splits, num_sms);
+    if (most < 1) return cudaErrorInvalidConfiguration;
+    const int clusters = (int)(items < most ? items : most);
+    CUtensorMap xmap, wmap;
+    if (!make_linear_maps(a, act == INKATTN_ACT_SWIGLU, &xmap, &wmap)) return cudaErrorInvalidValue;
+    return launch_dependent(k, dim3((unsigned)(2 * a.splits * clusters)), dim3(kThreads), kSmem, stream, 2 * a.splits, a,
+                            xmap, wmap);
+}
+
+}  // namespace inkattn

@@ -1,0 +1,332 @@
+// route.cu -- the router's choice of experts, and the weighted sum of the experts' rows.
+//
+// [SGLang と Miles が Inkling を初日からサポート, §Inkling のモデルアーキテクチャ]: sigmoid
+//  scores, the 6 best of 256 routed experts, 2 shared experts that join the normalisation of
+//  the weights but not the choice.
+//
+// Two launches.  k_route_choose: a warp per token holds the token's logits as ordered integer
+// keys in registers and takes the maximum top_k times (redux.sync on the key, then on the
+// index, so that equal logits go to the lower index).  k_route_place: a counting sort of the
+// (token, choice) pairs by expert, stable in (token, choice) order.  The order is made of
+// integer counts alone, so it does not depend on the scheduling:
+//   - the tokens are cut into chunks; a block places one chunk, and a warp a contiguous part
+//     of its pairs, 32 at a time (match.any gives a pair its rank among the 32);
+//   - a pair's row = offset of its expert + pairs of that expert in earlier chunks (each block
+//     adds up the counts that k_route_choose left per chunk), in earlier warps of the chunk
+//     and in earlier steps of the warp.
+// A batch that is one chunk needs no counts and no workspace.
+#include "common.cuh"
+#include "conv4.cuh"
+#include "internal.h"
+
+namespace inkattn {
+
+namespace {
+
+constexpr int kChooseThreads = 256;
+constexpr int kPlaceThreads = 1024;
+constexpr int kPlaceWarps = kPlaceThreads / 32;
+constexpr int kOneChunkPairs = 4096;               // pairs that one block places
+constexpr int kChunks = 152;                       // chunks of a larger batch, at most
+
+// Order-preserving integer key of a logit: larger logit, larger key; +0 and -0 alike; NaN as
+// -infinity.  Every logit's key is at least 0x007FFFFF, so 0 marks "taken" or "none".
+__device__ __forceinline__ uint32_t logit_key(float l) {
+    if (l != l) l = -INFINITY;
+    const uint32_t u = __float_as_uint(l + 0.0f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+}  // namespace
+
+// kPer = logits a lane holds (E <= 32 * kPer).  counts: [chunks][E], one row written by
+// each block, or NULL for a batch of one chunk.
+template <int kPer>
+__global__ void __launch_bounds__(kChooseThreads)
+k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *__restrict__ counts) {
+    extern __shared__ uint32_t s_hist[];               // [E], of this block's chunk
+    grid_dep_wait();
+    grid_dep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int width = p.E + p.n_shared, ws = p.top_k + p.n_shared;
+    if (counts) {
+        for (int e = threadIdx.x; e < p.E; e += kChooseThreads) s_hist[e] = 0;
+        __syncthreads();
+    }
+    const int t_lo = blockIdx.x * chunk_tokens, t_hi = min(p.N_tok, t_lo + chunk_tokens);
+    for (int t = t_lo + warp; t < t_hi; t += kChooseThreads / 32) {
+        const float *row = p.logits + (size_t)t * width;
+        uint32_t key[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = lane + 32 * i;
+            key[i] = e < p.E ? logit_key(__ldg(row + e)) : 0u;
+        }
+        // lane j < top_k: the j-th choice; the next n_shared lanes: the shared experts
+        float l = lane >= p.top_k && lane < ws ? __ldg(row + p.E + lane - p.top_k) : -INFINITY;
+        if (l != l) l = -INFINITY;
+        int id = 0;
+        for (int j = 0; j < p.top_k; ++j) {
+            uint32_t best = 0;
+            int at = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (key[i] > best) {
+                    best = key[i];
+                    at = i;
+                }
+            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+            const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(lane + 32 * at) : 0xffffffffu);
+            if (best == top && (uint32_t)(lane + 32 * at) == e) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (i == at) key[i] = 0;
+            }
+            if (lane == j) {
+                l = key_logit(top);
+                id = (int)e;
+            }
+        }
+        // scores up to a factor common to the token, so that they do not all vanish: softmax
+        // exp(l - m) with m the largest logit; sigmoid exp(l - m) / (1 + exp(l)) with m the
+        // largest logit or 0, whichever is less (for m = 0 that is the sigmoid itself)
+        float m = lane < ws ? l : -INFINITY;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const bool sigmoid = p.score == INKATTN_SCORE_SIGMOID;
+        if (sigmoid) m = fminf(m, 0.f);
+        float s = 0.f;
+        if (sigmoid && l > 0.f) s = 1.f / (1.f + expf(-l));
+        else if (l != -INFINITY) s = l == m ? 1.f : expf(l - m);         // (l == m: infinities too)
+        if (sigmoid && l <= 0.f) s = s / (1.f + expf(l));
+        float sum = lane < ws ? s : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane < ws) p.weights[(size_t)t * ws + lane] = sum > 0.f ? p.scale * (s / sum) : 0.f;
+        if (lane < p.top_k) {
+            p.topk_ids[(size_t)t * p.top_k + lane] = id;
+            if (counts) atomicAdd(&s_hist[id], 1u);    // (integers: the order does not show)
+        }
+    }
+    if (counts) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.E; e += kChooseThreads) counts[(size_t)blockIdx.x * p.E + e] = s_hist[e];
+    }
+}
+
+// One block per chunk.  Shared memory: base[E] (first row of the expert's pairs of this chunk),
+// scratch[2 kPlaceThreads], hist[kPlaceWarps][E] (16 bits: with 2^28 pairs in 152 chunks of 32
+// warps, a warp has fewer than 65536).
+__global__ void __launch_bounds__(kPlaceThreads)
+k_route_place(const inkattn_route_params p, int chunk_tokens, const uint32_t *__restrict__ counts) {
+    extern __shared__ uint32_t sm[];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int E = p.E, k = p.top_k;
+    uint32_t *base = sm, *scratch = sm + E;
+    uint16_t *hist = reinterpret_cast<uint16_t *>(scratch + 2 * kPlaceThreads);
+    for (int i = tid; i < kPlaceWarps * E; i += kPlaceThreads) hist[i] = 0;
+    __syncthreads();
+
+    // pairs of this warp: a contiguous part of the chunk, whole groups of 32
+    const long long q_lo = (long long)blockIdx.x * chunk_tokens * k;
+    const long long q_hi = min((long long)p.N_tok, (long long)(blockIdx.x + 1) * chunk_tokens) * k;
+    const int pairs = (int)max(q_hi - q_lo, 0ll);
+    const int per = ((pairs + kPlaceWarps - 1) / kPlaceWarps + 31) & ~31;
+    const int w_lo = min(pairs, warp * per), w_hi = min(pairs, w_lo + per);
+    uint16_t *mine = hist + warp * E;
+    for (int g = w_lo; g < w_hi; g += 32) {
+        const bool in = g + lane < w_hi;
+        const int e = in ? p.topk_ids[q_lo + g + lane] : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        if (in && lane == __ffs(same) - 1) mine[e] = (uint16_t)(mine[e] + __popc(same));
+        __syncwarp();
+    }
+    __syncthreads();
+
+    // per expert: pairs in earlier chunks, pairs in all chunks; then the prefix over the warps
+    uint32_t total = 0, before = 0;
+    if (counts) {
+        // several threads an expert, each over a part of the chunks
+        const int parts = max(1, kPlaceThreads / E), e = tid % E, part = tid / E;
+        const int chunks = gridDim.x;
+        const bool act = part < parts && E <= kPlaceThreads;
+        if (act) {
+            for (int c = part; c < chunks; c += parts) {
+                const uint32_t n = __ldg(counts + (size_t)c * E + e);
+                total += n;
+                before += c < (int)blockIdx.x ? n : 0u;
+            }
+            scratch[2 * tid] = total;
+            scratch[2 * tid + 1] = before;
+        }
+        __syncthreads();
+        total = before = 0;
+        if (tid < E) {
+            for (int q = 0; q < parts; ++q) {
+                total += scratch[2 * (q * E + tid)];
+                before += scratch[2 * (q * E + tid) + 1];
+            }
+        }
+        __syncthreads();
+    }
+    if (tid < E) {
+        uint32_t run = 0;
+        for (int w = 0; w < kPlaceWarps; ++w) {
+            const uint32_t n = hist[w * E + tid];
+            hist[w * E + tid] = (uint16_t)run;
+            run += n;
+        }
+        if (!counts) total = run;
+    }
+    // exclusive prefix of the totals over the experts
+    uint32_t v = tid < E ? total : 0u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t n = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += n;
+    }
+    if (lane == 31) scratch[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        uint32_t s = scratch[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t n = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += n;
+        }
+        scratch[lane] = s;
+    }
+    __syncthreads();
+    if (tid < E) {
+        const uint32_t incl = v + (warp > 0 ? scratch[warp - 1] : 0u);
+        base[tid] = incl - total + before;
+        if (blockIdx.x == 0) {
+            p.expert_offsets[tid + 1] = (int32_t)incl;
+            if (tid == 0) p.expert_offsets[0] = 0;
+        }
+    }
+    __syncthreads();
+
+    for (int g = w_lo; g < w_hi; g += 32) {
+        const bool in = g + lane < w_hi;
+        const long long q = q_lo + g + lane;
+        const int e = in ? p.topk_ids[q] : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        uint32_t row = 0;
+        if (in) row = base[e] + mine[e] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (in && lane == __ffs(same) - 1) mine[e] = (uint16_t)(mine[e] + __popc(same));
+        __syncwarp();
+        if (in) {
+            p.row_token[row] = (int32_t)(q / k);
+            p.token_rows[q] = (int32_t)row;
+        }
+    }
+}
+
+static bool one_chunk(const inkattn_route_params &p) { return (long long)p.N_tok * p.top_k <= kOneChunkPairs; }
+static int chunk_tokens(const inkattn_route_params &p) {
+    const int t = (p.N_tok + kChunks - 1) / kChunks;
+    return t < 32 ? 32 : t;
+}
+
+size_t route_workspace_bytes(const inkattn_route_params &p) {
+    if (one_chunk(p)) return 0;
+    const int t = chunk_tokens(p);
+    return (size_t)((p.N_tok + t - 1) / t) * p.E * 4;
+}
+
+cudaError_t launch_route(const inkattn_route_params &p, uint32_t *ws, cudaStream_t stream) {
+    const bool one = one_chunk(p);
+    // the choice of a small batch: a token per warp
+    const int choose_tokens = one ? kChooseThreads / 32 : chunk_tokens(p);
+    const int place_tokens = one ? (p.N_tok > 0 ? p.N_tok : 1) : chunk_tokens(p);
+    uint32_t *counts = one ? nullptr : ws;
+    cudaError_t err = cudaSuccess;
+    if (p.N_tok > 0) {
+        const dim3 grid((unsigned)((p.N_tok + choose_tokens - 1) / choose_tokens));
+        const size_t smem = one ? 0 : (size_t)p.E * 4;
+        auto go = [&](auto kernel) {
+            return launch_dependent(kernel, grid, dim3(kChooseThreads), smem, stream, 1, p, choose_tokens, counts);
+        };
+        err = p.E <= 64 ? go(k_route_choose<2>) : p.E <= 128 ? go(k_route_choose<4>) : p.E <= 256
+            ? go(k_route_choose<8>) : p.E <= 512 ? go(k_route_choose<16>) : go(k_route_choose<32>);
+        if (err != cudaSuccess) return err;
+    }
+    const size_t smem = (size_t)p.E * 4 + 2 * kPlaceThreads * 4 + (size_t)kPlaceWarps * p.E * 2;
+    err = cudaFuncSetAttribute(k_route_place, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               INKATTN_MAX_EXPERTS * 4 + 2 * kPlaceThreads * 4 + kPlaceWarps * INKATTN_MAX_EXPERTS * 2);
+    if (err != cudaSuccess) return err;
+    const dim3 grid((unsigned)(one ? 1 : (p.N_tok + place_tokens - 1) / place_tokens));
+    return launch_dependent(k_route_place, grid, dim3(kPlaceThreads), smem, stream, 1, p, place_tokens,
+                            static_cast<const uint32_t *>(counts));
+}
+
+// ---------------------------------------------------------------- the weighted sum
+// HBM-bound: top_k + n_shared rows read and one written per token.  A thread owns 8 features
+// of one token (a 16-byte piece of every row) and requests up to eight rows before it uses
+// the first; the sum is taken in fp32 in the order of the choices.
+
+namespace {
+constexpr int kSumThreads = 128;
+constexpr int kSumRows = 8;                        // rows requested at once
+}  // namespace
+
+__global__ void __launch_bounds__(kSumThreads)
+k_expert_combine(const inkattn_expert_combine_params p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int G = p.F >> 3;                            // 16-byte pieces of a row
+    const int blocks = (G + kSumThreads - 1) / kSumThreads;
+    const long long t = (long long)blockIdx.x / blocks;
+    const int g = (int)(blockIdx.x - t * blocks) * kSumThreads + threadIdx.x;
+    if (g >= G) return;
+    const int rows = p.top_k + p.n_shared;
+    const float *w = p.weights + t * rows;
+    const int32_t *tr = p.token_rows + t * p.top_k;
+    const uint4 *y = reinterpret_cast<const uint4 *>(p.y), *sh = reinterpret_cast<const uint4 *>(p.shared);
+    float acc[8] = {};
+    for (int j0 = 0; j0 < rows; j0 += kSumRows) {
+        uint4 v[kSumRows];
+        float c[kSumRows];
+#pragma unroll
+        for (int i = 0; i < kSumRows; ++i) {
+            const int j = j0 + i;
+            v[i] = make_uint4(0, 0, 0, 0);
+            c[i] = 0.f;
+            if (j >= rows) continue;
+            if (j < p.top_k) {
+                const int r = __ldg(tr + j);
+                if (r >= 0 && r < p.M) {
+                    c[i] = __ldg(w + j);
+                    v[i] = __ldcs(y + (size_t)r * G + g);
+                } else if (r != -1 && g == 0) {
+                    set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+                }
+            } else {
+                c[i] = __ldg(w + j);
+                v[i] = __ldcs(sh + ((size_t)(j - p.top_k) * p.N_tok + t) * G + g);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kSumRows; ++i) {
+            float x[8];
+            unpack8(v[i], x);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) acc[n] = fmaf(c[i], x[n], acc[n]);
+        }
+    }
+    reinterpret_cast<uint4 *>(p.out)[t * G + g] = pack8(acc);
+}
+
+cudaError_t launch_expert_combine(const inkattn_expert_combine_params &p, cudaStream_t stream) {
+    const long long blocks = (long long)p.N_tok * ((p.F / 8 + kSumThreads - 1) / kSumThreads);
+    return launch_dependent(k_expert_combine, dim3((unsigned)blocks), dim3(kSumThreads), 0, stream, 1, p);
+}
+
+}  // namespace inkattn

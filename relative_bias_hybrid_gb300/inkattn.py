@@ -28,6 +28,13 @@ INKATTN_DTYPE_BF16 = 0
 INKATTN_DTYPE_F32 = 1
 INKATTN_KV_BF16 = 0
 INKATTN_KV_E4M3 = 1
+INKATTN_ACT_NONE = 0
+INKATTN_ACT_RELU = 1
+INKATTN_ACT_GELU = 2
+INKATTN_ACT_SILU = 3
+INKATTN_ACT_SWIGLU = 4
+INKATTN_SCORE_SIGMOID = 0
+INKATTN_SCORE_SOFTMAX = 1
 
 _c_i32 = ctypes.c_int32
 _c_ptr = ctypes.c_void_p
@@ -94,6 +101,48 @@ class QkvrParams(ctypes.Structure):
     ]
 
 
+class LinearParams(ctypes.Structure):
+    """inkattn_linear_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("N_tok", _c_i32), ("K", _c_i32), ("F", _c_i32), ("act", _c_i32), ("out_dtype", _c_i32),
+        ("x", _c_ptr), ("w", _c_ptr), ("bias", _c_ptr), ("residual", _c_ptr), ("out", _c_ptr),
+        ("dev_status", _c_ptr),
+    ]
+
+
+class GroupedLinearParams(ctypes.Structure):
+    """inkattn_grouped_linear_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("E", _c_i32), ("M", _c_i32), ("N_x", _c_i32), ("K", _c_i32), ("F", _c_i32), ("act", _c_i32),
+        ("out_dtype", _c_i32),
+        ("x", _c_ptr), ("w", _c_ptr), ("bias", _c_ptr), ("expert_offsets", _c_ptr),
+        ("row_token", _c_ptr), ("out", _c_ptr), ("dev_status", _c_ptr),
+    ]
+
+
+class RouteParams(ctypes.Structure):
+    """inkattn_route_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("N_tok", _c_i32), ("E", _c_i32), ("n_shared", _c_i32), ("top_k", _c_i32), ("score", _c_i32),
+        ("scale", ctypes.c_float),
+        ("logits", _c_ptr), ("topk_ids", _c_ptr), ("weights", _c_ptr), ("expert_offsets", _c_ptr),
+        ("row_token", _c_ptr), ("token_rows", _c_ptr),
+    ]
+
+
+class ExpertCombineParams(ctypes.Structure):
+    """inkattn_expert_combine_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("N_tok", _c_i32), ("M", _c_i32), ("F", _c_i32), ("top_k", _c_i32), ("n_shared", _c_i32),
+        ("y", _c_ptr), ("shared", _c_ptr), ("weights", _c_ptr), ("token_rows", _c_ptr), ("out", _c_ptr),
+        ("dev_status", _c_ptr),
+    ]
+
+
 class InkattnError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -141,6 +190,16 @@ def lib():
             L.inkattn_prefill_workspace_bytes.restype = ctypes.c_size_t
             L.inkattn_prefill_e4m3.argtypes = [P(AttnParams), _c_ptr, ctypes.c_size_t, _c_ptr]
             L.inkattn_prefill_e4m3.restype = ctypes.c_int
+            L.inkattn_linear.argtypes = [P(LinearParams), _c_ptr]
+            L.inkattn_linear.restype = ctypes.c_int
+            L.inkattn_grouped_linear.argtypes = [P(GroupedLinearParams), _c_ptr]
+            L.inkattn_grouped_linear.restype = ctypes.c_int
+            L.inkattn_route_workspace_bytes.argtypes = [P(RouteParams)]
+            L.inkattn_route_workspace_bytes.restype = ctypes.c_size_t
+            L.inkattn_route.argtypes = [P(RouteParams), _c_ptr, ctypes.c_size_t, _c_ptr]
+            L.inkattn_route.restype = ctypes.c_int
+            L.inkattn_expert_combine.argtypes = [P(ExpertCombineParams), _c_ptr]
+            L.inkattn_expert_combine.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -235,6 +294,32 @@ def inkattn_output_conv(p: OutputConvParams, stream=None, raise_on_error=True) -
 
 def inkattn_qkvr_prologue(p: QkvrParams, stream=None, raise_on_error=True) -> int:
     return _check(lib().inkattn_qkvr_prologue(ctypes.byref(p), _stream(stream)), "inkattn_qkvr_prologue",
+                  raise_on_error)
+
+
+def inkattn_linear(p: LinearParams, stream=None, raise_on_error=True) -> int:
+    return _check(lib().inkattn_linear(ctypes.byref(p), _stream(stream)), "inkattn_linear", raise_on_error)
+
+
+def inkattn_grouped_linear(p: GroupedLinearParams, stream=None, raise_on_error=True) -> int:
+    return _check(lib().inkattn_grouped_linear(ctypes.byref(p), _stream(stream)), "inkattn_grouped_linear",
+                  raise_on_error)
+
+
+def inkattn_route_workspace_bytes(p: RouteParams) -> int:
+    return int(lib().inkattn_route_workspace_bytes(ctypes.byref(p)))
+
+
+def inkattn_route(p: RouteParams, workspace: Optional[torch.Tensor] = None, stream=None,
+                  raise_on_error=True) -> int:
+    ptr = workspace.data_ptr() if workspace is not None else None
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return _check(lib().inkattn_route(ctypes.byref(p), ptr, nbytes, _stream(stream)), "inkattn_route",
+                  raise_on_error)
+
+
+def inkattn_expert_combine(p: ExpertCombineParams, stream=None, raise_on_error=True) -> int:
+    return _check(lib().inkattn_expert_combine(ctypes.byref(p), _stream(stream)), "inkattn_expert_combine",
                   raise_on_error)
 
 
@@ -398,5 +483,111 @@ def qkvr_params(*, x, w, conv_w_k, conv_w_v, q_norm_w, k_norm_w, cu_seqlens_q, s
     p.k_cache = _ptr(k_cache, cache_dt, "k_cache"); p.v_cache = _ptr(v_cache, cache_dt, "v_cache")
     if p.kv_dtype == INKATTN_KV_E4M3:
         p.k_scale = _ptr(k_scale, f32, "k_scale"); p.v_scale = _ptr(v_scale, f32, "v_scale")
+    p.dev_status = _ptr(dev_status, i32, "dev_status")
+    return p
+
+
+ACTIVATIONS = {"none": INKATTN_ACT_NONE, "relu": INKATTN_ACT_RELU, "gelu": INKATTN_ACT_GELU,
+               "silu": INKATTN_ACT_SILU, "swiglu": INKATTN_ACT_SWIGLU}
+SCORES = {"sigmoid": INKATTN_SCORE_SIGMOID, "softmax": INKATTN_SCORE_SOFTMAX}
+
+
+def _out_dtype(out):
+    if out.dtype == torch.float32:
+        return INKATTN_DTYPE_F32
+    if out.dtype == torch.bfloat16:
+        return INKATTN_DTYPE_BF16
+    raise TypeError(f"out: expected bfloat16 or float32, got {out.dtype}")
+
+
+def _shape(t, shape, name):
+    """The sizes a params struct holds once must be those of every tensor that has them."""
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def linear_params(*, x, w, out, act: str = "none", bias=None, residual=None, dev_status=None) -> LinearParams:
+    """Fill an inkattn_linear_params from torch tensors (see include/inkattn.h): x [N][K],
+    w [F][K] (act "swiglu": [2F][K], the gate rows first), bias fp32 None or one per row of w,
+    residual None or [N][F], out [N][F] bf16 or fp32."""
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    N, K = x.shape
+    F = out.shape[1]
+    rows = 2 * F if act == "swiglu" else F
+    _shape(w, (rows, K), "w"); _shape(out, (N, F), "out"); _shape(bias, (rows,), "bias")
+    _shape(residual, (N, F), "residual")
+    p = LinearParams()
+    p.struct_size = ctypes.sizeof(LinearParams)
+    p.N_tok, p.K, p.F = N, K, F
+    p.act = ACTIVATIONS[act]
+    p.out_dtype = _out_dtype(out)
+    p.x = _ptr(x, bf, "x"); p.w = _ptr(w, bf, "w")
+    p.bias = _ptr(bias, f32, "bias"); p.residual = _ptr(residual, bf, "residual")
+    p.out = _ptr(out, None, "out")
+    p.dev_status = _ptr(dev_status, i32, "dev_status")
+    return p
+
+
+def grouped_linear_params(*, x, w, expert_offsets, out, act: str = "none", row_token=None, bias=None,
+                          dev_status=None) -> GroupedLinearParams:
+    """Fill an inkattn_grouped_linear_params from torch tensors (see include/inkattn.h):
+    x [N_x][K], w [E][F][K] (act "swiglu": [E][2F][K]), expert_offsets [E+1], row_token None or
+    [M], bias None or [E][rows of w], out [M][F] bf16 or fp32."""
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    N_x, K = x.shape
+    M, F = out.shape
+    E = w.shape[0]
+    rows = 2 * F if act == "swiglu" else F
+    _shape(w, (E, rows, K), "w"); _shape(expert_offsets, (E + 1,), "expert_offsets")
+    _shape(row_token, (M,), "row_token"); _shape(bias, (E, rows), "bias")
+    p = GroupedLinearParams()
+    p.struct_size = ctypes.sizeof(GroupedLinearParams)
+    p.E, p.M, p.N_x, p.K, p.F = E, M, N_x, K, F
+    p.act = ACTIVATIONS[act]
+    p.out_dtype = _out_dtype(out)
+    p.x = _ptr(x, bf, "x"); p.w = _ptr(w, bf, "w"); p.bias = _ptr(bias, f32, "bias")
+    p.expert_offsets = _ptr(expert_offsets, i32, "expert_offsets")
+    p.row_token = _ptr(row_token, i32, "row_token")
+    p.out = _ptr(out, None, "out")
+    p.dev_status = _ptr(dev_status, i32, "dev_status")
+    return p
+
+
+def route_params(*, logits, topk_ids, weights, expert_offsets, row_token, token_rows, n_shared: int = 0,
+                 score: str = "sigmoid", scale: float = 1.0) -> RouteParams:
+    """Fill an inkattn_route_params from torch tensors (see include/inkattn.h): logits
+    [N][E + n_shared], topk_ids [N][k], weights [N][k + n_shared], expert_offsets [E+1],
+    row_token [N*k], token_rows [N][k]."""
+    f32, i32 = torch.float32, torch.int32
+    N, k = topk_ids.shape
+    E = logits.shape[1] - int(n_shared)
+    _shape(logits, (N, E + n_shared), "logits"); _shape(weights, (N, k + n_shared), "weights")
+    _shape(expert_offsets, (E + 1,), "expert_offsets"); _shape(row_token, (N * k,), "row_token")
+    _shape(token_rows, (N, k), "token_rows")
+    p = RouteParams()
+    p.struct_size = ctypes.sizeof(RouteParams)
+    p.N_tok, p.E, p.n_shared, p.top_k = N, E, int(n_shared), k
+    p.score = SCORES[score]
+    p.scale = float(scale)
+    p.logits = _ptr(logits, f32, "logits"); p.topk_ids = _ptr(topk_ids, i32, "topk_ids")
+    p.weights = _ptr(weights, f32, "weights")
+    p.expert_offsets = _ptr(expert_offsets, i32, "expert_offsets")
+    p.row_token = _ptr(row_token, i32, "row_token"); p.token_rows = _ptr(token_rows, i32, "token_rows")
+    return p
+
+
+def expert_combine_params(*, y, weights, token_rows, out, shared=None, dev_status=None) -> ExpertCombineParams:
+    """Fill an inkattn_expert_combine_params from torch tensors (see include/inkattn.h): y [M][F],
+    weights [N][k + n_shared], token_rows [N][k], shared None or [n_shared][N][F], out [N][F]."""
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    M, F = y.shape
+    N, k = token_rows.shape
+    S = shared.shape[0] if shared is not None else 0
+    _shape(weights, (N, k + S), "weights"); _shape(out, (N, F), "out"); _shape(shared, (S, N, F), "shared")
+    p = ExpertCombineParams()
+    p.struct_size = ctypes.sizeof(ExpertCombineParams)
+    p.N_tok, p.M, p.F, p.top_k, p.n_shared = N, M, F, k, S
+    p.y = _ptr(y, bf, "y"); p.shared = _ptr(shared, bf, "shared"); p.weights = _ptr(weights, f32, "weights")
+    p.token_rows = _ptr(token_rows, i32, "token_rows"); p.out = _ptr(out, bf, "out")
     p.dev_status = _ptr(dev_status, i32, "dev_status")
     return p

@@ -1,0 +1,441 @@
+"""GPU parity of the linear layer, the grouped expert products, the router and the weighted
+sum against plain 64-bit forms (torch float64 on the CPU).
+
+Bars.  On grid inputs (x = i/8, w = j/64, bias and residual multiples of 2^-9, all small) every
+partial sum is a multiple of 2^-9 below 2^14, so it is exact in fp32 in any order: the products
+without a curved activation must then be bit-equal to the rounded 64-bit value, whatever the
+tile, the split or the path of the store.  With a curved activation the fp32 argument v is still
+exact and the tolerance is the rounding of the output (half a step) plus the fp32 evaluation of
+the curve, see _curve_slack.  On Gaussian inputs the sum itself is rounded: K fp32 additions, each
+off by at most one step (2^-23) of the sum of magnitudes."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, I32, F64 = torch.bfloat16, torch.float32, torch.int32, torch.float64
+HALF_STEP = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+
+
+@pytest.fixture(scope="module")
+def ia():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from relative_bias_hybrid_gb300 import build
+    build.build()
+    import relative_bias_hybrid_gb300.inkattn as ia
+    return ia
+
+
+def _grid(shape, g, lo, hi, unit, dtype=BF16):
+    return (torch.randint(lo, hi + 1, shape, generator=g).to(F64) * unit).to(dtype)
+
+
+def _act64(v, act):
+    if act == "relu":
+        return v.clamp(min=0)
+    if act == "gelu":
+        return 0.5 * v * torch.special.erfc(-v / 2 ** 0.5)
+    if act == "silu":
+        return v * torch.sigmoid(v)
+    if act == "swiglu":
+        a, b = v.chunk(2, dim=-1)
+        return a * torch.sigmoid(a) * b
+    return v
+
+
+def _curve_slack(v, act):
+    """Absolute error of the fp32 curve at an exact argument v.  __expf is within 2 + 1.173 |x|
+    units of 2^-23 of exp(x) (its documented bound), the sum 1 + exp and the division add a unit
+    each: silu is within (4 + 1.2 |v|) 2^-23 |silu|, and below -87 the exp leaves fp32's range,
+    where silu is under 1e-36.  erff is within 2 units of 2^-23 of a value up to 1; 1 + erf and
+    two products follow: gelu is within 4 * 2^-23 |v|."""
+    if act == "gelu":
+        return 4 * 2.0 ** -23 * v.abs()
+    if act == "silu":
+        return (4 + 1.2 * v.abs()) * 2.0 ** -23 * _act64(v, "silu").abs() + 1e-36
+    if act == "swiglu":
+        a, b = v.chunk(2, dim=-1)
+        return (5 + 1.2 * a.abs()) * 2.0 ** -23 * _act64(v, "swiglu").abs() + 1e-36 * b.abs()
+    return torch.zeros_like(v)
+
+
+def _check(got, v, act, residual=None, sum_slack=None):
+    """got [N][F] against act(v) + residual, v exact or off by at most sum_slack."""
+    y = _act64(v, act)
+    slack = _curve_slack(v, act)
+    if sum_slack is not None:
+        # every curve here has a slope below 1.13; of the product both factors move
+        if act == "swiglu":
+            a, b = v.chunk(2, dim=-1)
+            sa, sb = sum_slack.chunk(2, dim=-1)
+            slack = slack + 1.13 * sa * b.abs() + (a.abs() + sa) * sb
+        else:
+            slack = slack + 1.13 * sum_slack
+    if residual is not None:
+        y = y + residual
+        slack = slack + 2.0 ** -24 * (y.abs() + slack)          # the fp32 addition
+    if act in ("none", "relu") and sum_slack is None:
+        assert torch.equal(got.cpu(), y.to(F32).to(got.dtype))
+        return
+    err = (got.cpu().to(F64) - y).abs()
+    # (the smallest normal numbers: results below them may be flushed)
+    bound = slack + HALF_STEP[got.dtype] * (y.abs() + slack) + 2.0 ** -126
+    assert bool((err <= bound).all()), float((err - bound).max())
+
+
+def _linear_inputs(T, K, F, act, seed, grid=True):
+    g = torch.Generator().manual_seed(seed)
+    rows = 2 * F if act == "swiglu" else F
+    if grid:
+        return (_grid((T, K), g, -8, 8, 1 / 8), _grid((rows, K), g, -8, 8, 1 / 64),
+                _grid((rows,), g, -512, 512, 2.0 ** -9, F32), _grid((T, F), g, -64, 64, 1 / 8))
+    return (torch.randn((T, K), generator=g).to(BF16), (torch.randn((rows, K), generator=g) * K ** -0.5).to(BF16),
+            torch.randn((rows,), generator=g), torch.randn((T, F), generator=g).to(BF16))
+
+
+def _run_linear(ia, x, w, bias, residual, act, dtype, F, stream=None):
+    N = x.shape[0]
+    # the output sits between two guard rows that must stay as they are
+    buf = torch.full(((N + 2) * F + 16,), 7.0, dtype=dtype, device="cuda")
+    lead = (F + 15) // 16 * 16
+    out = buf[lead:lead + N * F].view(N, F)
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    dev = [t.cuda() if t is not None else None for t in (x, w, bias, residual)]
+    p = ia.linear_params(x=dev[0], w=dev[1], out=out, act=act, bias=dev[2], residual=dev[3], dev_status=status)
+    torch.cuda.synchronize()
+    ia.inkattn_linear(p, stream)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    assert bool((buf[:lead] == 7).all()) and bool((buf[lead + N * F:] == 7).all())
+    return out
+
+
+SIZES = [(1, 8, 1), (1, 8, 8), (1, 64, 256), (1, 4096, 2048), (2, 72, 7), (3, 520, 129), (9, 128, 250),
+         (31, 200, 64), (32, 64, 128), (33, 1000, 264), (64, 2048, 512), (127, 56, 15), (160, 328, 1021),
+         (256, 256, 256), (257, 512, 300), (288, 1024, 1024), (513, 192, 520), (1100, 96, 2600)]
+
+
+@pytest.mark.parametrize("T,K,F", SIZES)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_linear_exact_on_grid_inputs(ia, T, K, F, dtype):
+    x, w, bias, residual = _linear_inputs(T, K, F, "none", seed=T + K + F)
+    v = x.double() @ w.double().t()
+    _check(_run_linear(ia, x, w, None, None, "none", dtype, F), v, "none")
+    v = v + bias.double()
+    _check(_run_linear(ia, x, w, bias, residual, "none", dtype, F), v, "none", residual.double())
+    _check(_run_linear(ia, x, w, bias, None, "relu", dtype, F), v, "relu")
+
+
+@pytest.mark.parametrize("T,K,F", [(1, 8, 1), (1, 4096, 2048), (9, 128, 250), (33, 1000, 264), (300, 512, 1021)])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_linear_curved_activations(ia, T, K, F, act):
+    x, w, bias, residual = _linear_inputs(T, K, F, act, seed=7 * T + F)
+    v = x.double() @ w.double().t() + bias.double()
+    for dtype in (BF16, F32):
+        _check(_run_linear(ia, x, w, bias, None, act, dtype, F), v, act)
+        _check(_run_linear(ia, x, w, bias, residual, act, dtype, F), v, act, residual.double())
+
+
+@pytest.mark.parametrize("T,K,F", [(1, 8, 16), (1, 2048, 1024), (9, 128, 48), (33, 1000, 272), (300, 512, 1040)])
+def test_linear_swiglu(ia, T, K, F):
+    x, w, bias, residual = _linear_inputs(T, K, F, "swiglu", seed=11 * T + F)
+    v = x.double() @ w.double().t()
+    for dtype in (BF16, F32):
+        _check(_run_linear(ia, x, w, None, None, "swiglu", dtype, F), v, "swiglu")
+        _check(_run_linear(ia, x, w, bias, residual, "swiglu", dtype, F), v + bias.double(), "swiglu",
+               residual.double())
+
+
+@pytest.mark.parametrize("T,K,F,act", [(1, 8192, 512, "none"), (40, 8192, 512, "swiglu"), (700, 2048, 777, "gelu")])
+def test_linear_gaussian(ia, T, K, F, act):
+    x, w, bias, residual = _linear_inputs(T, K, F, act, seed=5, grid=False)
+    v = x.double() @ w.double().t() + bias.double()
+    mags = x.double().abs() @ w.double().abs().t() + bias.double().abs()
+    for dtype in (BF16, F32):
+        _check(_run_linear(ia, x, w, bias, residual, act, dtype, F), v, act, residual.double(),
+               sum_slack=(K + 1) * 2.0 ** -23 * mags)
+
+
+def test_linear_in_place_residual_and_infinities(ia):
+    """out == residual; infinities and NaN stay in their own token's row."""
+    T, K, F = 40, 128, 264
+    x, w, bias, residual = _linear_inputs(T, K, F, "none", seed=3)
+    x[5, 7] = float("inf"); x[6, 1] = float("nan")
+    dev = [t.cuda() for t in (x, w, bias, residual)]
+    ia.inkattn_linear(ia.linear_params(x=dev[0], w=dev[1], bias=dev[2], residual=dev[3], out=dev[3]))
+    torch.cuda.synchronize()
+    want = (x.double() @ w.double().t() + bias.double() + residual.double()).to(F32).to(BF16)
+    got = dev[3].cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got.float()), torch.nan_to_num(want.float()))
+
+
+def test_linear_no_tokens_and_repeatability(ia):
+    x, w, bias, residual = [t.cuda() for t in _linear_inputs(64, 4096, 512, "none", seed=9, grid=False)]
+    empty = torch.empty((0, 512), dtype=BF16, device="cuda")
+    assert ia.inkattn_linear(ia.linear_params(x=x[:0], w=w, out=empty)) == 0
+    outs = []
+    for _ in range(3):
+        out = torch.empty((64, 512), dtype=F32, device="cuda")
+        ia.inkattn_linear(ia.linear_params(x=x, w=w, bias=bias, residual=residual, out=out))
+        outs.append(out)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+# ---------------------------------------------------------------- grouped products
+
+def _grouped(ia, counts, K, F, act="none", gather=True, dtype=BF16, seed=0, bias=True, spare=3, N_x=0):
+    g = torch.Generator().manual_seed(seed)
+    E, M = len(counts), int(sum(counts))
+    rows = 2 * F if act == "swiglu" else F
+    N_x = N_x or (max(1, M // 2) if gather else M + spare)
+    x = _grid((N_x, K), g, -8, 8, 1 / 8)
+    w = _grid((E, rows, K), g, -8, 8, 1 / 64)
+    b = _grid((E, rows), g, -512, 512, 2.0 ** -9, F32) if bias else None
+    offs = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=I32)
+    tok = torch.randint(0, N_x, (M + spare,), generator=g).to(I32) if gather else None
+    out = torch.full((M + spare, F), 7.0, dtype=dtype, device="cuda")
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    dev = [None if t is None else t.cuda() for t in (x, w, b, offs, tok)]
+    p = ia.grouped_linear_params(x=dev[0], w=dev[1], bias=dev[2], expert_offsets=dev[3], row_token=dev[4], out=out,
+                                 act=act, dev_status=status)
+    ia.inkattn_grouped_linear(p)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    assert bool((out[M:] == 7).all())                       # rows behind the last expert's
+    for e in range(E):
+        lo, hi = int(offs[e]), int(offs[e + 1])
+        xe = x[tok[lo:hi].long()] if gather else x[lo:hi]
+        v = xe.double() @ w[e].double().t()
+        if b is not None:
+            v = v + b[e].double()
+        _check(out[lo:hi], v, act)
+
+
+COUNTS = {
+    "one expert, one row": [1],
+    "rows of one to three": [1, 0, 2, 3, 0, 1],
+    "around the tile": [31, 32, 33, 0, 127, 128, 129, 1],
+    "several tiles": [0, 257, 600, 5, 0],
+    "all rows to one": [0, 0, 300, 0],
+    "no rows": [0, 0, 0],
+}
+
+
+@pytest.mark.parametrize("name", list(COUNTS))
+@pytest.mark.parametrize("gather", [True, False])
+def test_grouped_row_counts(ia, name, gather):
+    _grouped(ia, COUNTS[name], K=136, F=200, gather=gather, seed=len(name))
+    _grouped(ia, COUNTS[name], K=512, F=272, gather=gather, act="swiglu", seed=len(name))
+
+
+@pytest.mark.parametrize("K,F", [(8, 1), (64, 33), (72, 255), (1000, 257), (2048, 600)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_grouped_sizes(ia, K, F, dtype):
+    _grouped(ia, [3, 70, 0, 9, 200], K=K, F=F, dtype=dtype, seed=K + F)
+    _grouped(ia, [3, 70, 0, 9, 200], K=K, F=F, dtype=dtype, seed=K + F, gather=False, act="silu", bias=False)
+    _grouped(ia, [3, 70, 0, 9, 200], K=K, F=16 * ((F + 15) // 16), dtype=dtype, seed=K, act="swiglu")
+
+
+def test_grouped_many_experts(ia):
+    g = np.random.default_rng(4)
+    counts = g.integers(0, 12, size=1024).tolist()
+    _grouped(ia, counts, K=64, F=136, seed=4)
+    _grouped(ia, [int(c) for c in g.integers(0, 60, size=300)], K=256, F=128, act="swiglu", seed=5)
+
+
+def test_grouped_split_over_k(ia):
+    """Few items and a long K: the K range is split over a cluster."""
+    for counts in ([1], [5, 0, 2], [40], [0, 260]):
+        for F in (8, 100, 256, 400):
+            _grouped(ia, counts, K=4096, F=F, seed=F)
+        _grouped(ia, counts, K=4096, F=320, act="swiglu", seed=6, dtype=F32)
+        _grouped(ia, counts, K=4096, F=101, act="gelu", seed=7, gather=False)
+
+
+def test_grouped_repeated_row_token(ia):
+    """Every row of every expert reads the same row of x."""
+    _grouped(ia, [40, 3, 90], K=128, F=128, N_x=1, seed=8)
+
+
+def test_grouped_bad_indices_are_flagged_and_left(ia):
+    """A row_token out of range and an expert with bad offsets: flagged, their rows untouched,
+    the others computed.  (The kernel checks both before it uses them.)"""
+    g = torch.Generator().manual_seed(1)
+    K, F, M = 64, 128, 50
+    x, w = _grid((10, K), g, -8, 8, 1 / 8), _grid((2, F, K), g, -8, 8, 1 / 64)
+    tok = torch.randint(0, 10, (M,), generator=g).to(I32)
+    tok[3], tok[40] = 10, -1
+    offs = torch.tensor([0, 20, M], dtype=I32)
+
+    def go(tok, offs):
+        out = torch.full((M, F), 7.0, dtype=BF16, device="cuda")
+        status = torch.zeros(1, dtype=I32, device="cuda")
+        dev = [t.cuda() for t in (x, w, offs, tok)]
+        ia.inkattn_grouped_linear(ia.grouped_linear_params(x=dev[0], w=dev[1], expert_offsets=dev[2],
+                                                           row_token=dev[3], out=out, dev_status=status))
+        torch.cuda.synchronize()
+        return out.cpu(), int(status)
+
+    out, status = go(tok, offs)
+    assert status == ia.INKATTN_ERR_DEVICE_BOUNDS
+    for i in range(M):
+        if i in (3, 40):
+            assert bool((out[i] == 7).all())
+        else:
+            v = x[int(tok[i])].double() @ w[0 if i < 20 else 1].double().t()
+            assert torch.equal(out[i], v.to(F32).to(BF16))
+    good = tok.clamp(0, 9)
+    for bad in ([0, 20, M + 1], [0, -4, M], [21, 20, M]):
+        out, status = go(good, torch.tensor(bad, dtype=I32))
+        assert status == ia.INKATTN_ERR_DEVICE_BOUNDS, bad
+        for e in range(2):
+            lo, hi = bad[e], bad[e + 1]
+            if not (0 <= lo <= hi <= M):
+                continue
+            for i in range(lo, hi):
+                assert torch.equal(out[i], (x[int(good[i])].double() @ w[e].double().t()).to(F32).to(BF16))
+        covered = {i for e in range(2) if 0 <= bad[e] <= bad[e + 1] <= M for i in range(bad[e], bad[e + 1])}
+        assert all(bool((out[i] == 7).all()) for i in range(M) if i not in covered)
+
+
+# ---------------------------------------------------------------- router and sum
+
+def _route(ia, logits, S, k, score="sigmoid", scale=1.0):
+    T, E = logits.shape[0], logits.shape[1] - S
+    o = {"topk_ids": torch.full((T, k), -7, dtype=I32), "weights": torch.full((T, k + S), -7.0),
+         "expert_offsets": torch.full((E + 1,), -7, dtype=I32), "row_token": torch.full((T * k,), -7, dtype=I32),
+         "token_rows": torch.full((T, k), -7, dtype=I32)}
+    o = {n: t.cuda() for n, t in o.items()}
+    dev = logits.cuda()
+    p = ia.route_params(logits=dev, n_shared=S, score=score, scale=scale, **o)
+    n = ia.inkattn_route_workspace_bytes(p)
+    ws = torch.full((n,), 0xAB, dtype=torch.uint8, device="cuda") if n else None
+    ia.inkattn_route(p, ws)
+    torch.cuda.synchronize()
+    return {n: t.cpu() for n, t in o.items()}
+
+
+def _check_route(got, logits, S, k, score, scale=1.0):
+    T, E = logits.shape[0], logits.shape[1] - S
+    clean = torch.where(torch.isnan(logits), torch.full_like(logits, -float("inf")), logits).double()
+    best = torch.sort(clean[:, :E], dim=1, descending=True, stable=True)
+    ids = best.indices[:, :k]
+    assert torch.equal(got["topk_ids"].long(), ids)
+    counts = torch.bincount(ids.reshape(-1), minlength=E)
+    assert torch.equal(got["expert_offsets"].long(), torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)]))
+    order = torch.sort(ids.reshape(-1), stable=True).indices
+    assert torch.equal(got["row_token"].long(), order // k)
+    rows = torch.empty_like(order)
+    rows[order] = torch.arange(T * k)
+    assert torch.equal(got["token_rows"].long().reshape(-1), rows)
+    z = torch.cat([best.values[:, :k], clean[:, E:]], 1)
+    if score == "sigmoid":
+        s = torch.sigmoid(z)
+    else:
+        m = z.amax(1, keepdim=True)
+        s = torch.where(z == m, torch.ones_like(z), torch.exp(z - m))
+        s[z == -float("inf")] = 0.0
+    total = s.sum(1, keepdim=True)
+    w = torch.where(total > 0, scale * s / total, torch.zeros_like(s))
+    # Units of 2^-23: expf 2; its argument is one fp32 subtraction l - m, off by 2^-24 |l - m|, with m
+    # the largest logit (sigmoid: or 0, if that is less); 1 + e, the quotients and the products one
+    # each; the sum of at most 32 terms 5 levels deep: 16 + |l - m| in all.  Below 2^-126 values may
+    # be flushed.
+    m = z.amax(1, keepdim=True)
+    if score == "sigmoid":
+        m = m.clamp(max=0.0)
+    arg = (z - m).abs().nan_to_num(0.0, 0.0, 0.0)
+    err = (got["weights"].double() - w).abs()
+    assert bool((err <= (16 + arg) * 2.0 ** -23 * w.abs() + abs(scale) * 2.0 ** -125).all()), float(err.max())
+
+
+@pytest.mark.parametrize("T,E,S,k", [(1, 1, 0, 1), (1, 256, 2, 6), (2, 2, 1, 2), (5, 16, 16, 16), (31, 33, 0, 3),
+                                     (288, 256, 2, 6), (300, 64, 1, 8), (683, 256, 2, 6), (700, 200, 0, 6),
+                                     (1500, 1024, 3, 4), (4097, 129, 2, 1), (9000, 384, 2, 8), (20001, 256, 2, 6)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route(ia, T, E, S, k, score):
+    g = torch.Generator().manual_seed(T + E)
+    logits = torch.randn((T, E + S), generator=g) * 2
+    _check_route(_route(ia, logits, S, k, score), logits, S, k, score)
+    tied = (logits * 2).round() / 2                          # many equal logits, -0 among them
+    tied[tied == 0] *= torch.where(torch.rand((T, E + S), generator=g) < 0.5, -1.0, 1.0)[tied == 0]
+    _check_route(_route(ia, tied, S, k, score, scale=2.5), tied, S, k, score, scale=2.5)
+
+
+@pytest.mark.parametrize("T", [7, 1000])
+def test_route_same_choice_for_every_token(ia, T):
+    """Every token takes the same experts: all rows in k groups."""
+    logits = torch.zeros((T, 96))
+    _check_route(_route(ia, logits, 0, 6), logits, 0, 6, "sigmoid")
+    logits[:, [90, 5, 17]] = 3.0
+    _check_route(_route(ia, logits, 0, 3), logits, 0, 3, "sigmoid")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_infinities_and_nan(ia, score):
+    """-infinity, NaN, +infinity and huge logits; a token whose every logit is -infinity gets
+    zero weights and the lowest indices."""
+    inf, nan = float("inf"), float("nan")
+    E, S, k = 40, 2, 4
+    logits = torch.randn((8, E + S), generator=torch.Generator().manual_seed(2))
+    logits[0, :] = -inf
+    logits[1, :E] = nan
+    logits[2, 3], logits[2, 30] = inf, nan
+    logits[3, :E - 2] = -inf
+    logits[4, :] = -300.0
+    logits[5, 7] = 3e38
+    logits[6, E:] = nan
+    logits[7, :] = nan
+    got = _route(ia, logits, S, k, score)
+    _check_route(got, logits, S, k, score)
+    assert got["topk_ids"][0].tolist() == [0, 1, 2, 3] and bool((got["weights"][0] == 0).all())
+
+
+def test_route_no_tokens(ia):
+    got = _route(ia, torch.zeros((0, 12)), 2, 3)
+    assert got["expert_offsets"].tolist() == [0] * 11
+
+
+@pytest.mark.parametrize("T,k,S,F", [(1, 1, 0, 8), (1, 6, 2, 8192), (3, 8, 2, 1032), (9, 16, 16, 264), (100, 3, 1, 2056),
+                                     (700, 6, 0, 520)])
+def test_expert_combine(ia, T, k, S, F):
+    g = torch.Generator().manual_seed(T + F)
+    M = T * k
+    y, sh = torch.randn((M, F), generator=g).to(BF16), torch.randn((S, T, F), generator=g).to(BF16)
+    w = torch.randn((T, k + S), generator=g)
+    rows = torch.randperm(M, generator=g).to(I32).reshape(T, k)
+    rows[0, 0] = -1                                          # a dropped row
+    out = torch.full((T + 1, F), 7.0, dtype=BF16, device="cuda")
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    dev = [t.cuda() for t in (y, sh, w, rows)]
+    ia.inkattn_expert_combine(ia.expert_combine_params(y=dev[0], shared=dev[1] if S else None, weights=dev[2],
+                                                       token_rows=dev[3], out=out[:T], dev_status=status))
+    torch.cuda.synchronize()
+    assert int(status) == 0 and bool((out[T] == 7).all())
+    picked = torch.where((rows >= 0)[..., None], y[rows.clamp(min=0).long()].double(), torch.zeros(1, dtype=F64))
+    terms = torch.cat([picked * w[:, :k, None].double(), sh.double().transpose(0, 1) * w[:, k:, None].double()], 1)
+    want, mags = terms.sum(1), terms.abs().sum(1)
+    slack = (k + S) * 2.0 ** -24 * mags                      # one rounding a term
+    err = (out[:T].cpu().double() - want).abs()
+    assert bool((err <= slack + 2.0 ** -8 * (want.abs() + slack) + 2.0 ** -126).all())
+
+
+def test_expert_combine_bad_rows_and_no_nan_from_dropped_ones(ia):
+    T, k, F = 3, 2, 16
+    y = torch.full((4, F), float("nan"), dtype=BF16)
+    y[1] = 2.0
+    rows = torch.tensor([[1, -1], [4, 1], [-2, -1]], dtype=I32)
+    w = torch.full((T, k), 0.5)
+    w[0, 1] = float("nan")                                    # the weight of a dropped row
+    out = torch.empty((T, F), dtype=BF16, device="cuda")
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    dev = [t.cuda() for t in (y, w, rows)]
+    ia.inkattn_expert_combine(ia.expert_combine_params(y=dev[0], weights=dev[1], token_rows=dev[2], out=out,
+                                                       dev_status=status))
+    torch.cuda.synchronize()
+    assert int(status) == ia.INKATTN_ERR_DEVICE_BOUNDS
+    assert torch.equal(out.cpu().float(), torch.tensor([1.0, 1.0, 0.0])[:, None].expand(T, F))
