@@ -445,7 +445,7 @@ INKATTN_API inkattn_status inkattn_qkvr_prologue(const inkattn_qkvr_params *p, v
  * fp32 sums, and round once to the output type.  With v = x w^T + bias:
  *   NONE v   RELU max(v, 0)   GELU v (1 + erf(v / sqrt 2)) / 2   SILU v / (1 + exp(-v))
  *   SWIGLU   w (and bias) hold 2 F rows, F gate rows first, then F up rows:
- *            SILU(gate) * up, F values; F must be a multiple of 16.
+ *            SILU(gate) * up, F values.
  * Results do not depend on the GPU's scheduling: every sum is added in a fixed order.
  * In these four calls an array without rows (N_tok == 0, M == 0) may be NULL.
  * ------------------------------------------------------------------------------ */

@@ -289,7 +289,6 @@ inkattn_status validate_product(int rows, int K, int F, int act, int out_dtype, 
                                 const void *residual, const void *out, const void *dev_status) {
     if (K < 8 || K % 8 != 0 || K > (1 << 20) || F < 1 || F > (1 << 20)) return INKATTN_ERR_INVALID_ARG;
     if (act < INKATTN_ACT_NONE || act > INKATTN_ACT_SWIGLU) return INKATTN_ERR_INVALID_ARG;
-    if (act == INKATTN_ACT_SWIGLU && F % 16 != 0) return INKATTN_ERR_INVALID_ARG;
     if (out_dtype != INKATTN_DTYPE_BF16 && out_dtype != INKATTN_DTYPE_F32) return INKATTN_ERR_INVALID_ARG;
     if (!w || (rows > 0 && (!x || !out)) || !aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16))
         return INKATTN_ERR_INVALID_ARG;
@@ -540,11 +539,11 @@ bool make_qkvr_maps(const inkattn_qkvr_params &p, CUtensorMap *xmap, CUtensorMap
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_linear_maps(const LinearArgs &a, bool gated, CUtensorMap *xmap, CUtensorMap *wmap) {
+bool make_linear_maps(const LinearArgs &a, bool gated, LinearMaps *maps) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
     if (!enc) return false;
     const cuuint64_t K = (cuuint64_t)a.K, F = (cuuint64_t)a.F, E = (cuuint64_t)a.E;
-    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
     auto encode = [&](CUtensorMap *map, cuuint32_t rank, const void *base, const cuuint64_t *dims,
                       const cuuint64_t *strides, const cuuint32_t *box) {
         return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, estr,
@@ -552,16 +551,18 @@ bool make_linear_maps(const LinearArgs &a, bool gated, CUtensorMap *xmap, CUtens
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     const cuuint64_t xdims[2] = {K, (cuuint64_t)a.N_x}, xstr[1] = {K * 2};
-    const cuuint32_t xbox[2] = {64, a.offsets ? 1u : (cuuint32_t)(a.tile_n / 2)};
-    if (!encode(xmap, 2, a.x, xdims, xstr, xbox)) return false;
+    for (int i = 0; !a.row_token && i < a.tile_n / 32; ++i) {
+        const cuuint32_t xbox[2] = {64, 16u * (cuuint32_t)(i + 1)};
+        if (!encode(&maps->x[i], 2, a.x, xdims, xstr, xbox)) return false;
+    }
     if (gated) {
-        const cuuint64_t dims[5] = {K, 16, F / 16, 2, E}, str[4] = {K * 2, 16 * K * 2, F * K * 2, 2 * F * K * 2};
-        const cuuint32_t box[5] = {64, 16, 1, 2, 1};
-        return encode(wmap, 5, a.w, dims, str, box);
+        const cuuint64_t dims[4] = {K, F, 2, E}, str[3] = {K * 2, F * K * 2, 2 * F * K * 2};
+        const cuuint32_t box[4] = {64, 64, 2, 1};
+        return encode(&maps->w, 4, a.w, dims, str, box);
     }
     const cuuint64_t dims[3] = {K, F, E}, str[2] = {K * 2, F * K * 2};
     const cuuint32_t box[3] = {64, 128, 1};
-    return encode(wmap, 3, a.w, dims, str, box);
+    return encode(&maps->w, 3, a.w, dims, str, box);
 }
 
 bool make_q_map(CUtensorMap *map, const void *base, int n_tok, int hq, int box_rows) {

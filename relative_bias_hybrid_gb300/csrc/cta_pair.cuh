@@ -67,19 +67,7 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *map, 
         : "memory");
 }
 
-// As tma_load_2d_pair, for four rows of the map named one by one (its box is one row high):
-// rows r0 .. r3 land one after another at dst.
-__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const void *map, int c0, int r0, int r1, int r2,
-                                                 int r3, uint32_t bar_pair) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3),
-           "r"(bar_pair)
-        : "memory");
-}
-
-// As tma_load_2d_pair, for maps of three and of five dimensions.
+// As tma_load_2d_pair, for maps of three and of four dimensions.
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *map, int c0, int c1, int c2,
                                                  uint32_t bar_pair) {
     asm volatile(
@@ -88,13 +76,12 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *map, 
         :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar_pair)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const void *map, int c0, int c1, int c2, int c3,
-                                                 int c4, uint32_t bar_pair) {
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void *map, int c0, int c1, int c2, int c3,
+                                                 uint32_t bar_pair) {
     asm volatile(
-        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4),
-           "r"(bar_pair)
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar_pair)
         : "memory");
 }
 

@@ -95,10 +95,14 @@ struct LinearArgs {
     uint64_t wait_ns;        // limit of every bounded wait
 };
 cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStream_t stream);
-// TMA descriptors of a launch: x rows (box 64 columns x tile_n / 2 rows; a single row where
-// the rows are gathered), the weights as [E][F][K] (box 64 x 128 rows) or, gated, as
-// [E][gate, up][F / 16][16][K] (box 64 x 16 gate and the 16 up rows); 128-byte swizzle.
-bool make_linear_maps(const LinearArgs &a, bool gated, CUtensorMap *xmap, CUtensorMap *wmap);
+// TMA descriptors of a launch: x rows in boxes of 64 columns x 16 (i + 1) rows, up to half a
+// token tile (none where the rows are gathered by index); the weights as [E][F][K] (box 64 x
+// 128 rows) or, gated, as [E][gate, up][F][K] (box 64 x 64 gate and the 64 up rows); 128-byte
+// swizzle.
+struct LinearMaps {
+    CUtensorMap w, x[8];
+};
+bool make_linear_maps(const LinearArgs &a, bool gated, LinearMaps *maps);
 
 size_t route_workspace_bytes(const inkattn_route_params &p);
 cudaError_t launch_route(const inkattn_route_params &p, uint32_t *ws, cudaStream_t stream);

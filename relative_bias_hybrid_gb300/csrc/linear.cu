@@ -16,17 +16,21 @@
 // eighth of the tensor time of N = 256), while the weights, which bound such a call, stream
 // through at full width.  Each CTA holds its own 128 weight rows and half of the tokens.
 //
-// The rows of a token tile are one box of x (a linear layer), or are gathered four at a time
-// by row index (grouped products): a gather costs what the tile's rows cost, and the copy of x
-// in expert order is never written.  SWIGLU: the CTA's 128 weight rows are 16 gate rows, the
-// 16 up rows of the same features, the next 16 gate rows ...; gate and up of a feature lie 16
-// lanes apart in one warp.
+// The rows of a token tile are one box of x, as many rows as the tile has (a tensor map for
+// each box height), or, with row indices, are gathered by four warps of their own with 16-byte
+// cp.async: the copy of x in expert order is never written.  (TMA's gather of four rows was
+// measured first: a K = 64 step of 128 rows took about 1800 cycles, 3.5 times its MMAs.)  SWIGLU: the CTA's 128 weight rows are
+// 64 gate rows and the 64 up rows of the same features, one box; the two warps that hold a
+// feature's gate and up exchange half of the tokens through shared memory.  (16 gate rows and 16
+// up rows in turn, a shuffle apart in one warp, were measured first: four boxes a stage made the
+// copies the bound, 0.78 ms where one box takes 0.57 for the same products.)
 //
 // One CTA per SM, 10 warps:
 //   warp 0      producer: copies of the weight rows and the token rows into a ring of stages
 //               of K = 64; as many stages as fit 192 KB
 //   warp 1      even CTA: MMA issuer, K = 16 steps into one of two TMEM accumulators (2 x 256
 //               columns), so that an item's epilogue overlaps the next item's MMAs
+//   warps 10-13 only with row indices: the gather; warp 14 hands its stages to the MMA warp
 //   warps 2-9   epilogue: a warp owns 32 TMEM lanes (weight rows) and every second block of 32
 //               columns (tokens); bias and activation per lane, then a turn through a private
 //               staging buffer, so that a token's features leave as 16-byte pieces
@@ -56,9 +60,11 @@ constexpr int kKStep = 64;                        // K per ring stage (one 128-b
 constexpr int kABytes = kRowsA * 128;             // 16 KB
 constexpr int kRingBytes = 192 * 1024;
 constexpr int kMaxStages = 12;
-constexpr int kThreads = 320;
+constexpr int kThreads = 320;                     // without a gather
+constexpr int kGatherThreads = 128;
+constexpr int kMaxThreads = kThreads + kGatherThreads + 32;
 constexpr int kEpiThreads = 256;
-constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpEpi = 2;
+constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpEpi = 2, kWarpGather = 10, kWarpRelay = 14;
 constexpr int kStgPitch = 36;                     // floats of a staging row: 32 features + 4
 constexpr int kStgBytes = 16 * kStgPitch * 4;     // 16 tokens, one buffer per epilogue warp
 constexpr int kRaster = 8;                        // feature blocks per raster group
@@ -70,7 +76,8 @@ constexpr int kOffBar = (kOffStart + (INKATTN_MAX_EXPERTS + 1) * 4 + 7) / 8 * 8;
 enum Bar {
     B_FULL = 0,
     B_EMPTY = B_FULL + kMaxStages,
-    B_ACC_FULL = B_EMPTY + kMaxStages,
+    B_GATHER = B_EMPTY + kMaxStages,
+    B_ACC_FULL = B_GATHER + kMaxStages,
     B_ACC_EMPTY = B_ACC_FULL + 2,
     B_DRAIN = B_ACC_EMPTY + 2,
     B_COUNT = B_DRAIN + 1
@@ -87,7 +94,7 @@ template <int kAct>
 __device__ __forceinline__ float activate(float v) {
     if (kAct == INKATTN_ACT_RELU) return fmaxf(v, 0.f);
     if (kAct == INKATTN_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    if (kAct == INKATTN_ACT_SILU) return v / (1.f + __expf(-v));
+    if (kAct == INKATTN_ACT_SILU) return __fdividef(v, 1.f + __expf(-v));
     return v;
 }
 
@@ -95,6 +102,39 @@ __device__ __forceinline__ void store_bf16(inkattn_bf16 *p, float v) {
     *reinterpret_cast<__nv_bfloat16 *>(p) = __float2bfloat16_rn(v);
 }
 __device__ __forceinline__ float load_bf16(const inkattn_bf16 *p) { return __uint_as_float((uint32_t)*p << 16); }
+
+// 16 bytes global -> shared without a register stop; all zeros where `live` is false
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(live ? 16 : 0) : "memory");
+}
+// arrives on the mbarrier once this thread's earlier cp.async have landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// bar.sync over n threads, and the same reducing a predicate with AND
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ bool named_all(int id, int n, bool v) {
+    int r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\t"
+                 "selp.s32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"((int)v), "r"(id), "r"(n) : "memory");
+    return r != 0;
+}
+
+// A position in the ring: stage and how often the ring has been passed (its low bit: the parity).
+struct RingPos {
+    int s = 0;
+    uint32_t lap = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == stages) {
+            s = 0;
+            ++lap;
+        }
+    }
+};
 
 __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
     float4 v;
@@ -106,8 +146,8 @@ __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
 }  // namespace
 
 template <int kAct>
-__global__ void __launch_bounds__(kThreads, 1)
-k_linear(const LinearArgs A, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap) {
+__global__ void __launch_bounds__(kMaxThreads, 1)
+k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     constexpr bool kGated = kAct == INKATTN_ACT_SWIGLU;
     constexpr int kFeat = kGated ? 64 : 128;           // output features of a CTA
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -136,7 +176,8 @@ k_linear(const LinearArgs A, const __grid_constant__ CUtensorMap xmap, const __g
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < A.stages; ++s) {
-            mbar_init(bar(B_FULL + s), 1);             // (the even CTA's counts both CTAs' copies)
+            mbar_init(bar(B_FULL + s), A.row_token ? 3 : 1);   // (the even CTA's: both CTAs' copies and relays)
+            mbar_init(bar(B_GATHER + s), kGatherThreads);
             mbar_init(bar(B_EMPTY + s), 1);            // released by the pair's MMAs
         }
         for (int s = 0; s < 2; ++s) {
@@ -213,60 +254,88 @@ k_linear(const LinearArgs A, const __grid_constant__ CUtensorMap xmap, const __g
 
     if (warp == kWarpProducer) {
         // ================================ producer ================================
-        const bool gather = A.offsets != nullptr;
-        int L = 0;                                     // stage loads issued
+        RingPos at;
         bool ok = true;
         if (lane == 0) {
-            tma_prefetch_desc(&xmap);
-            tma_prefetch_desc(&wmap);
+            tma_prefetch_desc(&maps.x[0]);
+            tma_prefetch_desc(&maps.w);
         }
         for (int w = cid; w < n_items && ok; w += nclusters) {
             const Item it = item(w);
-            const int hn = it.n >> 1;                  // token slots of a CTA
-            // gathers of four rows in each half of the tile; this lane's four rows
-            const int g0 = (min(it.nt, hn) + 3) >> 2, g1 = (max(it.nt - hn, 0) + 3) >> 2;
-            const int mine = half ? g1 : g0;
-            int r[4] = {0, 0, 0, 0};
-            if (gather && lane < mine) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = it.row0 + min(half * hn + 4 * lane + j, it.nt - 1);
-                    r[j] = A.row_token ? __ldg(A.row_token + i) : i;
-                    if (r[j] < 0 || r[j] >= A.N_x) r[j] = 0;   // (flagged and not stored by the epilogue)
-                }
-            }
-            const uint32_t bytes = 2 * kABytes + (gather ? (uint32_t)(g0 + g1) * 512u : (uint32_t)A.tile_n * 128u);
-            for (int k = k_lo; k < k_hi; ++k, ++L) {
-                const int s = L % A.stages;
-                if (L >= A.stages && !cwait(bar(B_EMPTY + s), ((L / A.stages) - 1) & 1)) {
+            const int hn = it.n >> 1;                  // tokens of a CTA's half of the tile
+            const uint32_t bytes = 2 * (kABytes + (A.row_token ? 0u : (uint32_t)hn * 128u));
+            const CUtensorMap *xm = &maps.x[(hn >> 4) - 1];
+            for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
+                if (at.lap > 0 && !cwait(bar(B_EMPTY + at.s), (at.lap - 1) & 1)) {
                     ok = false;
                     break;
                 }
-                const uint32_t dst = s_base + (uint32_t)(s * A.stage_bytes);
-                const uint32_t fb = mapa_shared(bar(B_FULL + s), even);
-                if (half == 0 && lane == 0) mbar_arrive_expect_tx(bar(B_FULL + s), bytes);
-                __syncwarp();
-                if (kGated) {
-                    if (lane < 4)
-                        tma_load_5d_pair(dst + (uint32_t)lane * 4096u, &wmap, k * kKStep, 0,
-                                         it.fb * 8 + half * 4 + lane, 0, it.e, fb);
-                } else if (lane == 0) {
-                    tma_load_3d_pair(dst, &wmap, k * kKStep, it.fb * 256 + half * kRowsA, it.e, fb);
-                }
-                if (gather) {
-                    if (lane < mine)
-                        tma_gather4_pair(dst + kABytes + (uint32_t)lane * 512u, &xmap, k * kKStep, r[0], r[1], r[2],
-                                         r[3], fb);
-                } else if (lane == 0) {
-                    tma_load_2d_pair(dst + kABytes, &xmap, k * kKStep, it.row0 + half * hn, fb);
+                const uint32_t dst = s_base + (uint32_t)(at.s * A.stage_bytes);
+                const uint32_t fb = mapa_shared(bar(B_FULL + at.s), even);
+                if (lane == 0) {
+                    if (half == 0) mbar_arrive_expect_tx(bar(B_FULL + at.s), bytes);
+                    if (kGated) tma_load_4d_pair(dst, &maps.w, k * kKStep, (it.fb * 2 + half) * kFeat, 0, it.e, fb);
+                    else tma_load_3d_pair(dst, &maps.w, k * kKStep, (it.fb * 2 + half) * kFeat, it.e, fb);
+                    if (!A.row_token) tma_load_2d_pair(dst + kABytes, xm, k * kKStep, it.row0 + half * hn, fb);
                 }
                 __syncwarp();
             }
         }
-        // nothing may still be landing in shared memory when the pair tears down (see qkvr.cu)
+        // nothing may still be landing in shared memory when the pair tears down: the even CTA
+        // waits for the last lap of both CTAs' copies (see qkvr.cu)
         if (lane == 0 && half == 0)
-            for (int l = max(0, L - A.stages); l < L; ++l)
-                mbar_drain(bar(B_FULL + l % A.stages), (l / A.stages) & 1, A.dev_status, A.wait_ns);
+            for (int l = 0; l < A.stages; ++l) {
+                const uint32_t laps = at.lap + (l < at.s ? 1u : 0u);      // uses of stage l
+                if (laps > 0) mbar_drain(bar(B_FULL + l), (laps - 1) & 1, A.dev_status, A.wait_ns);
+            }
+    } else if (warp == kWarpRelay) {
+        // ================================ relay ================================
+        // The gathered rows were written through the generic proxy and the MMAs read through the
+        // async one.  The fence between the two waits for every copy its thread has in flight, so
+        // it is not the gathering threads that execute it (that took 1 us a stage) but this warp,
+        // which has none, once a stage's rows have landed.
+        RingPos at;
+        bool ok = true;
+        for (int w = cid; w < n_items && ok; w += nclusters)
+            for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(B_GATHER + at.s), at.lap & 1, A.dev_status, abort_flag, A.wait_ns));
+                if (!ok) break;
+                fence_proxy_async_smem();
+                if (lane == 0) mbar_remote_arrive(bar(B_FULL + at.s), even);
+            }
+    } else if (warp >= kWarpGather) {
+        // ================================ gather ================================
+        // Eight lanes copy the 128 bytes of a row, 16 rows at a time, to the places that the
+        // 128-byte swizzle gives them.
+        const int gt = (int)threadIdx.x - kWarpGather * 32;
+        const int piece = gt & 7, r0 = gt >> 3;
+        RingPos at;
+        bool ok = true;
+        for (int w = cid; w < n_items && ok; w += nclusters) {
+            const Item it = item(w);
+            const int hn = it.n >> 1, mine = min(max(it.nt - half * hn, 0), hn);
+            const inkattn_bf16 *src[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                int r = r0 + 16 * j < mine ? __ldg(A.row_token + it.row0 + half * hn + r0 + 16 * j) : 0;
+                if (r < 0 || r >= A.N_x) r = 0;        // (flagged and not stored by the epilogue)
+                src[j] = A.x + (size_t)r * A.K + piece * 8;
+            }
+            for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
+                if (at.lap > 0 && !cwait(bar(B_EMPTY + at.s), (at.lap - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = s_base + (uint32_t)(at.s * A.stage_bytes + kABytes + r0 * 128 + ((piece ^ (r0 & 7)) << 4));
+                const bool live = k * kKStep + piece * 8 < A.K;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (r0 + 16 * j < mine)
+                        cp_async16(dst + (uint32_t)(j * 16 * 128), live ? src[j] + k * kKStep : src[j], live);
+                cp_async_arrive(bar(B_GATHER + at.s));
+            }
+        }
+        cp_async_wait_all();
     } else if (warp == kWarpMma && half != 0) {
         // the odd CTA issues no MMAs
     } else if (warp == kWarpMma) {
@@ -274,10 +343,10 @@ k_linear(const LinearArgs A, const __grid_constant__ CUtensorMap xmap, const __g
         const uint64_t da0 = tc::sdesc_sw128(s_base, 16, 1024);
         const uint64_t db0 = tc::sdesc_sw128(s_base + kABytes, 16, 1024);
         const uint16_t pair = (uint16_t)(3u << even);
-        // the last stages are not released, so that no arrival reaches a peer that has finished
+        // the last lap is not released, so that no arrival reaches a peer that has finished
         const int my_items = cid < n_items ? (n_items - cid + nclusters - 1) / nclusters : 0;
-        const long long total = (long long)my_items * (k_hi - k_lo);
-        long long L = 0;
+        long long left = (long long)my_items * (k_hi - k_lo);
+        RingPos at;
         bool ok = true;
         int i = 0;
         for (int w = cid; w < n_items && ok; w += nclusters, ++i) {
@@ -289,17 +358,17 @@ k_linear(const LinearArgs A, const __grid_constant__ CUtensorMap xmap, const __g
                 break;
             }
             tc::fence_after();
-            for (int k = k_lo; k < k_hi; ++k, ++L) {
-                const int s = (int)(L % A.stages);
-                if (!cwait(bar(B_FULL + s), (uint32_t)((L / A.stages) & 1))) {
+            for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
+                if (!cwait(bar(B_FULL + at.s), at.lap & 1)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after();
-                const uint64_t off = (uint64_t)(s * (A.stage_bytes >> 4));
+                const uint64_t off = (uint64_t)(at.s * (A.stage_bytes >> 4));
                 tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)(buf * kMaxN), da0 + off, db0 + off, id,
-                                                k > k_lo ? 1u : 0u, bar(B_EMPTY + s), L + A.stages < total ? 1u : 0u,
+                                                k > k_lo ? 1u : 0u, bar(B_EMPTY + at.s), left > A.stages ? 1u : 0u,
                                                 bar(B_ACC_FULL + buf), k == k_hi - 1 ? 1u : 0u, pair);
+                --left;
                 __syncwarp();
             }
         }
@@ -313,6 +382,9 @@ k_linear(const LinearArgs A, const __grid_constant__ CUtensorMap xmap, const __g
         const int e8 = (warp - kWarpEpi) >> 2;                // which of every two blocks of 32 tokens
         const int quarter = warp & 3;                         // TMEM lanes this warp may access
         float *stg = reinterpret_cast<float *>(smem + kOffStg + (warp - kWarpEpi) * kStgBytes);
+        // the warp that holds the other factor of the same features, and the barrier of the two
+        const float *stg_other = reinterpret_cast<const float *>(smem + kOffStg + (e8 * 4 + ((warp - kWarpEpi) & 3 ^ 2)) * kStgBytes);
+        const int swap_bar = 1 + e8 * 2 + (quarter & 1);
         const size_t F = (size_t)A.F;
         inkattn_bf16 *out16 = static_cast<inkattn_bf16 *>(A.out);
         float *out32 = static_cast<float *>(A.out);
@@ -322,14 +394,16 @@ k_linear(const LinearArgs A, const __grid_constant__ CUtensorMap xmap, const __g
         for (int w = cid; w < n_items; w += nclusters, ++i) {
             const Item it = item(w);
             const int buf = i & 1;
-            // the warp's features, this lane's weight row and its bias
-            const int f0 = it.fb * 2 * kFeat + half * kFeat + (kGated ? quarter * 16 : quarter * 32);
-            const int frow = kGated ? f0 + (lane & 15) : f0 + lane;      // feature of the lane's weight row
+            // the warp's 32 features (gated: quarters 0 and 1 hold gates, 2 and 3 the ups of the
+            // same features), the lane's feature and its bias
+            const int f0 = (it.fb * 2 + half) * kFeat + (kGated ? quarter & 1 : quarter) * 32;
+            const int frow = f0 + lane;
             float bias = 0.f;
             if (A.bias && frow < A.F)
-                bias = __ldg(A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + (kGated && lane >= 16 ? F : 0) + frow);
-            const bool ok = mbar_wait_cluster(bar(B_ACC_FULL + buf), (uint32_t)((i >> 1) & 1), A.dev_status,
-                                              abort_flag, A.wait_ns);
+                bias = __ldg(A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + (kGated && quarter >= 2 ? F : 0) + frow);
+            bool ok = mbar_wait_cluster(bar(B_ACC_FULL + buf), (uint32_t)((i >> 1) & 1), A.dev_status, abort_flag,
+                                        A.wait_ns);
+            if (kGated) ok = named_all(swap_bar, 64, ok);     // the two warps go on together
             if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after();
             const uint32_t taddr = tmem + (uint32_t)(buf * kMaxN) + ((uint32_t)(quarter * 32) << 16);
@@ -361,109 +435,86 @@ k_linear(const LinearArgs A, const __grid_constant__ CUtensorMap xmap, const __g
                     }
                 }
                 const uint32_t live = __ballot_sync(0xffffffffu, mine);
-                const size_t row_b = (size_t)(it.row0 + c * 32);
-                if (kGated) {
-                    // lanes 0-15 hold gates, 16-31 the ups of the same features: of two tokens the
-                    // lower lanes finish the first, the upper lanes the second
-                    __syncwarp();
+                // 16 finished tokens t0 .. t0 + 15 of the block, the lane's feature of each, to out
+                auto store16 = [&](const float (&y)[16], int t0) {
+                    const size_t row_b = (size_t)(it.row0 + c * 32 + t0);
+                    const uint32_t live16 = live >> t0;
+                    if (!vec) {                               // rows that start anywhere
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float a = __uint_as_float(v[j]) + bias, b = __uint_as_float(v[j + 1]) + bias;
-                        const float got = __shfl_xor_sync(0xffffffffu, lane < 16 ? b : a, 16);
-                        const float gate = lane < 16 ? a : got, up = lane < 16 ? got : b;
-                        const float y = activate<INKATTN_ACT_SILU>(gate) * up;
-                        stg[(j + (lane >> 4)) * 16 + (lane & 15)] = y;
+                        for (int j = 0; j < 16; ++j) {
+                            if (((live16 >> j) & 1u) && frow < A.F) {
+                                const size_t o = (row_b + j) * F + frow;
+                                const float z = A.residual ? y[j] + load_bf16(A.residual + o) : y[j];
+                                if (A.out_f32) out32[o] = z;
+                                else store_bf16(out16 + o, z);
+                            }
+                        }
+                        return;
                     }
                     __syncwarp();
-                    if (vec && !A.out_f32) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) stg[j * kStgPitch + lane] = y[j];
+                    __syncwarp();
+                    if (!A.out_f32) {
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const int t = q * 16 + (lane >> 1), f = f0 + (lane & 1) * 8;
-                            float y[8];
-                            *reinterpret_cast<float4 *>(y) = *reinterpret_cast<const float4 *>(stg + t * 16 + (lane & 1) * 8);
-                            *reinterpret_cast<float4 *>(y + 4) = *reinterpret_cast<const float4 *>(stg + t * 16 + (lane & 1) * 8 + 4);
-                            if (((live >> t) & 1u) && f < A.F) {
+                            const int t = q * 8 + (lane >> 2), f = f0 + (lane & 3) * 8;
+                            const float *src = stg + t * kStgPitch + (lane & 3) * 8;
+                            float z[8];
+                            *reinterpret_cast<float4 *>(z) = *reinterpret_cast<const float4 *>(src);
+                            *reinterpret_cast<float4 *>(z + 4) = *reinterpret_cast<const float4 *>(src + 4);
+                            if (((live16 >> t) & 1u) && f < A.F) {
                                 const size_t o = (row_b + t) * F + f;
                                 if (A.residual) {
                                     float r[8];
                                     unpack8(*reinterpret_cast<const uint4 *>(A.residual + o), r);
 #pragma unroll
-                                    for (int j = 0; j < 8; ++j) y[j] += r[j];
+                                    for (int j = 0; j < 8; ++j) z[j] += r[j];
                                 }
-                                *reinterpret_cast<uint4 *>(out16 + o) = pack8(y);
+                                *reinterpret_cast<uint4 *>(out16 + o) = pack8(z);
                             }
                         }
                     } else {
-                        // (F is a multiple of 16: four features a lane)
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const int t = q * 8 + (lane >> 2), f = f0 + (lane & 3) * 4;
-                            float4 y = *reinterpret_cast<const float4 *>(stg + t * 16 + (lane & 3) * 4);
-                            if (((live >> t) & 1u) && f < A.F) {
+                            const int t = q * 4 + (lane >> 3), f = f0 + (lane & 7) * 4;
+                            float4 z = *reinterpret_cast<const float4 *>(stg + t * kStgPitch + (lane & 7) * 4);
+                            if (((live16 >> t) & 1u) && f < A.F) {
                                 const size_t o = (row_b + t) * F + f;
                                 if (A.residual) {
-                                    y.x += load_bf16(A.residual + o); y.y += load_bf16(A.residual + o + 1);
-                                    y.z += load_bf16(A.residual + o + 2); y.w += load_bf16(A.residual + o + 3);
+                                    const uint2 r = *reinterpret_cast<const uint2 *>(A.residual + o);
+                                    z.x += bf16_lo(r.x); z.y += bf16_hi(r.x);
+                                    z.z += bf16_lo(r.y); z.w += bf16_hi(r.y);
                                 }
-                                *reinterpret_cast<float4 *>(out32 + o) = y;
+                                *reinterpret_cast<float4 *>(out32 + o) = z;
                             }
                         }
                     }
-                } else if (vec) {
+                };
+                float y[16];
+                if (kGated) {
+                    // the gate warp finishes the block's first 16 tokens, the up warp the others
+                    const int keep = quarter < 2 ? 0 : 16;
+                    __syncwarp();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {             // 16 tokens at a time
-                        __syncwarp();
+                    for (int j = 0; j < 16; ++j)
+                        stg[j * kStgPitch + lane] = __uint_as_float(quarter < 2 ? v[16 + j] : v[j]) + bias;
+                    named_sync(swap_bar, 64);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            stg[j * kStgPitch + lane] = activate<kAct>(__uint_as_float(v[16 * h + j]) + bias);
-                        __syncwarp();
-                        if (!A.out_f32) {
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const int t = q * 8 + (lane >> 2), f = f0 + (lane & 3) * 8;
-                                const float *src = stg + t * kStgPitch + (lane & 3) * 8;
-                                float y[8];
-                                *reinterpret_cast<float4 *>(y) = *reinterpret_cast<const float4 *>(src);
-                                *reinterpret_cast<float4 *>(y + 4) = *reinterpret_cast<const float4 *>(src + 4);
-                                if (((live >> (16 * h + t)) & 1u) && f < A.F) {
-                                    const size_t o = (row_b + 16 * h + t) * F + f;
-                                    if (A.residual) {
-                                        float r[8];
-                                        unpack8(*reinterpret_cast<const uint4 *>(A.residual + o), r);
-#pragma unroll
-                                        for (int j = 0; j < 8; ++j) y[j] += r[j];
-                                    }
-                                    *reinterpret_cast<uint4 *>(out16 + o) = pack8(y);
-                                }
-                            }
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int t = q * 4 + (lane >> 3), f = f0 + (lane & 7) * 4;
-                                float4 y = *reinterpret_cast<const float4 *>(stg + t * kStgPitch + (lane & 7) * 4);
-                                if (((live >> (16 * h + t)) & 1u) && f < A.F) {
-                                    const size_t o = (row_b + 16 * h + t) * F + f;
-                                    if (A.residual) {
-                                        const uint2 r = *reinterpret_cast<const uint2 *>(A.residual + o);
-                                        y.x += bf16_lo(r.x); y.y += bf16_hi(r.x);
-                                        y.z += bf16_lo(r.y); y.w += bf16_hi(r.y);
-                                    }
-                                    *reinterpret_cast<float4 *>(out32 + o) = y;
-                                }
-                            }
-                        }
+                    for (int j = 0; j < 16; ++j) {
+                        const float own = __uint_as_float(quarter < 2 ? v[j] : v[16 + j]) + bias;
+                        const float other = stg_other[j * kStgPitch + lane];
+                        const float gate = quarter < 2 ? own : other, up = quarter < 2 ? other : own;
+                        y[j] = activate<INKATTN_ACT_SILU>(gate) * up;
                     }
+                    named_sync(swap_bar, 64);                 // both have read
+                    store16(y, keep);
                 } else {
-                    // rows that start anywhere: a lane stores its own feature of each token
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (((live >> j) & 1u) && frow < A.F) {
-                            const size_t o = (row_b + j) * F + frow;
-                            float y = activate<kAct>(__uint_as_float(v[j]) + bias);
-                            if (A.residual) y += load_bf16(A.residual + o);
-                            if (A.out_f32) out32[o] = y;
-                            else store_bf16(out16 + o, y);
-                        }
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) y[j] = activate<kAct>(__uint_as_float(v[16 * h + j]) + bias);
+                        store16(y, 16 * h);
                     }
                 }
             }
@@ -474,14 +525,14 @@ k_linear(const LinearArgs A, const __grid_constant__ CUtensorMap xmap, const __g
         __syncwarp();
         cluster_sync();                                // every partial tile of the cluster is complete
         const int et = (int)threadIdx.x - kWarpEpi * 32;
-        if (et >= 0 && cid < n_items) {
+        if (et >= 0 && et < kEpiThreads && cid < n_items) {
             const Item it = item(cid);
             const size_t F = (size_t)A.F;
             // four features of one token per step; the cluster's pairs take the tokens in turn
             constexpr int kPer = kFeat / 4;            // steps of a token
             for (int u = et; u < ((it.nt - split + A.splits - 1) / A.splits) * kPer; u += kEpiThreads) {
                 const int t = (u / kPer) * A.splits + split, j = u % kPer;
-                const int f = it.fb * 2 * kFeat + half * kFeat + j * 4;
+                const int f = (it.fb * 2 + half) * kFeat + j * 4;
                 if (f >= A.F) continue;
                 const int i = it.row0 + t;
                 if (A.row_token) {
@@ -491,15 +542,14 @@ k_linear(const LinearArgs A, const __grid_constant__ CUtensorMap xmap, const __g
                         continue;
                     }
                 }
-                const int lane0 = kGated ? (j >> 2) * 32 + (j & 3) * 4 : j * 4;
-                const uint32_t src = s_base + (uint32_t)((t * kRowsA + lane0) * 4);
+                const uint32_t src = s_base + (uint32_t)((t * kRowsA + j * 4) * 4);
                 float y[4] = {0.f, 0.f, 0.f, 0.f}, up[4] = {0.f, 0.f, 0.f, 0.f};
                 for (int s = 0; s < A.splits; ++s) {
                     const uint32_t a = mapa_shared(src, (uint32_t)(2 * s + half));
                     const float4 p = ld_shared_cluster_f4(a);
                     y[0] += p.x; y[1] += p.y; y[2] += p.z; y[3] += p.w;
                     if (kGated) {
-                        const float4 q = ld_shared_cluster_f4(a + 64u);
+                        const float4 q = ld_shared_cluster_f4(a + 256u)      /* 64 rows on */;
                         up[0] += q.x; up[1] += q.y; up[2] += q.z; up[3] += q.w;
                     }
                 }
@@ -530,7 +580,7 @@ k_linear(const LinearArgs A, const __grid_constant__ CUtensorMap xmap, const __g
 
 namespace {
 
-using Kernel = void (*)(const LinearArgs, const CUtensorMap, const CUtensorMap);
+using Kernel = void (*)(const LinearArgs, const LinearMaps);
 
 Kernel kernel_of(int act) {
     switch (act) {
@@ -551,7 +601,7 @@ int resident_clusters(int ctas, int num_sms) {
     if (n > 0) return n;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas * (num_sms / ctas > 0 ? num_sms / ctas : 1)), 1, 1);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kMaxThreads);
     cfg.dynamicSmemBytes = kSmem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -593,10 +643,11 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     const int most = resident_clusters(2 * a.splits, num_sms);
     if (most < 1) return cudaErrorInvalidConfiguration;
     const int clusters = (int)(items < most ? items : most);
-    CUtensorMap xmap, wmap;
-    if (!make_linear_maps(a, act == INKATTN_ACT_SWIGLU, &xmap, &wmap)) return cudaErrorInvalidValue;
-    return launch_dependent(k, dim3((unsigned)(2 * a.splits * clusters)), dim3(kThreads), kSmem, stream, 2 * a.splits, a,
-                            xmap, wmap);
+    LinearMaps maps;
+    if (!make_linear_maps(a, act == INKATTN_ACT_SWIGLU, &maps)) return cudaErrorInvalidValue;
+    const int threads = a.row_token ? kMaxThreads : kThreads;
+    return launch_dependent(k, dim3((unsigned)(2 * a.splits * clusters)), dim3((unsigned)threads), kSmem, stream,
+                            2 * a.splits, a, maps);
 }
 
 }  // namespace inkattn
