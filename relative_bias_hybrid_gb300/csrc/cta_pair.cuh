@@ -47,6 +47,36 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
     }
 }
 
+// mbar_wait for a phase that TMA copies or tensor-core commits complete, from either CTA of a
+// pair: it polls like mbar_wait_cluster, but with the plain (CTA-scope) acquire.  Cluster
+// scope, needed behind another CTA's own arrivals, costs about 250 ns a wait, as much as the
+// MMAs of a K = 64 stage at N = 256.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_poll(uint32_t bar, uint32_t parity, int32_t *status,
+                                               volatile int *abort, uint64_t limit_ns) {
+    if (mbar_test_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_test_wait(bar, parity)) return true;
+        __nanosleep(20);
+        if ((n & 255u) == 0u) {
+            if (abort && *abort) return false;
+            if (globaltimer() - t0 > limit_ns) {
+                set_status(status, INKATTN_ERR_DEVICE_TIMEOUT);
+                if (abort) *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
 // One arrival, with release at cluster scope, on the mbarrier at `bar`'s offset in the
 // shared memory of CTA `cta_rank` of the cluster.
 __device__ __forceinline__ void mbar_remote_arrive(uint32_t bar, uint32_t cta_rank) {
@@ -83,6 +113,13 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void *map, 
         " [%0], [%1, {%2, %3, %4, %5}], [%6];"
         :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar_pair)
         : "memory");
+}
+
+// Bulk copy from this CTA's shared memory to another CTA's (dst and bar: shared::cluster
+// addresses in that CTA); 16-byte aligned, completes on the barrier's transaction count.
+__device__ __forceinline__ void bulk_copy_pair(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "r"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
 // The shared::cluster address of the object at `addr`'s offset in CTA `cta_rank`.

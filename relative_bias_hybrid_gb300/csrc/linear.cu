@@ -70,7 +70,9 @@ constexpr int kStgBytes = 16 * kStgPitch * 4;     // 16 tokens, one buffer per e
 constexpr int kRaster = 8;                        // feature blocks per raster group
 
 constexpr int kOffStg = kRingBytes;
-constexpr int kOffTiles = kOffStg + 8 * kStgBytes;                     // int tile prefix [E + 1]
+constexpr int kNoteBytes = 16;                    // the odd CTA's note that a gathered stage is complete
+constexpr int kOffNote = kOffStg + 8 * kStgBytes; // where it lands, and behind it what is sent
+constexpr int kOffTiles = kOffNote + 2 * kNoteBytes;                   // int tile prefix [E + 1]
 constexpr int kOffStart = kOffTiles + (INKATTN_MAX_EXPERTS + 1) * 4;   // int first row [E + 1]
 constexpr int kOffBar = (kOffStart + (INKATTN_MAX_EXPERTS + 1) * 4 + 7) / 8 * 8;
 enum Bar {
@@ -169,14 +171,15 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     int *s_start = reinterpret_cast<int *>(smem + kOffStart);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffBar + B_COUNT * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffBar + B_COUNT * 8 + 4);
-    auto cwait = [&](uint32_t addr, uint32_t parity) -> bool {
-        const bool r = mbar_wait_cluster(addr, parity, A.dev_status, abort_flag, A.wait_ns);
+    // a stage of the ring: completed by copies or by a commit, which carry their own ordering
+    auto pwait = [&](uint32_t addr, uint32_t parity) -> bool {
+        const bool r = mbar_wait_poll(addr, parity, A.dev_status, abort_flag, A.wait_ns);
         return __all_sync(0xffffffffu, r);
     };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < A.stages; ++s) {
-            mbar_init(bar(B_FULL + s), A.row_token ? 3 : 1);   // (the even CTA's: both CTAs' copies and relays)
+            mbar_init(bar(B_FULL + s), A.row_token ? 2 : 1);   // (the even CTA's: both CTAs' copies, its relay)
             mbar_init(bar(B_GATHER + s), kGatherThreads);
             mbar_init(bar(B_EMPTY + s), 1);            // released by the pair's MMAs
         }
@@ -186,6 +189,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         }
         mbar_init(bar(B_DRAIN), 1);
         *abort_flag = 0;
+        *reinterpret_cast<uint4 *>(smem + kOffNote + kNoteBytes) = make_uint4(0, 0, 0, 0);
         fence_mbar_init();
     }
     if (warp == kWarpMma) {                            // with the peer CTA's MMA warp
@@ -263,10 +267,10 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         for (int w = cid; w < n_items && ok; w += nclusters) {
             const Item it = item(w);
             const int hn = it.n >> 1;                  // tokens of a CTA's half of the tile
-            const uint32_t bytes = 2 * (kABytes + (A.row_token ? 0u : (uint32_t)hn * 128u));
+            const uint32_t bytes = 2 * kABytes + (A.row_token ? kNoteBytes : 2u * (uint32_t)hn * 128u);
             const CUtensorMap *xm = &maps.x[(hn >> 4) - 1];
             for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
-                if (at.lap > 0 && !cwait(bar(B_EMPTY + at.s), (at.lap - 1) & 1)) {
+                if (at.lap > 0 && !pwait(bar(B_EMPTY + at.s), (at.lap - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -291,9 +295,11 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     } else if (warp == kWarpRelay) {
         // ================================ relay ================================
         // The gathered rows were written through the generic proxy and the MMAs read through the
-        // async one.  The fence between the two waits for every copy its thread has in flight, so
-        // it is not the gathering threads that execute it (that took 1 us a stage) but this warp,
-        // which has none, once a stage's rows have landed.
+        // async one: a fence between the two, by a warp that has no copies of its own in flight,
+        // once a stage's rows have landed.  The odd CTA then tells the even one by a 16-byte bulk
+        // copy, an async operation that the fence orders behind the rows and whose bytes complete
+        // on the even CTA's barrier.  (A remote arrival with release at cluster scope stalled the
+        // warp for about 1 us a stage: 2.7 ms where this takes 1.1.)
         RingPos at;
         bool ok = true;
         for (int w = cid; w < n_items && ok; w += nclusters)
@@ -301,7 +307,12 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(B_GATHER + at.s), at.lap & 1, A.dev_status, abort_flag, A.wait_ns));
                 if (!ok) break;
                 fence_proxy_async_smem();
-                if (lane == 0) mbar_remote_arrive(bar(B_FULL + at.s), even);
+                __syncwarp();
+                if (lane == 0) {
+                    if (half == 0) mbar_arrive(bar(B_FULL + at.s));
+                    else bulk_copy_pair(mapa_shared(s_base + kOffNote, even), s_base + kOffNote + kNoteBytes, kNoteBytes,
+                                        mapa_shared(bar(B_FULL + at.s), even));
+                }
             }
     } else if (warp >= kWarpGather) {
         // ================================ gather ================================
@@ -322,7 +333,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                 src[j] = A.x + (size_t)r * A.K + piece * 8;
             }
             for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
-                if (at.lap > 0 && !cwait(bar(B_EMPTY + at.s), (at.lap - 1) & 1)) {
+                if (at.lap > 0 && !pwait(bar(B_EMPTY + at.s), (at.lap - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -353,13 +364,14 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             const int buf = i & 1;
             const uint32_t id = tc::idesc(2 * kRowsA, item(w).n, tc::kFmtBF16, 0, 0);
             // both CTAs' epilogues are done with this accumulator
-            if (i >= 2 && !cwait(bar(B_ACC_EMPTY + buf), ((i >> 1) - 1) & 1)) {
+            if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait_cluster(bar(B_ACC_EMPTY + buf), ((i >> 1) - 1) & 1,
+                                                                     A.dev_status, abort_flag, A.wait_ns))) {
                 ok = false;
                 break;
             }
             tc::fence_after();
             for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
-                if (!cwait(bar(B_FULL + at.s), at.lap & 1)) {
+                if (!pwait(bar(B_FULL + at.s), at.lap & 1)) {
                     ok = false;
                     break;
                 }
@@ -401,8 +413,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             float bias = 0.f;
             if (A.bias && frow < A.F)
                 bias = __ldg(A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + (kGated && quarter >= 2 ? F : 0) + frow);
-            bool ok = mbar_wait_cluster(bar(B_ACC_FULL + buf), (uint32_t)((i >> 1) & 1), A.dev_status, abort_flag,
-                                        A.wait_ns);
+            bool ok = mbar_wait_poll(bar(B_ACC_FULL + buf), (uint32_t)((i >> 1) & 1), A.dev_status, abort_flag, A.wait_ns);
             if (kGated) ok = named_all(swap_bar, 64, ok);     // the two warps go on together
             if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after();
@@ -629,12 +640,14 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     const int feat = act == INKATTN_ACT_SWIGLU ? 128 : 256;
     a.n_fblocks = (a.F + feat - 1) / feat;
     const int avg = a.M / a.E;
-    a.tile_n = a.E == 1 ? (a.M < kMaxN ? (a.M + 31) / 32 * 32 : kMaxN) : avg > 64 ? kMaxN : 128;
+    a.tile_n = !a.offsets ? (a.M < kMaxN ? (a.M + 31) / 32 * 32 : kMaxN) : avg > 64 ? kMaxN : 128;
     a.stage_bytes = kABytes + a.tile_n / 2 * 128;
     a.stages = kRingBytes / a.stage_bytes < kMaxStages ? kRingBytes / a.stage_bytes : kMaxStages;
     a.wait_ns = kernel_debug().wait_ns;
-    // at most this many items: full tiles, and one more for every expert that has rows
-    const long long items = ((long long)a.M / a.tile_n + (a.E < a.M ? a.E : a.M)) * a.n_fblocks;
+    // at most this many items: with experts, full tiles and one more for each that has rows
+    const long long tiles = a.offsets ? (long long)a.M / a.tile_n + (a.E < a.M ? a.E : a.M)
+                                      : ((long long)a.M + a.tile_n - 1) / a.tile_n;
+    const long long items = tiles * a.n_fblocks;
     if (items > INT_MAX / 2) return cudaErrorInvalidConfiguration;
     const int nk = (a.K + kKStep - 1) / kKStep;
     a.splits = 1;
