@@ -59,13 +59,14 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
+template <int kSleepNs>
 __device__ __forceinline__ bool mbar_wait_poll(uint32_t bar, uint32_t parity, int32_t *status,
                                                volatile int *abort, uint64_t limit_ns) {
     if (mbar_test_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
     for (uint32_t n = 1;; ++n) {
         if (mbar_test_wait(bar, parity)) return true;
-        __nanosleep(20);
+        if (kSleepNs > 0) __nanosleep(kSleepNs);
         if ((n & 255u) == 0u) {
             if (abort && *abort) return false;
             if (globaltimer() - t0 > limit_ns) {

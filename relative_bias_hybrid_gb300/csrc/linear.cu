@@ -153,8 +153,6 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     constexpr bool kGated = kAct == INKATTN_ACT_SWIGLU;
     constexpr int kFeat = kGated ? 64 : 128;           // output features of a CTA
     extern __shared__ __align__(1024) unsigned char smem[];
-    grid_dep_wait();
-    grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank();
     const int half = (int)(crank & 1u);                // CTA of the pair
@@ -163,6 +161,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     const int cid = (int)blockIdx.x / (2 * A.splits), nclusters = (int)gridDim.x / (2 * A.splits);
     const uint32_t s_base = smem_u32(smem);
     if ((s_base & 1023u) != 0u) {                      // the same in every CTA
+        grid_dep_wait();
         if (threadIdx.x == 0) set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
         return;
     }
@@ -173,7 +172,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffBar + B_COUNT * 8 + 4);
     // a stage of the ring: completed by copies or by a commit, which carry their own ordering
     auto pwait = [&](uint32_t addr, uint32_t parity) -> bool {
-        const bool r = mbar_wait_poll(addr, parity, A.dev_status, abort_flag, A.wait_ns);
+        const bool r = mbar_wait_poll<0>(addr, parity, A.dev_status, abort_flag, A.wait_ns);
         return __all_sync(0xffffffffu, r);
     };
 
@@ -196,7 +195,11 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         tc::tmem_alloc_pair(smem_u32(tmem_slot), 512);
         tc::tmem_relinquish_pair();
     }
+    // Everything up to here and, for a linear layer, the rest of the setup needs no global memory
+    // and runs while the kernel before this one on the stream finishes; each role waits for that
+    // kernel before it reads or writes global memory.
     if (warp == kWarpEpi) {
+        if (A.offsets) grid_dep_wait();
         // first row of every expert and the prefix of token tiles: s_tiles[e] = tiles of experts 0 .. e-1
         int carry = 0;
         if (lane == 0) s_tiles[0] = 0;
@@ -264,6 +267,8 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             tma_prefetch_desc(&maps.x[0]);
             tma_prefetch_desc(&maps.w);
         }
+        grid_dep_wait();
+        grid_dep_launch();
         for (int w = cid; w < n_items && ok; w += nclusters) {
             const Item it = item(w);
             const int hn = it.n >> 1;                  // tokens of a CTA's half of the tile
@@ -318,6 +323,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         // ================================ gather ================================
         // Eight lanes copy the 128 bytes of a row, 16 rows at a time, to the places that the
         // 128-byte swizzle gives them.
+        grid_dep_wait();
         const int gt = (int)threadIdx.x - kWarpGather * 32;
         const int piece = gt & 7, r0 = gt >> 3;
         RingPos at;
@@ -391,6 +397,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         __syncwarp();
     } else {
         // ================================ epilogue ================================
+        grid_dep_wait();
         const int e8 = (warp - kWarpEpi) >> 2;                // which of every two blocks of 32 tokens
         const int quarter = warp & 3;                         // TMEM lanes this warp may access
         float *stg = reinterpret_cast<float *>(smem + kOffStg + (warp - kWarpEpi) * kStgBytes);
@@ -413,7 +420,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             float bias = 0.f;
             if (A.bias && frow < A.F)
                 bias = __ldg(A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + (kGated && quarter >= 2 ? F : 0) + frow);
-            bool ok = mbar_wait_poll(bar(B_ACC_FULL + buf), (uint32_t)((i >> 1) & 1), A.dev_status, abort_flag, A.wait_ns);
+            bool ok = mbar_wait_poll<32>(bar(B_ACC_FULL + buf), (uint32_t)((i >> 1) & 1), A.dev_status, abort_flag, A.wait_ns);
             if (kGated) ok = named_all(swap_bar, 64, ok);     // the two warps go on together
             if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after();
