@@ -261,35 +261,37 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
 
     if (warp == kWarpProducer) {
         // ================================ producer ================================
+        // One lane alone: a step of its loop takes about 250 cycles, of which the two copies are
+        // 160, and the ring runs dry when a step approaches the MMAs' 512 cycles.
         RingPos at;
-        bool ok = true;
         if (lane == 0) {
             tma_prefetch_desc(&maps.x[0]);
             tma_prefetch_desc(&maps.w);
-        }
-        grid_dep_wait();
-        grid_dep_launch();
-        for (int w = cid; w < n_items && ok; w += nclusters) {
-            const Item it = item(w);
-            const int hn = it.n >> 1;                  // tokens of a CTA's half of the tile
-            const uint32_t bytes = 2 * kABytes + (A.row_token ? kNoteBytes : 2u * (uint32_t)hn * 128u);
-            const CUtensorMap *xm = &maps.x[(hn >> 4) - 1];
-            for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
-                if (at.lap > 0 && !pwait(bar(B_EMPTY + at.s), (at.lap - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t dst = s_base + (uint32_t)(at.s * A.stage_bytes);
-                const uint32_t fb = mapa_shared(bar(B_FULL + at.s), even);
-                if (lane == 0) {
+            grid_dep_wait();
+            grid_dep_launch();
+            const uint32_t full = mapa_shared(bar(B_FULL), even);
+            bool ok = true;
+            for (int w = cid; w < n_items && ok; w += nclusters) {
+                const Item it = item(w);
+                const int hn = it.n >> 1;              // tokens of a CTA's half of the tile
+                const uint32_t bytes = 2 * kABytes + (A.row_token ? kNoteBytes : 2u * (uint32_t)hn * 128u);
+                const CUtensorMap *xm = &maps.x[(hn >> 4) - 1];
+                const int wrow = (it.fb * 2 + half) * kFeat, xrow = it.row0 + half * hn;
+                for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
+                    if (at.lap > 0 && !mbar_wait_poll<0>(bar(B_EMPTY + at.s), (at.lap - 1) & 1, A.dev_status, abort_flag,
+                                                         A.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = s_base + (uint32_t)(at.s * A.stage_bytes), fb = full + 8u * (uint32_t)at.s;
                     if (half == 0) mbar_arrive_expect_tx(bar(B_FULL + at.s), bytes);
-                    if (kGated) tma_load_4d_pair(dst, &maps.w, k * kKStep, (it.fb * 2 + half) * kFeat, 0, it.e, fb);
-                    else tma_load_3d_pair(dst, &maps.w, k * kKStep, (it.fb * 2 + half) * kFeat, it.e, fb);
-                    if (!A.row_token) tma_load_2d_pair(dst + kABytes, xm, k * kKStep, it.row0 + half * hn, fb);
+                    if (kGated) tma_load_4d_pair(dst, &maps.w, k * kKStep, wrow, 0, it.e, fb);
+                    else tma_load_3d_pair(dst, &maps.w, k * kKStep, wrow, it.e, fb);
+                    if (!A.row_token) tma_load_2d_pair(dst + kABytes, xm, k * kKStep, xrow, fb);
                 }
-                __syncwarp();
             }
         }
+        __syncwarp();
         // nothing may still be landing in shared memory when the pair tears down: the even CTA
         // waits for the last lap of both CTAs' copies (see qkvr.cu)
         if (lane == 0 && half == 0)
