@@ -25,12 +25,14 @@
 // up rows in turn, a shuffle apart in one warp, were measured first: four boxes a stage made the
 // copies the bound, 0.78 ms where one box takes 0.57 for the same products.)
 //
-// One CTA per SM, 10 warps:
-//   warp 0      producer: copies of the weight rows and the token rows into a ring of stages
-//               of K = 64; as many stages as fit 192 KB
+// One CTA per SM, 11 warps (16 with row indices):
+//   warps 0, 10 producers, a lane of each: copies of the weight rows and the token rows into a
+//               ring of stages of K = 64, as many as fit 192 KB, the two taking turns: a stage
+//               costs its producer about 400 cycles (the wait, the barrier, two copies), which a
+//               single one made the bound of every tile below N = 256
 //   warp 1      even CTA: MMA issuer, K = 16 steps into one of two TMEM accumulators (2 x 256
 //               columns), so that an item's epilogue overlaps the next item's MMAs
-//   warps 10-13 only with row indices: the gather; warp 14 hands its stages to the MMA warp
+//   warps 11-14 only with row indices: the gather; warp 15 hands its stages to the MMA warp
 //   warps 2-9   epilogue: a warp owns 32 TMEM lanes (weight rows) and every second block of 32
 //               columns (tokens); bias and activation per lane, then a turn through a private
 //               staging buffer, so that a token's features leave as 16-byte pieces
@@ -38,9 +40,10 @@
 // release it in both, as in the qkvr kernel.
 //
 // Few items (a decode batch): the K range is split over the S pairs of one cluster.  Each CTA
-// leaves its fp32 partial tile in its own shared memory (the ring, idle by then) and the
-// CTAs then add the S partials in order through distributed shared memory, each for its
-// share of the tokens: no workspace, no atomics, one launch.
+// writes its fp32 partial tile, a share of the tokens to each pair, into the other CTAs' shared
+// memory (the rings, idle by then), and each adds the S partials of its share in order: no
+// workspace, no atomics, one launch.  (Reading the partials from the other CTAs instead took
+// 11000 cycles for 256 tokens and S = 4: 12 bytes a cycle.)
 #include <atomic>
 #include <climits>
 
@@ -60,11 +63,13 @@ constexpr int kKStep = 64;                        // K per ring stage (one 128-b
 constexpr int kABytes = kRowsA * 128;             // 16 KB
 constexpr int kRingBytes = 192 * 1024;
 constexpr int kMaxStages = 12;
-constexpr int kThreads = 320;                     // without a gather
+constexpr int kMaxSplits = 4;                     // pairs of a cluster (eight CTAs)
+constexpr int kThreads = 352;                     // without a gather
 constexpr int kGatherThreads = 128;
 constexpr int kMaxThreads = kThreads + kGatherThreads + 32;
 constexpr int kEpiThreads = 256;
-constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpEpi = 2, kWarpGather = 10, kWarpRelay = 14;
+constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpEpi = 2, kWarpProducer2 = 10, kWarpGather = 11,
+              kWarpRelay = 15;
 constexpr int kStgPitch = 36;                     // floats of a staging row: 32 features + 4
 constexpr int kStgBytes = 16 * kStgPitch * 4;     // 16 tokens, one buffer per epilogue warp
 constexpr int kRaster = 8;                        // feature blocks per raster group
@@ -130,19 +135,17 @@ __device__ __forceinline__ bool named_all(int id, int n, bool v) {
 struct RingPos {
     int s = 0;
     uint32_t lap = 0;
-    __device__ __forceinline__ void next(int stages) {
-        if (++s == stages) {
-            s = 0;
+    __device__ __forceinline__ void next(int stages, int by = 1) {
+        s += by;
+        if (s >= stages) {
+            s -= stages;
             ++lap;
         }
     }
 };
 
-__device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
-    return v;
+__device__ __forceinline__ void st_shared_cluster(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
 }
 
 }  // namespace
@@ -259,17 +262,21 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         return it;
     };
 
-    if (warp == kWarpProducer) {
-        // ================================ producer ================================
-        // One lane alone: a step of its loop takes about 250 cycles, of which the two copies are
-        // 160, and the ring runs dry when a step approaches the MMAs' 512 cycles.
-        RingPos at;
+    if (warp == kWarpProducer || warp == kWarpProducer2) {
+        // ================================ producers ================================
         if (lane == 0) {
-            tma_prefetch_desc(&maps.x[0]);
-            tma_prefetch_desc(&maps.w);
+            const int turn = warp == kWarpProducer ? 0 : 1;
+            if (turn == 0) {
+                tma_prefetch_desc(&maps.x[0]);
+                tma_prefetch_desc(&maps.w);
+            }
             grid_dep_wait();
-            grid_dep_launch();
+            if (turn == 0) grid_dep_launch();
             const uint32_t full = mapa_shared(bar(B_FULL), even);
+            RingPos at;
+            at.s = turn;
+            int first = turn, last = -1;               // of an item's loads, the first of this warp's; its newest load
+            int base = 0;                              // loads of the items before
             bool ok = true;
             for (int w = cid; w < n_items && ok; w += nclusters) {
                 const Item it = item(w);
@@ -277,7 +284,8 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                 const uint32_t bytes = 2 * kABytes + (A.row_token ? kNoteBytes : 2u * (uint32_t)hn * 128u);
                 const CUtensorMap *xm = &maps.x[(hn >> 4) - 1];
                 const int wrow = (it.fb * 2 + half) * kFeat, xrow = it.row0 + half * hn;
-                for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
+                int k = k_lo + first;
+                for (; k < k_hi; k += 2, at.next(A.stages, 2)) {
                     if (at.lap > 0 && !mbar_wait_poll<0>(bar(B_EMPTY + at.s), (at.lap - 1) & 1, A.dev_status, abort_flag,
                                                          A.wait_ns)) {
                         ok = false;
@@ -288,17 +296,19 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                     if (kGated) tma_load_4d_pair(dst, &maps.w, k * kKStep, wrow, 0, it.e, fb);
                     else tma_load_3d_pair(dst, &maps.w, k * kKStep, wrow, it.e, fb);
                     if (!A.row_token) tma_load_2d_pair(dst + kABytes, xm, k * kKStep, xrow, fb);
+                    last = base + k - k_lo;
                 }
+                first = k - k_hi;
+                base += k_hi - k_lo;
             }
+            // nothing may still be landing in shared memory when the pair tears down: the even
+            // CTA waits for the last lap of both CTAs' copies (see qkvr.cu), for the loads whose stage
+            // the other producer's newest load cannot have taken over
+            if (half == 0)
+                for (int l = last; l >= 0 && l > last + 1 - A.stages; l -= 2)
+                    mbar_drain(bar(B_FULL + l % A.stages), (uint32_t)(l / A.stages) & 1u, A.dev_status, A.wait_ns);
         }
         __syncwarp();
-        // nothing may still be landing in shared memory when the pair tears down: the even CTA
-        // waits for the last lap of both CTAs' copies (see qkvr.cu)
-        if (lane == 0 && half == 0)
-            for (int l = 0; l < A.stages; ++l) {
-                const uint32_t laps = at.lap + (l < at.s ? 1u : 0u);      // uses of stage l
-                if (laps > 0) mbar_drain(bar(B_FULL + l), (laps - 1) & 1, A.dev_status, A.wait_ns);
-            }
     } else if (warp == kWarpRelay) {
         // ================================ relay ================================
         // The gathered rows were written through the generic proxy and the MMAs read through the
@@ -426,11 +436,14 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             if (kGated) ok = named_all(swap_bar, 64, ok);     // the two warps go on together
             if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after();
+            if (A.splits > 1) break;                          // (one item; it is finished below)
             const uint32_t taddr = tmem + (uint32_t)(buf * kMaxN) + ((uint32_t)(quarter * 32) << 16);
+            const bool reused = w + 2 * nclusters < n_items;  // the MMA warp waits for this accumulator
             auto release = [&] {
+                if (!reused) return;
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_remote_arrive(bar(B_ACC_EMPTY + buf), even);   // its MMA warp waits
+                if (lane == 0) mbar_remote_arrive(bar(B_ACC_EMPTY + buf), even);
             };
             const int nblocks = (it.nt + 31) >> 5;
             if (e8 >= nblocks) release();
@@ -439,12 +452,6 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                 tc::ld32(taddr + (uint32_t)(c * 32), v);
                 tc::wait_ld();
                 if (c + 2 >= nblocks) release();
-                if (A.splits > 1) {                           // the partial tile [token][weight row]
-                    float *part = reinterpret_cast<float *>(smem) + (size_t)c * 32 * kRowsA + quarter * 32 + lane;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) part[j * kRowsA] = __uint_as_float(v[j]);
-                    continue;
-                }
                 // tokens of this block that are stored
                 bool mine = c * 32 + lane < it.nt;
                 if (A.row_token && mine) {
@@ -542,19 +549,48 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     }
 
     if (A.splits > 1) {
-        __syncwarp();
-        cluster_sync();                                // every partial tile of the cluster is complete
         const int et = (int)threadIdx.x - kWarpEpi * 32;
-        if (et >= 0 && et < kEpiThreads && cid < n_items) {
-            const Item it = item(cid);
+        const bool epi = et >= 0 && et < kEpiThreads && cid < n_items;
+        const Item it = cid < n_items ? item(cid) : Item{};
+        const int share = it.n / A.splits;             // tokens that a pair adds up, a multiple of 8
+        __syncwarp();
+        cluster_sync();                                // every pair's MMAs are done: the rings are idle
+        if (epi) {
+            const int quarter = warp & 3;
+            const uint32_t place = s_base + (uint32_t)((split * share * kRowsA + quarter * 32 + lane) * 4);
+            for (int c = (warp - kWarpEpi) >> 2; c * 32 < it.nt; c += 2) {
+                uint32_t v[32];
+                tc::ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(c * 32), v);
+                tc::wait_ld();
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int t = c * 32 + g * 8, owner = t / share;
+                    if (t >= it.nt) break;
+                    const uint32_t dst = mapa_shared(place, (uint32_t)(2 * owner + half)) +
+                                         (uint32_t)((t - owner * share) * kRowsA * 4);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) st_shared_cluster(dst + (uint32_t)(j * kRowsA * 4), v[g * 8 + j]);
+                }
+            }
+        }
+        tc::fence_before();
+        __syncwarp();
+        cluster_sync();                                // every partial tile has arrived, TMEM has been read
+        if (warp == kWarpMma) {                        // with the peer CTA's MMA warp
+            tc::fence_after();
+            tc::tmem_dealloc_pair(tmem, 512);
+        }
+        if (epi) {
             const size_t F = (size_t)A.F;
-            // four features of one token per step; the cluster's pairs take the tokens in turn
+            const bool vec = (A.F & 3) == 0;
+            // four features of one token per step
             constexpr int kPer = kFeat / 4;            // steps of a token
-            for (int u = et; u < ((it.nt - split + A.splits - 1) / A.splits) * kPer; u += kEpiThreads) {
-                const int t = (u / kPer) * A.splits + split, j = u % kPer;
+            const int mine = min(share, it.nt - split * share);
+            for (int u = et; u < mine * kPer; u += kEpiThreads) {
+                const int t = u / kPer, j = u % kPer;
                 const int f = (it.fb * 2 + half) * kFeat + j * 4;
                 if (f >= A.F) continue;
-                const int i = it.row0 + t;
+                const int i = it.row0 + split * share + t;
                 if (A.row_token) {
                     const int s = __ldg(A.row_token + i);
                     if (s < 0 || s >= A.N_x) {
@@ -562,31 +598,51 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                         continue;
                     }
                 }
-                const uint32_t src = s_base + (uint32_t)((t * kRowsA + j * 4) * 4);
-                float y[4] = {0.f, 0.f, 0.f, 0.f}, up[4] = {0.f, 0.f, 0.f, 0.f};
-                for (int s = 0; s < A.splits; ++s) {
-                    const uint32_t a = mapa_shared(src, (uint32_t)(2 * s + half));
-                    const float4 p = ld_shared_cluster_f4(a);
-                    y[0] += p.x; y[1] += p.y; y[2] += p.z; y[3] += p.w;
-                    if (kGated) {
-                        const float4 q = ld_shared_cluster_f4(a + 256u)      /* 64 rows on */;
-                        up[0] += q.x; up[1] += q.y; up[2] += q.z; up[3] += q.w;
+                const float4 *src = reinterpret_cast<const float4 *>(smem) + t * (kRowsA / 4) + j;
+                const int step = share * (kRowsA / 4);
+                float sum[4] = {}, up[4] = {};
+#pragma unroll
+                for (int s = 0; s < kMaxSplits; ++s) {
+                    if (s >= A.splits) break;
+                    const float4 q = src[s * step];
+                    sum[0] += q.x; sum[1] += q.y; sum[2] += q.z; sum[3] += q.w;
+                    if (kGated) {                      // the ups lie 64 rows on
+                        const float4 r = src[s * step + 16];
+                        up[0] += r.x; up[1] += r.y; up[2] += r.z; up[3] += r.w;
                     }
                 }
                 const float *b = A.bias ? A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + f : nullptr;
+                const size_t at = (size_t)i * F + f;
+                float y[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const bool in = f + n < A.F;
+                    y[n] = activate<kGated ? INKATTN_ACT_SILU : kAct>(sum[n] + (b && in ? __ldg(b + n) : 0.f));
+                    if (kGated) y[n] *= up[n] + (b && in ? __ldg(b + F + n) : 0.f);
+                }
+                if (vec) {
+                    if (A.residual) {
+                        const uint2 r = *reinterpret_cast<const uint2 *>(A.residual + at);
+                        y[0] += bf16_lo(r.x); y[1] += bf16_hi(r.x);
+                        y[2] += bf16_lo(r.y); y[3] += bf16_hi(r.y);
+                    }
+                    if (A.out_f32)
+                        *reinterpret_cast<float4 *>(static_cast<float *>(A.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+                    else
+                        *reinterpret_cast<uint2 *>(static_cast<inkattn_bf16 *>(A.out) + at) =
+                            make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+                    continue;
+                }
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     if (f + n >= A.F) break;
-                    const float v = y[n] + (b ? __ldg(b + n) : 0.f);
-                    float o = activate<kGated ? INKATTN_ACT_SILU : kAct>(v);
-                    if (kGated) o *= up[n] + (b ? __ldg(b + F + n) : 0.f);
-                    const size_t at = (size_t)i * F + f + n;
-                    if (A.residual) o += load_bf16(A.residual + at);
-                    if (A.out_f32) static_cast<float *>(A.out)[at] = o;
-                    else store_bf16(static_cast<inkattn_bf16 *>(A.out) + at, o);
+                    const float o = A.residual ? y[n] + load_bf16(A.residual + at + n) : y[n];
+                    if (A.out_f32) static_cast<float *>(A.out)[at + n] = o;
+                    else store_bf16(static_cast<inkattn_bf16 *>(A.out) + at + n, o);
                 }
             }
         }
+        return;                                        // (nothing of a peer is read or written after the barrier)
     }
 
     tc::fence_before();
@@ -660,7 +716,7 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     if (items > INT_MAX / 2) return cudaErrorInvalidConfiguration;
     const int nk = (a.K + kKStep - 1) / kKStep;
     a.splits = 1;
-    for (int s = 2; s <= 4; s *= 2)
+    for (int s = 2; s <= kMaxSplits; s *= 2)
         if (nk >= 4 * s && items <= resident_clusters(2 * s, num_sms)) a.splits = s;
     const int most = resident_clusters(2 * a.splits, num_sms);
     if (most < 1) return cudaErrorInvalidConfiguration;
