@@ -48,26 +48,18 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
 }
 
 // mbar_wait for a phase that TMA copies or tensor-core commits complete, from either CTA of a
-// pair: it polls like mbar_wait_cluster, but with the plain (CTA-scope) acquire.  Cluster
-// scope, needed behind another CTA's own arrivals, costs about 250 ns a wait, as much as the
-// MMAs of a K = 64 stage at N = 256.
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-template <int kSleepNs>
-__device__ __forceinline__ bool mbar_wait_poll(uint32_t bar, uint32_t parity, int32_t *status,
-                                               volatile int *abort, uint64_t limit_ns) {
-    if (mbar_test_wait(bar, parity)) return true;
+// pair: with the plain (CTA-scope) acquire, since those carry their own ordering (cluster scope,
+// needed behind another CTA's own arrivals, costs about 250 ns a wait), and in short suspensions,
+// so that neither a completion from the other CTA is missed for long nor a polling warp takes
+// the issue slots and shared-memory cycles of the others.
+template <int kSuspendNs>
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, int32_t *status, volatile int *abort,
+                                                uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
     for (uint32_t n = 1;; ++n) {
-        if (mbar_test_wait(bar, parity)) return true;
-        if (kSleepNs > 0) __nanosleep(kSleepNs);
-        if ((n & 255u) == 0u) {
+        if (mbar_try_wait_sleep(bar, parity, kSuspendNs)) return true;
+        if ((n & 63u) == 0u) {
             if (abort && *abort) return false;
             if (globaltimer() - t0 > limit_ns) {
                 set_status(status, INKATTN_ERR_DEVICE_TIMEOUT);

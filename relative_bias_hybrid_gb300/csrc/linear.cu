@@ -65,8 +65,8 @@ constexpr int kRingBytes = 192 * 1024;
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplits = 4;                     // pairs of a cluster (eight CTAs)
 constexpr int kThreads = 352;                     // without a gather
-constexpr int kGatherThreads = 128;
-constexpr int kMaxThreads = kThreads + kGatherThreads + 32;
+constexpr int kGatherWarps = 4;
+constexpr int kMaxThreads = kThreads + kGatherWarps * 32 + 32;
 constexpr int kEpiThreads = 256;
 constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpEpi = 2, kWarpProducer2 = 10, kWarpGather = 11,
               kWarpRelay = 15;
@@ -175,14 +175,14 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffBar + B_COUNT * 8 + 4);
     // a stage of the ring: completed by copies or by a commit, which carry their own ordering
     auto pwait = [&](uint32_t addr, uint32_t parity) -> bool {
-        const bool r = mbar_wait_poll<0>(addr, parity, A.dev_status, abort_flag, A.wait_ns);
+        const bool r = mbar_wait_short<200>(addr, parity, A.dev_status, abort_flag, A.wait_ns);
         return __all_sync(0xffffffffu, r);
     };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < A.stages; ++s) {
             mbar_init(bar(B_FULL + s), A.row_token ? 2 : 1);   // (the even CTA's: both CTAs' copies, its relay)
-            mbar_init(bar(B_GATHER + s), kGatherThreads);
+            mbar_init(bar(B_GATHER + s), kGatherWarps * 32);
             mbar_init(bar(B_EMPTY + s), 1);            // released by the pair's MMAs
         }
         for (int s = 0; s < 2; ++s) {
@@ -286,7 +286,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                 const int wrow = (it.fb * 2 + half) * kFeat, xrow = it.row0 + half * hn;
                 int k = k_lo + first;
                 for (; k < k_hi; k += 2, at.next(A.stages, 2)) {
-                    if (at.lap > 0 && !mbar_wait_poll<0>(bar(B_EMPTY + at.s), (at.lap - 1) & 1, A.dev_status, abort_flag,
+                    if (at.lap > 0 && !mbar_wait_short<200>(bar(B_EMPTY + at.s), (at.lap - 1) & 1, A.dev_status, abort_flag,
                                                          A.wait_ns)) {
                         ok = false;
                         break;
@@ -321,7 +321,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         bool ok = true;
         for (int w = cid; w < n_items && ok; w += nclusters)
             for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(B_GATHER + at.s), at.lap & 1, A.dev_status, abort_flag, A.wait_ns));
+                ok = pwait(bar(B_GATHER + at.s), at.lap & 1);
                 if (!ok) break;
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -376,7 +376,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         const int my_items = cid < n_items ? (n_items - cid + nclusters - 1) / nclusters : 0;
         long long left = (long long)my_items * (k_hi - k_lo);
         RingPos at;
-        bool ok = true;
+        bool ok = true, ready = false;
         int i = 0;
         for (int w = cid; w < n_items && ok; w += nclusters, ++i) {
             const int buf = i & 1;
@@ -388,18 +388,21 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                 break;
             }
             tc::fence_after();
-            for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
-                if (!pwait(bar(B_FULL + at.s), at.lap & 1)) {
+            for (int k = k_lo; k < k_hi; ++k) {
+                if (!ready && !pwait(bar(B_FULL + at.s), at.lap & 1)) {
                     ok = false;
                     break;
                 }
+                const RingPos now = at;
+                at.next(A.stages);
+                ready = left > 1 && mbar_test_wait(bar(B_FULL + at.s), at.lap & 1);   // seen while the MMAs are issued
                 tc::fence_after();
-                const uint64_t off = (uint64_t)(at.s * (A.stage_bytes >> 4));
+                const uint64_t off = (uint64_t)(now.s * (A.stage_bytes >> 4));
                 tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)(buf * kMaxN), da0 + off, db0 + off, id,
-                                                k > k_lo ? 1u : 0u, bar(B_EMPTY + at.s), left > A.stages ? 1u : 0u,
+                                                k > k_lo ? 1u : 0u, bar(B_EMPTY + now.s), left > A.stages ? 1u : 0u,
                                                 bar(B_ACC_FULL + buf), k == k_hi - 1 ? 1u : 0u, pair);
                 --left;
-                __syncwarp();
+                ready = __all_sync(0xffffffffu, ready);
             }
         }
         // every MMA of the pair has completed before TMEM is released
@@ -432,7 +435,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             float bias = 0.f;
             if (A.bias && frow < A.F)
                 bias = __ldg(A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + (kGated && quarter >= 2 ? F : 0) + frow);
-            bool ok = mbar_wait_poll<32>(bar(B_ACC_FULL + buf), (uint32_t)((i >> 1) & 1), A.dev_status, abort_flag, A.wait_ns);
+            bool ok = mbar_wait_short<1000>(bar(B_ACC_FULL + buf), (uint32_t)((i >> 1) & 1), A.dev_status, abort_flag, A.wait_ns);
             if (kGated) ok = named_all(swap_bar, 64, ok);     // the two warps go on together
             if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after();
