@@ -65,7 +65,7 @@ constexpr int kRingBytes = 192 * 1024;
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplits = 4;                     // pairs of a cluster (eight CTAs)
 constexpr int kThreads = 352;                     // without a gather
-constexpr int kGatherWarps = 4;
+constexpr int kGatherWarps = 4, kGatherTeam = 64;  // threads that gather a stage together
 constexpr int kMaxThreads = kThreads + kGatherWarps * 32 + 32;
 constexpr int kEpiThreads = 256;
 constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpEpi = 2, kWarpProducer2 = 10, kWarpGather = 11,
@@ -182,7 +182,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < A.stages; ++s) {
             mbar_init(bar(B_FULL + s), A.row_token ? 2 : 1);   // (the even CTA's: both CTAs' copies, its relay)
-            mbar_init(bar(B_GATHER + s), kGatherWarps * 32);
+            mbar_init(bar(B_GATHER + s), kGatherTeam);
             mbar_init(bar(B_EMPTY + s), 1);            // released by the pair's MMAs
         }
         for (int s = 0; s < 2; ++s) {
@@ -333,24 +333,28 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             }
     } else if (warp >= kWarpGather) {
         // ================================ gather ================================
-        // Eight lanes copy the 128 bytes of a row, 16 rows at a time, to the places that the
-        // 128-byte swizzle gives them.
+        // Eight lanes copy the 128 bytes of a row, to the places that the 128-byte swizzle gives
+        // them.  Two teams take the stages in turn: a stage's wait, about 200 cycles, comes up every
+        // other time (all four warps on every stage: 1.23 ms where this takes 1.12).
         grid_dep_wait();
         const int gt = (int)threadIdx.x - kWarpGather * 32;
-        const int piece = gt & 7, r0 = gt >> 3;
+        const int team = gt / kGatherTeam, piece = gt & 7, r0 = (gt % kGatherTeam) >> 3;
         RingPos at;
+        at.s = team;
+        int first = team;
         bool ok = true;
         for (int w = cid; w < n_items && ok; w += nclusters) {
             const Item it = item(w);
             const int hn = it.n >> 1, mine = min(max(it.nt - half * hn, 0), hn);
-            const inkattn_bf16 *src[8];
+            const inkattn_bf16 *src[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                int r = r0 + 16 * j < mine ? __ldg(A.row_token + it.row0 + half * hn + r0 + 16 * j) : 0;
+            for (int j = 0; j < 16; ++j) {
+                int r = r0 + 8 * j < mine ? __ldg(A.row_token + it.row0 + half * hn + r0 + 8 * j) : 0;
                 if (r < 0 || r >= A.N_x) r = 0;        // (flagged and not stored by the epilogue)
                 src[j] = A.x + (size_t)r * A.K + piece * 8;
             }
-            for (int k = k_lo; k < k_hi; ++k, at.next(A.stages)) {
+            int k = k_lo + first;
+            for (; k < k_hi; k += 2, at.next(A.stages, 2)) {
                 if (at.lap > 0 && !pwait(bar(B_EMPTY + at.s), (at.lap - 1) & 1)) {
                     ok = false;
                     break;
@@ -358,11 +362,12 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                 const uint32_t dst = s_base + (uint32_t)(at.s * A.stage_bytes + kABytes + r0 * 128 + ((piece ^ (r0 & 7)) << 4));
                 const bool live = k * kKStep + piece * 8 < A.K;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (r0 + 16 * j < mine)
-                        cp_async16(dst + (uint32_t)(j * 16 * 128), live ? src[j] + k * kKStep : src[j], live);
+                for (int j = 0; j < 16; ++j)
+                    if (r0 + 8 * j < mine)
+                        cp_async16(dst + (uint32_t)(j * 8 * 128), live ? src[j] + k * kKStep : src[j], live);
                 cp_async_arrive(bar(B_GATHER + at.s));
             }
+            first = k - k_hi;
         }
         cp_async_wait_all();
     } else if (warp == kWarpMma && half != 0) {

@@ -5,8 +5,10 @@
 //  the weights but not the choice.
 //
 // Two launches.  k_route_choose: a warp per token holds the token's logits as ordered integer
-// keys in registers and takes the maximum top_k times (redux.sync on the key, then on the
-// index, so that equal logits go to the lower index).  k_route_place: a counting sort of the
+// keys in registers, each lane knows its own two best, and top_k times the best of the lanes is
+// taken (redux.sync on the key, then on the index, so that equal logits go to the lower index).
+// A lane looks for its next two only when both are gone.  The next token's logits are requested
+// before this one's are used.  k_route_place: a counting sort of the
 // (token, choice) pairs by expert, stable in (token, choice) order.  The order is made of
 // integer counts alone, so it does not depend on the scheduling:
 //   - the tokens are cut into chunks; a block places one chunk, and a warp a contiguous part
@@ -23,85 +25,115 @@ namespace inkattn {
 
 namespace {
 
-constexpr int kChooseThreads = 256;
+constexpr int kChooseThreads = 1024;               // of a chunk; of one chunk alone, fewer
+constexpr int kChooseThreadsOne = 256;
 constexpr int kPlaceThreads = 1024;
 constexpr int kPlaceWarps = kPlaceThreads / 32;
 constexpr int kOneChunkPairs = 4096;               // pairs that one block places
 constexpr int kChunks = 152;                       // chunks of a larger batch, at most
 
 // Order-preserving integer key of a logit: larger logit, larger key; +0 and -0 alike; NaN as
-// -infinity.  Every logit's key is at least 0x007FFFFF, so 0 marks "taken" or "none".
+// -infinity.  Every key is at least 0x007FFFFF; 0 stands for no logit.
 __device__ __forceinline__ uint32_t logit_key(float l) {
-    if (l != l) l = -INFINITY;
-    const uint32_t u = __float_as_uint(l + 0.0f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    const uint32_t u = __float_as_uint(l == l ? l + 0.0f : -INFINITY);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
+
+// A lane's two best keys among those it holds that come after (top, e) in the order of choice,
+// and their places; equal keys in the order of their places.
+struct BestTwo {
+    uint32_t k1 = 0, k2 = 0;
+    int i1 = 0, i2 = 0;
+    __device__ __forceinline__ void add(uint32_t k, int i) {
+        const bool first = k > k1, second = k > k2;
+        i2 = first ? i1 : second ? i : i2;
+        k2 = first ? k1 : second ? k : k2;
+        i1 = first ? i : i1;
+        k1 = first ? k : k1;
+    }
+};
 
 }  // namespace
 
-// kPer = logits a lane holds (E <= 32 * kPer).  counts: [chunks][E], one row written by
-// each block, or NULL for a batch of one chunk.
+// kPer = logits a lane holds (E <= 32 * kPer); logit e in lane e % 32.  counts: [chunks][E], one
+// row written by each block, or NULL for a batch of one chunk.
 template <int kPer>
-__global__ void __launch_bounds__(kChooseThreads)
+__global__ void __launch_bounds__(kChooseThreads, 1)
 k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *__restrict__ counts) {
     extern __shared__ uint32_t s_hist[];               // [E], of this block's chunk
     grid_dep_wait();
     grid_dep_launch();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int width = p.E + p.n_shared, ws = p.top_k + p.n_shared;
     if (counts) {
-        for (int e = threadIdx.x; e < p.E; e += kChooseThreads) s_hist[e] = 0;
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) s_hist[e] = 0;
         __syncthreads();
     }
     const int t_lo = blockIdx.x * chunk_tokens, t_hi = min(p.N_tok, t_lo + chunk_tokens);
-    for (int t = t_lo + warp; t < t_hi; t += kChooseThreads / 32) {
+    const bool is_shared = lane >= p.top_k && lane < ws;
+    float next[kPer], next_shared = -INFINITY;
+    auto request = [&](int t) {
         const float *row = p.logits + (size_t)t * width;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) next[i] = lane + 32 * i < p.E ? __ldg(row + lane + 32 * i) : -INFINITY;
+        if (is_shared) next_shared = __ldg(row + p.E + lane - p.top_k);
+    };
+    if (t_lo + warp < t_hi) request(t_lo + warp);
+    for (int t = t_lo + warp; t < t_hi; t += warps) {
         uint32_t key[kPer];
+        BestTwo best;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int e = lane + 32 * i;
-            key[i] = e < p.E ? logit_key(__ldg(row + e)) : 0u;
+            key[i] = lane + 32 * i < p.E ? logit_key(next[i]) : 0u;
+            best.add(key[i], i);
         }
         // lane j < top_k: the j-th choice; the next n_shared lanes: the shared experts
-        float l = lane >= p.top_k && lane < ws ? __ldg(row + p.E + lane - p.top_k) : -INFINITY;
-        if (l != l) l = -INFINITY;
+        float l = next_shared == next_shared ? next_shared : -INFINITY;
         int id = 0;
+        if (t + warps < t_hi) request(t + warps);
+        bool two = true;                               // best.k2 is known
         for (int j = 0; j < p.top_k; ++j) {
-            uint32_t best = 0;
-            int at = 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at = i;
-                }
-            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-            const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(lane + 32 * at) : 0xffffffffu);
-            if (best == top && (uint32_t)(lane + 32 * at) == e) {
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (i == at) key[i] = 0;
-            }
+            const uint32_t top = __reduce_max_sync(0xffffffffu, best.k1);
+            const uint32_t mine = best.k1 == top ? (uint32_t)(lane + 32 * best.i1) : 0xffffffffu;
+            const uint32_t e = __reduce_min_sync(0xffffffffu, mine);
+            const bool taken = mine == e;
             if (lane == j) {
                 l = key_logit(top);
                 id = (int)e;
+            }
+            if (__any_sync(0xffffffffu, taken && !two)) {
+                BestTwo rest;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const bool after = key[i] < top || (key[i] == top && (uint32_t)(lane + 32 * i) > e);
+                    rest.add(after ? key[i] : 0u, i);
+                }
+                if (taken) {
+                    best = rest;
+                    two = true;
+                }
+            } else if (taken) {
+                best.k1 = best.k2;
+                best.i1 = best.i2;
+                two = false;
             }
         }
         // scores up to a factor common to the token, so that they do not all vanish: softmax
         // exp(l - m) with m the largest logit; sigmoid exp(l - m) / (1 + exp(l)) with m the
         // largest logit or 0, whichever is less (for m = 0 that is the sigmoid itself)
-        float m = lane < ws ? l : -INFINITY;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const bool sigmoid = p.score == INKATTN_SCORE_SIGMOID;
-        if (sigmoid) m = fminf(m, 0.f);
-        float s = 0.f;
-        if (sigmoid && l > 0.f) s = 1.f / (1.f + expf(-l));
-        else if (l != -INFINITY) s = l == m ? 1.f : expf(l - m);         // (l == m: infinities too)
-        if (sigmoid && l <= 0.f) s = s / (1.f + expf(l));
+        const uint32_t mk = __reduce_max_sync(0xffffffffu, lane < ws ? logit_key(l) : 0u);
+        const float m = sigmoid ? fminf(key_logit(mk), 0.f) : key_logit(mk);
+        float s;
+        if (sigmoid && l > 0.f) {
+            s = 1.f / (1.f + expf(-l));
+        } else {
+            s = l == -INFINITY ? 0.f : l == m ? 1.f : expf(l - m);           // (l == m: infinities too)
+            if (sigmoid) s = s / (1.f + expf(l));
+        }
         float sum = lane < ws ? s : 0.f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -113,7 +145,7 @@ k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *__restr
     }
     if (counts) {
         __syncthreads();
-        for (int e = threadIdx.x; e < p.E; e += kChooseThreads) counts[(size_t)blockIdx.x * p.E + e] = s_hist[e];
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) counts[(size_t)blockIdx.x * p.E + e] = s_hist[e];
     }
 }
 
@@ -129,7 +161,7 @@ k_route_place(const inkattn_route_params p, int chunk_tokens, const uint32_t *__
     const int E = p.E, k = p.top_k;
     uint32_t *base = sm, *scratch = sm + E;
     uint16_t *hist = reinterpret_cast<uint16_t *>(scratch + 2 * kPlaceThreads);
-    for (int i = tid; i < kPlaceWarps * E; i += kPlaceThreads) hist[i] = 0;
+    for (int i = tid; i < kPlaceWarps * E / 2; i += kPlaceThreads) reinterpret_cast<uint32_t *>(hist)[i] = 0;
     __syncthreads();
 
     // pairs of this warp: a contiguous part of the chunk, whole groups of 32
@@ -156,10 +188,18 @@ k_route_place(const inkattn_route_params p, int chunk_tokens, const uint32_t *__
         const int chunks = gridDim.x;
         const bool act = part < parts && E <= kPlaceThreads;
         if (act) {
-            for (int c = part; c < chunks; c += parts) {
-                const uint32_t n = __ldg(counts + (size_t)c * E + e);
-                total += n;
-                before += c < (int)blockIdx.x ? n : 0u;
+            for (int c0 = part; c0 < chunks; c0 += 8 * parts) {
+                uint32_t n[8];                         // requested together
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int c = c0 + q * parts;
+                    n[q] = c < chunks ? __ldg(counts + (size_t)c * E + e) : 0u;
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    total += n[q];
+                    before += c0 + q * parts < (int)blockIdx.x ? n[q] : 0u;
+                }
             }
             scratch[2 * tid] = total;
             scratch[2 * tid + 1] = before;
@@ -176,10 +216,16 @@ k_route_place(const inkattn_route_params p, int chunk_tokens, const uint32_t *__
     }
     if (tid < E) {
         uint32_t run = 0;
-        for (int w = 0; w < kPlaceWarps; ++w) {
-            const uint32_t n = hist[w * E + tid];
-            hist[w * E + tid] = (uint16_t)run;
-            run += n;
+#pragma unroll
+        for (int w0 = 0; w0 < kPlaceWarps; w0 += 8) {
+            uint32_t n[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) n[q] = hist[(w0 + q) * E + tid];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                hist[(w0 + q) * E + tid] = (uint16_t)run;
+                run += n[q];
+            }
         }
         if (!counts) total = run;
     }
@@ -244,7 +290,8 @@ size_t route_workspace_bytes(const inkattn_route_params &p) {
 cudaError_t launch_route(const inkattn_route_params &p, uint32_t *ws, cudaStream_t stream) {
     const bool one = one_chunk(p);
     // the choice of a small batch: a token per warp
-    const int choose_tokens = one ? kChooseThreads / 32 : chunk_tokens(p);
+    const int choose_threads = one ? kChooseThreadsOne : kChooseThreads;
+    const int choose_tokens = one ? kChooseThreadsOne / 32 : chunk_tokens(p);
     const int place_tokens = one ? (p.N_tok > 0 ? p.N_tok : 1) : chunk_tokens(p);
     uint32_t *counts = one ? nullptr : ws;
     cudaError_t err = cudaSuccess;
@@ -252,7 +299,7 @@ cudaError_t launch_route(const inkattn_route_params &p, uint32_t *ws, cudaStream
         const dim3 grid((unsigned)((p.N_tok + choose_tokens - 1) / choose_tokens));
         const size_t smem = one ? 0 : (size_t)p.E * 4;
         auto go = [&](auto kernel) {
-            return launch_dependent(kernel, grid, dim3(kChooseThreads), smem, stream, 1, p, choose_tokens, counts);
+            return launch_dependent(kernel, grid, dim3((unsigned)choose_threads), smem, stream, 1, p, choose_tokens, counts);
         };
         err = p.E <= 64 ? go(k_route_choose<2>) : p.E <= 128 ? go(k_route_choose<4>) : p.E <= 256
             ? go(k_route_choose<8>) : p.E <= 512 ? go(k_route_choose<16>) : go(k_route_choose<32>);
