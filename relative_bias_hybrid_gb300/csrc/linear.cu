@@ -46,6 +46,7 @@
 // 11000 cycles for 256 tokens and S = 4: 12 bytes a cycle.)
 #include <atomic>
 #include <climits>
+#include <cmath>
 
 #include "common.cuh"
 #include "conv4.cuh"
@@ -702,6 +703,23 @@ int resident_clusters(int ctas, int num_sms) {
     return n;
 }
 
+// What a launch would take, in microseconds: the model that picks the token tile and the
+// split.  Its constants are fits to measured times of the kernel (GB300, 76 pairs), 16 shapes
+// between 1 x 1024 x 1024 and 512 x 8192 x 8192 with every tile and split; it came within 15%
+// of all but the smallest and picked a shape within 4% of the best of each.
+//   stage   a K = 64 step of a tile of n tokens: 0.215 below n = 128 (the loop of the MMA warp),
+//           above that the copies from L2
+//   finish  an item's epilogue, which overlaps the next item's products
+//   join    of a split instead: the partial tiles through distributed shared memory
+//   and the weights come from HBM at 7 TB/s at best
+double launch_us(long long items, int n, int stages, int splits, int pairs, double weight_bytes) {
+    const double stage = fmax(0.215, 0.185 + 0.00031 * n), finish = 1.35 + 0.0107 * n, join = 1.45 + 0.0265 * n;
+    const double item = stages * stage / splits, hbm = weight_bytes / 7.0e6;
+    if (splits > 1) return 1.7 + fmax(item, hbm) + join;
+    const double waves = (double)((items + pairs - 1) / pairs);
+    return 1.7 + fmax(waves * fmax(item, finish), hbm) + fmin(item, finish);
+}
+
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStream_t stream) {
@@ -710,25 +728,43 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     cudaError_t err = cudaSuccess;
     for (Kernel f : {k, kernel_of(INKATTN_ACT_NONE)})
         if ((err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return err;
-    const int feat = act == INKATTN_ACT_SWIGLU ? 128 : 256;
+    const int feat = act == INKATTN_ACT_SWIGLU ? 128 : 256, nk = (a.K + kKStep - 1) / kKStep;
     a.n_fblocks = (a.F + feat - 1) / feat;
-    const int avg = a.M / a.E;
-    a.tile_n = !a.offsets ? (a.M < kMaxN ? (a.M + 31) / 32 * 32 : kMaxN) : avg > 64 ? kMaxN : 128;
+    a.wait_ns = kernel_debug().wait_ns;
+    // Where the split of the rows among the experts is known on the device alone, the model takes
+    // an even one over the experts that can have rows; a tile then leaves room for four times
+    // that, so that a busier expert's weights are not read for one small tile after another.
+    const long long owners = a.offsets ? (a.E < a.M ? a.E : a.M) : 1;
+    const long long rows = (a.M + owners - 1) / owners;
+    const double weight_bytes = (double)owners * a.n_fblocks * 2 * kRowsA * a.K * 2;
+    int most_n = kMaxN;
+    if (a.offsets && 4 * rows < kMaxN) most_n = rows < 16 ? 64 : (int)(4 * rows + 31) / 32 * 32;
+    double best = 0.0;
+    long long most_items = 0;
+    a.tile_n = 0;
+    for (int tile = most_n; tile >= 32; tile -= 32) {
+        const long long each = (rows + tile - 1) / tile;                   // tiles of an owner
+        const int n = (int)((rows + each - 1) / each + 31) / 32 * 32;
+        // items there can be: with experts, full tiles and one more for each that has rows
+        const long long bound = (a.offsets ? a.M / tile + owners : each) * a.n_fblocks;
+        if (bound > INT_MAX / 2) continue;
+        for (int s = 1; s <= kMaxSplits; s *= 2) {
+            if (s > 1 && (nk < 2 * s || bound > resident_clusters(2 * s, num_sms))) break;
+            const double us = launch_us(owners * each * a.n_fblocks, n, nk, s, resident_clusters(2, num_sms), weight_bytes);
+            if (a.tile_n == 0 || us < best) {
+                best = us;
+                most_items = bound;
+                a.tile_n = tile;
+                a.splits = s;
+            }
+        }
+    }
+    if (a.tile_n == 0) return cudaErrorInvalidConfiguration;
     a.stage_bytes = kABytes + a.tile_n / 2 * 128;
     a.stages = kRingBytes / a.stage_bytes < kMaxStages ? kRingBytes / a.stage_bytes : kMaxStages;
-    a.wait_ns = kernel_debug().wait_ns;
-    // at most this many items: with experts, full tiles and one more for each that has rows
-    const long long tiles = a.offsets ? (long long)a.M / a.tile_n + (a.E < a.M ? a.E : a.M)
-                                      : ((long long)a.M + a.tile_n - 1) / a.tile_n;
-    const long long items = tiles * a.n_fblocks;
-    if (items > INT_MAX / 2) return cudaErrorInvalidConfiguration;
-    const int nk = (a.K + kKStep - 1) / kKStep;
-    a.splits = 1;
-    for (int s = 2; s <= kMaxSplits; s *= 2)
-        if (nk >= 4 * s && items <= resident_clusters(2 * s, num_sms)) a.splits = s;
     const int most = resident_clusters(2 * a.splits, num_sms);
     if (most < 1) return cudaErrorInvalidConfiguration;
-    const int clusters = (int)(items < most ? items : most);
+    const int clusters = (int)(most_items < most ? most_items : most);
     LinearMaps maps;
     if (!make_linear_maps(a, act == INKATTN_ACT_SWIGLU, &maps)) return cudaErrorInvalidValue;
     const int threads = a.row_token ? kMaxThreads : kThreads;
