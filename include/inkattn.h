@@ -1,6 +1,6 @@
 /*
  * inkattn.h -- C ABI of libinkattn.so, the GB300 (sm_103a) attention hot path of
- * one Inkling decoder layer.
+ * one Inkling decoder layer, and the layer's products behind it.
  *
  * Sources, cited by page title and section heading:
  *   [SG] "SGLang と Miles が Inkling を初日からサポート：975Bのマルチモーダル最先端モデルが公開"
@@ -21,8 +21,9 @@
  *   - Kernels are chained by programmatic dependent launch: each may become resident on
  *     the GPU while the kernel before it on the stream finishes, and reads no global
  *     memory before that kernel has completed, so stream order holds as for any launch.
- *     inkattn_prologue, inkattn_output_conv and inkattn_qkvr_prologue let the next kernel
- *     be scheduled once all their CTAs have started; the attention kernels do not.  Every call can be captured
+ *     inkattn_prologue, inkattn_output_conv, inkattn_qkvr_prologue and the calls of the
+ *     layer's second half let the next kernel be scheduled once all their CTAs have
+ *     started; the attention kernels do not.  Every call can be captured
  *     into a CUDA graph.
  *   - Host-side validation runs before any launch; on failure the call returns
  *     INKATTN_ERR_INVALID_ARG or INKATTN_ERR_UNSUPPORTED and launches nothing.
@@ -41,8 +42,8 @@
  *   - Bounded device waits give up after 1 s.  For tests of that failure path only, two
  *     environment variables are read once per process: INKATTN_TEST_WAIT_LIMIT_US
  *     (100 .. 10000000: a shorter limit) and INKATTN_TEST_WITHHOLD_ARRIVAL=1 (the
- *     attention kernels' softmax withholds its first arrival before P V, and the qkvr
- *     kernel one release of an accumulator, so that the MMA warp's wait runs out).  Leave
+ *     attention kernels' softmax withholds its first arrival before P V, and the qkvr and
+ *     linear kernels one release of an accumulator, so that the MMA warp's wait runs out).  Leave
  *     both unset in normal use.
  */
 #ifndef INKATTN_H

@@ -19,8 +19,8 @@ constexpr int kBlock = 64;          // paged-cache block (tokens)
 // gives up after 1 s and nothing is withheld.  A test of the failure path sets the
 // environment variables INKATTN_TEST_WAIT_LIMIT_US (a shorter limit, 100 us .. 10 s) and
 // INKATTN_TEST_WITHHOLD_ARRIVAL=1 (the attention kernels' softmax withholds its first
-// arrival on the barrier the MMA warp waits on before P V, and the qkvr kernel's odd CTAs
-// their first accumulator release, so that wait runs out and the kernel winds down through
+// arrival on the barrier the MMA warp waits on before P V, and the odd CTAs of the qkvr and
+// linear kernels their first accumulator release, so that wait runs out and the kernel winds down through
 // its error path).
 struct KernelDebug {
     uint64_t wait_ns;
@@ -93,6 +93,8 @@ struct LinearArgs {
     int stages, stage_bytes; // the ring
     int splits;              // pairs of a cluster that share an item's K range
     uint64_t wait_ns;        // limit of every bounded wait
+    int withhold;            // failure-path test: one epilogue warp of each odd CTA withholds its
+                             // first accumulator release, so the MMA warp's wait runs out
 };
 cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStream_t stream);
 // TMA descriptors of a launch: x rows in boxes of 64 columns x 16 (i + 1) rows, up to half a

@@ -263,6 +263,9 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         return it;
     };
 
+    // a split's cluster has one item at most (worked out here, off the path behind the products)
+    const Item only = A.splits > 1 && cid < n_items ? item(cid) : Item{};
+
     if (warp == kWarpProducer || warp == kWarpProducer2) {
         // ================================ producers ================================
         if (lane == 0) {
@@ -307,7 +310,8 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             // the other producer's newest load cannot have taken over
             if (half == 0)
                 for (int l = last; l >= 0 && l > last + 1 - A.stages; l -= 2)
-                    mbar_drain(bar(B_FULL + l % A.stages), (uint32_t)(l / A.stages) & 1u, A.dev_status, A.wait_ns);
+                    (void)mbar_wait_short<200>(bar(B_FULL + l % A.stages), (uint32_t)(l / A.stages) & 1u, A.dev_status,
+                                               nullptr, A.wait_ns);
         }
         __syncwarp();
     } else if (warp == kWarpRelay) {
@@ -414,7 +418,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         // every MMA of the pair has completed before TMEM is released
         tc::commit_pair(bar(B_DRAIN));
         __syncwarp();
-        (void)mbar_drain(bar(B_DRAIN), 0, A.dev_status, A.wait_ns);
+        (void)mbar_wait_short<200>(bar(B_DRAIN), 0, A.dev_status, nullptr, A.wait_ns);
         __syncwarp();
     } else {
         // ================================ epilogue ================================
@@ -449,7 +453,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             const uint32_t taddr = tmem + (uint32_t)(buf * kMaxN) + ((uint32_t)(quarter * 32) << 16);
             const bool reused = w + 2 * nclusters < n_items;  // the MMA warp waits for this accumulator
             auto release = [&] {
-                if (!reused) return;
+                if (!reused || (A.withhold && i == 0 && half == 1 && warp == kWarpEpi)) return;
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_remote_arrive(bar(B_ACC_EMPTY + buf), even);
@@ -560,7 +564,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     if (A.splits > 1) {
         const int et = (int)threadIdx.x - kWarpEpi * 32;
         const bool epi = et >= 0 && et < kEpiThreads && cid < n_items;
-        const Item it = cid < n_items ? item(cid) : Item{};
+        const Item it = only;
         const int share = it.n / A.splits;             // tokens that a pair adds up, a multiple of 8
         __syncwarp();
         cluster_sync();                                // every pair's MMAs are done: the rings are idle
@@ -731,6 +735,7 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     const int feat = act == INKATTN_ACT_SWIGLU ? 128 : 256, nk = (a.K + kKStep - 1) / kKStep;
     a.n_fblocks = (a.F + feat - 1) / feat;
     a.wait_ns = kernel_debug().wait_ns;
+    a.withhold = kernel_debug().withhold;
     // Where the split of the rows among the experts is known on the device alone, the model takes
     // an even one over the experts that can have rows; a tile then leaves room for four times
     // that, so that a busier expert's weights are not read for one small tile after another.

@@ -114,7 +114,8 @@ _TENSOR_IDS = {"q": 1, "k": 2, "v": 3, "r": 4, "P": 5, "conv_w_k": 6, "conv_w_v"
                "q_norm_w": 8, "k_norm_w": 9, "conv_state_k": 10, "conv_state_v": 11,
                "k_cache": 12, "v_cache": 13, "perm": 14, "y": 15, "residual": 16,
                "oc_conv_w": 17, "oc_norm_w": 18, "oc_conv_state": 19, "k_cache_e4m3": 20,
-               "v_cache_e4m3": 21, "x": 22, "w_qkvr": 23}
+               "v_cache_e4m3": 21, "x": 22, "w_qkvr": 23, "w_o": 24, "w_router": 25, "w_up": 26,
+               "w_down": 27, "w_shared_up": 28, "w_shared_down": 29}
 
 
 def _gen(device, seed: int, tensor: str) -> torch.Generator:
@@ -270,6 +271,30 @@ def make_output_conv_inputs(w: Workload, seed: int = 0, device="cpu", D: int = 0
     cu = np.zeros(B + 1, dtype=np.int64)
     cu[1:] = np.cumsum(w.q_lens)
     out["cu_seqlens_q"] = torch.tensor(cu, dtype=torch.int32, device=device)
+    return out
+
+
+def make_layer_tail_inputs(w: Workload, seed: int = 0, device="cpu", D: int = 0, experts: int = 16,
+                           n_shared: int = 2, ff: int = 512) -> Dict[str, torch.Tensor]:
+    """Weights of what follows the attention in the layer, hidden width D (default Hq * head_dim),
+    experts of inner width ff, all bf16 in nn.Linear layout and N(0, 1 / input width): w_o
+    [D, Hq * head_dim], w_router [experts + n_shared, D], w_up [experts, 2 ff, D] (gate rows
+    first), w_down [experts, D, ff], w_shared_up [n_shared, 2 ff, D], w_shared_down
+    [n_shared, D, ff]; and under "attn" and "mlp" the inputs of the two output convs
+    (make_output_conv_inputs; their y is not used)."""
+    device = torch.device(device)
+    D = D or w.Hq * w.head_dim
+    bf, A = torch.bfloat16, w.Hq * w.head_dim
+    out = {
+        "w_o": _normal((D, A), A ** -0.5, device, seed, "w_o", bf),
+        "w_router": _normal((experts + n_shared, D), D ** -0.5, device, seed, "w_router", bf),
+        "w_up": _normal((experts, 2 * ff, D), D ** -0.5, device, seed, "w_up", bf),
+        "w_down": _normal((experts, D, ff), ff ** -0.5, device, seed, "w_down", bf),
+        "w_shared_up": _normal((n_shared, 2 * ff, D), D ** -0.5, device, seed, "w_shared_up", bf),
+        "w_shared_down": _normal((n_shared, D, ff), ff ** -0.5, device, seed, "w_shared_down", bf),
+    }
+    for i, name in enumerate(("attn", "mlp")):
+        out[name] = make_output_conv_inputs(w, seed=2 * seed + i, device=device, D=D)
     return out
 
 

@@ -162,3 +162,79 @@ class QkvrStep:
 
     def device_status(self) -> int:
         return int(self.status.item())
+
+
+class LayerTailStep:
+    """Buffers + calls of what follows the attention in a decoder layer, over a workload's new
+    tokens: the output projection (inkattn_linear), its conv with the residual add and RMSNorm
+    (inkattn_output_conv), the router's logits and choice (inkattn_linear, inkattn_route), the
+    routed experts (inkattn_grouped_linear twice), the shared experts (inkattn_linear), their
+    weighted sum (inkattn_expert_combine), and the MLP output's conv with the residual add and
+    RMSNorm (inkattn_output_conv).
+
+    `inputs` comes from inputs.make_layer_tail_inputs; attn_out [N, Hq, 128] bf16 is the
+    attention's output.  The residual stream is inputs["attn"]["residual"]; h (the new residual
+    stream) and out (its RMSNorm, the next layer's input) are buffers of this object.
+    """
+
+    def __init__(self, w: Workload, inputs: Dict[str, torch.Tensor], attn_out: torch.Tensor, top_k: int = 6):
+        dev, bf, f32, i32 = attn_out.device, torch.bfloat16, torch.float32, torch.int32
+        N, x = w.N_tok, inputs
+        D, E, S = x["w_o"].shape[0], x["w_up"].shape[0], x["w_shared_up"].shape[0]
+        ff, k = x["w_down"].shape[2], top_k
+        M, max_q = N * k, max(w.q_lens) if w.q_lens else 0
+        self.w, self.x = w, inputs
+        self.status = torch.zeros(1, dtype=i32, device=dev)
+
+        def buf(*shape, dtype=bf):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        self.proj, self.h_attn, self.normed = buf(N, D), buf(N, D), buf(N, D)
+        self.logits = buf(N, E + S, dtype=f32)
+        self.route = {"topk_ids": buf(N, k, dtype=i32), "weights": buf(N, k + S, dtype=f32),
+                      "expert_offsets": buf(E + 1, dtype=i32), "row_token": buf(M, dtype=i32),
+                      "token_rows": buf(N, k, dtype=i32)}
+        self.inner, self.rows = buf(M, ff), buf(M, D)
+        self.shared_inner, self.shared_rows = buf(N, ff), buf(S, N, D) if S else None
+        self.mlp, self.h, self.out = buf(N, D), buf(N, D), buf(N, D)
+
+        def conv(part, y, residual, h, out):
+            c = x[part]
+            return ia.output_conv_params(
+                y=y, conv_w=c["conv_w"], norm_w=c["norm_w"], cu_seqlens_q=c["cu_seqlens_q"],
+                state_slot=c["state_slot"], conv_state=c["conv_state"], residual=residual, h_out=h, out=out,
+                max_seqlen_q=max_q, eps=w.eps, dev_status=self.status)
+
+        st = dict(dev_status=self.status)
+        self.p_proj = ia.linear_params(x=attn_out.view(N, -1), w=x["w_o"], out=self.proj, **st)
+        self.p_conv = conv("attn", self.proj, x["attn"]["residual"], self.h_attn, self.normed)
+        self.p_logits = ia.linear_params(x=self.normed, w=x["w_router"], out=self.logits, **st)
+        self.p_route = ia.route_params(logits=self.logits, n_shared=S, **self.route)
+        self.workspace = torch.empty(ia.inkattn_route_workspace_bytes(self.p_route), dtype=torch.uint8, device=dev)
+        groups = dict(expert_offsets=self.route["expert_offsets"], **st)
+        self.p_up = ia.grouped_linear_params(x=self.normed, w=x["w_up"], out=self.inner, act="swiglu",
+                                             row_token=self.route["row_token"], **groups)
+        self.p_down = ia.grouped_linear_params(x=self.inner, w=x["w_down"], out=self.rows, **groups)
+        self.p_shared = [
+            (ia.linear_params(x=self.normed, w=x["w_shared_up"][s], out=self.shared_inner, act="swiglu", **st),
+             ia.linear_params(x=self.shared_inner, w=x["w_shared_down"][s], out=self.shared_rows[s], **st))
+            for s in range(S)]
+        self.p_sum = ia.expert_combine_params(y=self.rows, shared=self.shared_rows, weights=self.route["weights"],
+                                              token_rows=self.route["token_rows"], out=self.mlp, **st)
+        self.p_mlp_conv = conv("mlp", self.mlp, self.h_attn, self.h, self.out)
+
+    def run(self, stream=None):
+        ia.inkattn_linear(self.p_proj, stream)
+        ia.inkattn_output_conv(self.p_conv, stream)
+        ia.inkattn_linear(self.p_logits, stream)
+        ia.inkattn_route(self.p_route, self.workspace, stream)
+        ia.inkattn_grouped_linear(self.p_up, stream)
+        ia.inkattn_grouped_linear(self.p_down, stream)
+        for up, down in self.p_shared:
+            ia.inkattn_linear(up, stream)
+            ia.inkattn_linear(down, stream)
+        ia.inkattn_expert_combine(self.p_sum, stream)
+        ia.inkattn_output_conv(self.p_mlp_conv, stream)
+
+    def device_status(self) -> int:
+        return int(self.status.item())
