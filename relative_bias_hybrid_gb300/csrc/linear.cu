@@ -39,6 +39,12 @@
 // Both CTAs' copies of a stage complete on the even CTA's barrier, and the pair's commits
 // release it in both, as in the qkvr kernel.
 //
+// fp32 outputs (kFine).  The tensor cores add each K = 16 step to the accumulator without rounding
+// to nearest; over K = 8192 the error grows to about 1e-5 of the result, nothing next to a bf16
+// rounding but much for an fp32 one.  An fp32 output is therefore summed in parts of K = 512,
+// which the epilogue warps add up in registers, rounding to nearest (K = 1000: 4.6e-7 of the
+// result instead of 9.8e-7, and the same at K = 8192).  The registers hold 32 tokens a warp, so its tiles have 64 tokens.
+//
 // Few items (a decode batch): the K range is split over the S pairs of one cluster.  Each CTA
 // writes its fp32 partial tile, a share of the tokens to each pair, into the other CTAs' shared
 // memory (the rings, idle by then), and each adds the S partials of its share in order: no
@@ -73,6 +79,7 @@ constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpEpi = 2, kWarpProducer2 = 10
               kWarpRelay = 15;
 constexpr int kStgPitch = 36;                     // floats of a staging row: 32 features + 4
 constexpr int kStgBytes = 16 * kStgPitch * 4;     // 16 tokens, one buffer per epilogue warp
+constexpr int kFineSteps = 8, kFineN = 64;        // fp32 outputs: K steps of a part, tokens of a tile
 constexpr int kRaster = 8;                        // feature blocks per raster group
 
 constexpr int kOffStg = kRingBytes;
@@ -151,7 +158,8 @@ __device__ __forceinline__ void st_shared_cluster(uint32_t addr, uint32_t v) {
 
 }  // namespace
 
-template <int kAct>
+// kFine: fp32 output, summed in parts
+template <int kAct, bool kFine>
 __global__ void __launch_bounds__(kMaxThreads, 1)
 k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     constexpr bool kGated = kAct == INKATTN_ACT_SWIGLU;
@@ -236,6 +244,9 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     const int n_items = s_tiles[A.E] * A.n_fblocks;    // (the host checked that it fits)
     const int nk = (A.K + kKStep - 1) / kKStep;
     const int k_lo = (int)((long long)nk * split / A.splits), k_hi = (int)((long long)nk * (split + 1) / A.splits);
+    // the accumulations of an item, one after another in the two TMEM buffers
+    const int part = kFine ? kFineSteps : k_hi - k_lo, parts = kFine ? (k_hi - k_lo + part - 1) / part : 1;
+    const int my_items = cid < n_items ? (n_items - cid + nclusters - 1) / nclusters : 0;
     auto item = [&](int w) {
         Item it;
         const int t = w / A.n_fblocks;
@@ -265,6 +276,8 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
 
     // a split's cluster has one item at most (worked out here, off the path behind the products)
     const Item only = A.splits > 1 && cid < n_items ? item(cid) : Item{};
+
+    float fine[kFine ? 32 : 1];                        // an epilogue warp's sums of the parts
 
     if (warp == kWarpProducer || warp == kWarpProducer2) {
         // ================================ producers ================================
@@ -383,36 +396,37 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         const uint64_t db0 = tc::sdesc_sw128(s_base + kABytes, 16, 1024);
         const uint16_t pair = (uint16_t)(3u << even);
         // the last lap is not released, so that no arrival reaches a peer that has finished
-        const int my_items = cid < n_items ? (n_items - cid + nclusters - 1) / nclusters : 0;
         long long left = (long long)my_items * (k_hi - k_lo);
         RingPos at;
         bool ok = true, ready = false;
         int i = 0;
-        for (int w = cid; w < n_items && ok; w += nclusters, ++i) {
-            const int buf = i & 1;
+        for (int w = cid; w < n_items && ok; w += nclusters) {
             const uint32_t id = tc::idesc(2 * kRowsA, item(w).n, tc::kFmtBF16, 0, 0);
-            // both CTAs' epilogues are done with this accumulator
-            if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait_cluster(bar(B_ACC_EMPTY + buf), ((i >> 1) - 1) & 1,
-                                                                     A.dev_status, abort_flag, A.wait_ns))) {
-                ok = false;
-                break;
-            }
-            tc::fence_after();
-            for (int k = k_lo; k < k_hi; ++k) {
-                if (!ready && !pwait(bar(B_FULL + at.s), at.lap & 1)) {
+            for (int k0 = k_lo; k0 < k_hi && ok; k0 += part, ++i) {
+                const int buf = i & 1, k1 = min(k_hi, k0 + part);
+                // both CTAs' epilogues are done with this accumulator
+                if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait_cluster(bar(B_ACC_EMPTY + buf), ((i >> 1) - 1) & 1,
+                                                                         A.dev_status, abort_flag, A.wait_ns))) {
                     ok = false;
                     break;
                 }
-                const RingPos now = at;
-                at.next(A.stages);
-                ready = left > 1 && mbar_test_wait(bar(B_FULL + at.s), at.lap & 1);   // seen while the MMAs are issued
                 tc::fence_after();
-                const uint64_t off = (uint64_t)(now.s * (A.stage_bytes >> 4));
-                tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)(buf * kMaxN), da0 + off, db0 + off, id,
-                                                k > k_lo ? 1u : 0u, bar(B_EMPTY + now.s), left > A.stages ? 1u : 0u,
-                                                bar(B_ACC_FULL + buf), k == k_hi - 1 ? 1u : 0u, pair);
-                --left;
-                ready = __all_sync(0xffffffffu, ready);
+                for (int k = k0; k < k1; ++k) {
+                    if (!ready && !pwait(bar(B_FULL + at.s), at.lap & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const RingPos now = at;
+                    at.next(A.stages);
+                    ready = left > 1 && mbar_test_wait(bar(B_FULL + at.s), at.lap & 1);   // seen while the MMAs are issued
+                    tc::fence_after();
+                    const uint64_t off = (uint64_t)(now.s * (A.stage_bytes >> 4));
+                    tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)(buf * kMaxN), da0 + off, db0 + off, id,
+                                                    k > k0 ? 1u : 0u, bar(B_EMPTY + now.s), left > A.stages ? 1u : 0u,
+                                                    bar(B_ACC_FULL + buf), k == k1 - 1 ? 1u : 0u, pair);
+                    --left;
+                    ready = __all_sync(0xffffffffu, ready);
+                }
             }
         }
         // every MMA of the pair has completed before TMEM is released
@@ -433,11 +447,27 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         inkattn_bf16 *out16 = static_cast<inkattn_bf16 *>(A.out);
         float *out32 = static_cast<float *>(A.out);
         // 16-byte pieces of a row start on 16-byte boundaries
-        const bool vec = A.out_f32 ? (A.F & 3) == 0 && (A.residual == nullptr || (A.F & 7) == 0) : (A.F & 7) == 0;
+        const bool vec = kFine ? (A.F & 3) == 0 && (A.residual == nullptr || (A.F & 7) == 0) : (A.F & 7) == 0;
+        const int accs = my_items * parts;                    // accumulations in all
         int i = 0;
-        for (int w = cid; w < n_items; w += nclusters, ++i) {
+        bool ok = true;
+        // the accumulator of accumulation i is complete / may be written again
+        auto acc_full = [&] {
+            bool r = mbar_wait_short<1000>(bar(B_ACC_FULL + (i & 1)), (uint32_t)((i >> 1) & 1), A.dev_status, abort_flag,
+                                           A.wait_ns);
+            if (kGated) r = named_all(swap_bar, 64, r);       // the two warps go on together
+            ok = __all_sync(0xffffffffu, r);
+            tc::fence_after();
+            return ok;
+        };
+        auto release = [&] {
+            if (i + 2 >= accs || (A.withhold && i == 0 && half == 1 && warp == kWarpEpi)) return;
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_remote_arrive(bar(B_ACC_EMPTY + (i & 1)), even);   // its MMA warp waits
+        };
+        for (int w = cid; w < n_items && ok; w += nclusters, ++i) {
             const Item it = item(w);
-            const int buf = i & 1;
             // the warp's 32 features (gated: quarters 0 and 1 hold gates, 2 and 3 the ups of the
             // same features), the lane's feature and its bias
             const int f0 = (it.fb * 2 + half) * kFeat + (kGated ? quarter & 1 : quarter) * 32;
@@ -445,26 +475,37 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             float bias = 0.f;
             if (A.bias && frow < A.F)
                 bias = __ldg(A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + (kGated && quarter >= 2 ? F : 0) + frow);
-            bool ok = mbar_wait_short<1000>(bar(B_ACC_FULL + buf), (uint32_t)((i >> 1) & 1), A.dev_status, abort_flag, A.wait_ns);
-            if (kGated) ok = named_all(swap_bar, 64, ok);     // the two warps go on together
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc::fence_after();
+            if (kFine) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) fine[j] = 0.f;
+                for (int q = 0; q < parts; ++q) {
+                    if (!acc_full()) break;
+                    uint32_t v[32];
+                    tc::ld32(tmem + (uint32_t)((i & 1) * kMaxN + e8 * 32) + ((uint32_t)(quarter * 32) << 16), v);
+                    tc::wait_ld();
+                    release();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) fine[j] += __uint_as_float(v[j]);
+                    if (q < parts - 1) ++i;
+                }
+                if (!ok) break;
+            } else if (!acc_full()) {
+                break;
+            }
             if (A.splits > 1) break;                          // (one item; it is finished below)
-            const uint32_t taddr = tmem + (uint32_t)(buf * kMaxN) + ((uint32_t)(quarter * 32) << 16);
-            const bool reused = w + 2 * nclusters < n_items;  // the MMA warp waits for this accumulator
-            auto release = [&] {
-                if (!reused || (A.withhold && i == 0 && half == 1 && warp == kWarpEpi)) return;
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_remote_arrive(bar(B_ACC_EMPTY + buf), even);
-            };
+            const uint32_t taddr = tmem + (uint32_t)((i & 1) * kMaxN) + ((uint32_t)(quarter * 32) << 16);
             const int nblocks = (it.nt + 31) >> 5;
-            if (e8 >= nblocks) release();
+            if (!kFine && e8 >= nblocks) release();
             for (int c = e8; c < nblocks; c += 2) {
                 uint32_t v[32];
-                tc::ld32(taddr + (uint32_t)(c * 32), v);
-                tc::wait_ld();
-                if (c + 2 >= nblocks) release();
+                if (kFine) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(fine[j]);
+                } else {
+                    tc::ld32(taddr + (uint32_t)(c * 32), v);
+                    tc::wait_ld();
+                    if (c + 2 >= nblocks) release();
+                }
                 // tokens of this block that are stored
                 bool mine = c * 32 + lane < it.nt;
                 if (A.row_token && mine) {
@@ -485,7 +526,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                             if (((live16 >> j) & 1u) && frow < A.F) {
                                 const size_t o = (row_b + j) * F + frow;
                                 const float z = A.residual ? y[j] + load_bf16(A.residual + o) : y[j];
-                                if (A.out_f32) out32[o] = z;
+                                if (kFine) out32[o] = z;
                                 else store_bf16(out16 + o, z);
                             }
                         }
@@ -495,7 +536,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) stg[j * kStgPitch + lane] = y[j];
                     __syncwarp();
-                    if (!A.out_f32) {
+                    if (!kFine) {
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const int t = q * 8 + (lane >> 2), f = f0 + (lane & 3) * 8;
@@ -573,8 +614,13 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             const uint32_t place = s_base + (uint32_t)((split * share * kRowsA + quarter * 32 + lane) * 4);
             for (int c = (warp - kWarpEpi) >> 2; c * 32 < it.nt; c += 2) {
                 uint32_t v[32];
-                tc::ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(c * 32), v);
-                tc::wait_ld();
+                if (kFine) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(fine[j]);
+                } else {
+                    tc::ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(c * 32), v);
+                    tc::wait_ld();
+                }
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int t = c * 32 + g * 8, owner = t / share;
@@ -639,7 +685,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                         y[0] += bf16_lo(r.x); y[1] += bf16_hi(r.x);
                         y[2] += bf16_lo(r.y); y[3] += bf16_hi(r.y);
                     }
-                    if (A.out_f32)
+                    if (kFine)
                         *reinterpret_cast<float4 *>(static_cast<float *>(A.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
                     else
                         *reinterpret_cast<uint2 *>(static_cast<inkattn_bf16 *>(A.out) + at) =
@@ -650,7 +696,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                 for (int n = 0; n < 4; ++n) {
                     if (f + n >= A.F) break;
                     const float o = A.residual ? y[n] + load_bf16(A.residual + at + n) : y[n];
-                    if (A.out_f32) static_cast<float *>(A.out)[at + n] = o;
+                    if (kFine) static_cast<float *>(A.out)[at + n] = o;
                     else store_bf16(static_cast<inkattn_bf16 *>(A.out) + at + n, o);
                 }
             }
@@ -671,13 +717,14 @@ namespace {
 
 using Kernel = void (*)(const LinearArgs, const LinearMaps);
 
+template <bool kFine>
 Kernel kernel_of(int act) {
     switch (act) {
-        case INKATTN_ACT_RELU: return k_linear<INKATTN_ACT_RELU>;
-        case INKATTN_ACT_GELU: return k_linear<INKATTN_ACT_GELU>;
-        case INKATTN_ACT_SILU: return k_linear<INKATTN_ACT_SILU>;
-        case INKATTN_ACT_SWIGLU: return k_linear<INKATTN_ACT_SWIGLU>;
-        default: return k_linear<INKATTN_ACT_NONE>;
+        case INKATTN_ACT_RELU: return k_linear<INKATTN_ACT_RELU, kFine>;
+        case INKATTN_ACT_GELU: return k_linear<INKATTN_ACT_GELU, kFine>;
+        case INKATTN_ACT_SILU: return k_linear<INKATTN_ACT_SILU, kFine>;
+        case INKATTN_ACT_SWIGLU: return k_linear<INKATTN_ACT_SWIGLU, kFine>;
+        default: return k_linear<INKATTN_ACT_NONE, kFine>;
     }
 }
 
@@ -699,7 +746,7 @@ int resident_clusters(int ctas, int num_sms) {
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, k_linear<INKATTN_ACT_NONE>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, k_linear<INKATTN_ACT_NONE, false>, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();
         return 0;
     }
@@ -728,9 +775,9 @@ double launch_us(long long items, int n, int stages, int splits, int pairs, doub
 
 cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStream_t stream) {
     LinearArgs a = args;
-    const Kernel k = kernel_of(act);
+    const Kernel k = a.out_f32 ? kernel_of<true>(act) : kernel_of<false>(act);
     cudaError_t err = cudaSuccess;
-    for (Kernel f : {k, kernel_of(INKATTN_ACT_NONE)})
+    for (Kernel f : {k, kernel_of<false>(INKATTN_ACT_NONE)})
         if ((err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return err;
     const int feat = act == INKATTN_ACT_SWIGLU ? 128 : 256, nk = (a.K + kKStep - 1) / kKStep;
     a.n_fblocks = (a.F + feat - 1) / feat;
@@ -742,8 +789,8 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     const long long owners = a.offsets ? (a.E < a.M ? a.E : a.M) : 1;
     const long long rows = (a.M + owners - 1) / owners;
     const double weight_bytes = (double)owners * a.n_fblocks * 2 * kRowsA * a.K * 2;
-    int most_n = kMaxN;
-    if (a.offsets && 4 * rows < kMaxN) most_n = rows < 16 ? 64 : (int)(4 * rows + 31) / 32 * 32;
+    int most_n = a.out_f32 ? kFineN : kMaxN;
+    if (a.offsets && 4 * rows < most_n) most_n = rows < 16 ? 64 : (int)(4 * rows + 31) / 32 * 32;
     double best = 0.0;
     long long most_items = 0;
     a.tile_n = 0;
