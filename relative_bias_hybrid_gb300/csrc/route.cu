@@ -8,15 +8,14 @@
 // keys in registers, each lane knows its own two best, and top_k times the best of the lanes is
 // taken (redux.sync on the key, then on the index, so that equal logits go to the lower index).
 // A lane looks for its next two only when both are gone.  The next token's logits are requested
-// before this one's are used.  k_route_place: a counting sort of the
-// (token, choice) pairs by expert, stable in (token, choice) order.  The order is made of
-// integer counts alone, so it does not depend on the scheduling:
-//   - the tokens are cut into chunks; a block places one chunk, and a warp a contiguous part
-//     of its pairs, 32 at a time (match.any gives a pair its rank among the 32);
-//   - a pair's row = offset of its expert + pairs of that expert in earlier chunks (each block
-//     adds up the counts that k_route_choose left per chunk), in earlier warps of the chunk
-//     and in earlier steps of the warp.
-// A batch that is one chunk needs no counts and no workspace.
+// before this one's are used.  k_route_place: a counting sort
+// of the (token, choice) pairs by expert, stable in (token, choice) order.  A token takes an
+// expert once at most, so the pairs of an expert are a set of tokens, a bitmap: bits are set in
+// any order, and the rank of a token among them is a count of bits.  Each block places a chunk of
+// the tokens; a pair's row = offset of its expert + pairs of that expert in earlier chunks (each
+// block adds up the counts that k_route_choose left per chunk) + bits before its own.  A batch
+// that is one chunk needs no counts and no workspace.  (Ranks by match.any and a histogram for
+// each warp took 1.6 times as long for one chunk: two passes over the pairs, 32 counts an expert.)
 #include "common.cuh"
 #include "conv4.cuh"
 #include "internal.h"
@@ -28,8 +27,7 @@ namespace {
 constexpr int kChooseThreads = 1024;               // of a chunk; of one chunk alone, fewer
 constexpr int kChooseThreadsOne = 256;
 constexpr int kPlaceThreads = 1024;
-constexpr int kPlaceWarps = kPlaceThreads / 32;
-constexpr int kOneChunkPairs = 4096;               // pairs that one block places
+constexpr int kPlaceTokens = 1024;                 // tokens of a bitmap, a multiple of 32
 constexpr int kChunks = 152;                       // chunks of a larger batch, at most
 
 // Order-preserving integer key of a logit: larger logit, larger key; +0 and -0 alike; NaN as
@@ -149,45 +147,47 @@ k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *__restr
     }
 }
 
-// One block per chunk.  Shared memory: base[E] (first row of the expert's pairs of this chunk),
-// scratch[2 kPlaceThreads], hist[kPlaceWarps][E] (16 bits: with 2^28 pairs in 152 chunks of 32
-// warps, a warp has fewer than 65536).
+// One block per chunk.  Shared memory: base[E] (row of the expert's next pair), scratch[2
+// kPlaceThreads], bits[words][E], before[words][E] (16 bits: bits in earlier words).
 __global__ void __launch_bounds__(kPlaceThreads)
-k_route_place(const inkattn_route_params p, int chunk_tokens, const uint32_t *__restrict__ counts) {
+k_route_place(const inkattn_route_params p, int chunk_tokens, int words, const uint32_t *__restrict__ counts) {
     extern __shared__ uint32_t sm[];
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int E = p.E, k = p.top_k;
-    uint32_t *base = sm, *scratch = sm + E;
-    uint16_t *hist = reinterpret_cast<uint16_t *>(scratch + 2 * kPlaceThreads);
-    for (int i = tid; i < kPlaceWarps * E / 2; i += kPlaceThreads) reinterpret_cast<uint32_t *>(hist)[i] = 0;
-    __syncthreads();
+    uint32_t *base = sm, *scratch = sm + E, *bits = scratch + 2 * kPlaceThreads;
+    uint16_t *earlier = reinterpret_cast<uint16_t *>(bits + words * E);
+    const int t_lo = (int)min((long long)blockIdx.x * chunk_tokens, (long long)p.N_tok);
+    const int t_hi = min(p.N_tok - t_lo, chunk_tokens) + t_lo;
 
-    // pairs of this warp: a contiguous part of the chunk, whole groups of 32
-    const long long q_lo = (long long)blockIdx.x * chunk_tokens * k;
-    const long long q_hi = min((long long)p.N_tok, (long long)(blockIdx.x + 1) * chunk_tokens) * k;
-    const int pairs = (int)max(q_hi - q_lo, 0ll);
-    const int per = ((pairs + kPlaceWarps - 1) / kPlaceWarps + 31) & ~31;
-    const int w_lo = min(pairs, warp * per), w_hi = min(pairs, w_lo + per);
-    uint16_t *mine = hist + warp * E;
-    for (int g = w_lo; g < w_hi; g += 32) {
-        const bool in = g + lane < w_hi;
-        const int e = in ? p.topk_ids[q_lo + g + lane] : -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        if (in && lane == __ffs(same) - 1) mine[e] = (uint16_t)(mine[e] + __popc(same));
-        __syncwarp();
-    }
-    __syncthreads();
-
-    // per expert: pairs in earlier chunks, pairs in all chunks; then the prefix over the warps
-    uint32_t total = 0, before = 0;
+    // base and expert_offsets from the totals of the experts; `before`: pairs of earlier chunks
+    auto start_rows = [&](uint32_t total, uint32_t before) {
+        uint32_t v = tid < E ? total : 0u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t n = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += n;
+        }
+        if (lane == 31) scratch[warp] = v;
+        __syncthreads();
+        uint32_t s = lane < warp ? scratch[lane] : 0u;         // (32 warps: the totals of the earlier ones)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (tid < E) {
+            const uint32_t incl = v + s;
+            base[tid] = incl - total + before;
+            if (blockIdx.x == 0) {
+                p.expert_offsets[tid + 1] = (int32_t)incl;
+                if (tid == 0) p.expert_offsets[0] = 0;
+            }
+        }
+    };
     if (counts) {
         // several threads an expert, each over a part of the chunks
-        const int parts = max(1, kPlaceThreads / E), e = tid % E, part = tid / E;
-        const int chunks = gridDim.x;
-        const bool act = part < parts && E <= kPlaceThreads;
-        if (act) {
+        const int parts = kPlaceThreads / E, e = tid % E, part = tid / E, chunks = gridDim.x;
+        uint32_t total = 0, before = 0;
+        if (part < parts) {
             for (int c0 = part; c0 < chunks; c0 += 8 * parts) {
                 uint32_t n[8];                         // requested together
 #pragma unroll
@@ -213,69 +213,46 @@ k_route_place(const inkattn_route_params p, int chunk_tokens, const uint32_t *__
             }
         }
         __syncthreads();
+        start_rows(total, before);
     }
-    if (tid < E) {
+    int t0 = t_lo;
+    do {                                               // (once at least: an empty batch has offsets too)
+        const int t1 = min(t_hi, t0 + 32 * words);
+        for (int i = tid; i < words * E; i += kPlaceThreads) bits[i] = 0;
+        __syncthreads();
+        const int pairs = (t1 - t0) * k;
+        const int32_t *ids = p.topk_ids + (size_t)t0 * k;
+        for (int q = tid; q < pairs; q += kPlaceThreads) {
+            const int t = q / k;
+            atomicOr(&bits[(t >> 5) * E + ids[q]], 1u << (t & 31));
+        }
+        __syncthreads();
         uint32_t run = 0;
-#pragma unroll
-        for (int w0 = 0; w0 < kPlaceWarps; w0 += 8) {
-            uint32_t n[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) n[q] = hist[(w0 + q) * E + tid];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                hist[(w0 + q) * E + tid] = (uint16_t)run;
-                run += n[q];
+        if (tid < E) {
+#pragma unroll 4
+            for (int w = 0; w < words; ++w) {
+                earlier[w * E + tid] = (uint16_t)run;
+                run += __popc(bits[w * E + tid]);
             }
         }
-        if (!counts) total = run;
-    }
-    // exclusive prefix of the totals over the experts
-    uint32_t v = tid < E ? total : 0u;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t n = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += n;
-    }
-    if (lane == 31) scratch[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-        uint32_t s = scratch[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t n = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += n;
+        if (!counts) start_rows(run, 0);
+        __syncthreads();
+        for (int q = tid; q < pairs; q += kPlaceThreads) {
+            const int t = q / k, e = ids[q], w = t >> 5;
+            const uint32_t row = base[e] + earlier[w * E + e] + __popc(bits[w * E + e] & ((1u << (t & 31)) - 1u));
+            p.row_token[row] = t0 + t;
+            p.token_rows[(size_t)t0 * k + q] = (int32_t)row;
         }
-        scratch[lane] = s;
-    }
-    __syncthreads();
-    if (tid < E) {
-        const uint32_t incl = v + (warp > 0 ? scratch[warp - 1] : 0u);
-        base[tid] = incl - total + before;
-        if (blockIdx.x == 0) {
-            p.expert_offsets[tid + 1] = (int32_t)incl;
-            if (tid == 0) p.expert_offsets[0] = 0;
+        t0 += 32 * words;
+        if (t0 < t_hi) {
+            __syncthreads();
+            if (tid < E) base[tid] += run;
+            __syncthreads();
         }
-    }
-    __syncthreads();
-
-    for (int g = w_lo; g < w_hi; g += 32) {
-        const bool in = g + lane < w_hi;
-        const long long q = q_lo + g + lane;
-        const int e = in ? p.topk_ids[q] : -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        uint32_t row = 0;
-        if (in) row = base[e] + mine[e] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (in && lane == __ffs(same) - 1) mine[e] = (uint16_t)(mine[e] + __popc(same));
-        __syncwarp();
-        if (in) {
-            p.row_token[row] = (int32_t)(q / k);
-            p.token_rows[q] = (int32_t)row;
-        }
-    }
+    } while (t0 < t_hi);
 }
 
-static bool one_chunk(const inkattn_route_params &p) { return (long long)p.N_tok * p.top_k <= kOneChunkPairs; }
+static bool one_chunk(const inkattn_route_params &p) { return p.N_tok <= kPlaceTokens; }
 static int chunk_tokens(const inkattn_route_params &p) {
     const int t = (p.N_tok + kChunks - 1) / kChunks;
     return t < 32 ? 32 : t;
@@ -305,12 +282,13 @@ cudaError_t launch_route(const inkattn_route_params &p, uint32_t *ws, cudaStream
             ? go(k_route_choose<8>) : p.E <= 512 ? go(k_route_choose<16>) : go(k_route_choose<32>);
         if (err != cudaSuccess) return err;
     }
-    const size_t smem = (size_t)p.E * 4 + 2 * kPlaceThreads * 4 + (size_t)kPlaceWarps * p.E * 2;
+    const int words = ((place_tokens < kPlaceTokens ? place_tokens : kPlaceTokens) + 31) / 32;
+    auto smem_of = [](int E, int w) { return (size_t)E * 4 + 2 * kPlaceThreads * 4 + (size_t)w * E * 6; };
     err = cudaFuncSetAttribute(k_route_place, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               INKATTN_MAX_EXPERTS * 4 + 2 * kPlaceThreads * 4 + kPlaceWarps * INKATTN_MAX_EXPERTS * 2);
+                               (int)smem_of(INKATTN_MAX_EXPERTS, kPlaceTokens / 32));
     if (err != cudaSuccess) return err;
     const dim3 grid((unsigned)(one ? 1 : (p.N_tok + place_tokens - 1) / place_tokens));
-    return launch_dependent(k_route_place, grid, dim3(kPlaceThreads), smem, stream, 1, p, place_tokens,
+    return launch_dependent(k_route_place, grid, dim3(kPlaceThreads), smem_of(p.E, words), stream, 1, p, place_tokens, words,
                             static_cast<const uint32_t *>(counts));
 }
 

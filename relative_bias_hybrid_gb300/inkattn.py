@@ -212,8 +212,14 @@ def abi_version() -> int:
     return int(lib().inkattn_abi_version())
 
 
+# The current stream's handle without building a torch.cuda.Stream for it (2.8 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream

@@ -355,8 +355,8 @@ def _check_route(got, logits, S, k, score, scale=1.0):
 
 
 @pytest.mark.parametrize("T,E,S,k", [(1, 1, 0, 1), (1, 256, 2, 6), (2, 2, 1, 2), (5, 16, 16, 16), (31, 33, 0, 3),
-                                     (288, 256, 2, 6), (300, 64, 1, 8), (683, 256, 2, 6), (700, 200, 0, 6),
-                                     (1500, 1024, 3, 4), (4097, 129, 2, 1), (9000, 384, 2, 8), (20001, 256, 2, 6)])
+                                     (288, 256, 2, 6), (300, 64, 1, 8), (683, 256, 2, 6), (700, 200, 0, 6), (1023, 1024, 1, 16), (1024, 60, 2, 6), (1025, 60, 2, 6),
+                                     (1500, 1024, 3, 4), (4097, 129, 2, 1), (9000, 384, 2, 8), (20001, 256, 2, 6), (200000, 20, 0, 2)])
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_route(ia, T, E, S, k, score):
     g = torch.Generator().manual_seed(T + E)
