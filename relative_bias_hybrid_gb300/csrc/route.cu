@@ -71,6 +71,7 @@ k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *__restr
         __syncthreads();
     }
     const int t_lo = blockIdx.x * chunk_tokens, t_hi = min(p.N_tok, t_lo + chunk_tokens);
+    const bool sigmoid = p.score == INKATTN_SCORE_SIGMOID;
     const bool is_shared = lane >= p.top_k && lane < ws;
     float next[kPer], next_shared = -INFINITY;
     auto request = [&](int t) {
@@ -89,8 +90,8 @@ k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *__restr
             best.add(key[i], i);
         }
         // lane j < top_k: the j-th choice; the next n_shared lanes: the shared experts
-        float l = next_shared == next_shared ? next_shared : -INFINITY;
-        int id = 0;
+        uint32_t chosen = is_shared ? logit_key(next_shared) : 0u;
+        uint32_t id = 0;
         if (t + warps < t_hi) request(t + warps);
         bool two = true;                               // best.k2 is known
         for (int j = 0; j < p.top_k; ++j) {
@@ -99,8 +100,8 @@ k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *__restr
             const uint32_t e = __reduce_min_sync(0xffffffffu, mine);
             const bool taken = mine == e;
             if (lane == j) {
-                l = key_logit(top);
-                id = (int)e;
+                chosen = top;
+                id = e;
             }
             if (__any_sync(0xffffffffu, taken && !two)) {
                 BestTwo rest;
@@ -119,25 +120,26 @@ k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *__restr
                 two = false;
             }
         }
-        // scores up to a factor common to the token, so that they do not all vanish: softmax
-        // exp(l - m) with m the largest logit; sigmoid exp(l - m) / (1 + exp(l)) with m the
-        // largest logit or 0, whichever is less (for m = 0 that is the sigmoid itself)
-        const bool sigmoid = p.score == INKATTN_SCORE_SIGMOID;
-        const uint32_t mk = __reduce_max_sync(0xffffffffu, lane < ws ? logit_key(l) : 0u);
-        const float m = sigmoid ? fminf(key_logit(mk), 0.f) : key_logit(mk);
+        // Scores up to a factor common to the token, so that they do not all vanish: softmax
+        // exp(l - m) with m the largest logit; sigmoid exp(l - m) / (1 + exp(l)) with m the largest
+        // logit or 0, whichever is less.  For m = 0 that is the sigmoid, from one exponential:
+        // with e = exp(-|l|), 1 / (1 + e) for a positive l and e / (1 + e) for others.
+        const float l = key_logit(chosen), top_l = key_logit(__reduce_max_sync(0xffffffffu, chosen));
         float s;
-        if (sigmoid && l > 0.f) {
-            s = 1.f / (1.f + expf(-l));
+        if (sigmoid && top_l >= 0.f) {
+            const float e = expf(-fabsf(l));
+            s = __fdividef(l > 0.f ? 1.f : e, 1.f + e);
         } else {
-            s = l == -INFINITY ? 0.f : l == m ? 1.f : expf(l - m);           // (l == m: infinities too)
-            if (sigmoid) s = s / (1.f + expf(l));
+            s = l == top_l ? 1.f : expf(l - top_l);                          // (equal infinities too)
+            if (sigmoid) s = __fdividef(s, 1.f + expf(l));
         }
-        float sum = lane < ws ? s : 0.f;
+        if (lane >= ws || l == -INFINITY) s = 0.f;
+        float sum = s;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane < ws) p.weights[(size_t)t * ws + lane] = sum > 0.f ? p.scale * (s / sum) : 0.f;
+        if (lane < ws) p.weights[(size_t)t * ws + lane] = sum > 0.f ? p.scale * __fdividef(s, sum) : 0.f;
         if (lane < p.top_k) {
-            p.topk_ids[(size_t)t * p.top_k + lane] = id;
+            p.topk_ids[(size_t)t * p.top_k + lane] = (int32_t)id;
             if (counts) atomicAdd(&s_hist[id], 1u);    // (integers: the order does not show)
         }
     }
