@@ -504,7 +504,7 @@ typedef struct inkattn_grouped_linear_params {
     int32_t *dev_status;       /* nullable                                               */
 } inkattn_grouped_linear_params;
 
-/* Runs the grouped products.  Alignment and overlap rules as inkattn_linear's. */
+/* Runs the grouped products.  Rules of memory, alignment and overlap as inkattn_linear's. */
 INKATTN_API inkattn_status inkattn_grouped_linear(const inkattn_grouped_linear_params *p, void *stream);
 
 /* The router's choice.  Token t has E routed logits and, behind them, n_shared logits of
@@ -541,7 +541,7 @@ typedef struct inkattn_route_params {
 /* Bytes of workspace inkattn_route needs: 0 for small batches, or if the params are invalid. */
 INKATTN_API size_t inkattn_route_workspace_bytes(const inkattn_route_params *p);
 
-/* Runs the router.  All arrays 4-byte aligned; the outputs overlap neither each other nor the
+/* Runs the router.  All arrays 4-byte aligned, in memory of the current device; the outputs overlap neither each other nor the
  * logits.  workspace: device memory, 16-byte aligned, at least inkattn_route_workspace_bytes
  * bytes (nullable when that is 0), need not be cleared; calls whose GPU work overlaps need one
  * each. */
@@ -568,7 +568,8 @@ typedef struct inkattn_expert_combine_params {
     int32_t *dev_status;       /* nullable                                               */
 } inkattn_expert_combine_params;
 
-/* Runs the sum.  y, shared and out must be 16-byte aligned; out overlaps no input. */
+/* Runs the sum.  y, shared and out must be 16-byte aligned; all arrays in memory of the current
+ * device; out overlaps no input. */
 INKATTN_API inkattn_status inkattn_expert_combine(const inkattn_expert_combine_params *p, void *stream);
 
 #ifdef __cplusplus

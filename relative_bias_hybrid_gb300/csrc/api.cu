@@ -256,7 +256,8 @@ inkattn_status validate_locations(const inkattn_attn_params *p) {
     return INKATTN_OK;
 }
 
-// Device memory of the current device, as TMA reads it.
+// Device memory of the current device: what TMA reads, and, where nothing is read by TMA, one or
+// two arrays of a call, so that a call made under another current device is refused.
 inkattn_status validate_on_device(const void *const *ptrs, int n) {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -697,6 +698,8 @@ inkattn_status inkattn_route(const inkattn_route_params *p, void *workspace, siz
     const size_t need = route_workspace_bytes(*p);
     if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return INKATTN_ERR_INVALID_ARG;
     if ((st = check_device(nullptr)) != INKATTN_OK) return st;
+    const void *read[] = {p->expert_offsets, p->logits};
+    if ((st = validate_on_device(read, p->N_tok > 0 ? 2 : 1)) != INKATTN_OK) return st;
     return launch_status(launch_route(*p, static_cast<uint32_t *>(workspace), static_cast<cudaStream_t>(stream)));
 }
 
@@ -705,6 +708,8 @@ inkattn_status inkattn_expert_combine(const inkattn_expert_combine_params *p, vo
     if (st != INKATTN_OK) return st;
     if ((st = check_device(nullptr)) != INKATTN_OK) return st;
     if (p->N_tok == 0) return INKATTN_OK;
+    const void *read[] = {p->out, p->weights};
+    if ((st = validate_on_device(read, 2)) != INKATTN_OK) return st;
     return launch_status(launch_expert_combine(*p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -209,7 +209,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     }
     // Everything up to here and, for a linear layer, the rest of the setup needs no global memory
     // and runs while the kernel before this one on the stream finishes; each role waits for that
-    // kernel before it reads or writes global memory.
+    // kernel before it reads or writes global memory, and before its first wait with a limit.
     if (warp == kWarpEpi) {
         if (A.offsets) grid_dep_wait();
         // first row of every expert and the prefix of token tiles: s_tiles[e] = tiles of experts 0 .. e-1
@@ -335,6 +335,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         // copy, an async operation that the fence orders behind the rows and whose bytes complete
         // on the even CTA's barrier.  (A remote arrival with release at cluster scope stalled the
         // warp for about 1 us a stage: 2.7 ms where this takes 1.1.)
+        grid_dep_wait();
         RingPos at;
         bool ok = true;
         for (int w = cid; w < n_items && ok; w += nclusters)
@@ -392,6 +393,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         // the odd CTA issues no MMAs
     } else if (warp == kWarpMma) {
         // ================================ even CTA: MMA issuer ================================
+        grid_dep_wait();
         const uint64_t da0 = tc::sdesc_sw128(s_base, 16, 1024);
         const uint64_t db0 = tc::sdesc_sw128(s_base + kABytes, 16, 1024);
         const uint16_t pair = (uint16_t)(3u << even);

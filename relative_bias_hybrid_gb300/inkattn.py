@@ -512,6 +512,13 @@ def _shape(t, shape, name):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _one_device(*tensors):
+    """A call's tensors lie on one device; the library compares it with the current one."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) > 1:
+        raise ValueError(f"tensors on several devices: {sorted(map(str, devices))}")
+
+
 def linear_params(*, x, w, out, act: str = "none", bias=None, residual=None, dev_status=None) -> LinearParams:
     """Fill an inkattn_linear_params from torch tensors (see include/inkattn.h): x [N][K],
     w [F][K] (act "swiglu": [2F][K], the gate rows first), bias fp32 None or one per row of w,
@@ -520,6 +527,7 @@ def linear_params(*, x, w, out, act: str = "none", bias=None, residual=None, dev
     N, K = x.shape
     F = out.shape[1]
     rows = 2 * F if act == "swiglu" else F
+    _one_device(x, w, out, bias, residual, dev_status)
     _shape(w, (rows, K), "w"); _shape(out, (N, F), "out"); _shape(bias, (rows,), "bias")
     _shape(residual, (N, F), "residual")
     p = LinearParams()
@@ -544,6 +552,7 @@ def grouped_linear_params(*, x, w, expert_offsets, out, act: str = "none", row_t
     M, F = out.shape
     E = w.shape[0]
     rows = 2 * F if act == "swiglu" else F
+    _one_device(x, w, expert_offsets, out, row_token, bias, dev_status)
     _shape(w, (E, rows, K), "w"); _shape(expert_offsets, (E + 1,), "expert_offsets")
     _shape(row_token, (M,), "row_token"); _shape(bias, (E, rows), "bias")
     p = GroupedLinearParams()
@@ -567,6 +576,7 @@ def route_params(*, logits, topk_ids, weights, expert_offsets, row_token, token_
     f32, i32 = torch.float32, torch.int32
     N, k = topk_ids.shape
     E = logits.shape[1] - int(n_shared)
+    _one_device(logits, topk_ids, weights, expert_offsets, row_token, token_rows)
     _shape(logits, (N, E + n_shared), "logits"); _shape(weights, (N, k + n_shared), "weights")
     _shape(expert_offsets, (E + 1,), "expert_offsets"); _shape(row_token, (N * k,), "row_token")
     _shape(token_rows, (N, k), "token_rows")
@@ -589,6 +599,7 @@ def expert_combine_params(*, y, weights, token_rows, out, shared=None, dev_statu
     M, F = y.shape
     N, k = token_rows.shape
     S = shared.shape[0] if shared is not None else 0
+    _one_device(y, weights, token_rows, out, shared, dev_status)
     _shape(weights, (N, k + S), "weights"); _shape(out, (N, F), "out"); _shape(shared, (S, N, F), "shared")
     p = ExpertCombineParams()
     p.struct_size = ctypes.sizeof(ExpertCombineParams)

@@ -147,6 +147,27 @@ def test_calls_wait_for_the_work_before_them(env):
     assert torch.equal(a.float(), first.float() * 64)
 
 
+def test_host_memory_is_refused(env):
+    """Tensors in host memory, pinned or not: refused by the library, nothing launched."""
+    _, ia, _ = env
+    x, w, out = (torch.zeros(s, dtype=BF16) for s in ((4, 16), (8, 16), (4, 8)))
+    i32 = torch.int32
+    for pin in (False, True):
+        a, b, c = (t.pin_memory() if pin else t for t in (x, w, out))
+        calls = [
+            (ia.inkattn_linear, ia.linear_params(x=a, w=b, out=c)),
+            (ia.inkattn_grouped_linear, ia.grouped_linear_params(
+                x=a, w=b[None], out=c, expert_offsets=torch.zeros(2, dtype=i32))),
+            (ia.inkattn_expert_combine, ia.expert_combine_params(
+                y=a, weights=torch.zeros(4, 1), token_rows=torch.zeros(4, 1, dtype=i32), out=torch.zeros_like(a))),
+            (ia.inkattn_route, ia.route_params(
+                logits=torch.zeros(4, 8), topk_ids=torch.zeros(4, 1, dtype=i32), weights=torch.zeros(4, 1),
+                expert_offsets=torch.zeros(9, dtype=i32), row_token=torch.zeros(4, dtype=i32),
+                token_rows=torch.zeros(4, 1, dtype=i32)))]
+        for call, p in calls:
+            assert call(p, raise_on_error=False) == ia.INKATTN_ERR_INVALID_ARG, call.__name__
+
+
 def test_arrays_past_32_bits(env):
     """Outputs, weights and inputs of more than 2^31 elements: rows at the far end."""
     _, ia, _ = env

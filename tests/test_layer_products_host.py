@@ -151,6 +151,8 @@ def test_binding_refusals(ia):
     for kw in (dict(x=x.float()), dict(out=out.half()), dict(bias=torch.zeros(8, dtype=bf))):
         with pytest.raises(TypeError):
             ia.linear_params(**{**dict(x=x, w=w, out=out), **kw})
+    with pytest.raises(ValueError):
+        ia.linear_params(x=x, w=w.to("meta"), out=out)
     with pytest.raises(KeyError):
         ia.linear_params(x=x, w=w, out=out, act="tanh")
     good = dict(x=x, w=torch.zeros(3, 8, 16, dtype=bf), expert_offsets=torch.zeros(4, dtype=i32),
