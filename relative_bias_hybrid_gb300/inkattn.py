@@ -539,6 +539,7 @@ def linear_params(*, x, w, out, act: str = "none", bias=None, residual=None, dev
     p.bias = _ptr(bias, f32, "bias"); p.residual = _ptr(residual, bf, "residual")
     p.out = _ptr(out, None, "out")
     p.dev_status = _ptr(dev_status, i32, "dev_status")
+    p.tensors = (x, w, out, bias, residual, dev_status)     # alive as long as the params
     return p
 
 
@@ -565,6 +566,7 @@ def grouped_linear_params(*, x, w, expert_offsets, out, act: str = "none", row_t
     p.row_token = _ptr(row_token, i32, "row_token")
     p.out = _ptr(out, None, "out")
     p.dev_status = _ptr(dev_status, i32, "dev_status")
+    p.tensors = (x, w, expert_offsets, out, row_token, bias, dev_status)     # alive as long as the params
     return p
 
 
@@ -589,6 +591,7 @@ def route_params(*, logits, topk_ids, weights, expert_offsets, row_token, token_
     p.weights = _ptr(weights, f32, "weights")
     p.expert_offsets = _ptr(expert_offsets, i32, "expert_offsets")
     p.row_token = _ptr(row_token, i32, "row_token"); p.token_rows = _ptr(token_rows, i32, "token_rows")
+    p.tensors = (logits, topk_ids, weights, expert_offsets, row_token, token_rows)     # alive as long as the params
     return p
 
 
@@ -607,4 +610,5 @@ def expert_combine_params(*, y, weights, token_rows, out, shared=None, dev_statu
     p.y = _ptr(y, bf, "y"); p.shared = _ptr(shared, bf, "shared"); p.weights = _ptr(weights, f32, "weights")
     p.token_rows = _ptr(token_rows, i32, "token_rows"); p.out = _ptr(out, bf, "out")
     p.dev_status = _ptr(dev_status, i32, "dev_status")
+    p.tensors = (y, weights, token_rows, out, shared, dev_status)     # alive as long as the params
     return p

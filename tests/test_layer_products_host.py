@@ -178,3 +178,20 @@ def test_binding_refusals(ia):
     for kw in (dict(shared=None), dict(weights=torch.zeros(4, 2)), dict(out=torch.zeros(4, 8, dtype=bf))):
         with pytest.raises(ValueError):
             ia.expert_combine_params(**{**c, **kw})
+
+
+def test_params_keep_their_tensors(ia):
+    """A params struct holds addresses; the tensors behind them live as long as it does."""
+    import gc
+    import weakref
+    bias = torch.zeros(8)
+    seen = weakref.ref(bias)
+    p = ia.linear_params(x=torch.zeros(4, 16, dtype=torch.bfloat16), w=torch.zeros(8, 16, dtype=torch.bfloat16),
+                         out=torch.zeros(4, 8, dtype=torch.bfloat16), bias=bias)
+    address = bias.data_ptr()
+    del bias
+    gc.collect()
+    assert p.bias == address and seen() is not None
+    del p
+    gc.collect()
+    assert seen() is None
