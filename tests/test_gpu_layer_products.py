@@ -49,8 +49,10 @@ def _curve_slack(v, act):
     """Absolute error of the fp32 curve at an exact argument v.  __expf is within 2 + 1.173 |x|
     units of 2^-23 of exp(x) (its documented bound), the sum 1 + exp and the division add a unit
     each: silu is within (4 + 1.2 |v|) 2^-23 |silu|, and below -87 the exp leaves fp32's range,
-    where silu is under 1e-36.  erff is within 2 units of 2^-23 of a value up to 1; 1 + erf and
-    two products follow: gelu is within 4 * 2^-23 |v|."""
+    where silu is under 1e-36.  gelu takes |v| / 2 times an erfc that is within 1.5e-7 (1.3 units of
+    2^-23) by its formula, and by its evaluation within about 5 units of its own value, at most 1 (the
+    exponential, 2 + 1.173 x^2 times exp(-x^2), is within 2.5 units; the division and the polynomial
+    2; the products 1): (1.3 + 5.5) / 2 < 4 units of |v|."""
     if act == "gelu":
         return 4 * 2.0 ** -23 * v.abs()
     if act == "silu":
@@ -163,7 +165,7 @@ def test_linear_in_place_residual_and_infinities(ia):
     """out == residual; infinities and NaN stay in their own token's row."""
     T, K, F = 40, 128, 264
     x, w, bias, residual = _linear_inputs(T, K, F, "none", seed=3)
-    x[5, 7] = float("inf"); x[6, 1] = float("nan")
+    x[5, 7] = float("inf"); x[6, 1] = float("nan"); x[7, 3] = -float("inf")
     dev = [t.cuda() for t in (x, w, bias, residual)]
     ia.inkattn_linear(ia.linear_params(x=dev[0], w=dev[1], bias=dev[2], residual=dev[3], out=dev[3]))
     torch.cuda.synchronize()
@@ -171,6 +173,24 @@ def test_linear_in_place_residual_and_infinities(ia):
     got = dev[3].cpu()
     assert torch.equal(torch.isnan(got), torch.isnan(want))
     assert torch.equal(torch.nan_to_num(got.float()), torch.nan_to_num(want.float()))
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu", "swiglu"])
+def test_linear_activations_of_wide_arguments(ia, act):
+    """Arguments from -60 to 60 in steps of 1/32, and NaN: an identity weight passes them through."""
+    v = torch.arange(-1920, 1921).double() / 32
+    K = 8 * ((v.numel() + 7) // 8)
+    x = torch.zeros((2, K), dtype=BF16)
+    x[0, :v.numel()] = v.to(BF16)                      # (rounded to bf16: the arguments are what x holds)
+    x[1, 5] = float("nan")
+    w = torch.eye(K, dtype=BF16)
+    if act == "swiglu":
+        w = torch.cat([w, w.flip(0)])
+    for dtype in (BF16, F32):
+        got = _run_linear(ia, x, w, None, None, act, dtype, K)
+        arg = torch.cat([x[:1].double(), x[:1].double().flip(1)], 1) if act == "swiglu" else x[:1].double()
+        _check(got[:1], arg, act)
+        assert bool(torch.isnan(got[1]).all())         # NaN times a zero weight is a NaN everywhere
 
 
 def test_linear_no_tokens_and_repeatability(ia):

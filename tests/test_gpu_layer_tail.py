@@ -34,8 +34,8 @@ def _tail(env, q_lens, seed=0, Hq=4, **kw):
     gen, _, LayerTailStep = env
     w = gen.custom("tail", Hq=Hq, Hkv=1, q_lens=q_lens, prefix_lens=[5] * len(q_lens))
     x = gen.make_layer_tail_inputs(w, seed=seed, device="cuda", **kw)
-    attn = torch.randn((w.N_tok, Hq, 128), device="cuda", generator=torch.Generator("cuda").manual_seed(seed))
-    return LayerTailStep(w, x, attn.to(BF16), top_k=3), x, attn.to(BF16)
+    attn = torch.randn((w.N_tok, Hq, 128), device="cuda", generator=torch.Generator("cuda").manual_seed(seed)).to(BF16)
+    return LayerTailStep(w, x, attn, top_k=3), x, attn
 
 
 def _near_product(got, x, w, act="none"):
