@@ -484,8 +484,9 @@ INKATTN_API inkattn_status inkattn_linear(const inkattn_linear_params *p, void *
  * expert_offsets lies on the device, so the same call (or captured graph) serves any split of
  * the rows among the experts; an expert without rows costs nothing.  Rows at and behind
  * expert_offsets[E] are neither read nor written.  An expert whose offsets are negative,
- * decrease or pass M is flagged (INKATTN_ERR_DEVICE_BOUNDS) and its rows left as they were,
- * and so is a row whose row_token lies outside [0, N_x). */
+ * decrease, pass M or reach back behind an earlier expert's end is flagged
+ * (INKATTN_ERR_DEVICE_BOUNDS) and its rows left as they were, and so is a row whose row_token
+ * lies outside [0, N_x). */
 #define INKATTN_MAX_EXPERTS 1024
 typedef struct inkattn_grouped_linear_params {
     size_t struct_size;        /* = sizeof(inkattn_grouped_linear_params)                */

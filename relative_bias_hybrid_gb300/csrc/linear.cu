@@ -19,11 +19,13 @@
 // The rows of a token tile are one box of x, as many rows as the tile has (a tensor map for
 // each box height), or, with row indices, are gathered by four warps of their own with 16-byte
 // cp.async: the copy of x in expert order is never written.  (TMA's gather of four rows was
-// measured first: a K = 64 step of 128 rows took about 1800 cycles, 3.5 times its MMAs.)  SWIGLU: the CTA's 128 weight rows are
-// 64 gate rows and the 64 up rows of the same features, one box; the two warps that hold a
-// feature's gate and up exchange half of the tokens through shared memory.  (16 gate rows and 16
-// up rows in turn, a shuffle apart in one warp, were measured first: four boxes a stage made the
-// copies the bound, 0.78 ms where one box takes 0.57 for the same products.)
+// measured first: a K = 64 step of 128 rows took about 1800 cycles, 3.5 times its MMAs.)
+//
+// SWIGLU: the CTA's 128 weight rows are 64 gate rows and the 64 up rows of the same features, one
+// box; the two warps that hold a feature's gate and up exchange half of the tokens through shared
+// memory.  (16 gate rows and 16 up rows in turn, a shuffle apart in one warp, were measured first:
+// four boxes a stage made the copies the bound, 0.78 ms where one box takes 0.57 for the same
+// products.)
 //
 // One CTA per SM, 11 warps (16 with row indices):
 //   warps 0, 10 producers, a lane of each: copies of the weight rows and the token rows into a
@@ -43,7 +45,8 @@
 // to nearest; over K = 8192 the error grows to about 1e-5 of the result, nothing next to a bf16
 // rounding but much for an fp32 one.  An fp32 output is therefore summed in parts of K = 512,
 // which the epilogue warps add up in registers, rounding to nearest (K = 1000: 4.6e-7 of the
-// result instead of 9.8e-7, and the same at K = 8192).  The registers hold 32 tokens a warp, so its tiles have 64 tokens.
+// result instead of 9.8e-7, and the same at K = 8192).  The registers hold 32 tokens a warp, so
+// its tiles have 64 tokens at most: 8192 x 8192 x 8192 takes 1.58 ms instead of 0.57.
 //
 // Few items (a decode batch): the K range is split over the S pairs of one cluster.  Each CTA
 // writes its fp32 partial tile, a share of the tokens to each pair, into the other CTAs' shared
@@ -222,18 +225,35 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     // kernel before it reads or writes global memory, and before its first wait with a limit.
     if (warp == kWarpEpi) {
         if (A.offsets) grid_dep_wait();
-        // first row of every expert and the prefix of token tiles: s_tiles[e] = tiles of experts 0 .. e-1
-        int carry = 0;
+        // First row of every expert and the prefix of token tiles: s_tiles[e] = tiles of experts
+        // 0 .. e-1.  An expert that reaches back into the rows of an earlier one is refused like
+        // one with impossible offsets: the accepted ones hold M rows together at most, so that the
+        // items stay within what the launch was sized for.
+        int carry = 0, reached = 0;                    // tiles, and the largest end, so far
         if (lane == 0) s_tiles[0] = 0;
         for (int e0 = 0; e0 < A.E; e0 += 32) {
             const int e = e0 + lane;
-            int tiles = 0;
+            int tiles = 0, start = 0, end = 0;
             if (e < A.E) {
-                const int start = A.offsets ? A.offsets[e] : 0, end = A.offsets ? A.offsets[e + 1] : A.M;
-                if (start < 0 || end < start || end > A.M) set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
-                else tiles = (end - start + A.tile_n - 1) / A.tile_n;
+                start = A.offsets ? A.offsets[e] : 0;
+                end = A.offsets ? A.offsets[e + 1] : A.M;
                 s_start[e] = start;
                 if (e == A.E - 1) s_start[A.E] = end;
+            }
+            bool valid = start >= 0 && end >= start && end <= A.M;
+            int most = valid ? end : 0;                // largest end up to this lane, then before it
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int n = __shfl_up_sync(0xffffffffu, most, o);
+                if (lane >= o) most = max(most, n);
+            }
+            const int all = max(reached, __shfl_sync(0xffffffffu, most, 31));
+            most = __shfl_up_sync(0xffffffffu, most, 1);
+            valid = valid && start >= max(reached, lane ? most : 0);
+            reached = all;
+            if (e < A.E) {
+                if (valid) tiles = (end - start + A.tile_n - 1) / A.tile_n;
+                else set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
             }
             int v = tiles;
 #pragma unroll
@@ -801,6 +821,7 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     const long long owners = a.offsets ? (a.E < a.M ? a.E : a.M) : 1;
     const long long rows = (a.M + owners - 1) / owners;
     const double weight_bytes = (double)owners * a.n_fblocks * 2 * kRowsA * a.K * 2;
+    if (resident_clusters(2, num_sms) < 1) return cudaErrorInvalidConfiguration;
     int most_n = a.out_f32 ? kFineN : kMaxN;
     if (a.offsets && 4 * rows < most_n) most_n = rows < 16 ? 64 : (int)(4 * rows + 31) / 32 * 32;
     double best = 0.0;
@@ -827,7 +848,6 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     a.stage_bytes = kABytes + a.tile_n / 2 * 128;
     a.stages = kRingBytes / a.stage_bytes < kMaxStages ? kRingBytes / a.stage_bytes : kMaxStages;
     const int most = resident_clusters(2 * a.splits, num_sms);
-    if (most < 1) return cudaErrorInvalidConfiguration;
     const int clusters = (int)(most_items < most ? most_items : most);
     LinearMaps maps;
     if (!make_linear_maps(a, act == INKATTN_ACT_SWIGLU, &maps)) return cudaErrorInvalidValue;

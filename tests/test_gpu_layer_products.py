@@ -323,6 +323,29 @@ def test_grouped_bad_indices_are_flagged_and_left(ia):
         assert all(bool((out[i] == 7).all()) for i in range(M) if i not in covered)
 
 
+def test_grouped_overlapping_experts_are_flagged_and_left(ia):
+    """Offsets that go back: of experts 0..30, 30..10, 10..50, 50..60 the second decreases and the
+    third reaches into the first one's rows; the first and the last are computed.  Many such
+    experts must not make more work than the launch was sized for."""
+    g = torch.Generator().manual_seed(6)
+    K, F, M = 1024, 128, 60
+    for offsets, good in (([0, 30, 10, 50, 60], [(0, 0, 30), (3, 50, 60)]),
+                          ([0, M] * 40, [(0, 0, M)])):
+        E = len(offsets) - 1
+        x, w = _grid((M, K), g, -8, 8, 1 / 8), _grid((E, F, K), g, -8, 8, 1 / 64)
+        out = torch.full((M, F), 7.0, dtype=BF16, device="cuda")
+        status = torch.zeros(1, dtype=I32, device="cuda")
+        dev = [t.cuda() for t in (x, w, torch.tensor(offsets, dtype=I32))]
+        ia.inkattn_grouped_linear(ia.grouped_linear_params(x=dev[0], w=dev[1], expert_offsets=dev[2], out=out,
+                                                           dev_status=status))
+        torch.cuda.synchronize()
+        assert int(status) == ia.INKATTN_ERR_DEVICE_BOUNDS
+        want = torch.full((M, F), 7.0, dtype=BF16)
+        for e, lo, hi in good:
+            want[lo:hi] = (x[lo:hi].double() @ w[e].double().t()).to(F32).to(BF16)
+        assert torch.equal(out.cpu(), want)
+
+
 # ---------------------------------------------------------------- router and sum
 
 def _route(ia, logits, S, k, score="sigmoid", scale=1.0):
