@@ -44,9 +44,9 @@
 // fp32 outputs (kFine).  The tensor cores add each K = 16 step to the accumulator without rounding
 // to nearest; over K = 8192 the error grows to about 1e-5 of the result, nothing next to a bf16
 // rounding but much for an fp32 one.  An fp32 output is therefore summed in parts of K = 512,
-// which the epilogue warps add up in registers, rounding to nearest (K = 1000: 4.6e-7 of the
-// result instead of 9.8e-7, and the same at K = 8192).  The registers hold 32 tokens a warp, so
-// its tiles have 64 tokens at most: 8192 x 8192 x 8192 takes 1.58 ms instead of 0.57.
+// which the epilogue warps add up in TMEM, rounding to nearest (K = 1000: 4.6e-7 of the result
+// instead of 9.8e-7, and the same at K = 8192).  The two accumulators and the sums share the 512
+// TMEM columns, so the tiles have 160 tokens at most: 8192 x 8192 x 8192 takes 0.79 ms instead of 0.57.
 //
 // Few items (a decode batch): the K range is split over the S pairs of one cluster.  Each CTA
 // writes its fp32 partial tile, a share of the tokens to each pair, into the other CTAs' shared
@@ -82,7 +82,7 @@ constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpEpi = 2, kWarpProducer2 = 10
               kWarpRelay = 15;
 constexpr int kStgPitch = 36;                     // floats of a staging row: 32 features + 4
 constexpr int kStgBytes = 16 * kStgPitch * 4;     // 16 tokens, one buffer per epilogue warp
-constexpr int kFineSteps = 8, kFineN = 64;        // fp32 outputs: K steps of a part, tokens of a tile
+constexpr int kFineSteps = 8, kFineN = 160;       // fp32 outputs: K steps of a part, tokens of a tile
 constexpr int kRaster = 8;                        // feature blocks per raster group
 
 constexpr int kOffStg = kRingBytes;
@@ -277,6 +277,8 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     // the accumulations of an item, one after another in the two TMEM buffers
     const int part = kFine ? kFineSteps : k_hi - k_lo, parts = kFine ? (k_hi - k_lo + part - 1) / part : 1;
     const int my_items = cid < n_items ? (n_items - cid + nclusters - 1) / nclusters : 0;
+    constexpr int kAccCols = kFine ? kFineN : kMaxN;           // TMEM columns of an accumulator
+    const uint32_t t_sums = tmem + 2 * kFineN;                 // kFine: the sums of the parts so far
     auto item = [&](int w) {
         Item it;
         const int t = w / A.n_fblocks;
@@ -306,8 +308,6 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
 
     // a split's cluster has one item at most (worked out here, off the path behind the products)
     const Item only = A.splits > 1 && cid < n_items ? item(cid) : Item{};
-
-    float fine[kFine ? 32 : 1];                        // an epilogue warp's sums of the parts
 
     if (warp == kWarpProducer || warp == kWarpProducer2) {
         // ================================ producers ================================
@@ -453,7 +453,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                     ready = left > 1 && mbar_test_wait(bar(B_FULL + at.s), at.lap & 1);   // seen while the MMAs are issued
                     tc::fence_after();
                     const uint64_t off = (uint64_t)(now.s * (A.stage_bytes >> 4));
-                    tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)(buf * kMaxN), da0 + off, db0 + off, id,
+                    tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)(buf * kAccCols), da0 + off, db0 + off, id,
                                                     k > k0 ? 1u : 0u, bar(B_EMPTY + now.s), left > A.stages ? 1u : 0u,
                                                     bar(B_ACC_FULL + buf), k == k1 - 1 ? 1u : 0u, pair);
                     --left;
@@ -498,7 +498,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             __syncwarp();
             if (lane == 0) mbar_remote_arrive(bar(B_ACC_EMPTY + (i & 1)), even);   // its MMA warp waits
         };
-        for (int w = cid; w < n_items && ok; w += nclusters, ++i) {
+        for (int w = cid; w < n_items; w += nclusters) {
             const Item it = item(w);
             // the warp's 32 features (gated: quarters 0 and 1 hold gates, 2 and 3 the ups of the
             // same features), the lane's feature and its bias
@@ -507,130 +507,126 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             float bias = 0.f;
             if (A.bias && frow < A.F)
                 bias = __ldg(A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + (kGated && quarter >= 2 ? F : 0) + frow);
-            if (kFine) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) fine[j] = 0.f;
-                for (int q = 0; q < parts; ++q) {
-                    if (!acc_full()) break;
-                    uint32_t v[32];
-                    tc::ld32(tmem + (uint32_t)((i & 1) * kMaxN + e8 * 32) + ((uint32_t)(quarter * 32) << 16), v);
-                    tc::wait_ld();
-                    release();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) fine[j] += __uint_as_float(v[j]);
-                    if (q < parts - 1) ++i;
-                }
-                if (!ok) break;
-            } else if (!acc_full()) {
-                break;
-            }
-            if (A.splits > 1) break;                          // (one item; it is finished below)
-            const uint32_t taddr = tmem + (uint32_t)((i & 1) * kMaxN) + ((uint32_t)(quarter * 32) << 16);
+            const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
             const int nblocks = (it.nt + 31) >> 5;
-            if (!kFine && e8 >= nblocks) release();
-            for (int c = e8; c < nblocks; c += 2) {
-                uint32_t v[32];
-                if (kFine) {
+            for (int q = 0; q < parts; ++q, ++i) {
+                if (!acc_full()) break;
+                if (A.splits > 1 && parts == 1) break;        // (the tile is finished below, from this accumulator)
+                if (e8 >= nblocks) release();
+                for (int c = e8; c < nblocks; c += 2) {
+                    uint32_t v[32];
+                    tc::ld32(tmem + (uint32_t)((i & 1) * kAccCols + c * 32) + lanes, v);
+                    if (kFine && q > 0) {
+                        uint32_t before[32];
+                        tc::ld32(t_sums + (uint32_t)(c * 32) + lanes, before);
+                        tc::wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(fine[j]);
-                } else {
-                    tc::ld32(taddr + (uint32_t)(c * 32), v);
-                    tc::wait_ld();
-                    if (c + 2 >= nblocks) release();
-                }
-                // tokens of this block that are stored
-                bool mine = c * 32 + lane < it.nt;
-                if (A.row_token && mine) {
-                    const int t = __ldg(A.row_token + it.row0 + c * 32 + lane);
-                    if (t < 0 || t >= A.N_x) {
-                        mine = false;
-                        set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = __float_as_uint(__uint_as_float(before[j]) + __uint_as_float(v[j]));
+                    } else {
+                        tc::wait_ld();
                     }
-                }
-                const uint32_t live = __ballot_sync(0xffffffffu, mine);
-                // 16 finished tokens t0 .. t0 + 15 of the block, the lane's feature of each, to out
-                auto store16 = [&](const float (&y)[16], int t0) {
-                    const size_t row_b = (size_t)(it.row0 + c * 32 + t0);
-                    const uint32_t live16 = live >> t0;
-                    if (!vec) {                               // rows that start anywhere
+                    if (c + 2 >= nblocks) release();
+                    if (kFine && (q < parts - 1 || A.splits > 1)) {
+                        tc::st32(t_sums + (uint32_t)(c * 32) + lanes, v);
+                        tc::wait_st();
+                        continue;
+                    }
+                    // tokens of this block that are stored
+                    bool mine = c * 32 + lane < it.nt;
+                    if (A.row_token && mine) {
+                        const int t = __ldg(A.row_token + it.row0 + c * 32 + lane);
+                        if (t < 0 || t >= A.N_x) {
+                            mine = false;
+                            set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+                        }
+                    }
+                    const uint32_t live = __ballot_sync(0xffffffffu, mine);
+                    // 16 finished tokens t0 .. t0 + 15 of the block, the lane's feature of each, to out
+                    auto store16 = [&](const float (&y)[16], int t0) {
+                        const size_t row_b = (size_t)(it.row0 + c * 32 + t0);
+                        const uint32_t live16 = live >> t0;
+                        if (!vec) {                               // rows that start anywhere
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                if (((live16 >> j) & 1u) && frow < A.F) {
+                                    const size_t o = (row_b + j) * F + frow;
+                                    const float z = A.residual ? y[j] + load_bf16(A.residual + o) : y[j];
+                                    if (kFine) out32[o] = z;
+                                    else store_bf16(out16 + o, z);
+                                }
+                            }
+                            return;
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) stg[j * kStgPitch + lane] = y[j];
+                        __syncwarp();
+                        if (!kFine) {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const int t = q * 8 + (lane >> 2), f = f0 + (lane & 3) * 8;
+                                const float *src = stg + t * kStgPitch + (lane & 3) * 8;
+                                float z[8];
+                                *reinterpret_cast<float4 *>(z) = *reinterpret_cast<const float4 *>(src);
+                                *reinterpret_cast<float4 *>(z + 4) = *reinterpret_cast<const float4 *>(src + 4);
+                                if (((live16 >> t) & 1u) && f < A.F) {
+                                    const size_t o = (row_b + t) * F + f;
+                                    if (A.residual) {
+                                        float r[8];
+                                        unpack8(*reinterpret_cast<const uint4 *>(A.residual + o), r);
+#pragma unroll
+                                        for (int j = 0; j < 8; ++j) z[j] += r[j];
+                                    }
+                                    *reinterpret_cast<uint4 *>(out16 + o) = pack8(z);
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int t = q * 4 + (lane >> 3), f = f0 + (lane & 7) * 4;
+                                float4 z = *reinterpret_cast<const float4 *>(stg + t * kStgPitch + (lane & 7) * 4);
+                                if (((live16 >> t) & 1u) && f < A.F) {
+                                    const size_t o = (row_b + t) * F + f;
+                                    if (A.residual) {
+                                        const uint2 r = *reinterpret_cast<const uint2 *>(A.residual + o);
+                                        z.x += bf16_lo(r.x); z.y += bf16_hi(r.x);
+                                        z.z += bf16_lo(r.y); z.w += bf16_hi(r.y);
+                                    }
+                                    *reinterpret_cast<float4 *>(out32 + o) = z;
+                                }
+                            }
+                        }
+                    };
+                    float y[16];
+                    if (kGated) {
+                        // the gate warp finishes the block's first 16 tokens, the up warp the others
+                        const int keep = quarter < 2 ? 0 : 16;
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            stg[j * kStgPitch + lane] = __uint_as_float(quarter < 2 ? v[16 + j] : v[j]) + bias;
+                        named_sync(swap_bar, 64);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            if (((live16 >> j) & 1u) && frow < A.F) {
-                                const size_t o = (row_b + j) * F + frow;
-                                const float z = A.residual ? y[j] + load_bf16(A.residual + o) : y[j];
-                                if (kFine) out32[o] = z;
-                                else store_bf16(out16 + o, z);
-                            }
+                            const float own = __uint_as_float(quarter < 2 ? v[j] : v[16 + j]) + bias;
+                            const float other = stg_other[j * kStgPitch + lane];
+                            const float gate = quarter < 2 ? own : other, up = quarter < 2 ? other : own;
+                            y[j] = activate<INKATTN_ACT_SILU>(gate) * up;
                         }
-                        return;
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) stg[j * kStgPitch + lane] = y[j];
-                    __syncwarp();
-                    if (!kFine) {
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const int t = q * 8 + (lane >> 2), f = f0 + (lane & 3) * 8;
-                            const float *src = stg + t * kStgPitch + (lane & 3) * 8;
-                            float z[8];
-                            *reinterpret_cast<float4 *>(z) = *reinterpret_cast<const float4 *>(src);
-                            *reinterpret_cast<float4 *>(z + 4) = *reinterpret_cast<const float4 *>(src + 4);
-                            if (((live16 >> t) & 1u) && f < A.F) {
-                                const size_t o = (row_b + t) * F + f;
-                                if (A.residual) {
-                                    float r[8];
-                                    unpack8(*reinterpret_cast<const uint4 *>(A.residual + o), r);
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) z[j] += r[j];
-                                }
-                                *reinterpret_cast<uint4 *>(out16 + o) = pack8(z);
-                            }
-                        }
+                        named_sync(swap_bar, 64);                 // both have read
+                        store16(y, keep);
                     } else {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int t = q * 4 + (lane >> 3), f = f0 + (lane & 7) * 4;
-                            float4 z = *reinterpret_cast<const float4 *>(stg + t * kStgPitch + (lane & 7) * 4);
-                            if (((live16 >> t) & 1u) && f < A.F) {
-                                const size_t o = (row_b + t) * F + f;
-                                if (A.residual) {
-                                    const uint2 r = *reinterpret_cast<const uint2 *>(A.residual + o);
-                                    z.x += bf16_lo(r.x); z.y += bf16_hi(r.x);
-                                    z.z += bf16_lo(r.y); z.w += bf16_hi(r.y);
-                                }
-                                *reinterpret_cast<float4 *>(out32 + o) = z;
-                            }
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) y[j] = activate<kAct>(__uint_as_float(v[16 * h + j]) + bias);
+                            store16(y, 16 * h);
                         }
-                    }
-                };
-                float y[16];
-                if (kGated) {
-                    // the gate warp finishes the block's first 16 tokens, the up warp the others
-                    const int keep = quarter < 2 ? 0 : 16;
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        stg[j * kStgPitch + lane] = __uint_as_float(quarter < 2 ? v[16 + j] : v[j]) + bias;
-                    named_sync(swap_bar, 64);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float own = __uint_as_float(quarter < 2 ? v[j] : v[16 + j]) + bias;
-                        const float other = stg_other[j * kStgPitch + lane];
-                        const float gate = quarter < 2 ? own : other, up = quarter < 2 ? other : own;
-                        y[j] = activate<INKATTN_ACT_SILU>(gate) * up;
-                    }
-                    named_sync(swap_bar, 64);                 // both have read
-                    store16(y, keep);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) y[j] = activate<kAct>(__uint_as_float(v[16 * h + j]) + bias);
-                        store16(y, 16 * h);
                     }
                 }
             }
+            if (!ok || A.splits > 1) break;                   // (of a split: one item)
         }
     }
 
@@ -646,13 +642,8 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             const uint32_t place = s_base + (uint32_t)((split * share * kRowsA + quarter * 32 + lane) * 4);
             for (int c = (warp - kWarpEpi) >> 2; c * 32 < it.nt; c += 2) {
                 uint32_t v[32];
-                if (kFine) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(fine[j]);
-                } else {
-                    tc::ld32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(c * 32), v);
-                    tc::wait_ld();
-                }
+                tc::ld32((parts > 1 ? t_sums : tmem) + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(c * 32), v);
+                tc::wait_ld();
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int t = c * 32 + g * 8, owner = t / share;

@@ -161,6 +161,26 @@ def test_linear_gaussian(ia, T, K, F, act):
                sum_slack=(K + 1) * 2.0 ** -23 * mags)
 
 
+@pytest.mark.parametrize("T,K,F,act", [(161, 4104, 300, "none"), (400, 1032, 1030, "relu"), (1000, 520, 264, "swiglu"),
+                                       (5000, 1600, 700, "none")])
+def test_linear_fp32_output_in_parts(ia, T, K, F, act):
+    """fp32 outputs over several parts of K and several items a pair: exact on grid inputs."""
+    x, w, bias, residual = _linear_inputs(T, K, F, act, seed=K)
+    v = x.double() @ w.double().t() + bias.double()
+    _check(_run_linear(ia, x, w, bias, None if act == "relu" else residual, act, F32, F), v, act,
+           None if act == "relu" else residual.double())
+
+
+def test_linear_fp32_output_is_summed_to_nearest(ia):
+    """K = 8192 in fp32: the parts' sums keep the error of the whole output below 1e-6 of its norm
+    (64 steps to nearest over each part's 32, of random sign, measure 5e-7; one long accumulation in
+    the tensor cores measured 8e-6)."""
+    x, w, _, _ = _linear_inputs(64, 8192, 512, "none", seed=4, grid=False)
+    got = _run_linear(ia, x, w, None, None, "none", F32, 512).cpu().double()
+    want = x.double() @ w.double().t()
+    assert float((got - want).norm() / want.norm()) < 1e-6
+
+
 def test_linear_in_place_residual_and_infinities(ia):
     """out == residual; infinities and NaN stay in their own token's row."""
     T, K, F = 40, 128, 264
