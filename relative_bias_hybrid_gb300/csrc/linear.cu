@@ -56,6 +56,7 @@
 #include <atomic>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "conv4.cuh"
@@ -68,7 +69,8 @@ namespace inkattn {
 namespace {
 
 constexpr int kRowsA = 128;                       // weight rows of a CTA
-constexpr int kMaxN = 256;                        // tokens of an item
+constexpr int kMaxN = 256;                        // tokens of an MMA, and of an item
+constexpr int kWideN = 384;                       // tokens of the one item of a split's cluster
 constexpr int kKStep = 64;                        // K per ring stage (one 128-byte row)
 constexpr int kABytes = kRowsA * 128;             // 16 KB
 constexpr int kRingBytes = 192 * 1024;
@@ -101,12 +103,24 @@ enum Bar {
     B_COUNT = B_DRAIN + 1
 };
 constexpr int kSmem = kOffBar + B_COUNT * 8 + 16;
+static_assert(kWideN / 32 <= sizeof(LinearMaps::x) / sizeof(CUtensorMap), "a map for each box height");
 static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
-static_assert(kMaxN * kRowsA * 4 <= kRingBytes, "a split's partial tile lies in the ring");
+static_assert(kWideN * kRowsA * 4 <= kRingBytes, "a split's partial tile lies in the ring");
 
 struct Item {
     int e, row0, nt, n, fb;      // expert, first row, rows, MMA N (rows rounded up to 32), feature block
 };
+
+// An item of more than 256 tokens (a split's) takes two MMAs a step: the first over `first_n`
+// columns, the second over the others.  Each MMA's columns are half the even CTA's token rows and
+// half the odd one's, so the columns are not in token order: the token of column c.
+__device__ __forceinline__ int first_n(int n) { return n <= kMaxN ? n : ((n >> 1) + 31) & ~31; }
+__device__ __forceinline__ int token_of(int c, int n) {
+    const int a = first_n(n) >> 1, hn = n >> 1, b = hn - a;    // rows of a CTA in the first, in all, in the second
+    if (c < 2 * a) return c < a ? c : hn + c - a;
+    c -= 2 * a;
+    return c < b ? a + c : hn + a + c - b;
+}
 
 template <int kAct>
 __device__ __forceinline__ float activate(float v) {
@@ -432,8 +446,32 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         RingPos at;
         bool ok = true, ready = false;
         int i = 0;
+        // K steps k0 .. k1 into accumulator buf; kWide: two MMAs a step
+        auto steps = [&](auto wide, int n, int buf, int k0, int k1) {
+            constexpr bool kWide = decltype(wide)::value;
+            const int n1 = kWide ? first_n(n) : n;
+            const uint32_t id = tc::idesc(2 * kRowsA, n1, tc::kFmtBF16, 0, 0);
+            const uint32_t id2 = tc::idesc(2 * kRowsA, n - n1, tc::kFmtBF16, 0, 0);
+            for (int k = k0; k < k1; ++k) {
+                if (!ready && !pwait(bar(B_FULL + at.s), at.lap & 1)) return false;
+                const RingPos now = at;
+                at.next(A.stages);
+                ready = left > 1 && mbar_test_wait(bar(B_FULL + at.s), at.lap & 1);   // seen while the MMAs are issued
+                tc::fence_after();
+                const uint64_t off = (uint64_t)(now.s * (A.stage_bytes >> 4));
+                if (kWide)
+                    tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)n1, da0 + off, db0 + off + (uint64_t)(n1 / 2 * 8), id2,
+                                                    k > k0 ? 1u : 0u, 0, 0, 0, 0, pair);
+                tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)(buf * kAccCols), da0 + off, db0 + off, id,
+                                                k > k0 ? 1u : 0u, bar(B_EMPTY + now.s), left > A.stages ? 1u : 0u,
+                                                bar(B_ACC_FULL + buf), k == k1 - 1 ? 1u : 0u, pair);
+                --left;
+                ready = __all_sync(0xffffffffu, ready);
+            }
+            return true;
+        };
         for (int w = cid; w < n_items && ok; w += nclusters) {
-            const uint32_t id = tc::idesc(2 * kRowsA, item(w).n, tc::kFmtBF16, 0, 0);
+            const int n = item(w).n;
             for (int k0 = k_lo; k0 < k_hi && ok; k0 += part, ++i) {
                 const int buf = i & 1, k1 = min(k_hi, k0 + part);
                 // both CTAs' epilogues are done with this accumulator
@@ -443,22 +481,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                     break;
                 }
                 tc::fence_after();
-                for (int k = k0; k < k1; ++k) {
-                    if (!ready && !pwait(bar(B_FULL + at.s), at.lap & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    const RingPos now = at;
-                    at.next(A.stages);
-                    ready = left > 1 && mbar_test_wait(bar(B_FULL + at.s), at.lap & 1);   // seen while the MMAs are issued
-                    tc::fence_after();
-                    const uint64_t off = (uint64_t)(now.s * (A.stage_bytes >> 4));
-                    tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)(buf * kAccCols), da0 + off, db0 + off, id,
-                                                    k > k0 ? 1u : 0u, bar(B_EMPTY + now.s), left > A.stages ? 1u : 0u,
-                                                    bar(B_ACC_FULL + buf), k == k1 - 1 ? 1u : 0u, pair);
-                    --left;
-                    ready = __all_sync(0xffffffffu, ready);
-                }
+                ok = !kFine && n > kMaxN ? steps(std::true_type{}, n, buf, k0, k1) : steps(std::false_type{}, n, buf, k0, k1);
             }
         }
         // every MMA of the pair has completed before TMEM is released
@@ -640,14 +663,14 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         if (epi) {
             const int quarter = warp & 3;
             const uint32_t place = s_base + (uint32_t)((split * share * kRowsA + quarter * 32 + lane) * 4);
-            for (int c = (warp - kWarpEpi) >> 2; c * 32 < it.nt; c += 2) {
+            for (int c = (warp - kWarpEpi) >> 2; c * 32 < it.n; c += 2) {
                 uint32_t v[32];
                 tc::ld32((parts > 1 ? t_sums : tmem) + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(c * 32), v);
                 tc::wait_ld();
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const int t = c * 32 + g * 8, owner = t / share;
-                    if (t >= it.nt) break;
+                    const int t = token_of(c * 32 + g * 8, it.n), owner = t / share;
+                    if (t >= it.nt) continue;
                     const uint32_t dst = mapa_shared(place, (uint32_t)(2 * owner + half)) +
                                          (uint32_t)((t - owner * share) * kRowsA * 4);
 #pragma unroll
@@ -818,19 +841,21 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     double best = 0.0;
     long long most_items = 0;
     a.tile_n = 0;
-    for (int tile = most_n; tile >= 32; tile -= 32) {
+    // (a tile above 256 tokens: a split's single item of a linear layer)
+    for (int tile = !a.offsets && !a.out_f32 ? kWideN : most_n; tile >= 32; tile -= 32) {
         const long long each = (rows + tile - 1) / tile;                   // tiles of an owner
         const int n = (int)((rows + each - 1) / each + 31) / 32 * 32;
+        if (n > kMaxN && each > 1) continue;
         // items there can be: with experts, full tiles and one more for each that has rows
         const long long bound = (a.offsets ? a.M / tile + owners : each) * a.n_fblocks;
         if (bound > INT_MAX / 2) continue;
-        for (int s = 1; s <= kMaxSplits; s *= 2) {
+        for (int s = n > kMaxN ? 2 : 1; s <= kMaxSplits; s *= 2) {
             if (s > 1 && (nk < 2 * s || bound > resident_clusters(2 * s, num_sms))) break;
             const double us = launch_us(owners * each * a.n_fblocks, n, nk, s, resident_clusters(2, num_sms), weight_bytes);
             if (a.tile_n == 0 || us < best) {
                 best = us;
                 most_items = bound;
-                a.tile_n = tile;
+                a.tile_n = a.offsets ? tile : n;       // (no larger than the tiles are: the ring gets more stages)
                 a.splits = s;
             }
         }

@@ -171,6 +171,16 @@ def test_linear_fp32_output_in_parts(ia, T, K, F, act):
            None if act == "relu" else residual.double())
 
 
+@pytest.mark.parametrize("T,K,F,act", [(257, 8200, 5000, "none"), (300, 8192, 3000, "relu"), (384, 8192, 5001, "none"),
+                                       (350, 9000, 2500, "swiglu"), (384, 9000, 1900, "swiglu")])
+def test_linear_one_wide_tile_with_k_split(ia, T, K, F, act):
+    """Between 257 and 384 tokens over a long K: one tile, two MMAs a step, the K range split."""
+    x, w, bias, residual = _linear_inputs(T, K, F, act, seed=F)
+    v = x.double() @ w.double().t() + bias.double()
+    _check(_run_linear(ia, x, w, bias, None if act == "relu" else residual, act, BF16, F), v, act,
+           None if act == "relu" else residual.double())
+
+
 def test_linear_fp32_output_is_summed_to_nearest(ia):
     """K = 8192 in fp32: the parts' sums keep the error of the whole output below 1e-6 of its norm
     (64 steps to nearest over each part's 32, of random sign, measure 5e-7; one long accumulation in
