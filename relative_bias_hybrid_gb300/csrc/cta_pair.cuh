@@ -78,6 +78,15 @@ __device__ __forceinline__ void mbar_remote_arrive(uint32_t bar, uint32_t cta_ra
                  :: "r"(bar), "r"(cta_rank) : "memory");
 }
 
+// As mbar_remote_arrive, with release at CTA scope: for a barrier that stands for tensor memory
+// alone, whose accesses the tcgen05 fences order (release at cluster scope also waits for the
+// thread's stores to global memory, some 800 cycles in an epilogue).
+__device__ __forceinline__ void mbar_pair_arrive(uint32_t bar, uint32_t cta_rank) {
+    asm volatile("{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %0, %1;\n\t"
+                 "mbarrier.arrive.release.cta.shared::cluster.b64 _, [ra];\n\t}"
+                 :: "r"(bar), "r"(cta_rank) : "memory");
+}
+
 // As tma_load_2d, for a CTA pair: the box lands in this CTA's shared memory and its bytes
 // complete on the mbarrier `bar_pair` of the even CTA of the pair (a shared::cluster
 // address, from mapa), which counts the copies of both CTAs.

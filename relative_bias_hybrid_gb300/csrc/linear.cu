@@ -92,7 +92,8 @@ constexpr int kNoteBytes = 16;                    // the odd CTA's note that a g
 constexpr int kOffNote = kOffStg + 8 * kStgBytes; // where it lands, and behind it what is sent
 constexpr int kOffTiles = kOffNote + 2 * kNoteBytes;                   // int tile prefix [E + 1]
 constexpr int kOffStart = kOffTiles + (INKATTN_MAX_EXPERTS + 1) * 4;   // int first row [E + 1]
-constexpr int kOffBar = (kOffStart + (INKATTN_MAX_EXPERTS + 1) * 4 + 7) / 8 * 8;
+constexpr int kOffPer = kOffStart + (INKATTN_MAX_EXPERTS + 1) * 4;     // int rows of a tile [E]
+constexpr int kOffBar = (kOffPer + INKATTN_MAX_EXPERTS * 4 + 7) / 8 * 8;
 enum Bar {
     B_FULL = 0,
     B_EMPTY = B_FULL + kMaxStages,
@@ -207,6 +208,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     auto bar = [&](int i) { return s_base + kOffBar + 8u * (uint32_t)i; };
     int *s_tiles = reinterpret_cast<int *>(smem + kOffTiles);
     int *s_start = reinterpret_cast<int *>(smem + kOffStart);
+    int *s_per = reinterpret_cast<int *>(smem + kOffPer);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffBar + B_COUNT * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffBar + B_COUNT * 8 + 4);
     // a stage of the ring: completed by copies or by a commit, which carry their own ordering
@@ -268,6 +270,8 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             if (e < A.E) {
                 if (valid) tiles = (end - start + A.tile_n - 1) / A.tile_n;
                 else set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+                // tiles of near-equal size, a multiple of 32 rows
+                s_per[e] = tiles > 0 ? ((end - start + tiles - 1) / tiles + 31) & ~31 : 0;
             }
             int v = tiles;
 #pragma unroll
@@ -294,26 +298,27 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     constexpr int kAccCols = kFine ? kFineN : kMaxN;           // TMEM columns of an accumulator
     const uint32_t t_sums = tmem + 2 * kFineN;                 // kFine: the sums of the parts so far
     auto item = [&](int w) {
+        // (integer divisions are some hundred cycles together: as few as there can be)
         Item it;
-        const int t = w / A.n_fblocks;
         int lo = 0, hi = A.E;                          // s_tiles[lo] <= t < s_tiles[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_tiles[mid] <= t) lo = mid;
-            else hi = mid;
+        if (hi > 1) {
+            const int t = w / A.n_fblocks;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_tiles[mid] <= t) lo = mid;
+                else hi = mid;
+            }
         }
         it.e = lo;
         // the expert's items: groups of kRaster feature blocks, inside a group the token tiles
         // one after another, so that the group's weights stay in L2 while they stream past
         const int mt = s_tiles[lo + 1] - s_tiles[lo];
         const int rem = w - s_tiles[lo] * A.n_fblocks;
-        const int grp = rem / (kRaster * mt), in = rem - grp * kRaster * mt;
+        const int grp = mt == 1 ? rem / kRaster : rem / (kRaster * mt), in = rem - grp * kRaster * mt;
         const int gsz = min(kRaster, A.n_fblocks - grp * kRaster);
-        const int m = in / gsz;
+        const int m = mt == 1 ? 0 : gsz == kRaster ? in / kRaster : in / gsz;
         it.fb = grp * kRaster + (in - m * gsz);
-        // tiles of near-equal size, a multiple of 32 rows
-        const int rows = s_start[lo + 1] - s_start[lo];
-        const int per = ((rows + mt - 1) / mt + 31) & ~31;
+        const int rows = s_start[lo + 1] - s_start[lo], per = s_per[lo];
         it.row0 = s_start[lo] + m * per;
         it.nt = min(per, rows - m * per);
         it.n = (it.nt + 31) & ~31;
@@ -475,8 +480,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             for (int k0 = k_lo; k0 < k_hi && ok; k0 += part, ++i) {
                 const int buf = i & 1, k1 = min(k_hi, k0 + part);
                 // both CTAs' epilogues are done with this accumulator
-                if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait_cluster(bar(B_ACC_EMPTY + buf), ((i >> 1) - 1) & 1,
-                                                                         A.dev_status, abort_flag, A.wait_ns))) {
+                if (i >= 2 && !pwait(bar(B_ACC_EMPTY + buf), ((i >> 1) - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -508,7 +512,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         bool ok = true;
         // the accumulator of accumulation i is complete / may be written again
         auto acc_full = [&] {
-            bool r = mbar_wait_short<1000>(bar(B_ACC_FULL + (i & 1)), (uint32_t)((i >> 1) & 1), A.dev_status, abort_flag,
+            bool r = mbar_wait_short<200>(bar(B_ACC_FULL + (i & 1)), (uint32_t)((i >> 1) & 1), A.dev_status, abort_flag,
                                            A.wait_ns);
             if (kGated) r = named_all(swap_bar, 64, r);       // the two warps go on together
             ok = __all_sync(0xffffffffu, r);
@@ -519,7 +523,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             if (i + 2 >= accs || (A.withhold && i == 0 && half == 1 && warp == kWarpEpi)) return;
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) mbar_remote_arrive(bar(B_ACC_EMPTY + (i & 1)), even);   // its MMA warp waits
+            if (lane == 0) mbar_pair_arrive(bar(B_ACC_EMPTY + (i & 1)), even);   // its MMA warp waits
         };
         for (int w = cid; w < n_items; w += nclusters) {
             const Item it = item(w);
