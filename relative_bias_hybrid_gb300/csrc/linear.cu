@@ -507,6 +507,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         float *out32 = static_cast<float *>(A.out);
         // 16-byte pieces of a row start on 16-byte boundaries
         const bool vec = kFine ? (A.F & 3) == 0 && (A.residual == nullptr || (A.F & 7) == 0) : (A.F & 7) == 0;
+        const bool paired = !kFine && vec && A.residual == nullptr;
         const int accs = my_items * parts;                    // accumulations in all
         int i = 0;
         bool ok = true;
@@ -569,6 +570,34 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                         }
                     }
                     const uint32_t live = __ballot_sync(0xffffffffu, mine);
+                    // 2 kPairs finished tokens from t0 on, as bf16 pairs of tokens of the lane's feature, to out:
+                    // half the shared-memory traffic of fp32 values
+                    auto store_pairs = [&](auto pairs, const uint32_t *u, int t0) {
+                        constexpr int kPairs = decltype(pairs)::value;
+                        uint32_t *words = reinterpret_cast<uint32_t *>(stg);
+                        inkattn_bf16 *to = out16 + (size_t)(it.row0 + c * 32 + t0) * F;
+                        const uint32_t live_t = live >> t0;
+                        __syncwarp();
+#pragma unroll
+                        for (int p = 0; p < kPairs; ++p) words[p * kStgPitch + lane] = u[p];
+                        __syncwarp();
+#pragma unroll
+                        for (int q = 0; q < kPairs / 8; ++q) {
+                            const int p = q * 8 + (lane >> 2), f = f0 + (lane & 3) * 8;
+                            const uint4 a = *reinterpret_cast<const uint4 *>(words + p * kStgPitch + (lane & 3) * 8);
+                            const uint4 b = *reinterpret_cast<const uint4 *>(words + p * kStgPitch + (lane & 3) * 8 + 4);
+                            if (f >= A.F) continue;
+                            inkattn_bf16 *row = to + (size_t)(2 * p) * F + f;
+                            if ((live_t >> (2 * p)) & 1u)
+                                *reinterpret_cast<uint4 *>(row) =
+                                    make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                               __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
+                            if ((live_t >> (2 * p + 1)) & 1u)
+                                *reinterpret_cast<uint4 *>(row + F) =
+                                    make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                               __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
+                        }
+                    };
                     // 16 finished tokens t0 .. t0 + 15 of the block, the lane's feature of each, to out
                     auto store16 = [&](const float (&y)[16], int t0) {
                         const size_t row_b = (size_t)(it.row0 + c * 32 + t0);
@@ -642,7 +671,21 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                             y[j] = activate<INKATTN_ACT_SILU>(gate) * up;
                         }
                         named_sync(swap_bar, 64);                 // both have read
-                        store16(y, keep);
+                        if (paired) {
+                            uint32_t u[8];
+#pragma unroll
+                            for (int p = 0; p < 8; ++p) u[p] = pack_bf16(y[2 * p], y[2 * p + 1]);
+                            store_pairs(std::integral_constant<int, 8>{}, u, keep);
+                        } else {
+                            store16(y, keep);
+                        }
+                    } else if (paired) {
+                        uint32_t u[16];
+#pragma unroll
+                        for (int p = 0; p < 16; ++p)
+                            u[p] = pack_bf16(activate<kAct>(__uint_as_float(v[2 * p]) + bias),
+                                             activate<kAct>(__uint_as_float(v[2 * p + 1]) + bias));
+                        store_pairs(std::integral_constant<int, 16>{}, u, 0);
                     } else {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
