@@ -102,7 +102,7 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
 // 128 rows) or, gated, as [E][gate, up][F][K] (box 64 x 64 gate and the 64 up rows); 128-byte
 // swizzle.
 struct LinearMaps {
-    CUtensorMap w, x[12];
+    CUtensorMap w, x[8];
 };
 bool make_linear_maps(const LinearArgs &a, bool gated, LinearMaps *maps);
 

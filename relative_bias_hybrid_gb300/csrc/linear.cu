@@ -69,8 +69,7 @@ namespace inkattn {
 namespace {
 
 constexpr int kRowsA = 128;                       // weight rows of a CTA
-constexpr int kMaxN = 256;                        // tokens of an MMA, and of an item
-constexpr int kWideN = 384;                       // tokens of the one item of a split's cluster
+constexpr int kMaxN = 256;                        // tokens of an item
 constexpr int kKStep = 64;                        // K per ring stage (one 128-byte row)
 constexpr int kABytes = kRowsA * 128;             // 16 KB
 constexpr int kRingBytes = 192 * 1024;
@@ -104,24 +103,13 @@ enum Bar {
     B_COUNT = B_DRAIN + 1
 };
 constexpr int kSmem = kOffBar + B_COUNT * 8 + 16;
-static_assert(kWideN / 32 <= sizeof(LinearMaps::x) / sizeof(CUtensorMap), "a map for each box height");
+static_assert(kMaxN / 32 <= sizeof(LinearMaps::x) / sizeof(CUtensorMap), "a map for each box height");
 static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KB a CTA may use");
-static_assert(kWideN * kRowsA * 4 <= kRingBytes, "a split's partial tile lies in the ring");
+static_assert(kMaxN * kRowsA * 4 <= kRingBytes, "a split's partial tile lies in the ring");
 
 struct Item {
     int e, row0, nt, n, fb;      // expert, first row, rows, MMA N (rows rounded up to 32), feature block
 };
-
-// An item of more than 256 tokens (a split's) takes two MMAs a step: the first over `first_n`
-// columns, the second over the others.  Each MMA's columns are half the even CTA's token rows and
-// half the odd one's, so the columns are not in token order: the token of column c.
-__device__ __forceinline__ int first_n(int n) { return n <= kMaxN ? n : ((n >> 1) + 31) & ~31; }
-__device__ __forceinline__ int token_of(int c, int n) {
-    const int a = first_n(n) >> 1, hn = n >> 1, b = hn - a;    // rows of a CTA in the first, in all, in the second
-    if (c < 2 * a) return c < a ? c : hn + c - a;
-    c -= 2 * a;
-    return c < b ? a + c : hn + a + c - b;
-}
 
 template <int kAct>
 __device__ __forceinline__ float activate(float v) {
@@ -451,32 +439,8 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         RingPos at;
         bool ok = true, ready = false;
         int i = 0;
-        // K steps k0 .. k1 into accumulator buf; kWide: two MMAs a step
-        auto steps = [&](auto wide, int n, int buf, int k0, int k1) {
-            constexpr bool kWide = decltype(wide)::value;
-            const int n1 = kWide ? first_n(n) : n;
-            const uint32_t id = tc::idesc(2 * kRowsA, n1, tc::kFmtBF16, 0, 0);
-            const uint32_t id2 = tc::idesc(2 * kRowsA, n - n1, tc::kFmtBF16, 0, 0);
-            for (int k = k0; k < k1; ++k) {
-                if (!ready && !pwait(bar(B_FULL + at.s), at.lap & 1)) return false;
-                const RingPos now = at;
-                at.next(A.stages);
-                ready = left > 1 && mbar_test_wait(bar(B_FULL + at.s), at.lap & 1);   // seen while the MMAs are issued
-                tc::fence_after();
-                const uint64_t off = (uint64_t)(now.s * (A.stage_bytes >> 4));
-                if (kWide)
-                    tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)n1, da0 + off, db0 + off + (uint64_t)(n1 / 2 * 8), id2,
-                                                    k > k0 ? 1u : 0u, 0, 0, 0, 0, pair);
-                tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)(buf * kAccCols), da0 + off, db0 + off, id,
-                                                k > k0 ? 1u : 0u, bar(B_EMPTY + now.s), left > A.stages ? 1u : 0u,
-                                                bar(B_ACC_FULL + buf), k == k1 - 1 ? 1u : 0u, pair);
-                --left;
-                ready = __all_sync(0xffffffffu, ready);
-            }
-            return true;
-        };
         for (int w = cid; w < n_items && ok; w += nclusters) {
-            const int n = item(w).n;
+            const uint32_t id = tc::idesc(2 * kRowsA, item(w).n, tc::kFmtBF16, 0, 0);
             for (int k0 = k_lo; k0 < k_hi && ok; k0 += part, ++i) {
                 const int buf = i & 1, k1 = min(k_hi, k0 + part);
                 // both CTAs' epilogues are done with this accumulator
@@ -485,7 +449,22 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                     break;
                 }
                 tc::fence_after();
-                ok = !kFine && n > kMaxN ? steps(std::true_type{}, n, buf, k0, k1) : steps(std::false_type{}, n, buf, k0, k1);
+                for (int k = k0; k < k1; ++k) {
+                    if (!ready && !pwait(bar(B_FULL + at.s), at.lap & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const RingPos now = at;
+                    at.next(A.stages);
+                    ready = left > 1 && mbar_test_wait(bar(B_FULL + at.s), at.lap & 1);   // seen while the MMAs are issued
+                    tc::fence_after();
+                    const uint64_t off = (uint64_t)(now.s * (A.stage_bytes >> 4));
+                    tc::mma_pair_bf16_ss_k64_commit(tmem + (uint32_t)(buf * kAccCols), da0 + off, db0 + off, id,
+                                                    k > k0 ? 1u : 0u, bar(B_EMPTY + now.s), left > A.stages ? 1u : 0u,
+                                                    bar(B_ACC_FULL + buf), k == k1 - 1 ? 1u : 0u, pair);
+                    --left;
+                    ready = __all_sync(0xffffffffu, ready);
+                }
             }
         }
         // every MMA of the pair has completed before TMEM is released
@@ -710,14 +689,14 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         if (epi) {
             const int quarter = warp & 3;
             const uint32_t place = s_base + (uint32_t)((split * share * kRowsA + quarter * 32 + lane) * 4);
-            for (int c = (warp - kWarpEpi) >> 2; c * 32 < it.n; c += 2) {
+            for (int c = (warp - kWarpEpi) >> 2; c * 32 < it.nt; c += 2) {
                 uint32_t v[32];
                 tc::ld32((parts > 1 ? t_sums : tmem) + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(c * 32), v);
                 tc::wait_ld();
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const int t = token_of(c * 32 + g * 8, it.n), owner = t / share;
-                    if (t >= it.nt) continue;
+                    const int t = c * 32 + g * 8, owner = t / share;
+                    if (t >= it.nt) break;
                     const uint32_t dst = mapa_shared(place, (uint32_t)(2 * owner + half)) +
                                          (uint32_t)((t - owner * share) * kRowsA * 4);
 #pragma unroll
@@ -848,20 +827,22 @@ int resident_clusters(int ctas, int num_sms) {
 }
 
 // What a launch would take, in microseconds: the model that picks the token tile and the
-// split.  Its constants are fits to measured times of the kernel (GB300, 76 pairs), 16 shapes
-// between 1 x 1024 x 1024 and 512 x 8192 x 8192 with every tile and split; it came within 15%
-// of all but the smallest and picked a shape within 4% of the best of each.
-//   stage   a K = 64 step of a tile of n tokens: 0.215 below n = 128 (the loop of the MMA warp),
-//           above that the copies from L2
-//   finish  an item's epilogue, which overlaps the next item's products
+// split.  Its constants are fits to measured times of the kernel (GB300, 76 pairs): 19 shapes
+// between 1 x 1024 x 1024 and 512 x 8192 x 8192, each with every tile and split.
+//   stage   a K = 64 step of a tile of n tokens: the loop of the MMA warp (0.16), the bytes into an
+//           SM, which come faster to few of them, or the MMAs
+//   finish  an item's epilogue, which overlaps the next item's products; more where rows do not
+//           start on 16-byte boundaries and features leave one by one
 //   join    of a split instead: the partial tiles through distributed shared memory
-//   and the weights come from HBM at 7 TB/s at best
-double launch_us(long long items, int n, int stages, int splits, int pairs, double weight_bytes) {
-    const double stage = fmax(0.215, 0.185 + 0.00031 * n), finish = 1.35 + 0.0107 * n, join = 1.45 + 0.0265 * n;
-    const double item = stages * stage / splits, hbm = weight_bytes / 7.0e6;
-    if (splits > 1) return 1.7 + fmax(item, hbm) + join;
+//   and the weights come from HBM at 7 TB/s at best, 88 GB/s for each SM that asks
+double launch_us(long long items, int n, int stages, int splits, int pairs, double weight_bytes, bool vec) {
+    const double busy = fmin((double)(items * splits), (double)pairs);
+    const double stage = fmax(fmax(0.16, (16.4 + 0.0655 * n) / (busy <= 40 ? 150.0 : 118.0)), 0.00104 * n);
+    const double finish = 0.6 + (vec ? 0.0071 : 0.03) * n, join = 1.2 + 0.024 * n, start = 1.4 + 0.015 * busy;
+    const double item = stages * stage / splits, hbm = weight_bytes / fmin(7.0e6, 0.176e6 * busy);
+    if (splits > 1) return start + fmax(item, hbm) + join;
     const double waves = (double)((items + pairs - 1) / pairs);
-    return 1.7 + fmax(waves * fmax(item, finish), hbm) + fmin(item, finish);
+    return start + fmax(waves * fmax(item, finish), hbm) + fmin(item, finish);
 }
 
 }  // namespace
@@ -888,17 +869,16 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     double best = 0.0;
     long long most_items = 0;
     a.tile_n = 0;
-    // (a tile above 256 tokens: a split's single item of a linear layer)
-    for (int tile = !a.offsets && !a.out_f32 ? kWideN : most_n; tile >= 32; tile -= 32) {
+    for (int tile = most_n; tile >= 32; tile -= 32) {
         const long long each = (rows + tile - 1) / tile;                   // tiles of an owner
         const int n = (int)((rows + each - 1) / each + 31) / 32 * 32;
-        if (n > kMaxN && each > 1) continue;
         // items there can be: with experts, full tiles and one more for each that has rows
         const long long bound = (a.offsets ? a.M / tile + owners : each) * a.n_fblocks;
         if (bound > INT_MAX / 2) continue;
-        for (int s = n > kMaxN ? 2 : 1; s <= kMaxSplits; s *= 2) {
+        for (int s = 1; s <= kMaxSplits; s *= 2) {
             if (s > 1 && (nk < 2 * s || bound > resident_clusters(2 * s, num_sms))) break;
-            const double us = launch_us(owners * each * a.n_fblocks, n, nk, s, resident_clusters(2, num_sms), weight_bytes);
+            const double us = launch_us(owners * each * a.n_fblocks, n, nk, s, resident_clusters(2, num_sms), weight_bytes,
+                                        a.F % 8 == 0);
             if (a.tile_n == 0 || us < best) {
                 best = us;
                 most_items = bound;

@@ -173,8 +173,8 @@ def test_linear_fp32_output_in_parts(ia, T, K, F, act):
 
 @pytest.mark.parametrize("T,K,F,act", [(257, 8200, 5000, "none"), (300, 8192, 3000, "relu"), (384, 8192, 5001, "none"),
                                        (350, 9000, 2500, "swiglu"), (384, 9000, 1900, "swiglu")])
-def test_linear_one_wide_tile_with_k_split(ia, T, K, F, act):
-    """Between 257 and 384 tokens over a long K: one tile, two MMAs a step, the K range split."""
+def test_linear_between_one_and_two_full_tiles(ia, T, K, F, act):
+    """Between 257 and 384 tokens over a long K: few tiles, split or not."""
     x, w, bias, residual = _linear_inputs(T, K, F, act, seed=F)
     v = x.double() @ w.double().t() + bias.double()
     _check(_run_linear(ia, x, w, bias, None if act == "relu" else residual, act, BF16, F), v, act,
