@@ -139,6 +139,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool l
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                  :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(live ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<uint64_t>(p)));
+}
 // arrives on the mbarrier once this thread's earlier cp.async have landed
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
@@ -516,6 +519,15 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                 bias = __ldg(A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + (kGated && quarter >= 2 ? F : 0) + frow);
             const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
             const int nblocks = (it.nt + 31) >> 5;
+            if (A.residual && f0 < A.F) {
+                // the residual rows on their way into L2 while the products run
+                for (int c = e8; c < nblocks; c += 2)
+                    if (c * 32 + lane < it.nt) {
+                        const inkattn_bf16 *from = A.residual + (size_t)(it.row0 + c * 32 + lane) * F + f0;
+                        prefetch_l2(from);
+                        prefetch_l2(from + min(31, A.F - 1 - f0));
+                    }
+            }
             for (int q = 0; q < parts; ++q, ++i) {
                 if (!acc_full()) break;
                 if (A.splits > 1 && parts == 1) break;        // (the tile is finished below, from this accumulator)
@@ -538,6 +550,18 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                         tc::st32(t_sums + (uint32_t)(c * 32) + lanes, v);
                         tc::wait_st();
                         continue;
+                    }
+                    // the block's residual values, all requested before the first is used
+                    uint4 resid[kFine ? 1 : 4];
+                    if (!kFine && vec && A.residual) {
+#pragma unroll
+                        for (int q4 = 0; q4 < (kGated ? 2 : 4); ++q4) {
+                            const int t = c * 32 + (kGated ? (quarter < 2 ? 0 : 16) : 0) + q4 * 8 + (lane >> 2);
+                            const int f = f0 + (lane & 3) * 8;
+                            resid[kFine ? 0 : q4] = make_uint4(0, 0, 0, 0);
+                            if (t < it.nt && f < A.F)
+                                resid[kFine ? 0 : q4] = *reinterpret_cast<const uint4 *>(A.residual + (size_t)(it.row0 + t) * F + f);
+                        }
                     }
                     // tokens of this block that are stored
                     bool mine = c * 32 + lane < it.nt;
@@ -609,7 +633,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                                     const size_t o = (row_b + t) * F + f;
                                     if (A.residual) {
                                         float r[8];
-                                        unpack8(*reinterpret_cast<const uint4 *>(A.residual + o), r);
+                                        unpack8(resid[kFine ? 0 : (kGated ? 0 : t0 >> 3) + q], r);
 #pragma unroll
                                         for (int j = 0; j < 8; ++j) z[j] += r[j];
                                     }
