@@ -16,6 +16,9 @@
 // block adds up the counts that k_route_choose left per chunk) + bits before its own.  A batch
 // that is one chunk needs no counts and no workspace.  (Ranks by match.any and a histogram for
 // each warp took 1.6 times as long for one chunk: two passes over the pairs, 32 counts an expert.)
+//
+// Measured, 6 of 256 + 2: 32768 tokens 27 us (the choice about 19, 475 instructions a token at 0.54
+// of the issue rate; 48 warps an SM without the requests ahead took 30), 288 tokens 6.4 us.
 #include "common.cuh"
 #include "conv4.cuh"
 #include "internal.h"
@@ -297,7 +300,8 @@ cudaError_t launch_route(const inkattn_route_params &p, uint32_t *ws, cudaStream
 // ---------------------------------------------------------------- the weighted sum
 // HBM-bound: top_k + n_shared rows read and one written per token.  A thread owns 8 features
 // of one token (a 16-byte piece of every row) and requests up to eight rows before it uses
-// the first; the sum is taken in fp32 in the order of the choices.
+// the first; the sum is taken in fp32 in the order of the choices.  Measured: 8192 tokens x 8
+// rows of 8192 in 182 us, 6.6 TB/s (98% of the copy rate); 288 tokens in 9.2 us.
 
 namespace {
 constexpr int kSumThreads = 128;
