@@ -445,7 +445,8 @@ INKATTN_API inkattn_status inkattn_qkvr_prologue(const inkattn_qkvr_params *p, v
  * The two products accumulate in fp32 on the tensor cores, apply bias and activation to the
  * fp32 sums, and round once to the output type.  With v = x w^T + bias:
  *   NONE v   RELU max(v, 0)   GELU v (1 + erf(v / sqrt 2)) / 2   SILU v / (1 + exp(-v))
- *   (erf within 1.5e-7; a NaN stays a NaN)
+ *   (erf within 1.5e-7; a NaN stays a NaN; an infinite v as in the formula, so that GELU and
+ *   SILU of -infinity are NaN)
  *   SWIGLU   w (and bias) hold 2 F rows, F gate rows first, then F up rows:
  *            SILU(gate) * up, F values.
  * Results do not depend on the GPU's scheduling: every sum is added in a fixed order.

@@ -130,7 +130,8 @@ __device__ __forceinline__ float activate(float v) {
         const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
                                  0.254829592f);
         const float half_erfc = 0.5f * p * __expf(-x * x);
-        return v > 0.f ? fmaf(-v, half_erfc, v) : v * half_erfc;
+        // (half_erfc is 0 from v = 15 on; the bound keeps infinity from being multiplied by it)
+        return v > 0.f ? fmaf(-fminf(v, 15.f), half_erfc, v) : v * half_erfc;
     }
     if (kAct == INKATTN_ACT_SILU) return __fdividef(v, 1.f + __expf(-v));
     return v;

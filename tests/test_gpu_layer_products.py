@@ -223,6 +223,31 @@ def test_linear_activations_of_wide_arguments(ia, act):
         assert bool(torch.isnan(got[1]).all())         # NaN times a zero weight is a NaN everywhere
 
 
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu", "swiglu"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,K,F", [(3, 64, 24), (3, 1024, 24), (200, 64, 24), (200, 64, 27)])
+def test_linear_infinite_sums(ia, act, dtype, T, K, F):
+    """A sum of +infinity or -infinity takes the formula's value (infinity, 0 or NaN), through the
+    split's join and both kinds of stores alike; the features beside it keep theirs."""
+    inf = float("inf")
+    rows = F * (2 if act == "swiglu" else 1)
+    x, w = torch.ones((T, K), dtype=BF16), torch.zeros((rows, K), dtype=BF16)
+    bias = torch.ones(rows, dtype=F32)
+    bias[:6] = torch.tensor([inf, -inf, float("nan"), 3.0e38, -3.0e38, 0.0])
+    if act == "swiglu":
+        bias[F + 6:F + 8] = torch.tensor([inf, -inf])
+    got = _run_linear(ia, x, w, bias, None, act, dtype, F).cpu()
+    want = _act64(bias.double().expand(T, rows), act)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.isinf(got), torch.isinf(want.to(dtype)))
+    assert torch.equal(got[torch.isinf(got)].double(), want.to(dtype)[torch.isinf(got)].double())
+    live = torch.isfinite(want) & torch.isfinite(got.double())
+    # half a step, and the curve: its arguments are 1, 0 or so large that a limit is reached, and at 1
+    # _curve_slack's bounds are 4 (gelu), 5.2 (silu) and 6.2 (swiglu) units of 2^-23, under 8 of the value
+    slack = (HALF_STEP[dtype] + 8 * 2.0 ** -23) * want.abs() + 1e-36
+    assert bool(((got.double() - want).abs() <= slack)[live].all())
+
+
 def test_linear_no_tokens_and_repeatability(ia):
     x, w, bias, residual = [t.cuda() for t in _linear_inputs(64, 4096, 512, "none", seed=9, grid=False)]
     empty = torch.empty((0, 512), dtype=BF16, device="cuda")
