@@ -544,10 +544,11 @@ typedef struct inkattn_route_params {
 /* Bytes of workspace inkattn_route needs: 0 for small batches, or if the params are invalid. */
 INKATTN_API size_t inkattn_route_workspace_bytes(const inkattn_route_params *p);
 
-/* Runs the router.  All arrays 4-byte aligned, in memory of the current device; the outputs overlap neither each other nor the
- * logits.  workspace: device memory, 16-byte aligned, at least inkattn_route_workspace_bytes
- * bytes (nullable when that is 0), need not be cleared; calls whose GPU work overlaps need one
- * each. */
+/* Runs the router.  All arrays 4-byte aligned, in memory of the current device; the outputs
+ * overlap neither each other nor the logits.  workspace: device memory, 16-byte aligned, at
+ * least inkattn_route_workspace_bytes bytes (nullable when that is 0), which overlap none of the
+ * arrays; need not be cleared; calls whose GPU work overlaps need one each (two that share one
+ * give wrong places, within the arrays all the same). */
 INKATTN_API inkattn_status inkattn_route(const inkattn_route_params *p, void *workspace,
                                          size_t workspace_bytes, void *stream);
 

@@ -336,7 +336,7 @@ inkattn_status validate_grouped_linear(const inkattn_grouped_linear_params *p) {
     return INKATTN_OK;
 }
 
-inkattn_status validate_route(const inkattn_route_params *p) {
+inkattn_status validate_route(const inkattn_route_params *p, const void *workspace, size_t workspace_bytes) {
     if (!p || p->struct_size != sizeof(inkattn_route_params) || p->N_tok < 0 || p->E < 1 ||
         p->E > INKATTN_MAX_EXPERTS || p->n_shared < 0 || p->n_shared > INKATTN_MAX_SHARED || p->top_k < 1 ||
         p->top_k > INKATTN_MAX_TOP_K || p->top_k > p->E || !std::isfinite(p->scale))
@@ -350,9 +350,9 @@ inkattn_status validate_route(const inkattn_route_params *p) {
     const size_t T = (size_t)p->N_tok;
     const Range r[] = {{p->logits, T * (p->E + p->n_shared) * 4}, {p->topk_ids, T * p->top_k * 4},
                        {p->weights, T * (p->top_k + p->n_shared) * 4}, {p->expert_offsets, (size_t)(p->E + 1) * 4},
-                       {p->row_token, T * p->top_k * 4}, {p->token_rows, T * p->top_k * 4}};
-    for (int i = 0; i < 6; ++i)
-        for (int j = i + 1; j < 6; ++j)
+                       {p->row_token, T * p->top_k * 4}, {p->token_rows, T * p->top_k * 4}, {workspace, workspace_bytes}};
+    for (int i = 0; i < 7; ++i)
+        for (int j = i + 1; j < 7; ++j)
             if (overlap(r[i], r[j])) return INKATTN_ERR_INVALID_ARG;
     return INKATTN_OK;
 }
@@ -689,17 +689,17 @@ inkattn_status inkattn_grouped_linear(const inkattn_grouped_linear_params *p, vo
 }
 
 size_t inkattn_route_workspace_bytes(const inkattn_route_params *p) {
-    return validate_route(p) == INKATTN_OK ? route_workspace_bytes(*p) : 0;
+    return validate_route(p, nullptr, 0) == INKATTN_OK ? route_workspace_bytes(*p) : 0;
 }
 
 inkattn_status inkattn_route(const inkattn_route_params *p, void *workspace, size_t workspace_bytes, void *stream) {
-    inkattn_status st = validate_route(p);
+    const size_t need = inkattn_route_workspace_bytes(p);
+    inkattn_status st = validate_route(p, need ? workspace : nullptr, need);
     if (st != INKATTN_OK) return st;
-    const size_t need = route_workspace_bytes(*p);
     if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return INKATTN_ERR_INVALID_ARG;
     if ((st = check_device(nullptr)) != INKATTN_OK) return st;
-    const void *read[] = {p->expert_offsets, p->logits};
-    if ((st = validate_on_device(read, p->N_tok > 0 ? 2 : 1)) != INKATTN_OK) return st;
+    const void *read[] = {p->expert_offsets, p->N_tok > 0 ? p->logits : nullptr, workspace};
+    if ((st = validate_on_device(read, need ? 3 : p->N_tok > 0 ? 2 : 1)) != INKATTN_OK) return st;
     return launch_status(launch_route(*p, static_cast<uint32_t *>(workspace), static_cast<cudaStream_t>(stream)));
 }
 

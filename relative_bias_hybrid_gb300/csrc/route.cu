@@ -161,6 +161,7 @@ k_route_place(const inkattn_route_params p, int chunk_tokens, int words, const u
     grid_dep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int E = p.E, k = p.top_k;
+    const uint32_t all = (uint32_t)p.N_tok * (uint32_t)k;
     uint32_t *base = sm, *scratch = sm + E, *bits = scratch + 2 * kPlaceThreads;
     uint16_t *earlier = reinterpret_cast<uint16_t *>(bits + words * E);
     const int t_lo = (int)min((long long)blockIdx.x * chunk_tokens, (long long)p.N_tok);
@@ -245,7 +246,7 @@ k_route_place(const inkattn_route_params p, int chunk_tokens, int words, const u
         for (int q = tid; q < pairs; q += kPlaceThreads) {
             const int t = q / k, e = ids[q], w = t >> 5;
             const uint32_t row = base[e] + earlier[w * E + e] + __popc(bits[w * E + e] & ((1u << (t & 31)) - 1u));
-            p.row_token[row] = t0 + t;
+            if (row < all) p.row_token[row] = t0 + t;  // (always, unless another call wrote the counts)
             p.token_rows[(size_t)t0 * k + q] = (int32_t)row;
         }
         t0 += 32 * words;

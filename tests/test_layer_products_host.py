@@ -126,6 +126,17 @@ def test_route_refusals_and_workspace(ia):
     assert ia.inkattn_route_workspace_bytes(_route(ia, N_tok=288)) == 0
 
 
+def test_route_workspace_overlaps_no_array(ia):
+    p = _route(ia)
+    need = ia.inkattn_route_workspace_bytes(p)
+    for i in range(6):
+        assert ia.lib().inkattn_route(ctypes.byref(p), ctypes.c_void_p(_at(i)), need, None) == ia.INKATTN_ERR_INVALID_ARG
+    assert ia.lib().inkattn_route(ctypes.byref(p), ctypes.c_void_p(_at(4) + 5000 * 6 * 4 - 16), need, None) == \
+        ia.INKATTN_ERR_INVALID_ARG
+    # one beside them passes this check and meets the next, which wants a device
+    assert ia.lib().inkattn_route(ctypes.byref(p), ctypes.c_void_p(_at(9)), need, None) != ia.INKATTN_OK
+
+
 def test_expert_combine_refusals(ia):
     bad = [dict(struct_size=8), dict(N_tok=-1), dict(M=-1), dict(F=0), dict(F=12), dict(F=(1 << 20) + 8),
            dict(top_k=0), dict(top_k=17), dict(n_shared=-1), dict(n_shared=17), dict(y=None), dict(shared=None),
