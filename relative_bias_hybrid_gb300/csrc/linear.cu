@@ -36,8 +36,11 @@
 //               columns), so that an item's epilogue overlaps the next item's MMAs
 //   warps 11-14 only with row indices: the gather; warp 15 hands its stages to the MMA warp
 //   warps 2-9   epilogue: a warp owns 32 TMEM lanes (weight rows) and every second block of 32
-//               columns (tokens); bias and activation per lane, then a turn through a private
-//               staging buffer, so that a token's features leave as 16-byte pieces
+//               columns (tokens); bias and activation per lane, and each value leaves from the lane
+//               that has it, a token's 32 features together.  (Turned through shared memory first, so
+//               that they left as 16-byte pieces: 24.5 us where this takes 24.9 for 8192 x 512 x 4096, 46
+//               against 45 with a residual.  What the stores do cost is a predicate each: blocks
+//               whose tokens are all there go without, 54 -> 30 us for 8192 x 512 x 4095.)
 // Both CTAs' copies of a stage complete on the even CTA's barrier, and the pair's commits
 // release it in both, as in the qkvr kernel.
 //
@@ -66,7 +69,6 @@
 #include <type_traits>
 
 #include "common.cuh"
-#include "conv4.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
 #include "cta_pair.cuh"
@@ -88,7 +90,7 @@ constexpr int kMaxThreads = kThreads + kGatherWarps * 32 + 32;
 constexpr int kEpiThreads = 256;
 constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpEpi = 2, kWarpProducer2 = 10, kWarpGather = 11,
               kWarpRelay = 15;
-constexpr int kStgPitch = 36;                     // floats of a staging row: 32 features + 4
+constexpr int kStgPitch = 32;                     // SWIGLU: floats of a row of the exchange, 32 features
 constexpr int kStgBytes = 16 * kStgPitch * 4;     // 16 tokens, one buffer per epilogue warp
 constexpr int kFineSteps = 8, kFineN = 160;       // fp32 outputs: K steps of a part, tokens of a tile
 constexpr int kRaster = 8;                        // feature blocks per raster group
@@ -118,22 +120,29 @@ struct Item {
     int e, row0, nt, n, fb;      // expert, first row, rows, MMA N (rows rounded up to 32), feature block
 };
 
+// The unit's own 1 / x, within one unit of the last place; results below 2^-126 are 0.
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <int kAct>
 __device__ __forceinline__ float activate(float v) {
     if (kAct == INKATTN_ACT_RELU) return v <= 0.f ? 0.f : v;      // (a NaN stays one)
     if (kAct == INKATTN_ACT_GELU) {
         // v (1 + erf(x)) / 2 at x = v / sqrt 2, from erfc(|x|) by Abramowitz and Stegun, formula
         // 7.1.26: within 1.5e-7, without a branch (erff diverges within a warp, and its 32
-        // copies in the epilogue spilled: 12.5 us for 777 x 1000 x 1021 where this takes 11)
-        const float x = fabsf(v) * 0.70710678118654752f;
-        const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-        const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
-                                 0.254829592f);
-        const float half_erfc = 0.5f * p * __expf(-x * x);
+        // copies in the epilogue spilled: 12.5 us for 777 x 1000 x 1021 where this takes 9.6).
+        // The formula's exp(-x^2) is 2^(-v^2 log2(e) / 2).
+        const float t = reciprocal(fmaf(0.3275911f * 0.70710678f, fabsf(v), 1.f));
+        const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f), 0.5f * 1.421413741f),
+                                         0.5f * -0.284496736f), 0.5f * 0.254829592f);
+        const float half_erfc = p * fast_exp2(v * v * -0.72134752f);
         // (half_erfc is 0 from v = 15 on; the bound keeps infinity from being multiplied by it)
         return v > 0.f ? fmaf(-fminf(v, 15.f), half_erfc, v) : v * half_erfc;
     }
-    if (kAct == INKATTN_ACT_SILU) return __fdividef(v, 1.f + __expf(-v));
+    if (kAct == INKATTN_ACT_SILU) return v * reciprocal(1.f + fast_exp2(v * -1.44269504f));
     return v;
 }
 
@@ -185,9 +194,10 @@ __device__ __forceinline__ void st_shared_cluster(uint32_t addr, uint32_t v) {
 
 }  // namespace
 
-// kFine: fp32 output, summed in parts
-template <int kAct, bool kFine>
-__global__ void __launch_bounds__(kMaxThreads, 1)
+// kFine: fp32 output, summed in parts.  kResid: with a residual, and then without row indices (the
+// registers of the gather's threads hold residual values).
+template <int kAct, bool kFine, bool kResid>
+__global__ void __launch_bounds__(kResid ? kThreads : kMaxThreads, 1)
 k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     constexpr bool kGated = kAct == INKATTN_ACT_SWIGLU;
     constexpr int kFeat = kGated ? 64 : 128;           // output features of a CTA
@@ -493,11 +503,6 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         const float *stg_other = reinterpret_cast<const float *>(smem + kOffStg + (e8 * 4 + ((warp - kWarpEpi) & 3 ^ 2)) * kStgBytes);
         const int swap_bar = 1 + e8 * 2 + (quarter & 1);
         const size_t F = (size_t)A.F;
-        inkattn_bf16 *out16 = static_cast<inkattn_bf16 *>(A.out);
-        float *out32 = static_cast<float *>(A.out);
-        // 16-byte pieces of a row start on 16-byte boundaries
-        const bool vec = kFine ? (A.F & 3) == 0 && (A.residual == nullptr || (A.F & 7) == 0) : (A.F & 7) == 0;
-        const bool paired = !kFine && vec && A.residual == nullptr;
         const int accs = my_items * parts;                    // accumulations in all
         int i = 0;
         bool ok = true;
@@ -516,8 +521,49 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             __syncwarp();
             if (lane == 0) mbar_pair_arrive(bar(B_ACC_EMPTY + (i & 1)), even);   // its MMA warp waits
         };
+        // Residual values of the block that comes next, requested as those of the block before it are
+        // used: 16 tokens of the lane's feature (h = 0, 1: halves of a block; gated: the half that the
+        // warp finishes).  Their rows are on their way into L2 an item ahead.  (8192 x 512 x 4096 fp32
+        // with residual 132 us where this takes 54, when each value was requested before its store.)
+        constexpr int kHalves = kGated ? 1 : 2;
+        uint32_t resid[kResid ? kHalves : 1][kResid ? 16 : 1];
+        auto request_residual = [&](const Item &it, int c, int h) {
+            const int f0 = (it.fb * 2 + half) * kFeat + (kGated ? quarter & 1 : quarter) * 32;
+            const int t0 = c * 32 + (kGated ? (quarter < 2 ? 0 : 16) : 16 * h);
+            const inkattn_bf16 *from = A.residual + (size_t)(it.row0 + t0) * F + f0 + lane;
+            const int n = f0 + lane < A.F ? it.nt - t0 : 0;
+            if (n >= 16) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j, from += F) resid[h][j] = *from;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j, from += F)
+                    if (j < n) resid[h][j] = *from;
+            }
+        };
+        auto prefetch_residual = [&](const Item &it) {
+            const int f0 = (it.fb * 2 + half) * kFeat + (kGated ? quarter & 1 : quarter) * 32;
+            if (f0 >= A.F) return;
+            for (int t = e8 * 32 + lane; t < it.nt; t += 64) {
+                const inkattn_bf16 *from = A.residual + (size_t)(it.row0 + t) * F + f0;
+                prefetch_l2(from);
+                prefetch_l2(from + min(31, A.F - 1 - f0));
+            }
+        };
+        Item ahead = {};
+        bool requested = false;                               // of the next item's first block
+        if (kResid && cid < n_items) prefetch_residual(ahead = item(cid));
         for (int w = cid; w < n_items; w += nclusters) {
-            const Item it = item(w);
+            const Item it = kResid ? ahead : item(w);
+            if (kResid) {
+                if (!requested && A.splits == 1 && e8 * 32 < it.nt) {
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) request_residual(it, e8, h);
+                }
+                requested = false;
+                ahead.nt = 0;
+                if (w + nclusters < n_items) prefetch_residual(ahead = item(w + nclusters));
+            }
             // the warp's 32 features (gated: quarters 0 and 1 hold gates, 2 and 3 the ups of the
             // same features), the lane's feature and its bias
             const int f0 = (it.fb * 2 + half) * kFeat + (kGated ? quarter & 1 : quarter) * 32;
@@ -527,15 +573,6 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                 bias = __ldg(A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + (kGated && quarter >= 2 ? F : 0) + frow);
             const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
             const int nblocks = (it.nt + 31) >> 5;
-            if (A.residual && f0 < A.F) {
-                // the residual rows on their way into L2 while the products run
-                for (int c = e8; c < nblocks; c += 2)
-                    if (c * 32 + lane < it.nt) {
-                        const inkattn_bf16 *from = A.residual + (size_t)(it.row0 + c * 32 + lane) * F + f0;
-                        prefetch_l2(from);
-                        prefetch_l2(from + min(31, A.F - 1 - f0));
-                    }
-            }
             for (int q = 0; q < parts; ++q, ++i) {
                 if (!acc_full()) break;
                 if (A.splits > 1 && parts == 1) break;        // (the tile is finished below, from this accumulator)
@@ -559,21 +596,17 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                         tc::wait_st();
                         continue;
                     }
-                    // the block's residual values, all requested before the first is used
-                    uint4 resid[kFine ? 1 : 4];
-                    if (!kFine && vec && A.residual) {
-#pragma unroll
-                        for (int q4 = 0; q4 < (kGated ? 2 : 4); ++q4) {
-                            const int t = c * 32 + (kGated ? (quarter < 2 ? 0 : 16) : 0) + q4 * 8 + (lane >> 2);
-                            const int f = f0 + (lane & 3) * 8;
-                            resid[kFine ? 0 : q4] = make_uint4(0, 0, 0, 0);
-                            if (t < it.nt && f < A.F)
-                                resid[kFine ? 0 : q4] = *reinterpret_cast<const uint4 *>(A.residual + (size_t)(it.row0 + t) * F + f);
-                        }
-                    }
+                    // the block whose residual values are requested as this one's are used
+                    const bool more = c + 2 < nblocks;
+                    const int c_next = more ? c + 2 : e8;
+                    auto request_next = [&](int h) {
+                        if (more) request_residual(it, c_next, h);
+                        else if (c_next * 32 < ahead.nt) request_residual(ahead, c_next, h);
+                    };
+                    if (kResid && !more) requested = c_next * 32 < ahead.nt;
                     // tokens of this block that are stored
                     bool mine = c * 32 + lane < it.nt;
-                    if (A.row_token && mine) {
+                    if (!kResid && A.row_token && mine) {
                         const int t = __ldg(A.row_token + it.row0 + c * 32 + lane);
                         if (t < 0 || t >= A.N_x) {
                             mine = false;
@@ -581,89 +614,27 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                         }
                     }
                     const uint32_t live = __ballot_sync(0xffffffffu, mine);
-                    // 2 kPairs finished tokens from t0 on, as bf16 pairs of tokens of the lane's feature, to out:
-                    // half the shared-memory traffic of fp32 values
-                    auto store_pairs = [&](auto pairs, const uint32_t *u, int t0) {
-                        constexpr int kPairs = decltype(pairs)::value;
-                        uint32_t *words = reinterpret_cast<uint32_t *>(stg);
-                        inkattn_bf16 *to = out16 + (size_t)(it.row0 + c * 32 + t0) * F;
-                        const uint32_t live_t = live >> t0;
-                        __syncwarp();
-#pragma unroll
-                        for (int p = 0; p < kPairs; ++p) words[p * kStgPitch + lane] = u[p];
-                        __syncwarp();
-#pragma unroll
-                        for (int q = 0; q < kPairs / 8; ++q) {
-                            const int p = q * 8 + (lane >> 2), f = f0 + (lane & 3) * 8;
-                            const uint4 a = *reinterpret_cast<const uint4 *>(words + p * kStgPitch + (lane & 3) * 8);
-                            const uint4 b = *reinterpret_cast<const uint4 *>(words + p * kStgPitch + (lane & 3) * 8 + 4);
-                            if (f >= A.F) continue;
-                            inkattn_bf16 *row = to + (size_t)(2 * p) * F + f;
-                            if ((live_t >> (2 * p)) & 1u)
-                                *reinterpret_cast<uint4 *>(row) =
-                                    make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
-                                               __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
-                            if ((live_t >> (2 * p + 1)) & 1u)
-                                *reinterpret_cast<uint4 *>(row + F) =
-                                    make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
-                                               __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
-                        }
-                    };
                     // 16 finished tokens t0 .. t0 + 15 of the block, the lane's feature of each, to out
+                    // (with one test for all of them where all are stored)
                     auto store16 = [&](const float (&y)[16], int t0) {
-                        const size_t row_b = (size_t)(it.row0 + c * 32 + t0);
-                        const uint32_t live16 = live >> t0;
-                        if (!vec) {                               // rows that start anywhere
+                        using Out = std::conditional_t<kFine, float, inkattn_bf16>;
+                        const int h = kGated ? 0 : t0 >> 4;
+                        Out *to = static_cast<Out *>(A.out) + (size_t)(it.row0 + c * 32 + t0) * F + frow;
+                        const uint32_t at = frow < A.F ? live >> t0 & 0xffffu : 0u;
+                        auto put = [&](int j) {
+                            const float z = kResid ? y[j] + __uint_as_float(resid[h][kResid ? j : 0] << 16) : y[j];
+                            if constexpr (kFine) *to = z;
+                            else store_bf16(to, z);
+                        };
+                        if (at == 0xffffu) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                if (((live16 >> j) & 1u) && frow < A.F) {
-                                    const size_t o = (row_b + j) * F + frow;
-                                    const float z = A.residual ? y[j] + load_bf16(A.residual + o) : y[j];
-                                    if (kFine) out32[o] = z;
-                                    else store_bf16(out16 + o, z);
-                                }
-                            }
-                            return;
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) stg[j * kStgPitch + lane] = y[j];
-                        __syncwarp();
-                        if (!kFine) {
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const int t = q * 8 + (lane >> 2), f = f0 + (lane & 3) * 8;
-                                const float *src = stg + t * kStgPitch + (lane & 3) * 8;
-                                float z[8];
-                                *reinterpret_cast<float4 *>(z) = *reinterpret_cast<const float4 *>(src);
-                                *reinterpret_cast<float4 *>(z + 4) = *reinterpret_cast<const float4 *>(src + 4);
-                                if (((live16 >> t) & 1u) && f < A.F) {
-                                    const size_t o = (row_b + t) * F + f;
-                                    if (A.residual) {
-                                        float r[8];
-                                        unpack8(resid[kFine ? 0 : (kGated ? 0 : t0 >> 3) + q], r);
-#pragma unroll
-                                        for (int j = 0; j < 8; ++j) z[j] += r[j];
-                                    }
-                                    *reinterpret_cast<uint4 *>(out16 + o) = pack8(z);
-                                }
-                            }
+                            for (int j = 0; j < 16; ++j, to += F) put(j);
                         } else {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int t = q * 4 + (lane >> 3), f = f0 + (lane & 7) * 4;
-                                float4 z = *reinterpret_cast<const float4 *>(stg + t * kStgPitch + (lane & 7) * 4);
-                                if (((live16 >> t) & 1u) && f < A.F) {
-                                    const size_t o = (row_b + t) * F + f;
-                                    if (A.residual) {
-                                        const uint2 r = *reinterpret_cast<const uint2 *>(A.residual + o);
-                                        z.x += bf16_lo(r.x); z.y += bf16_hi(r.x);
-                                        z.z += bf16_lo(r.y); z.w += bf16_hi(r.y);
-                                    }
-                                    *reinterpret_cast<float4 *>(out32 + o) = z;
-                                }
-                            }
+                            for (int j = 0; j < 16; ++j, to += F)
+                                if ((at >> j) & 1u) put(j);
                         }
+                        if (kResid) request_next(h);
                     };
                     float y[16];
                     if (kGated) {
@@ -682,21 +653,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                             y[j] = activate<INKATTN_ACT_SILU>(gate) * up;
                         }
                         named_sync(swap_bar, 64);                 // both have read
-                        if (paired) {
-                            uint32_t u[8];
-#pragma unroll
-                            for (int p = 0; p < 8; ++p) u[p] = pack_bf16(y[2 * p], y[2 * p + 1]);
-                            store_pairs(std::integral_constant<int, 8>{}, u, keep);
-                        } else {
-                            store16(y, keep);
-                        }
-                    } else if (paired) {
-                        uint32_t u[16];
-#pragma unroll
-                        for (int p = 0; p < 16; ++p)
-                            u[p] = pack_bf16(activate<kAct>(__uint_as_float(v[2 * p]) + bias),
-                                             activate<kAct>(__uint_as_float(v[2 * p + 1]) + bias));
-                        store_pairs(std::integral_constant<int, 16>{}, u, 0);
+                        store16(y, keep);
                     } else {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -784,7 +741,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                     if (kGated) y[n] *= up[n] + (b && in ? __ldg(b + F + n) : 0.f);
                 }
                 if (vec) {
-                    if (A.residual) {
+                    if (kResid) {
                         const uint2 r = *reinterpret_cast<const uint2 *>(A.residual + at);
                         y[0] += bf16_lo(r.x); y[1] += bf16_hi(r.x);
                         y[2] += bf16_lo(r.y); y[3] += bf16_hi(r.y);
@@ -799,7 +756,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     if (f + n >= A.F) break;
-                    const float o = A.residual ? y[n] + load_bf16(A.residual + at + n) : y[n];
+                    const float o = kResid ? y[n] + load_bf16(A.residual + at + n) : y[n];
                     if (kFine) static_cast<float *>(A.out)[at + n] = o;
                     else store_bf16(static_cast<inkattn_bf16 *>(A.out) + at + n, o);
                 }
@@ -821,14 +778,14 @@ namespace {
 
 using Kernel = void (*)(const LinearArgs, const LinearMaps);
 
-template <bool kFine>
+template <bool kFine, bool kResid>
 Kernel kernel_of(int act) {
     switch (act) {
-        case INKATTN_ACT_RELU: return k_linear<INKATTN_ACT_RELU, kFine>;
-        case INKATTN_ACT_GELU: return k_linear<INKATTN_ACT_GELU, kFine>;
-        case INKATTN_ACT_SILU: return k_linear<INKATTN_ACT_SILU, kFine>;
-        case INKATTN_ACT_SWIGLU: return k_linear<INKATTN_ACT_SWIGLU, kFine>;
-        default: return k_linear<INKATTN_ACT_NONE, kFine>;
+        case INKATTN_ACT_RELU: return k_linear<INKATTN_ACT_RELU, kFine, kResid>;
+        case INKATTN_ACT_GELU: return k_linear<INKATTN_ACT_GELU, kFine, kResid>;
+        case INKATTN_ACT_SILU: return k_linear<INKATTN_ACT_SILU, kFine, kResid>;
+        case INKATTN_ACT_SWIGLU: return k_linear<INKATTN_ACT_SWIGLU, kFine, kResid>;
+        default: return k_linear<INKATTN_ACT_NONE, kFine, kResid>;
     }
 }
 
@@ -850,7 +807,7 @@ int resident_clusters(int ctas, int num_sms) {
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, k_linear<INKATTN_ACT_NONE, false>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, k_linear<INKATTN_ACT_NONE, false, false>, &cfg) != cudaSuccess) {
         (void)cudaGetLastError();
         return 0;
     }
@@ -863,14 +820,13 @@ int resident_clusters(int ctas, int num_sms) {
 // between 1 x 1024 x 1024 and 512 x 8192 x 8192, each with every tile and split.
 //   stage   a K = 64 step of a tile of n tokens: the loop of the MMA warp (0.16), the bytes into an
 //           SM, which come faster to few of them, or the MMAs
-//   finish  an item's epilogue, which overlaps the next item's products; more where rows do not
-//           start on 16-byte boundaries and features leave one by one
+//   finish  an item's epilogue, which overlaps the next item's products
 //   join    of a split instead: the partial tiles through distributed shared memory
 //   and the weights come from HBM at 7 TB/s at best, 88 GB/s for each SM that asks
-double launch_us(long long items, int n, int stages, int splits, int pairs, double weight_bytes, bool vec) {
+double launch_us(long long items, int n, int stages, int splits, int pairs, double weight_bytes) {
     const double busy = fmin((double)(items * splits), (double)pairs);
     const double stage = fmax(fmax(0.16, (16.4 + 0.0655 * n) / (busy <= 40 ? 150.0 : 118.0)), 0.00104 * n);
-    const double finish = 0.6 + (vec ? 0.0071 : 0.03) * n, join = 1.2 + 0.024 * n, start = 1.4 + 0.015 * busy;
+    const double finish = 0.6 + 0.0071 * n, join = 1.2 + 0.024 * n, start = 1.4 + 0.015 * busy;
     const double item = stages * stage / splits, hbm = weight_bytes / fmin(7.0e6, 0.176e6 * busy);
     if (splits > 1) return start + fmax(item, hbm) + join;
     const double waves = (double)((items + pairs - 1) / pairs);
@@ -881,9 +837,10 @@ double launch_us(long long items, int n, int stages, int splits, int pairs, doub
 
 cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStream_t stream) {
     LinearArgs a = args;
-    const Kernel k = a.out_f32 ? kernel_of<true>(act) : kernel_of<false>(act);
+    const Kernel k = a.residual ? (a.out_f32 ? kernel_of<true, true>(act) : kernel_of<false, true>(act))
+                                : (a.out_f32 ? kernel_of<true, false>(act) : kernel_of<false, false>(act));
     cudaError_t err = cudaSuccess;
-    for (Kernel f : {k, kernel_of<false>(INKATTN_ACT_NONE)})
+    for (Kernel f : {k, kernel_of<false, false>(INKATTN_ACT_NONE)})
         if ((err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return err;
     const int feat = act == INKATTN_ACT_SWIGLU ? 128 : 256, nk = (a.K + kKStep - 1) / kKStep;
     a.n_fblocks = (a.F + feat - 1) / feat;
@@ -909,8 +866,7 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
         if (bound > INT_MAX / 2) continue;
         for (int s = 1; s <= kMaxSplits; s *= 2) {
             if (s > 1 && (nk < 2 * s || bound > resident_clusters(2 * s, num_sms))) break;
-            const double us = launch_us(owners * each * a.n_fblocks, n, nk, s, resident_clusters(2, num_sms), weight_bytes,
-                                        a.F % 8 == 0);
+            const double us = launch_us(owners * each * a.n_fblocks, n, nk, s, resident_clusters(2, num_sms), weight_bytes);
             if (a.tile_n == 0 || us < best) {
                 best = us;
                 most_items = bound;
@@ -926,6 +882,7 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     const int clusters = (int)(most_items < most ? most_items : most);
     LinearMaps maps = {};
     if (!make_linear_maps(a, act == INKATTN_ACT_SWIGLU, &maps)) return cudaErrorInvalidValue;
+    if (a.residual && a.row_token) return cudaErrorInvalidValue;   // (no such call)
     const int threads = a.row_token ? kMaxThreads : kThreads;
     return launch_dependent(k, dim3((unsigned)(2 * a.splits * clusters)), dim3((unsigned)threads), kSmem, stream,
                             2 * a.splits, a, maps);
