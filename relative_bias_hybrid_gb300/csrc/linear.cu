@@ -93,6 +93,7 @@ constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpEpi = 2, kWarpProducer2 = 10
 constexpr int kStgPitch = 32;                     // SWIGLU: floats of a row of the exchange, 32 features
 constexpr int kStgBytes = 16 * kStgPitch * 4;     // 16 tokens, one buffer per epilogue warp
 constexpr int kFineSteps = 8, kFineN = 160;       // fp32 outputs: K steps of a part, tokens of a tile
+constexpr int kSetupBar = 5;                      // named barrier (1 to 4: SWIGLU's exchanges)
 constexpr int kRaster = 8;                        // feature blocks per raster group
 
 constexpr int kOffStg = kRingBytes;
@@ -152,9 +153,9 @@ __device__ __forceinline__ void store_bf16(inkattn_bf16 *p, float v) {
 __device__ __forceinline__ float load_bf16(const inkattn_bf16 *p) { return __uint_as_float((uint32_t)*p << 16); }
 
 // 16 bytes global -> shared without a register stop; all zeros where `live` is false
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, uint64_t src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(live ? 16 : 0) : "memory");
+                 :: "r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<uint64_t>(p)));
@@ -190,6 +191,74 @@ struct RingPos {
 
 __device__ __forceinline__ void st_shared_cluster(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
+}
+
+// The token tiles of the experts, in shared memory: the prefix of their counts, each expert's
+// first row (and the last one's end), and the rows of a tile.
+struct Tiles {
+    int *prefix, *start, *per;
+    int most;                                          // units of 32 rows of a tile
+    // An expert's tiles: of near-equal size, a multiple of 32 rows.
+    __device__ __forceinline__ int enter(int e, int first, int rows) const {
+        const int units = (int)(((uint32_t)rows + 31) >> 5);
+        int tiles = units > 0, each = units;
+        if (units > most) {
+            tiles = (units - 1) / most + 1;
+            each = (units - 1) / tiles + 1;
+        }
+        start[e] = first;
+        per[e] = each * 32;
+        return tiles;
+    }
+};
+
+// The tiles of more than 32 experts from their offsets, by warps w = 0 .. 7 (by one, 32 experts at a
+// time, each took 0.6 us: a token for 256 experts 10.3 us where this takes 6.3).  A function of its
+// own, of rolled loops: it runs once, from a cold instruction cache, and beside the code that follows
+// it slowed everything down (linear layers by 0.4 us, eight experts a lane unrolled all by 1.3).
+__device__ __noinline__ void setup_experts(Tiles t, const int32_t *offsets, int E, int M, int w, int lane, int *scan,
+                                           int32_t *dev_status) {
+    constexpr int kWarps = kEpiThreads / 32;
+    int carry = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int e0 = 0, round = 0; e0 < E; e0 += kEpiThreads, round ^= kWarps) {
+        const int e = e0 + w * 32 + lane;
+        int v = 0;                                     // tiles, then tiles up to this expert
+        if (e < E) {
+            const int first = offsets[e], end = offsets[e + 1];
+            const bool possible = first >= 0 && end >= first && end <= M;
+            ok = ok && possible;
+            v = t.enter(e, first, possible ? end - first : 0);
+            if (e == E - 1) t.start[E] = end;
+        }
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += n;
+        }
+        if (lane == 31) scan[round + w] = v;           // (two halves in turn: the next round's writes)
+        ok = named_all(kSetupBar, kEpiThreads, ok);
+        const int of = lane < kWarps ? scan[round + lane] : 0;
+        v += carry + __reduce_add_sync(0xffffffffu, lane < w ? of : 0);
+        carry += __reduce_add_sync(0xffffffffu, of);
+        if (e < E) t.prefix[e + 1] = v;
+    }
+    if (!ok) named_sync(kSetupBar, kEpiThreads);       // (nobody writes after the thread below)
+    if (w > 0 || lane > 0) return;
+    t.prefix[0] = 0;
+    if (ok) return;
+    // Some offsets are impossible: one expert after another.
+    set_status(dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+    int reached = 0, before = 0;
+#pragma unroll 1
+    for (int e = 0; e < E; ++e) {
+        const int first = offsets[e], end = offsets[e + 1];
+        const bool possible = first >= 0 && end >= first && end <= M;
+        before += t.enter(e, first, possible && first >= reached ? end - first : 0);
+        t.prefix[e + 1] = before;
+        if (possible) reached = max(reached, end);
+    }
 }
 
 }  // namespace
@@ -248,49 +317,41 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
     // Everything up to here and, for a linear layer, the rest of the setup needs no global memory
     // and runs while the kernel before this one on the stream finishes; each role waits for that
     // kernel before it reads or writes global memory, and before its first wait with a limit.
-    if (warp == kWarpEpi) {
-        if (A.offsets) grid_dep_wait();
-        // First row of every expert and the prefix of token tiles: s_tiles[e] = tiles of experts
-        // 0 .. e-1.  An expert that reaches back into the rows of an earlier one is refused like
-        // one with impossible offsets: the accepted ones hold M rows together at most, so that the
-        // items stay within what the launch was sized for.
-        int carry = 0, reached = 0;                    // tiles, and the largest end, so far
-        if (lane == 0) s_tiles[0] = 0;
-        for (int e0 = 0; e0 < A.E; e0 += 32) {
-            const int e = e0 + lane;
-            int tiles = 0, start = 0, end = 0;
-            if (e < A.E) {
-                start = A.offsets ? A.offsets[e] : 0;
-                end = A.offsets ? A.offsets[e + 1] : A.M;
-                s_start[e] = start;
-                if (e == A.E - 1) s_start[A.E] = end;
-            }
-            bool valid = start >= 0 && end >= start && end <= A.M;
-            int most = valid ? end : 0;                // largest end up to this lane, then before it
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int n = __shfl_up_sync(0xffffffffu, most, o);
-                if (lane >= o) most = max(most, n);
-            }
-            const int all = max(reached, __shfl_sync(0xffffffffu, most, 31));
-            most = __shfl_up_sync(0xffffffffu, most, 1);
-            valid = valid && start >= max(reached, lane ? most : 0);
-            reached = all;
-            if (e < A.E) {
-                if (valid) tiles = (end - start + A.tile_n - 1) / A.tile_n;
-                else set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
-                // tiles of near-equal size, a multiple of 32 rows
-                s_per[e] = tiles > 0 ? ((end - start + tiles - 1) / tiles + 31) & ~31 : 0;
-            }
-            int v = tiles;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int n = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += n;
-            }
-            if (e < A.E) s_tiles[e + 1] = carry + v;
-            carry += __shfl_sync(0xffffffffu, v, 31);
+    // First row of every expert, rows of its token tiles, and the prefix of the tiles: s_tiles[e] =
+    // tiles of experts 0 .. e-1.  An expert that reaches back into the rows of an earlier one is refused
+    // like one with impossible offsets: the accepted ones hold M rows together at most, so that the
+    // items stay within what the launch was sized for.
+    const Tiles tiles = {s_tiles, s_start, s_per, A.tile_n >> 5};
+    if (A.E > 32) {
+        if (warp >= kWarpEpi && warp < kWarpEpi + kEpiThreads / 32) {
+            grid_dep_wait();
+            setup_experts(tiles, A.offsets, A.E, A.M, warp - kWarpEpi, lane, reinterpret_cast<int *>(smem + kOffStg),
+                          A.dev_status);
         }
+    } else if (warp == kWarpEpi) {
+        if (A.offsets) grid_dep_wait();
+        const bool there = lane < A.E;
+        const int start = there && A.offsets ? A.offsets[lane] : 0;
+        const int end = there ? A.offsets ? A.offsets[lane + 1] : A.M : 0;
+        bool valid = start >= 0 && end >= start && end <= A.M;
+        int most = valid ? end : 0;                    // largest end up to this lane, then before it
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, most, o);
+            if (lane >= o) most = max(most, n);
+        }
+        most = __shfl_up_sync(0xffffffffu, most, 1);
+        valid = valid && there && start >= (lane ? most : 0);
+        int v = there ? tiles.enter(lane, start, valid ? end - start : 0) : 0;
+        if (there && !valid) set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += n;
+        }
+        if (there) s_tiles[lane + 1] = v;
+        if (lane == A.E - 1) s_start[A.E] = end;
+        if (lane == 0) s_tiles[0] = 0;
     }
     tc::fence_before();
     __syncthreads();
@@ -423,12 +484,11 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
         for (int w = cid; w < n_items && ok; w += nclusters) {
             const Item it = item(w);
             const int hn = it.n >> 1, mine = min(max(it.nt - half * hn, 0), hn);
-            const inkattn_bf16 *src[16];
+            uint32_t row[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                int r = r0 + 8 * j < mine ? __ldg(A.row_token + it.row0 + half * hn + r0 + 8 * j) : 0;
-                if (r < 0 || r >= A.N_x) r = 0;        // (flagged and not stored by the epilogue)
-                src[j] = A.x + (size_t)r * A.K + piece * 8;
+                row[j] = r0 + 8 * j < mine ? (uint32_t)__ldg(A.row_token + it.row0 + half * hn + r0 + 8 * j) : 0u;
+                if (row[j] >= (uint32_t)A.N_x) row[j] = 0;    // (flagged and not stored by the epilogue)
             }
             int k = k_lo + first;
             for (; k < k_hi; k += 2, at.next(A.stages, 2)) {
@@ -438,10 +498,11 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                 }
                 const uint32_t dst = s_base + (uint32_t)(at.s * A.stage_bytes + kABytes + r0 * 128 + ((piece ^ (r0 & 7)) << 4));
                 const bool live = k * kKStep + piece * 8 < A.K;
+                const uint64_t from = reinterpret_cast<uint64_t>(A.x + piece * 8 + (live ? k * kKStep : 0));
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     if (r0 + 8 * j < mine)
-                        cp_async16(dst + (uint32_t)(j * 8 * 128), live ? src[j] + k * kKStep : src[j], live);
+                        cp_async16(dst + (uint32_t)(j * 8 * 128), from + (uint64_t)row[j] * ((uint32_t)A.K * 2), live);
                 cp_async_arrive(bar(B_GATHER + at.s));
             }
             first = k - k_hi;

@@ -401,6 +401,39 @@ def test_grouped_overlapping_experts_are_flagged_and_left(ia):
         assert torch.equal(out.cpu(), want)
 
 
+@pytest.mark.parametrize("E", [31, 32, 33, 255, 256, 257, 600, 1024])
+@pytest.mark.parametrize("bad", [False, True])
+def test_grouped_tiles_of_many_experts(ia, E, bad):
+    """Offsets read by one warp or by eight, once or in rounds: every expert at its rows; with two
+    impossible offsets, the experts beside them are flagged and left and all others computed."""
+    g = torch.Generator().manual_seed(E)
+    K, F = 64, 40
+    counts = torch.randint(0, 4, (E,), generator=g)
+    counts[E // 3] = 300                                       # several tiles
+    offs = torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)]).to(I32)
+    M = int(offs[-1])
+    x, w = _grid((M, K), g, -8, 8, 1 / 8), _grid((E, F, K), g, -8, 8, 1 / 64)
+    if bad:
+        offs[E // 2], offs[E - 3] = -5, M + 1
+    owner = torch.full((M,), -1)
+    reached = 0
+    for e in range(E):
+        lo, hi = int(offs[e]), int(offs[e + 1])
+        if 0 <= lo <= hi <= M:
+            if lo >= reached:
+                owner[lo:hi] = e
+            reached = max(reached, hi)
+    out = torch.full((M, F), 7.0, dtype=BF16, device="cuda")
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    ia.inkattn_grouped_linear(ia.grouped_linear_params(x=x.cuda(), w=w.cuda(), expert_offsets=offs.cuda(), out=out,
+                                                       dev_status=status))
+    torch.cuda.synchronize()
+    assert int(status) == (ia.INKATTN_ERR_DEVICE_BOUNDS if bad else 0)
+    want = torch.einsum("mk,mfk->mf", x.double(), w.double()[owner.clamp(min=0)]).to(F32).to(BF16)
+    want[owner < 0] = 7.0
+    assert torch.equal(out.cpu(), want)
+
+
 # ---------------------------------------------------------------- router and sum
 
 def _route(ia, logits, S, k, score="sigmoid", scale=1.0):
