@@ -19,6 +19,8 @@
 //
 // Measured, 6 of 256 + 2: 32768 tokens 27 us (the choice about 19, 475 instructions a token at 0.54
 // of the issue rate; 48 warps an SM without the requests ahead took 30), 288 tokens 6.4 us.
+#include <type_traits>
+
 #include "common.cuh"
 #include "conv4.cuh"
 #include "internal.h"
@@ -300,65 +302,98 @@ cudaError_t launch_route(const inkattn_route_params &p, uint32_t *ws, cudaStream
 
 // ---------------------------------------------------------------- the weighted sum
 // HBM-bound: top_k + n_shared rows read and one written per token.  A thread owns 8 features
-// of one token (a 16-byte piece of every row) and requests up to eight rows before it uses
-// the first; the sum is taken in fp32 in the order of the choices.  Measured: 8192 tokens x 8
-// rows of 8192 in 182 us, 6.6 TB/s (98% of the copy rate); 288 tokens in 9.2 us.
+// (a 16-byte piece of every row) of one token, or, where a token has few rows, of two, four or
+// eight, and requests up to eight pieces before it uses the first; the sum is taken in fp32 in the
+// order of the choices.  Narrow rows: several tokens a block.  Measured: 8192 tokens x 8 rows of
+// 8192 in 182 us, 6.6 TB/s (98% of the copy rate); 288 tokens in 9.2 us; 8192 tokens with one row of
+// 8192 49 us (94 with one token a thread), with ten of 64 4.7 us (12 with one token a block).
 
 namespace {
 constexpr int kSumThreads = 128;
-constexpr int kSumRows = 8;                        // rows requested at once
+constexpr int kSumRows = 8;                        // pieces requested at once
+constexpr int kSumResident = 152 * 2048 / kSumThreads;   // blocks that run at once
 }  // namespace
 
+// A thread sums kRows rows of kTokens tokens at a time.  kWide: the block is one token's (the same
+// in every thread, so that its weights and rows are read once a warp: 182 us where 192 otherwise),
+// else 1 << shift threads are; chunks: blocks of a row's pieces.
+template <bool kWide, int kRows, int kTokens>
 __global__ void __launch_bounds__(kSumThreads)
-k_expert_combine(const inkattn_expert_combine_params p) {
+k_expert_combine(const inkattn_expert_combine_params p, int shift, int chunks) {
+    static_assert(kRows * kTokens <= kSumRows, "pieces requested at once");
     grid_dep_wait();
     grid_dep_launch();
     const int G = p.F >> 3;                            // 16-byte pieces of a row
-    const int blocks = (G + kSumThreads - 1) / kSumThreads;
-    const long long t = (long long)blockIdx.x / blocks;
-    const int g = (int)(blockIdx.x - t * blocks) * kSumThreads + threadIdx.x;
-    if (g >= G) return;
+    const int tokens = kWide ? 1 : kSumThreads >> shift;   // side by side in the block
+    const int group = (int)blockIdx.x / chunks, chunk = (int)blockIdx.x - group * chunks;
+    const int g = kWide ? chunk * kSumThreads + (int)threadIdx.x : (int)threadIdx.x & ((1 << shift) - 1);
+    const long long t0 = (long long)group * (tokens * kTokens) + (kWide ? 0 : (int)threadIdx.x >> shift);
+    if (g >= G || t0 >= p.N_tok) return;
     const int rows = p.top_k + p.n_shared;
-    const float *w = p.weights + t * rows;
-    const int32_t *tr = p.token_rows + t * p.top_k;
     const uint4 *y = reinterpret_cast<const uint4 *>(p.y), *sh = reinterpret_cast<const uint4 *>(p.shared);
-    float acc[8] = {};
-    for (int j0 = 0; j0 < rows; j0 += kSumRows) {
-        uint4 v[kSumRows];
-        float c[kSumRows];
+    float acc[kTokens][8] = {};
+    for (int j0 = 0; j0 < rows; j0 += kRows) {
+        uint4 v[kTokens][kRows];
+        float c[kTokens][kRows];
 #pragma unroll
-        for (int i = 0; i < kSumRows; ++i) {
-            const int j = j0 + i;
-            v[i] = make_uint4(0, 0, 0, 0);
-            c[i] = 0.f;
-            if (j >= rows) continue;
-            if (j < p.top_k) {
-                const int r = __ldg(tr + j);
-                if (r >= 0 && r < p.M) {
-                    c[i] = __ldg(w + j);
-                    v[i] = __ldcs(y + (size_t)r * G + g);
-                } else if (r != -1 && g == 0) {
-                    set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+        for (int n = 0; n < kTokens; ++n) {
+            const long long t = t0 + n * tokens;
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int j = j0 + i;
+                v[n][i] = make_uint4(0, 0, 0, 0);
+                c[n][i] = 0.f;
+                if (j >= rows || (kTokens > 1 && t >= p.N_tok)) continue;
+                if (j < p.top_k) {
+                    const int r = __ldg(p.token_rows + t * p.top_k + j);
+                    if (r >= 0 && r < p.M) {
+                        c[n][i] = __ldg(p.weights + t * rows + j);
+                        v[n][i] = __ldcs(y + (size_t)r * G + g);
+                    } else if (r != -1 && g == 0) {
+                        set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+                    }
+                } else {
+                    c[n][i] = __ldg(p.weights + t * rows + j);
+                    v[n][i] = __ldcs(sh + ((size_t)(j - p.top_k) * p.N_tok + t) * G + g);
                 }
-            } else {
-                c[i] = __ldg(w + j);
-                v[i] = __ldcs(sh + ((size_t)(j - p.top_k) * p.N_tok + t) * G + g);
             }
         }
 #pragma unroll
-        for (int i = 0; i < kSumRows; ++i) {
-            float x[8];
-            unpack8(v[i], x);
+        for (int n = 0; n < kTokens; ++n)
 #pragma unroll
-            for (int n = 0; n < 8; ++n) acc[n] = fmaf(c[i], x[n], acc[n]);
-        }
+            for (int i = 0; i < kRows; ++i) {
+                float x[8];
+                unpack8(v[n][i], x);
+#pragma unroll
+                for (int m = 0; m < 8; ++m) acc[n][m] = fmaf(c[n][i], x[m], acc[n][m]);
+            }
     }
-    reinterpret_cast<uint4 *>(p.out)[t * G + g] = pack8(acc);
+#pragma unroll
+    for (int n = 0; n < kTokens; ++n) {
+        const long long t = t0 + n * tokens;
+        if (kTokens == 1 || t < p.N_tok) reinterpret_cast<uint4 *>(p.out)[t * G + g] = pack8(acc[n]);
+    }
 }
 
 cudaError_t launch_expert_combine(const inkattn_expert_combine_params &p, cudaStream_t stream) {
-    const long long blocks = (long long)p.N_tok * ((p.F / 8 + kSumThreads - 1) / kSumThreads);
-    return launch_dependent(k_expert_combine, dim3((unsigned)blocks), dim3(kSumThreads), 0, stream, 1, p);
+    const int G = p.F / 8, rows = p.top_k + p.n_shared;
+    int shift = 0;
+    while ((1 << shift) < G && (1 << shift) < kSumThreads) ++shift;
+    const int chunks = (G + (1 << shift) - 1) >> shift, tokens = kSumThreads >> shift;
+    auto blocks = [&](int n) { return ((long long)p.N_tok + tokens * n - 1) / (tokens * n) * chunks; };
+    auto go = [&](auto kernel, int n) {
+        return launch_dependent(kernel, dim3((unsigned)blocks(n)), dim3(kSumThreads), 0, stream, 1, p, shift, chunks);
+    };
+    // Several tokens a thread only for more blocks than run at once: with fewer, more threads
+    // are more requests in flight.
+    auto pick = [&](auto wide) {
+        constexpr bool kWide = decltype(wide)::value;
+        if (rows > 4 || blocks(1) <= kSumResident) return go(k_expert_combine<kWide, 8, 1>, 1);
+        if (rows > 2) return go(k_expert_combine<kWide, 4, 2>, 2);
+        if (rows > 1) return go(k_expert_combine<kWide, 2, 4>, 4);
+        return go(k_expert_combine<kWide, 1, 8>, 8);
+    };
+    return tokens == 1 ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace inkattn

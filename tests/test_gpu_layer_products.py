@@ -571,3 +571,37 @@ def test_expert_combine_bad_rows_and_no_nan_from_dropped_ones(ia):
     torch.cuda.synchronize()
     assert int(status) == ia.INKATTN_ERR_DEVICE_BOUNDS
     assert torch.equal(out.cpu().float(), torch.tensor([1.0, 1.0, 0.0])[:, None].expand(T, F))
+
+
+@pytest.mark.parametrize("T,k,S,F", [(2501, 1, 0, 1000), (2500, 1, 1, 1024), (2497, 2, 0, 520), (2463, 3, 1, 1032),
+                                     (2600, 2, 1, 2056), (40001, 1, 0, 64), (40000, 2, 0, 56), (20003, 3, 1, 136),
+                                     (77777, 1, 1, 8), (50001, 7, 2, 24)])
+def test_expert_combine_of_many_tokens(ia, T, k, S, F):
+    """More blocks than run at once: several tokens a thread where they have few rows, and several
+    a block where the rows are narrow; with dropped and bad rows among them."""
+    g = torch.Generator(device="cuda").manual_seed(T + F)
+    M = T * k
+    y, sh = (torch.randn(s, generator=g, device="cuda").to(BF16) for s in ((M, F), (S, T, F)))
+    w = torch.randn((T, k + S), generator=g, device="cuda")
+    rows = torch.randperm(M, generator=g, device="cuda").to(I32).reshape(T, k)
+    rows[::7, 0] = -1
+    for bad in (False, True):
+        if bad:
+            rows[T - 1, 0], rows[5, k - 1] = M, -2
+        out = torch.full((T + 1, F), 7.0, dtype=BF16, device="cuda")
+        status = torch.zeros(1, dtype=I32, device="cuda")
+        ia.inkattn_expert_combine(ia.expert_combine_params(y=y, shared=sh if S else None, weights=w, token_rows=rows,
+                                                           out=out[:T], dev_status=status))
+        torch.cuda.synchronize()
+        assert int(status) == (ia.INKATTN_ERR_DEVICE_BOUNDS if bad else 0) and bool((out[T] == 7).all())
+        want, mags = torch.zeros((T, F), dtype=F64, device="cuda"), torch.zeros((T, F), dtype=F64, device="cuda")
+        for j in range(k + S):
+            if j < k:
+                r = rows[:, j].long()
+                term = torch.where(((r >= 0) & (r < M))[:, None], y[r.clamp(0, M - 1)].double() * w[:, j, None].double(), 0.0)
+            else:
+                term = sh[j - k].double() * w[:, j, None].double()
+            want, mags = want + term, mags + term.abs()
+        slack = (k + S) * 2.0 ** -24 * mags                  # one rounding a term
+        err = (out[:T].double() - want).abs()
+        assert bool((err <= slack + 2.0 ** -8 * (want.abs() + slack) + 2.0 ** -126).all())
