@@ -31,8 +31,11 @@ namespace {
 
 constexpr int kChooseThreads = 1024;               // of a chunk; of one chunk alone, fewer
 constexpr int kChooseThreadsOne = 256;
+// (keys of more than 512 experts want more than the 64 registers of a thread of 1024)
+constexpr int choose_threads(int per) { return per > 16 ? kChooseThreads / 2 : kChooseThreads; }
 constexpr int kPlaceThreads = 1024;
 constexpr int kPlaceTokens = 1024;                 // tokens of a bitmap, a multiple of 32
+constexpr int kPlaceOnePairs = 3000;               // pairs of a batch that one block places
 constexpr int kChunks = 152;                       // chunks of a larger batch, at most
 
 // Order-preserving integer key of a logit: larger logit, larger key; +0 and -0 alike; NaN as
@@ -64,7 +67,7 @@ struct BestTwo {
 // kPer = logits a lane holds (E <= 32 * kPer); logit e in lane e % 32.  counts: [chunks][E], one
 // row written by each block, or NULL for a batch of one chunk.
 template <int kPer>
-__global__ void __launch_bounds__(kChooseThreads, 1)
+__global__ void __launch_bounds__(choose_threads(kPer), 1)
 k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *__restrict__ counts) {
     extern __shared__ uint32_t s_hist[];               // [E], of this block's chunk
     grid_dep_wait();
@@ -260,7 +263,11 @@ k_route_place(const inkattn_route_params p, int chunk_tokens, int words, const u
     } while (t0 < t_hi);
 }
 
-static bool one_chunk(const inkattn_route_params &p) { return p.N_tok <= kPlaceTokens; }
+// One block places few pairs sooner than many blocks do, which need the counts first: 500 tokens
+// with 6 choices 7.7 us against 8.2, 1000 tokens 10.4 against 8.4 (and 64 experts, 4 choices 7.7 against 6.3).
+static bool one_chunk(const inkattn_route_params &p) {
+    return p.N_tok <= kPlaceTokens && p.N_tok * p.top_k <= kPlaceOnePairs;
+}
 static int chunk_tokens(const inkattn_route_params &p) {
     const int t = (p.N_tok + kChunks - 1) / kChunks;
     return t < 32 ? 32 : t;
@@ -275,7 +282,6 @@ size_t route_workspace_bytes(const inkattn_route_params &p) {
 cudaError_t launch_route(const inkattn_route_params &p, uint32_t *ws, cudaStream_t stream) {
     const bool one = one_chunk(p);
     // the choice of a small batch: a token per warp
-    const int choose_threads = one ? kChooseThreadsOne : kChooseThreads;
     const int choose_tokens = one ? kChooseThreadsOne / 32 : chunk_tokens(p);
     const int place_tokens = one ? (p.N_tok > 0 ? p.N_tok : 1) : chunk_tokens(p);
     uint32_t *counts = one ? nullptr : ws;
@@ -283,11 +289,13 @@ cudaError_t launch_route(const inkattn_route_params &p, uint32_t *ws, cudaStream
     if (p.N_tok > 0) {
         const dim3 grid((unsigned)((p.N_tok + choose_tokens - 1) / choose_tokens));
         const size_t smem = one ? 0 : (size_t)p.E * 4;
-        auto go = [&](auto kernel) {
-            return launch_dependent(kernel, grid, dim3((unsigned)choose_threads), smem, stream, 1, p, choose_tokens, counts);
+        auto go = [&](auto kernel, int per) {
+            const int threads = one ? kChooseThreadsOne : choose_threads(per);
+            return launch_dependent(kernel, grid, dim3((unsigned)threads), smem, stream, 1, p, choose_tokens, counts);
         };
-        err = p.E <= 64 ? go(k_route_choose<2>) : p.E <= 128 ? go(k_route_choose<4>) : p.E <= 256
-            ? go(k_route_choose<8>) : p.E <= 512 ? go(k_route_choose<16>) : go(k_route_choose<32>);
+        err = p.E <= 64 ? go(k_route_choose<2>, 2) : p.E <= 128 ? go(k_route_choose<4>, 4) : p.E <= 256
+            ? go(k_route_choose<8>, 8) : p.E <= 384 ? go(k_route_choose<12>, 12) : p.E <= 512 ? go(k_route_choose<16>, 16)
+            : go(k_route_choose<32>, 32);
         if (err != cudaSuccess) return err;
     }
     const int words = ((place_tokens < kPlaceTokens ? place_tokens : kPlaceTokens) + 31) / 32;

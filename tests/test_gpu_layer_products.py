@@ -498,6 +498,17 @@ def test_route(ia, T, E, S, k, score):
     _check_route(_route(ia, tied, S, k, score, scale=2.5), tied, S, k, score, scale=2.5)
 
 
+@pytest.mark.parametrize("T,E,S,k", [(500, 64, 1, 6), (501, 64, 1, 6), (375, 300, 0, 8), (376, 300, 0, 8), (1000, 384, 2, 3),
+                                     (1001, 385, 2, 3), (1024, 20, 0, 2), (1025, 20, 0, 2), (1024, 6, 1, 1), (700, 513, 0, 4),
+                                     (701, 1000, 1, 5), (33, 1024, 16, 16)])
+def test_route_around_one_block(ia, T, E, S, k):
+    """Batches that one block places, just not any more, and few choices of many tokens."""
+    g = torch.Generator().manual_seed(T + E)
+    logits = torch.randn((T, E + S), generator=g)
+    logits[::3] = torch.round(logits[::3] * 2) / 2             # ties
+    _check_route(_route(ia, logits, S, k), logits, S, k, "sigmoid")
+
+
 @pytest.mark.parametrize("T", [7, 1000])
 def test_route_same_choice_for_every_token(ia, T):
     """Every token takes the same experts: all rows in k groups."""
