@@ -97,6 +97,10 @@ struct LinearArgs {
                              // first accumulator release, so the MMA warp's wait runs out
 };
 cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStream_t stream);
+// A linear layer of few tokens without the tensor cores (csrc/linear_few.cu), and whether it is
+// taken.
+bool linear_few(const LinearArgs &a, int act);
+cudaError_t launch_linear_few(const LinearArgs &a, int act, cudaStream_t stream);
 // TMA descriptors of a launch: x rows in boxes of 64 columns x 16 (i + 1) rows, up to half a
 // token tile (none where the rows are gathered by index); the weights as [E][F][K] (box 64 x
 // 128 rows) or, gated, as [E][gate, up][F][K] (box 64 x 64 gate and the 64 up rows); 128-byte

@@ -248,6 +248,42 @@ def test_linear_infinite_sums(ia, act, dtype, T, K, F):
     assert bool(((got.double() - want).abs() <= slack)[live].all())
 
 
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 7, 8])
+@pytest.mark.parametrize("K,F", [(8, 1), (8, 5), (264, 33), (512, 7), (520, 250), (2056, 1021), (4096, 3), (4104, 700),
+                                 (8200, 129)])
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "swiglu"])
+def test_linear_few_tokens(ia, T, K, F, act):
+    """Few tokens: every count of them, rows of one, a few and many pieces of 16 bytes, odd widths."""
+    x, w, bias, residual = _linear_inputs(T, K, F, act, seed=T + K + F)
+    v = x.double() @ w.double().t()
+    for dtype in (BF16, F32):
+        for b, r in ((bias, residual), (None, None)):
+            if act == "relu" and r is not None:
+                continue                                       # (a sum that is not a grid value)
+            got = _run_linear(ia, x, w, b, r, act, dtype, F)
+            _check(got, v + b.double() if b is not None else v, act, r.double() if r is not None else None)
+
+
+@pytest.mark.parametrize("T,K,F,act", [(1, 8192, 8192, "none"), (2, 8192, 1000, "swiglu"), (3, 4096, 2800, "gelu"),
+                                       (4, 4096, 3000, "none"), (6, 2048, 2900, "none"), (8, 2048, 3000, "silu")])
+def test_linear_few_tokens_gaussian(ia, T, K, F, act):
+    """Both sides of the sizes up to which the tensor cores are left out; in place, and NaN and
+    infinity in one token's row leave the others as they are."""
+    x, w, bias, residual = _linear_inputs(T, K, F, act, seed=T + K + F, grid=False)
+    v = x.double() @ w.double().t() + bias.double()
+    mags = x.double().abs() @ w.double().abs().t() + bias.double().abs()
+    _check(_run_linear(ia, x, w, bias, residual, act, F32, F), v, act, residual.double(), sum_slack=K * 2.0 ** -23 * mags)
+    dev = [t.cuda() for t in (x, w, bias)]
+    out = residual.cuda()
+    ia.inkattn_linear(ia.linear_params(x=dev[0], w=dev[1], out=out, act=act, bias=dev[2], residual=out))
+    torch.cuda.synchronize()
+    _check(out, v, act, residual.double(), sum_slack=K * 2.0 ** -23 * mags)
+    if T > 1:
+        x[T - 1, 3], x[T - 1, 7] = float("nan"), float("inf")
+        dirty = _run_linear(ia, x, w, bias, residual, act, BF16, F)
+        assert torch.equal(dirty[:T - 1], out[:T - 1]) and bool(torch.isnan(dirty[T - 1]).all())
+
+
 def test_linear_no_tokens_and_repeatability(ia):
     x, w, bias, residual = [t.cuda() for t in _linear_inputs(64, 4096, 512, "none", seed=9, grid=False)]
     empty = torch.empty((0, 512), dtype=BF16, device="cuda")
