@@ -7,7 +7,8 @@
 //  routed and shared experts.
 //
 // out[i][f] = act( sum_k x[s_i][k] w[e][f][k] + bias[e][f] ) + residual[i][f] over the rows i of
-// each expert e; a linear layer is the case of one expert that owns every row.
+// each expert e; a linear layer is the case of one expert that owns every row (of few tokens:
+// linear_few.cu).
 //
 // Orientation.  The weight rows are the MMA's M side and the tokens its N side: a work item is
 // 256 weight rows times up to 256 tokens, computed by the two CTAs of a pair as one
@@ -58,10 +59,10 @@
 // 11000 cycles for 256 tokens and S = 4: 12 bytes a cycle.)
 //
 // Measured (back to back on one GB300): 8192 x 8192 x 8192 0.56 ms, 1950 TFLOP/s in a burst with
-// the tensor pipe 89.5% active, 1670 under the power cap; 1 x 8192 x 8192 24 us, the weights at 7.2
+// the tensor pipe 89.5% active, 1710 under the power cap; 4 x 8192 x 8192 23.3 us, the weights at 7.2
 // TB/s for 18.5 of them; 288 x 8192 x 8192 34 us, bound by the 64 bytes a cycle into an SM; 256
 // experts 8192 -> 2 x 1024 for 1728 gathered rows 1.03 ms, 8.3 TB/s of weights; 64 experts 4096 ->
-// 2 x 2048 for 49152 gathered rows 1.04 ms, 1590 TFLOP/s (tensor pipe 75%; 0.98 ms on contiguous
+// 2 x 2048 for 49152 gathered rows 1.02 ms, 1615 TFLOP/s (tensor pipe 75%; 0.98 ms on contiguous
 // rows).
 #include <atomic>
 #include <climits>
