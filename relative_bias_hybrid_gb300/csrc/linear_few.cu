@@ -1,4 +1,4 @@
-// linear_few.cu -- linear layers of up to eight tokens, without the tensor cores.
+// linear_few.cu -- linear layers of few tokens, or small ones, without the tensor cores.
 //
 // out[t][f] = act( sum_k x[t][k] w[f][k] + bias[f] ) + residual[t][f]
 //
@@ -30,6 +30,7 @@ namespace {
 
 __host__ __device__ constexpr int rows_of_group(int tok) { return tok > 4 ? 4 : 2; }   // weight rows
 constexpr int kU = 4;                              // pieces of a row requested together
+constexpr int kMostTokens = 256;
 constexpr int kFewThreads = 128;                   // of a block, or one group of more
 
 __device__ __forceinline__ float activate_any(int act, float v) {
@@ -43,7 +44,7 @@ __device__ __forceinline__ float activate_any(int act, float v) {
 
 }  // namespace
 
-// kTok: tokens, or more; kWarps: warps of a group.  Tokens behind the last and rows behind the last
+// kTok: tokens of a block, or more; kWarps: warps of a group.  Tokens behind the last and rows behind the last
 // feature read the last one's and are not stored.
 template <int kTok, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32 > kFewThreads ? kWarps * 32 : kFewThreads)
@@ -58,7 +59,7 @@ k_linear_few(const LinearArgs A, int act) {
     const int group = (int)blockIdx.x * kGroups + warp / kWarps;
     const bool gated = act == INKATTN_ACT_SWIGLU;
     const int feats = gated ? kR / 2 : kR, f0 = group * feats;
-    const int pieces = A.K >> 3;
+    const int pieces = A.K >> 3, t0 = (int)blockIdx.y * kTok;
     const uint4 *w[kR], *x[kTok];
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
@@ -66,7 +67,7 @@ k_linear_few(const LinearArgs A, int act) {
         w[r] = reinterpret_cast<const uint4 *>(A.w) + ((size_t)f + (gated && r >= kR / 2 ? (size_t)A.F : 0)) * pieces;
     }
 #pragma unroll
-    for (int t = 0; t < kTok; ++t) x[t] = reinterpret_cast<const uint4 *>(A.x) + (size_t)min(t, A.M - 1) * pieces;
+    for (int t = 0; t < kTok; ++t) x[t] = reinterpret_cast<const uint4 *>(A.x) + (size_t)min(t0 + t, A.M - 1) * pieces;
     float2 acc[kR][kTok] = {};
     constexpr int kStep = kWarps * 32;
     for (int p0 = (warp % kWarps) * 32 + lane; p0 < pieces; p0 += kStep * kU) {
@@ -127,13 +128,13 @@ k_linear_few(const LinearArgs A, int act) {
     // one thread an output
     const int i = kWarps > 1 ? (int)threadIdx.x : lane;
     if (i >= feats * kTok) return;
-    const int t = i / feats, f = f0 + i % feats;
+    const int n0 = i / feats * kR + i % feats, t = t0 + i / feats, f = f0 + i % feats;
     if (t >= A.M || f >= A.F) return;
     float y[2];                                    // (gated: the gate and the up)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float s = 0.f;
-        const int n = t * kR + i % feats + (h ? kR / 2 : 0);
+        const int n = n0 + (h ? kR / 2 : 0);
         if (h == 0 || gated) {
 #pragma unroll
             for (int q = 0; q < kWarps; ++q) s += s_part[kWarps > 1 ? q : warp][n];
@@ -151,11 +152,19 @@ k_linear_few(const LinearArgs A, int act) {
 
 // Whether it is faster than the tensor-core kernel: up to two tokens always; three and four up to
 // 24 MB of weights (4096 x 2048 6.9 us against 7.6, 4096 x 4096 10.2 against 9.9); five to eight up to
-// 12 MB (2048 x 2048 5.6 against 6.0, 4096 x 2048 8.0 against 7.6).
+// 12 MB (2048 x 2048 5.6 against 6.0, 4096 x 2048 8.0 against 7.6).  More tokens read the weights once
+// for every eight, from L2, and what that reads decides: up to 4 MB (16 tokens 1024 x 1024 4.1
+// against 4.4, 24 tokens 5.4 against 4.4; 64 tokens 512 x 512 3.0 against 4.4), or more where the
+// tensor cores have one feature block and a long K (64 tokens 8192 x 128 6.8 against 8.5); and the
+// rows, whose ends cost as much as short rows do (64 tokens 64 x 1000 3.9 against 3.6).
 bool linear_few(const LinearArgs &a, int act) {
-    if (a.offsets || a.M > 8) return false;
-    const double bytes = 2.0 * a.F * a.K * (act == INKATTN_ACT_SWIGLU ? 2 : 1);
-    return a.M <= 2 || bytes <= (a.M <= 4 ? 24e6 : 12e6);
+    if (a.offsets || a.M > kMostTokens) return false;
+    const int times = (a.M + 7) / 8, factor = act == INKATTN_ACT_SWIGLU ? 2 : 1;
+    const double rows = (double)a.F * factor, bytes = 2.0 * rows * a.K;
+    if (a.M <= 4) return a.M <= 2 || bytes <= 24e6;
+    if (rows * times > 6000) return false;
+    if (a.M <= 8) return bytes <= 12e6;
+    return bytes * times <= 4.2e6 * (rows <= 256 && a.K > 2048 ? a.K / 2048.0 : 1.0);
 }
 
 cudaError_t launch_linear_few(const LinearArgs &a, int act, cudaStream_t stream) {
@@ -165,7 +174,7 @@ cudaError_t launch_linear_few(const LinearArgs &a, int act, cudaStream_t stream)
     auto go = [&](auto kernel, int warps) {
         const int threads = warps * 32 > kFewThreads ? warps * 32 : kFewThreads;
         const int per = threads / (warps * 32);
-        return launch_dependent(kernel, dim3((unsigned)((groups + per - 1) / per)), dim3((unsigned)threads), 0, stream, 1, a, act);
+        return launch_dependent(kernel, dim3((unsigned)((groups + per - 1) / per), (unsigned)((a.M + 7) / 8)), dim3((unsigned)threads), 0, stream, 1, a, act);
     };
     // (sixteen warps a row where there are few rows, so that the SMs have enough requests in flight)
     const int warps = pieces <= 64 ? 1 : groups <= 304 && pieces >= 512 ? 16 : 4;

@@ -264,6 +264,17 @@ def test_linear_few_tokens(ia, T, K, F, act):
             _check(got, v + b.double() if b is not None else v, act, r.double() if r is not None else None)
 
 
+@pytest.mark.parametrize("T", [9, 16, 17, 63, 129, 255, 256, 257])
+@pytest.mark.parametrize("K,F", [(8, 1), (64, 37), (72, 300), (512, 24), (1000, 129), (4104, 30)])
+@pytest.mark.parametrize("act", ["none", "silu", "swiglu"])
+def test_linear_of_small_layers(ia, T, K, F, act):
+    """Small layers of more tokens, eight at a time, and the sizes from which the tensor cores take over."""
+    x, w, bias, residual = _linear_inputs(T, K, F, act, seed=T + K + F)
+    v = x.double() @ w.double().t()
+    _check(_run_linear(ia, x, w, bias, residual, act, BF16, F), v + bias.double(), act, residual.double())
+    _check(_run_linear(ia, x, w, None, None, act, F32, F), v, act)
+
+
 @pytest.mark.parametrize("T,K,F,act", [(1, 8192, 8192, "none"), (2, 8192, 1000, "swiglu"), (3, 4096, 2800, "gelu"),
                                        (4, 4096, 3000, "none"), (6, 2048, 2900, "none"), (8, 2048, 3000, "silu")])
 def test_linear_few_tokens_gaussian(ia, T, K, F, act):
