@@ -463,7 +463,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             uint32_t row[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                row[j] = r0 + 8 * j < mine ? (uint32_t)__ldg(A.row_token + it.row0 + half * hn + r0 + 8 * j) : 0u;
+                row[j] = r0 + 8 * j < mine ? (uint32_t)load_i32(A.row_token + it.row0 + half * hn + r0 + 8 * j) : 0u;
                 if (row[j] >= (uint32_t)A.N_x) row[j] = 0;    // (flagged and not stored by the epilogue)
             }
             int k = k_lo + first;
@@ -607,7 +607,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
             const int frow = f0 + lane;
             float bias = 0.f;
             if (A.bias && frow < A.F)
-                bias = __ldg(A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + (kGated && quarter >= 2 ? F : 0) + frow);
+                bias = load_f32(A.bias + (size_t)it.e * F * (kGated ? 2 : 1) + (kGated && quarter >= 2 ? F : 0) + frow);
             const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
             const int nblocks = (it.nt + 31) >> 5;
             for (int q = 0; q < parts; ++q, ++i) {
@@ -644,7 +644,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                     // tokens of this block that are stored
                     bool mine = c * 32 + lane < it.nt;
                     if (!kResid && A.row_token && mine) {
-                        const int t = __ldg(A.row_token + it.row0 + c * 32 + lane);
+                        const int t = load_i32(A.row_token + it.row0 + c * 32 + lane);
                         if (t < 0 || t >= A.N_x) {
                             mine = false;
                             set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
@@ -749,7 +749,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                 if (f >= A.F) continue;
                 const int i = it.row0 + split * share + t;
                 if (A.row_token) {
-                    const int s = __ldg(A.row_token + i);
+                    const int s = load_i32(A.row_token + i);
                     if (s < 0 || s >= A.N_x) {
                         if (j == 0) set_status(A.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
                         continue;
@@ -774,8 +774,8 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     const bool in = f + n < A.F;
-                    y[n] = activate<kGated ? INKATTN_ACT_SILU : kAct>(sum[n] + (b && in ? __ldg(b + n) : 0.f));
-                    if (kGated) y[n] *= up[n] + (b && in ? __ldg(b + F + n) : 0.f);
+                    y[n] = activate<kGated ? INKATTN_ACT_SILU : kAct>(sum[n] + (b && in ? load_f32(b + n) : 0.f));
+                    if (kGated) y[n] *= up[n] + (b && in ? load_f32(b + F + n) : 0.f);
                 }
                 if (vec) {
                     if (kResid) {

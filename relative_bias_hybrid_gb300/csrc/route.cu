@@ -68,7 +68,7 @@ struct BestTwo {
 // row written by each block, or NULL for a batch of one chunk.
 template <int kPer>
 __global__ void __launch_bounds__(choose_threads(kPer), 1)
-k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *__restrict__ counts) {
+k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *counts) {
     extern __shared__ uint32_t s_hist[];               // [E], of this block's chunk
     grid_dep_wait();
     grid_dep_launch();
@@ -85,8 +85,8 @@ k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *__restr
     auto request = [&](int t) {
         const float *row = p.logits + (size_t)t * width;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) next[i] = lane + 32 * i < p.E ? __ldg(row + lane + 32 * i) : -INFINITY;
-        if (is_shared) next_shared = __ldg(row + p.E + lane - p.top_k);
+        for (int i = 0; i < kPer; ++i) next[i] = lane + 32 * i < p.E ? load_f32(row + lane + 32 * i) : -INFINITY;
+        if (is_shared) next_shared = load_f32(row + p.E + lane - p.top_k);
     };
     if (t_lo + warp < t_hi) request(t_lo + warp);
     for (int t = t_lo + warp; t < t_hi; t += warps) {
@@ -160,7 +160,7 @@ k_route_choose(const inkattn_route_params p, int chunk_tokens, uint32_t *__restr
 // One block per chunk.  Shared memory: base[E] (row of the expert's next pair), scratch[2
 // kPlaceThreads], bits[words][E], before[words][E] (16 bits: bits in earlier words).
 __global__ void __launch_bounds__(kPlaceThreads)
-k_route_place(const inkattn_route_params p, int chunk_tokens, int words, const uint32_t *__restrict__ counts) {
+k_route_place(const inkattn_route_params p, int chunk_tokens, int words, const uint32_t *counts) {
     extern __shared__ uint32_t sm[];
     grid_dep_wait();
     grid_dep_launch();
@@ -204,7 +204,7 @@ k_route_place(const inkattn_route_params p, int chunk_tokens, int words, const u
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     const int c = c0 + q * parts;
-                    n[q] = c < chunks ? __ldg(counts + (size_t)c * E + e) : 0u;
+                    n[q] = c < chunks ? (uint32_t)load_i32(reinterpret_cast<const int32_t *>(counts) + (size_t)c * E + e) : 0u;
                 }
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -353,16 +353,16 @@ k_expert_combine(const inkattn_expert_combine_params p, int shift, int chunks) {
                 c[n][i] = 0.f;
                 if (j >= rows || (kTokens > 1 && t >= p.N_tok)) continue;
                 if (j < p.top_k) {
-                    const int r = __ldg(p.token_rows + t * p.top_k + j);
+                    const int r = load_i32(p.token_rows + t * p.top_k + j);
                     if (r >= 0 && r < p.M) {
-                        c[n][i] = __ldg(p.weights + t * rows + j);
-                        v[n][i] = __ldcs(y + (size_t)r * G + g);
+                        c[n][i] = load_f32(p.weights + t * rows + j);
+                        v[n][i] = load_stream(y + (size_t)r * G + g);
                     } else if (r != -1 && g == 0) {
                         set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
                     }
                 } else {
-                    c[n][i] = __ldg(p.weights + t * rows + j);
-                    v[n][i] = __ldcs(sh + ((size_t)(j - p.top_k) * p.N_tok + t) * G + g);
+                    c[n][i] = load_f32(p.weights + t * rows + j);
+                    v[n][i] = load_stream(sh + ((size_t)(j - p.top_k) * p.N_tok + t) * G + g);
                 }
             }
         }
