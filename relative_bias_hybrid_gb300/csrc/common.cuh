@@ -55,12 +55,17 @@ __device__ __forceinline__ int load_i32(const int32_t *p) {
     asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(reinterpret_cast<uint64_t>(p)));
     return v;
 }
+__device__ __forceinline__ uint32_t load_u32(const void *p) {
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(reinterpret_cast<uint64_t>(p)));
+    return v;
+}
 __device__ __forceinline__ float load_f32(const float *p) {
     float v;
     asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(reinterpret_cast<uint64_t>(p)));
     return v;
 }
-__device__ __forceinline__ uint4 load_u32x4(const uint4 *p) {
+__device__ __forceinline__ uint4 load_u32x4(const void *p) {
     uint4 v;
     asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(reinterpret_cast<uint64_t>(p)));

@@ -493,7 +493,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                             const int tt = gq + ((e & 1) << 3);
                             const int col = kk * 16 + 2 * tq + ((e >> 1) << 3);
                             const uint32_t w2 = tt < q_len
-                                ? __ldg(reinterpret_cast<const uint32_t *>(rh + (size_t)tt * 32 * p.Hq + col))
+                                ? load_u32(rh + (size_t)tt * 32 * p.Hq + col)
                                 : 0u;
                             rv[kk][e][0] = bf16_lo(w2);
                             rv[kk][e][1] = bf16_hi(w2);

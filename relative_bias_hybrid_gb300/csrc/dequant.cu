@@ -67,12 +67,11 @@ k_dequant_e4m3(const inkattn_attn_params p, inkattn_bf16 *k_out, inkattn_bf16 *v
     for (int i = 0; i < 4; ++i) o[i] = make_uint4(0, 0, 0, 0);
     if (phys_ok && (long long)j * kBlock + r < T) {
         const size_t src_row = ((size_t)phys * p.Hkv + hk) * kBlock + r;
-        const float s = __ldg((stream == 0 ? p.k_scale : p.v_scale) + src_row);
+        const float s = load_f32((stream == 0 ? p.k_scale : p.v_scale) + src_row);
         if (s >= 0x1p-24f && s <= 0x1p7f) {
             const unsigned char *codes =
                 static_cast<const unsigned char *>(stream == 0 ? p.k_cache : p.v_cache) + src_row * kHeadDim + qd * 32;
-            const uint4 c[2] = {__ldg(reinterpret_cast<const uint4 *>(codes)),
-                                __ldg(reinterpret_cast<const uint4 *>(codes + 16))};
+            const uint4 c[2] = {load_u32x4(codes), load_u32x4(codes + 16)};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t w[4] = {c[h].x, c[h].y, c[h].z, c[h].w};

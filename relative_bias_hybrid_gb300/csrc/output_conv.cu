@@ -77,12 +77,12 @@ __global__ void __launch_bounds__(kOcThreads, 2) k_output_conv(const inkattn_out
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             const int xi = t0 + i;
-            xr[i] = xi < 3 ? state[(size_t)xi * G + g] : __ldg(y + (size_t)(xi - 3) * G + g);
+            xr[i] = *((xi < 3 ? state + (size_t)xi * G : y + (size_t)(xi - 3) * G) + g);
         }
 #pragma unroll
         for (int j = 0; j < kOcTokens; ++j) {
             if (j < nt) {
-                xr[3 + j] = __ldg(y + (size_t)(t0 + j) * G + g);
+                xr[3 + j] = y[(size_t)(t0 + j) * G + g];
                 rv[j] = res[(size_t)j * G + g];
             }
         }
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kOcThreads, 2) k_output_conv(const inkattn_out
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 const int xi = q_len + i;
-                nv[i] = xi < 3 ? state[(size_t)xi * G + g] : __ldg(y + (size_t)(xi - 3) * G + g);
+                nv[i] = *((xi < 3 ? state + (size_t)xi * G : y + (size_t)(xi - 3) * G) + g);
             }
 #pragma unroll
             for (int i = 0; i < 3; ++i) state[(size_t)i * G + g] = nv[i];

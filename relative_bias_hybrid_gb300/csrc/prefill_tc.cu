@@ -428,7 +428,7 @@ k_prefill_tc(const TcArgs A, const __grid_constant__ CUtensorMap qmap,
                 if (row < q_len) {
                     const uint4 *src = reinterpret_cast<const uint4 *>(p.r + ((size_t)(start + row) * p.Hq + h) * d_r);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) u[j] = __ldg(src + j);
+                    for (int j = 0; j < 4; ++j) u[j] = load_u32x4(src + j);
                 }
                 float n2 = 0.f;
 #pragma unroll

@@ -99,8 +99,7 @@ k_prologue(const inkattn_prologue_params p, const int kv_tiles) {
                 qraw[j] = make_uint4(0, 0, 0, 0);
                 if (row < q_rows) {
                     const int tt = div_g(row), h = hk * g + (row - tt * g);
-                    qraw[j] = __ldg(reinterpret_cast<const uint4 *>(
-                        qb + (uint32_t)((tt * p.Hq + h) * kHeadDim + c0)));
+                    qraw[j] = load_u32x4(qb + (uint32_t)((tt * p.Hq + h) * kHeadDim + c0));
                 }
             }
 #pragma unroll
@@ -158,8 +157,8 @@ k_prologue(const inkattn_prologue_params p, const int kv_tiles) {
             vv = *reinterpret_cast<const uint4 *>(p.conv_state_v + o);
         } else {
             const size_t o = ((size_t)start + idx - 3) * C + ch;
-            vk = __ldg(reinterpret_cast<const uint4 *>(p.k + o));
-            vv = __ldg(reinterpret_cast<const uint4 *>(p.v + o));
+            vk = load_u32x4(p.k + o);
+            vv = load_u32x4(p.v + o);
         }
         s_x[0][r][chunk] = vk;
         s_x[1][r][chunk] = vv;
@@ -267,7 +266,7 @@ k_prologue(const inkattn_prologue_params p, const int kv_tiles) {
             nv = *reinterpret_cast<const uint4 *>(st + ((size_t)slot * 3 + idx) * C + ch);
         } else {
             const inkattn_bf16 *src = sstream == 0 ? p.k : p.v;
-            nv = __ldg(reinterpret_cast<const uint4 *>(src + ((size_t)start + idx - 3) * C + ch));
+            nv = load_u32x4(src + ((size_t)start + idx - 3) * C + ch);
         }
     }
     __syncthreads();   // every read of the old state (the staged rows and the rows above) is done

@@ -204,7 +204,7 @@ k_route_place(const inkattn_route_params p, int chunk_tokens, int words, const u
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     const int c = c0 + q * parts;
-                    n[q] = c < chunks ? (uint32_t)load_i32(reinterpret_cast<const int32_t *>(counts) + (size_t)c * E + e) : 0u;
+                    n[q] = c < chunks ? load_u32(counts + (size_t)c * E + e) : 0u;
                 }
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {

@@ -16,3 +16,17 @@ def test_no_non_coherent_loads(name):
     load, so nothing keeps it behind the wait."""
     text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
     assert re.findall(r"__ldg|__ldcs|ld\.global\.nc|__restrict__", text) == []
+
+
+@pytest.mark.parametrize("name,arrays", [
+    ("output_conv.cu", ["y"]),                       # of inkattn_linear or inkattn_expert_combine
+    ("prologue.cu", [r"reinterpret_cast<const uint4 \*>\(\s*qb", r"reinterpret_cast<const uint4 \*>\(p\.[kv] ",
+                     r"reinterpret_cast<const uint4 \*>\(src"]),   # q, k and v, of inkattn_linear
+    ("prefill_tc.cu", [r"src \+ j\);\s*\}\s*float n2"]),           # r, of inkattn_qkvr_prologue
+    ("decode_tc.cu", [r"reinterpret_cast<const uint32_t \*>\(rh"]),
+    ("dequant.cu", [r"\(stream == 0 \? p\.k_scale", r"reinterpret_cast<const uint4 \*>\(codes"])])   # of the prologue
+def test_outputs_of_early_kernels_are_read_coherently(name, arrays):
+    """The same for what the other kernels read of a kernel that lets its successor start early."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+    for a in arrays:
+        assert not re.search(r"__ldg\(" + a, text), a
