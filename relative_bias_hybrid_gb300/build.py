@@ -16,7 +16,7 @@ LIB = os.path.join(PKG, "libinkattn.so")
 SOURCES = ["api.cu", "prologue.cu", "decode.cu", "decode_tc.cu", "prefill_tc.cu", "prefill_2q.cu", "decode_noalloc.cu",
            "output_conv.cu", "qkvr.cu", "dequant.cu", "linear.cu", "linear_few.cu", "route.cu"]
 HEADERS = ["common.cuh", "internal.h", "tcgen05.cuh", "context_cache.h", "conv4.cuh", "fp8.cuh", "cta_pair.cuh",
-           "activation.cuh"]
+           "activation.cuh", "device_table.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-Xptxas", "-warn-spills"]

@@ -64,13 +64,13 @@
 // experts 8192 -> 2 x 1024 for 1728 gathered rows 1.03 ms, 8.3 TB/s of weights; 64 experts 4096 ->
 // 2 x 2048 for 49152 gathered rows 1.02 ms, 1615 TFLOP/s (tensor pipe 75%; 0.98 ms on contiguous
 // rows).
-#include <atomic>
 #include <climits>
 #include <cmath>
 #include <type_traits>
 
 #include "activation.cuh"
 #include "common.cuh"
+#include "device_table.h"
 #include "internal.h"
 #include "tcgen05.cuh"
 #include "cta_pair.cuh"
@@ -826,30 +826,29 @@ Kernel kernel_of(int act) {
     }
 }
 
-// Clusters of `ctas` CTAs that are resident at once (one CTA per SM; every activation's kernel
-// has the same launch shape).
-int resident_clusters(int ctas, int num_sms) {
-    static std::atomic<int> known[4];
-    std::atomic<int> &slot = known[ctas == 2 ? 0 : ctas == 4 ? 1 : 2];
-    int n = slot.load(std::memory_order_relaxed);
-    if (n > 0) return n;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(ctas * (num_sms / ctas > 0 ? num_sms / ctas : 1)), 1, 1);
-    cfg.blockDim = dim3(kMaxThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)ctas;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, k_linear<INKATTN_ACT_NONE, false, false>, &cfg) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return 0;
-    }
-    slot.store(n, std::memory_order_relaxed);
-    return n;
+// Clusters of `ctas` CTAs that are resident at once on the current device `dev` (one CTA per SM;
+// every activation's kernel has the same launch shape).
+int resident_clusters(int dev, int ctas, int num_sms) {
+    static DeviceTable<64, 3> table;
+    return table.get(dev, ctas == 2 ? 0 : ctas == 4 ? 1 : 2, [&] {
+        int n = 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(ctas * (num_sms / ctas > 0 ? num_sms / ctas : 1)), 1, 1);
+        cfg.blockDim = dim3(kMaxThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)ctas;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, k_linear<INKATTN_ACT_NONE, false, false>, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return 0;
+        }
+        return n;
+    });
 }
 
 // What a launch would take, in microseconds: the model that picks the token tile and the
@@ -890,7 +889,10 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     const long long owners = a.offsets ? (a.E < a.M ? a.E : a.M) : 1;
     const long long rows = (a.M + owners - 1) / owners;
     const double weight_bytes = (double)owners * a.n_fblocks * 2 * kRowsA * a.K * 2;
-    if (resident_clusters(2, num_sms) < 1) return cudaErrorInvalidConfiguration;
+    int dev = 0;
+    if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
+    auto resident = [&](int ctas) { return resident_clusters(dev, ctas, num_sms); };
+    if (resident(2) < 1) return cudaErrorInvalidConfiguration;
     int most_n = a.out_f32 ? kFineN : kMaxN;
     if (a.offsets && 4 * rows < most_n) most_n = rows < 16 ? 64 : (int)(4 * rows + 31) / 32 * 32;
     double best = 0.0;
@@ -903,8 +905,8 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
         const long long bound = (a.offsets ? a.M / tile + owners : each) * a.n_fblocks;
         if (bound > INT_MAX / 2) continue;
         for (int s = 1; s <= kMaxSplits; s *= 2) {
-            if (s > 1 && (nk < 2 * s || bound > resident_clusters(2 * s, num_sms))) break;
-            const double us = launch_us(owners * each * a.n_fblocks, n, nk, s, resident_clusters(2, num_sms), weight_bytes);
+            if (s > 1 && (nk < 2 * s || bound > resident(2 * s))) break;
+            const double us = launch_us(owners * each * a.n_fblocks, n, nk, s, resident(2), weight_bytes);
             if (a.tile_n == 0 || us < best) {
                 best = us;
                 most_items = bound;
@@ -916,7 +918,7 @@ cudaError_t launch_linear(const LinearArgs &args, int act, int num_sms, cudaStre
     if (a.tile_n == 0) return cudaErrorInvalidConfiguration;
     a.stage_bytes = kABytes + a.tile_n / 2 * 128;
     a.stages = kRingBytes / a.stage_bytes < kMaxStages ? kRingBytes / a.stage_bytes : kMaxStages;
-    const int most = resident_clusters(2 * a.splits, num_sms);
+    const int most = resident(2 * a.splits);
     const int clusters = (int)(most_items < most ? most_items : most);
     LinearMaps maps = {};
     if (!make_linear_maps(a, act == INKATTN_ACT_SWIGLU, &maps)) return cudaErrorInvalidValue;
