@@ -250,8 +250,7 @@ def inkattn_prefill_workspace_bytes(p: AttnParams) -> int:
 
 def inkattn_prefill_e4m3(p: AttnParams, workspace: Optional[torch.Tensor], stream=None,
                          raise_on_error=True) -> int:
-    ptr = workspace.data_ptr() if workspace is not None else None
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ptr, nbytes = _workspace(workspace)
     return _check(lib().inkattn_prefill_e4m3(ctypes.byref(p), ptr, nbytes, _stream(stream)),
                   "inkattn_prefill_e4m3", raise_on_error)
 
@@ -266,16 +265,14 @@ def inkattn_decode_workspace_bytes(p: AttnParams, num_splits: int) -> int:
 
 def inkattn_decode(p: AttnParams, num_splits: int, workspace: Optional[torch.Tensor], stream=None,
                    raise_on_error=True) -> int:
-    ptr = workspace.data_ptr() if workspace is not None else None
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ptr, nbytes = _workspace(workspace)
     return _check(lib().inkattn_decode(ctypes.byref(p), int(num_splits), ptr, nbytes, _stream(stream)),
                   "inkattn_decode", raise_on_error)
 
 
 def inkattn_combine(p: AttnParams, num_splits: int, workspace: Optional[torch.Tensor], stream=None,
                     raise_on_error=True) -> int:
-    ptr = workspace.data_ptr() if workspace is not None else None
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ptr, nbytes = _workspace(workspace)
     return _check(lib().inkattn_combine(ctypes.byref(p), int(num_splits), ptr, nbytes, _stream(stream)),
                   "inkattn_combine", raise_on_error)
 
@@ -318,8 +315,7 @@ def inkattn_route_workspace_bytes(p: RouteParams) -> int:
 
 def inkattn_route(p: RouteParams, workspace: Optional[torch.Tensor] = None, stream=None,
                   raise_on_error=True) -> int:
-    ptr = workspace.data_ptr() if workspace is not None else None
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ptr, nbytes = _workspace(workspace)
     return _check(lib().inkattn_route(ctypes.byref(p), ptr, nbytes, _stream(stream)), "inkattn_route",
                   raise_on_error)
 
@@ -337,6 +333,16 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, name="tensor") -> Optional[int]:
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _workspace(t: Optional[torch.Tensor]):
+    """Address and bytes of a workspace tensor.  One whose elements share memory (an expanded tensor)
+    has fewer bytes than elements and is refused."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous() and 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())) < t.numel():
+        raise ValueError("workspace: elements that share memory")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _kv_dtype(cache):
