@@ -48,8 +48,8 @@ __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol
 // stream may have written.  Coherent ones: ld.global.nc (__ldg, or a const __restrict__ pointer)
 // promises that nobody writes the memory while the kernel is resident, which a kernel resident
 // before its predecessor has finished cannot promise.  Volatile, so that the compiler keeps
-// them behind grid_dep_wait(); without a clobber of memory, so that they may still move past the
-// kernel's own stores.  load_stream: data that is not read again soon.
+// them behind grid_dep_wait() (as it does __ldcs, a volatile coherent load too); without a clobber
+// of memory, so that they may still move past the kernel's own stores.
 __device__ __forceinline__ int load_i32(const int32_t *p) {
     int v;
     asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(reinterpret_cast<uint64_t>(p)));
@@ -71,13 +71,6 @@ __device__ __forceinline__ uint4 load_u32x4(const void *p) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(reinterpret_cast<uint64_t>(p)));
     return v;
 }
-__device__ __forceinline__ uint4 load_stream(const uint4 *p) {
-    uint4 v;
-    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(reinterpret_cast<uint64_t>(p)));
-    return v;
-}
-
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -77,14 +77,14 @@ k_linear_few(const LinearArgs A, int act) {
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
                 v[u][r] = make_uint4(0, 0, 0, 0);
-                if (p0 + u * kStep < pieces) v[u][r] = load_stream(w[r] + p0 + u * kStep);
+                if (p0 + u * kStep < pieces) v[u][r] = __ldcs(w[r] + p0 + u * kStep);
             }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             if (p0 + u * kStep >= pieces) break;
 #pragma unroll
             for (int t = 0; t < kTok; ++t) {
-                const uint4 q = load_u32x4(x[t] + p0 + u * kStep);
+                const uint4 q = x[t][p0 + u * kStep];
                 const float2 x0 = make_float2(bf16_lo(q.x), bf16_hi(q.x)), x1 = make_float2(bf16_lo(q.y), bf16_hi(q.y));
                 const float2 x2 = make_float2(bf16_lo(q.z), bf16_hi(q.z)), x3 = make_float2(bf16_lo(q.w), bf16_hi(q.w));
 #pragma unroll

@@ -356,13 +356,13 @@ k_expert_combine(const inkattn_expert_combine_params p, int shift, int chunks) {
                     const int r = load_i32(p.token_rows + t * p.top_k + j);
                     if (r >= 0 && r < p.M) {
                         c[n][i] = load_f32(p.weights + t * rows + j);
-                        v[n][i] = load_stream(y + (size_t)r * G + g);
+                        v[n][i] = __ldcs(y + (size_t)r * G + g);
                     } else if (r != -1 && g == 0) {
                         set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
                     }
                 } else {
                     c[n][i] = load_f32(p.weights + t * rows + j);
-                    v[n][i] = load_stream(sh + ((size_t)(j - p.top_k) * p.N_tok + t) * G + g);
+                    v[n][i] = __ldcs(sh + ((size_t)(j - p.top_k) * p.N_tok + t) * G + g);
                 }
             }
         }

