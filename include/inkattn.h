@@ -445,8 +445,10 @@ INKATTN_API inkattn_status inkattn_qkvr_prologue(const inkattn_qkvr_params *p, v
  * The two products accumulate in fp32 on the tensor cores, apply bias and activation to the
  * fp32 sums, and round once to the output type.  With v = x w^T + bias:
  *   NONE v   RELU max(v, 0)   GELU v (1 + erf(v / sqrt 2)) / 2   SILU v / (1 + exp(-v))
- *   (erf within 1.5e-7; a NaN stays a NaN; an infinite v as in the formula, so that GELU and
- *   SILU of -infinity are NaN)
+ *   (a NaN stays a NaN; an infinite v as in the formula, so that GELU and SILU of -infinity are
+ *   NaN.  fp32 outputs: SILU within 11 units of 2^-24 of the value, GELU within 18, and 1.25 v^2
+ *   more for negative v.  bf16 outputs, before their rounding: GELU within 1.5e-7 |v| / 2, SILU
+ *   within (4 + 1.2 |v|) 2^-23 of the value and 0 below 2^-126)
  *   SWIGLU   w (and bias) hold 2 F rows, F gate rows first, then F up rows:
  *            SILU(gate) * up, F values.
  * Results do not depend on the GPU's scheduling: every sum is added in a fixed order.

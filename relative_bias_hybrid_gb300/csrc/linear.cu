@@ -687,7 +687,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
                             const float own = __uint_as_float(quarter < 2 ? v[j] : v[16 + j]) + bias;
                             const float other = stg_other[j * kStgPitch + lane];
                             const float gate = quarter < 2 ? own : other, up = quarter < 2 ? other : own;
-                            y[j] = activate<INKATTN_ACT_SILU>(gate) * up;
+                            y[j] = activate<INKATTN_ACT_SILU, kFine>(gate) * up;
                         }
                         named_sync(swap_bar, 64);                 // both have read
                         store16(y, keep);
@@ -695,7 +695,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) y[j] = activate<kAct>(__uint_as_float(v[16 * h + j]) + bias);
+                            for (int j = 0; j < 16; ++j) y[j] = activate<kAct, kFine>(__uint_as_float(v[16 * h + j]) + bias);
                             store16(y, 16 * h);
                         }
                     }
@@ -774,7 +774,7 @@ k_linear(const LinearArgs A, const __grid_constant__ LinearMaps maps) {
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     const bool in = f + n < A.F;
-                    y[n] = activate<kGated ? INKATTN_ACT_SILU : kAct>(sum[n] + (b && in ? load_f32(b + n) : 0.f));
+                    y[n] = activate<kGated ? INKATTN_ACT_SILU : kAct, kFine>(sum[n] + (b && in ? load_f32(b + n) : 0.f));
                     if (kGated) y[n] *= up[n] + (b && in ? load_f32(b + F + n) : 0.f);
                 }
                 if (vec) {

@@ -33,11 +33,12 @@ constexpr int kU = 4;                              // pieces of a row requested 
 constexpr int kMostTokens = 256;
 constexpr int kFewThreads = 128;                   // of a block, or one group of more
 
+template <bool kExact>
 __device__ __forceinline__ float activate_any(int act, float v) {
     switch (act) {
-        case INKATTN_ACT_RELU: return activate<INKATTN_ACT_RELU>(v);
-        case INKATTN_ACT_GELU: return activate<INKATTN_ACT_GELU>(v);
-        case INKATTN_ACT_SILU: case INKATTN_ACT_SWIGLU: return activate<INKATTN_ACT_SILU>(v);
+        case INKATTN_ACT_RELU: return activate<INKATTN_ACT_RELU, kExact>(v);
+        case INKATTN_ACT_GELU: return activate<INKATTN_ACT_GELU, kExact>(v);
+        case INKATTN_ACT_SILU: case INKATTN_ACT_SWIGLU: return activate<INKATTN_ACT_SILU, kExact>(v);
         default: return v;
     }
 }
@@ -143,7 +144,7 @@ k_linear_few(const LinearArgs A, int act) {
         y[h] = s;
     }
     const size_t o = (size_t)t * A.F + f;
-    float out = activate_any(act, y[0]);
+    float out = A.out_f32 ? activate_any<true>(act, y[0]) : activate_any<false>(act, y[0]);
     if (gated) out *= y[1];
     if (A.residual) out += __uint_as_float((uint32_t)A.residual[o] << 16);
     if (A.out_f32) static_cast<float *>(A.out)[o] = out;
