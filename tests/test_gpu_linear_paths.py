@@ -1,0 +1,207 @@
+"""The tensor-core kernel behind inkattn_linear and inkattn_grouped_linear (k_linear), path by path, at
+sizes that really reach it.  inkattn_linear gives few tokens and small layers to k_linear_few (always
+up to 2 tokens; up to 256 tokens where the layer is small enough), so every test here names the
+kernel that it is about and asserts, from a captured graph, that the call launches it; more than
+256 tokens never go to k_linear_few, and neither do grouped products.
+
+Whether the K range is split shows in the grid: two CTAs for each item (256 weight rows, 128 for
+SWIGLU, times a tile of at least 32 tokens) and each part of K, as long as these are fewer than the SMs."""
+import os
+import re
+import warnings
+
+import pytest
+import torch
+
+from test_gpu_layer_products import BF16, F32, F64, HALF_STEP, I32, _act64, _grid, _linear_inputs, _run_linear
+
+pytestmark = pytest.mark.gpu
+
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def ia():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from relative_bias_hybrid_gb300 import build
+    build.build()
+    import relative_bias_hybrid_gb300.inkattn as ia
+    return ia
+
+
+def launches(call, tmp_path):
+    """(mangled kernel name, blocks) of every launch of call, from the graph that it is captured into."""
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    graph.enable_debug_mode()
+    with torch.cuda.graph(graph):
+        call()
+    path = os.path.join(str(tmp_path), f"graph{len(os.listdir(str(tmp_path)))}.dot")
+    with warnings.catch_warnings():
+        warnings.simplefilter("ignore")                        # (it announces the file)
+        graph.debug_dump(path)
+    found = re.findall(r"\| (_ZN7inkattn\w+)\\<\\<\\<(\d+),", open(path).read())
+    return [(name, int(blocks)) for name, blocks in found]
+
+
+def is_linear(name, act, dtype, residual):
+    return name.startswith(f"_ZN7inkattn8k_linearILi{ACTS[act]}ELb{int(dtype == F32)}ELb{int(residual)}E")
+
+
+def the_launch(ia, tmp_path, T, K, F, act, dtype, residual):
+    """The launch of a linear layer of these sizes: it must be k_linear's kernel for them.  Its blocks."""
+    rows = F * (2 if act == "swiglu" else 1)
+    x, w, out = (torch.zeros(s, dtype=d, device="cuda") for s, d in
+                 (((T, K), BF16), ((rows, K), BF16), ((T, F), dtype)))
+    res = torch.zeros((T, F), dtype=BF16, device="cuda") if residual else None
+    p = ia.linear_params(x=x, w=w, out=out, act=act, residual=res)
+    (name, blocks), = launches(lambda: ia.inkattn_linear(p), tmp_path)
+    assert is_linear(name, act, dtype, residual), name
+    return blocks
+
+
+def items(F, act, tiles):
+    feat = 128 if act == "swiglu" else 256
+    return (F + feat - 1) // feat * tiles
+
+
+def curve_slack(v, act, dtype):
+    """Absolute error of the curve at an exact argument v, before the output's rounding.  In units of 2^-24.
+    fp32: SILU 11 of the value and GELU 18 + 1.25 v^2 (see test_gpu_linear_curves.py).
+    bf16, SILU v / (1 + 2^(-v log2 e)): the exponent has two roundings (2 |v|), 2^x is within 2^-22 (4), the
+    sum and the product round once each (2), the reciprocal is within a step (2): 8 + 2 |v| of the value,
+    and below 2^-126 it may be 0.  bf16, GELU v h or v - v h, absolute in h: the formula (2.5 / 2); t = 1 / (1 +
+    c |v|) within 3 of itself, times 3.5 (the formula's slope against t) times h <= 1/2 (5.3); five
+    steps of values up to 0.73 (3.7); 2^x 4 h + 2.5 v^2 / 2 h (2.5); the product (0.5): 14 |v|."""
+    if act == "silu":
+        y = v * torch.sigmoid(v)
+        return 11 * U * y.abs() + 2.0 ** -141 if dtype == F32 else (8 + 2 * v.abs()) * U * y.abs() + 2.0 ** -119
+    if act == "gelu":
+        y = _act64(v, "gelu")
+        return (18 + 1.25 * v * v) * U * y.abs() + 2.0 ** -141 if dtype == F32 else 14 * U * v.abs()
+    if act == "swiglu":
+        a, b = v.chunk(2, dim=-1)
+        return (curve_slack(a, "silu", dtype) + U * (a * torch.sigmoid(a)).abs()) * b.abs() + 2.0 ** -141
+    return torch.zeros_like(v)
+
+
+def check(got, v, act, residual=None):
+    """got against act(v) + residual at the exact argument v: bit for bit where the curve is straight."""
+    y, slack = _act64(v, act), curve_slack(v, act, got.dtype)
+    if residual is not None:
+        y = y + residual
+        slack = slack + U * (y.abs() + slack)                  # the fp32 addition
+    got = got.cpu()
+    if act in ("none", "relu"):
+        assert torch.equal(got, y.to(F32).to(got.dtype))
+        return
+    over = (got.to(F64) - y).abs() - (slack + HALF_STEP[got.dtype] * (y.abs() + slack) + 2.0 ** -134)
+    assert bool((over <= 0).all()), float(over.max())
+
+
+# ---------------------------------------------------------------- infinite sums, wide arguments
+
+# More than 256 tokens: k_linear.  The short K cannot be split (fewer than four steps of 64); the long
+# one of few items is.  64 tokens of 256 features read 4 MB of weights eight times: far above what
+# k_linear_few takes for more than eight tokens.
+INF_SHAPES = [(300, 64, 24, False), (300, 64, 27, False), (300, 64, 260, False), (64, 8192, 256, True),
+              (64, 8192, 253, True)]
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("with_residual", [False, True])
+@pytest.mark.parametrize("T,K,F,split", INF_SHAPES)
+def test_infinite_sums(ia, tmp_path, act, dtype, with_residual, T, K, F, split):
+    """A sum of +infinity or -infinity takes the formula's value (infinity, 0 or NaN) through the unsplit
+    epilogue and the split's join, with stores of whole words and single values; the features beside
+    it keep theirs."""
+    blocks = the_launch(ia, tmp_path, T, K, F, act, dtype, with_residual)
+    if split:
+        assert blocks > 2 * items(F, act, 2)                   # (64 tokens are two tiles at most)
+    inf, rows = float("inf"), F * (2 if act == "swiglu" else 1)
+    x, w = torch.ones((T, K), dtype=BF16), torch.zeros((rows, K), dtype=BF16)
+    bias = torch.ones(rows, dtype=F32)
+    bias[:6] = torch.tensor([inf, -inf, float("nan"), 3.0e38, -3.0e38, 0.0])
+    if act == "swiglu":
+        bias[F + 6:F + 8] = torch.tensor([inf, -inf])
+    residual = torch.full((T, F), 0.5, dtype=BF16) if with_residual else None
+    got = _run_linear(ia, x, w, bias, residual, act, dtype, F).cpu()
+    want = _act64(bias.double().expand(T, rows), act) + (0.5 if with_residual else 0.0)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.isinf(got), torch.isinf(want.to(dtype)))
+    assert torch.equal(got[torch.isinf(got)].double(), want.to(dtype)[torch.isinf(got)].double())
+    live = torch.isfinite(want) & torch.isfinite(got.double())
+    # half a step, and the curves at 0, at 1 and at their limits: at 1, 14 units of 2^-24 (gelu) of at least
+    # 0.73, 11 (silu) and 12 (swiglu) of the value, and the residual's rounding: under 24 units in all
+    slack = (HALF_STEP[dtype] + 24 * U) * want.abs() + 1e-36
+    assert bool(((got.double() - want).abs() <= slack)[live].all())
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu", "swiglu"])
+@pytest.mark.parametrize("T,split", [(300, False), (32, True)])
+def test_activations_of_wide_arguments(ia, tmp_path, act, T, split):
+    """Arguments from -60 to 60, and NaN, through an identity weight of 2568 features: 11 blocks of
+    them (SWIGLU 21), which 32 tokens, one tile, split over K."""
+    v = torch.arange(-1280, 1281).double() * (60.0 / 1280)
+    K = 8 * ((v.numel() + 7) // 8)
+    x = torch.zeros((T, K), dtype=BF16)
+    x[:, :v.numel()] = v.to(BF16)                      # (the arguments are what x holds)
+    x[1, 5] = float("nan")
+    w = torch.eye(K, dtype=BF16)
+    if act == "swiglu":
+        w = torch.cat([w, w.flip(0)])
+    for dtype in (BF16, F32):
+        blocks = the_launch(ia, tmp_path, T, K, K, act, dtype, False)
+        if split:
+            assert blocks > 2 * items(K, act, 1)
+        got = _run_linear(ia, x, w, None, None, act, dtype, K)
+        rows = torch.tensor([0, 2, T // 2, T - 1])
+        a = x[rows].double()
+        check(got[rows.cuda()], torch.cat([a, a.flip(1)], 1) if act == "swiglu" else a, act)
+        assert bool(torch.isnan(got[1]).all())         # NaN times a zero weight is a NaN everywhere
+
+
+# ---------------------------------------------------------------- residuals
+
+# 5000 tokens are 20 tiles of at most 256: 80 items of 1021 features, 160 of 2000, 100 of 600 with SWIGLU;
+# fp32 outputs, in tiles of 160: 128 items of 1021.  More than the 76 pairs of SMs, so that pairs
+# take a second item, whose first residual values are requested while the first is stored.
+@pytest.mark.parametrize("T,K,F,act,dtype,in_place", [
+    (5000, 128, 1021, "none", BF16, True), (5000, 128, 1021, "none", BF16, False), (5000, 72, 2000, "none", BF16, True),
+    (5000, 200, 2000, "none", BF16, False), (5003, 128, 600, "swiglu", BF16, True), (5003, 128, 599, "swiglu", BF16, True),
+    (5003, 136, 599, "swiglu", BF16, False), (5000, 64, 1024, "gelu", BF16, True), (5000, 64, 1021, "silu", BF16, False),
+    (5000, 600, 1021, "none", F32, False), (5003, 136, 599, "swiglu", F32, False), (5000, 64, 1024, "gelu", F32, False),
+    (300, 64, 33, "none", BF16, True), (300, 128, 1024, "none", BF16, True), (321, 128, 261, "swiglu", BF16, True)])
+def test_residual_of_several_items(ia, tmp_path, T, K, F, act, dtype, in_place):
+    """A residual through the unsplit epilogue, which requests its values a block and an item ahead: also
+    where the output is the residual array itself, so that requested values lie beside stored ones."""
+    blocks = the_launch(ia, tmp_path, T, K, F, act, dtype, True)
+    if T >= 5000:
+        assert blocks < 2 * items(F, act, (T + (159 if dtype == F32 else 255)) // (160 if dtype == F32 else 256))
+    x, w, bias, residual = _linear_inputs(T, K, F, act, seed=T + K + F)
+    v = x.double() @ w.double().t() + bias.double()
+    if in_place:
+        dev = [t.cuda() for t in (x, w, bias, residual)]
+        ia.inkattn_linear(ia.linear_params(x=dev[0], w=dev[1], bias=dev[2], residual=dev[3], out=dev[3], act=act))
+        torch.cuda.synchronize()
+        check(dev[3], v, act, residual.double())
+    else:
+        check(_run_linear(ia, x, w, bias, residual, act, dtype, F), v, act, residual.double())
+
+
+@pytest.mark.parametrize("T,K,F", [(700, 128, 264), (700, 128, 261)])
+def test_in_place_residual_and_infinities(ia, tmp_path, T, K, F):
+    """out == residual; infinities and NaN of a token or a residual stay in their own place."""
+    the_launch(ia, tmp_path, T, K, F, "none", BF16, True)
+    x, w, bias, residual = _linear_inputs(T, K, F, "none", seed=3)
+    x[5, 7], x[300, 1], x[699, 3] = float("inf"), float("nan"), -float("inf")
+    residual[44, 7], residual[45, F - 1], residual[260, 0] = float("inf"), float("nan"), -float("inf")
+    dev = [t.cuda() for t in (x, w, bias, residual)]
+    ia.inkattn_linear(ia.linear_params(x=dev[0], w=dev[1], bias=dev[2], residual=dev[3], out=dev[3]))
+    torch.cuda.synchronize()
+    want = (x.double() @ w.double().t() + bias.double() + residual.double()).to(F32).to(BF16)
+    got = dev[3].cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got.float()), torch.nan_to_num(want.float()))
