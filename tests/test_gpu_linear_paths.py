@@ -8,6 +8,8 @@ Whether the K range is split shows in the grid: two CTAs for each item (256 weig
 SWIGLU, times a tile of at least 32 tokens) and each part of K, as long as these are fewer than the SMs."""
 import os
 import re
+import subprocess
+import sys
 import warnings
 
 import pytest
@@ -17,6 +19,7 @@ from test_gpu_layer_products import BF16, F32, F64, HALF_STEP, I32, _act64, _gri
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
 U = 2.0 ** -24
 
@@ -205,3 +208,102 @@ def test_in_place_residual_and_infinities(ia, tmp_path, T, K, F):
     got = dev[3].cpu()
     assert torch.equal(torch.isnan(got), torch.isnan(want))
     assert torch.equal(torch.nan_to_num(got.float()), torch.nan_to_num(want.float()))
+
+
+# ---------------------------------------------------------------- behind other calls
+
+@pytest.mark.parametrize("T,K,split", [(300, 512, False), (64, 2048, True)])
+def test_calls_wait_for_the_work_before_them(ia, tmp_path, T, K, split):
+    """A product reads what the calls just before it on the stream wrote, over and over: k_linear sets
+    itself up, and each of its roles waits, before the kernel in front has finished."""
+    blocks = the_launch(ia, tmp_path, T, K, K, "none", BF16, True)
+    if split:
+        assert blocks > 2 * items(K, "none", 2)
+    g = torch.Generator().manual_seed(1)
+    eye = torch.eye(K, dtype=BF16, device="cuda")
+    a = _grid((T, K), g, -8, 8, 1 / 8).cuda()
+    b, first = torch.empty_like(a), a.clone()
+    p = [ia.linear_params(x=a, w=eye, out=b), ia.linear_params(x=b, w=eye, out=a, residual=b)]
+    for _ in range(12):                                        # a <- 2 a, exactly, each round
+        ia.inkattn_linear(p[0])
+        ia.inkattn_linear(p[1])
+    torch.cuda.synchronize()
+    assert torch.equal(a.double(), first.double() * 2 ** 12)
+
+
+def test_kernels_of_every_length_wait_for_each_other(ia, tmp_path):
+    """Short kernels that let their successor start early in front of long ones and behind them, on
+    the same buffers: k_linear_few doubles four rows, k_linear copies all, the grouped products
+    gather them in another order (rows of two experts, whose weights are 1 and 2), the weighted sum
+    brings them back halved where they were doubled."""
+    T, K = 300, 512
+    g = torch.Generator().manual_seed(2)
+    eye = torch.eye(K, dtype=BF16, device="cuda")
+    a = _grid((T, K), g, -8, 8, 1 / 8).cuda()
+    want = a.clone()
+    few, b = torch.empty((4, K), dtype=BF16, device="cuda"), torch.empty_like(a)
+    rows = torch.empty_like(a)
+    order = torch.randperm(T, generator=g)
+    place = torch.empty_like(order)
+    place[order] = torch.arange(T)
+    tok, place = order.to(I32).cuda(), place.to(I32).cuda()[:, None].contiguous()
+    offs = torch.tensor([0, 131, T], dtype=I32, device="cuda")
+    w2 = torch.stack([eye, 2 * eye])
+    weights = torch.where(place < 131, 1.0, 0.5).contiguous()
+    calls = [(ia.inkattn_linear, ia.linear_params(x=a[:4], w=eye, out=few)),
+             (ia.inkattn_linear, ia.linear_params(x=few, w=eye, out=a[:4], residual=few)),
+             (ia.inkattn_linear, ia.linear_params(x=a, w=eye, out=b)),
+             (ia.inkattn_grouped_linear, ia.grouped_linear_params(x=b, w=w2, expert_offsets=offs, row_token=tok, out=rows)),
+             (ia.inkattn_expert_combine, ia.expert_combine_params(y=rows, weights=weights, token_rows=place, out=a))]
+
+    def once():
+        for call, p in calls:
+            call(p)
+
+    names = [n for n, _ in launches(once, tmp_path)]
+    assert ["k_linear_few" in n for n in names] == [True, True, False, False, False]
+    assert is_linear(names[2], "none", BF16, False) and is_linear(names[3], "none", BF16, False)
+    for _ in range(10):
+        once()
+    torch.cuda.synchronize()
+    want[:4] *= 2 ** 10
+    assert torch.equal(a, want)
+
+
+FIRST = r"""
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+import relative_bias_hybrid_gb300.inkattn as ia
+BF, I = torch.bfloat16, torch.int32
+T, K, E = 300, 64, 4
+g = torch.Generator().manual_seed(0)
+x = (torch.randint(-8, 9, (T, K), generator=g) / 8).to(BF).cuda()
+eye = torch.eye(K, dtype=BF, device="cuda")
+r = dict(topk_ids=torch.empty((T, 1), dtype=I, device="cuda"), weights=torch.empty((T, 1), device="cuda"),
+         expert_offsets=torch.empty(E + 1, dtype=I, device="cuda"), row_token=torch.empty(T, dtype=I, device="cuda"),
+         token_rows=torch.empty((T, 1), dtype=I, device="cuda"))
+logits = torch.randn((T, E), generator=g).cuda()
+y, rows, back = (torch.zeros_like(x) for _ in range(3))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    ia.inkattn_linear(ia.linear_params(x=x, w=eye, out=y))
+    ia.inkattn_route(ia.route_params(logits=logits, **r))
+    ia.inkattn_grouped_linear(ia.grouped_linear_params(x=y, w=eye.expand(E, K, K).contiguous(), out=rows,
+                              expert_offsets=r["expert_offsets"], row_token=r["row_token"]))
+    ia.inkattn_expert_combine(ia.expert_combine_params(y=rows, weights=r["weights"], token_rows=r["token_rows"], out=back))
+assert not bool(back.any())
+for _ in range(3):
+    back.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(back, x)
+print("FIRST CALLS CAPTURED")
+"""
+
+
+def test_first_calls_of_a_process_can_be_captured(ia):
+    """What the library asks of the runtime once, it may ask during a capture."""
+    r = subprocess.run([sys.executable, "-c", FIRST, ROOT], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "FIRST CALLS CAPTURED" in r.stdout, r.stdout[-2000:] + r.stderr[-4000:]
