@@ -307,3 +307,68 @@ def test_first_calls_of_a_process_can_be_captured(ia):
     """What the library asks of the runtime once, it may ask during a capture."""
     r = subprocess.run([sys.executable, "-c", FIRST, ROOT], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "FIRST CALLS CAPTURED" in r.stdout, r.stdout[-2000:] + r.stderr[-4000:]
+
+
+# ---------------------------------------------------------------- the size of the error
+
+def _norm_error(got, want):
+    return float((got.cpu().double() - want).norm() / want.norm())
+
+
+# k_linear_few with 1, 4 and 16 warps a row (K up to 512; longer; a K of 4096 and more with at most 304
+# groups of rows), then k_linear: split, unsplit, and one part of K alone.
+@pytest.mark.parametrize("T,K,F,few", [(4, 512, 500, True), (8, 2048, 700, True), (2, 8192, 258, True), (64, 8192, 512, False),
+                                       (300, 8192, 2048, False), (700, 1000, 1021, False), (2100, 512, 3000, False)])
+def test_error_of_the_whole_output(ia, tmp_path, T, K, F, few):
+    """fp32 outputs to 1e-6 of their norm (as rounding to nearest of random sign gives with up to 128 terms
+    in a row: 2^-24 / sqrt 3 * sqrt(128 / 2) = 2.8e-7; and the tensor cores' parts of 512: 5e-7 measured where
+    they were chosen).  bf16 outputs: what rounding the exact values costs, within a hundredth of it, and
+    2e-5 for sums that the tensor cores did not round to nearest (1e-5 at K = 8192)."""
+    x, w, _, _ = _linear_inputs(T, K, F, "none", seed=T + K, grid=False)
+    want = x.double() @ w.double().t()
+    for dtype in (F32, BF16):
+        out = torch.empty((T, F), dtype=dtype, device="cuda")
+        dev = [x.cuda(), w.cuda()]
+        p = ia.linear_params(x=dev[0], w=dev[1], out=out)
+        (name, _), = launches(lambda: ia.inkattn_linear(p), tmp_path)
+        assert ("k_linear_few" in name) == few
+        err = _norm_error(_run_linear(ia, x, w, None, None, "none", dtype, F), want)
+        bound = 1e-6 if dtype == F32 else 1.01 * _norm_error(want.to(F32).to(BF16), want) + 2e-5
+        assert err <= bound, (err, bound)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_error_of_grouped_products(ia, gather, dtype):
+    """The same bounds, rows of 5 experts, K = 4096."""
+    g = torch.Generator().manual_seed(3)
+    counts, K, F = [40, 0, 300, 1, 90], 4096, 600
+    M = sum(counts)
+    x, w = torch.randn((M, K), generator=g).to(BF16), (torch.randn((5, F, K), generator=g) * K ** -0.5).to(BF16)
+    tok = torch.randperm(M, generator=g) if gather else torch.arange(M)
+    offs = torch.tensor([0, *torch.tensor(counts).cumsum(0).tolist()], dtype=I32)
+    out = torch.empty((M, F), dtype=dtype, device="cuda")
+    ia.inkattn_grouped_linear(ia.grouped_linear_params(x=x.cuda(), w=w.cuda(), expert_offsets=offs.cuda(), out=out,
+                                                       row_token=tok.to(I32).cuda() if gather else None))
+    torch.cuda.synchronize()
+    want = torch.cat([x[tok[offs[e]:offs[e + 1]]].double() @ w[e].double().t() for e in range(5)])
+    err = _norm_error(out, want)
+    bound = 1e-6 if dtype == F32 else 1.01 * _norm_error(want.to(F32).to(BF16), want) + 2e-5
+    assert err <= bound, (err, bound)
+
+
+@pytest.mark.parametrize("T,K,F,act,dtype", [(288, 8192, 2048, "none", BF16), (2000, 4096, 1024, "swiglu", BF16),
+                                             (300, 4096, 1021, "gelu", F32), (64, 8192, 512, "none", BF16)])
+def test_every_call_gives_the_same_bits(ia, T, K, F, act, dtype):
+    """Twenty calls, others between them: no sum depends on which CTA came first."""
+    x, w, bias, residual = [t.cuda() for t in _linear_inputs(T, K, F, act, seed=9, grid=False)]
+    outs = [torch.empty((T, F), dtype=dtype, device="cuda") for _ in range(2)]
+    other = torch.empty((40, F), dtype=dtype, device="cuda")
+    first = None
+    for i in range(20):
+        out = outs[i & 1].zero_()
+        ia.inkattn_linear(ia.linear_params(x=x, w=w, bias=bias, residual=residual, out=out, act=act))
+        ia.inkattn_linear(ia.linear_params(x=x[:40], w=w, bias=bias, out=other, act=act))
+        if first is None:
+            first = out.clone()
+        assert torch.equal(out, first)
