@@ -442,8 +442,12 @@ INKATTN_API inkattn_status inkattn_qkvr_prologue(const inkattn_qkvr_params *p, v
  * (inkattn_output_conv again).  inkattn_linear, inkattn_route, inkattn_grouped_linear and
  * inkattn_expert_combine are those products and what lies between them.
  *
- * The two products accumulate in fp32 on the tensor cores, apply bias and activation to the
- * fp32 sums, and round once to the output type.  With v = x w^T + bias:
+ * The two products accumulate in fp32, apply bias and activation to the fp32 sums, and round
+ * once to the output type.  They run on the tensor cores, except linear layers of few tokens or
+ * of a small size, which are summed by fp32 multiply-adds.  The tensor cores do not round their
+ * sums to nearest: fp32 outputs are therefore summed in parts of K = 512 (5e-7 of the result at
+ * any K), bf16 outputs in one (1e-5 at K = 8192, before a rounding of up to 4e-3).  With
+ * v = x w^T + bias:
  *   NONE v   RELU max(v, 0)   GELU v (1 + erf(v / sqrt 2)) / 2   SILU v / (1 + exp(-v))
  *   (a NaN stays a NaN; an infinite v as in the formula, so that GELU and SILU of -infinity are
  *   NaN.  fp32 outputs: SILU within 11 units of 2^-24 of the value, GELU within 18, and 1.25 v^2
@@ -477,16 +481,16 @@ typedef struct inkattn_linear_params {
     int32_t *dev_status;       /* nullable, see the conventions above                    */
 } inkattn_linear_params;
 
-/* Runs the linear layer.  x and w are read by TMA (device memory of the current device,
- * 16-byte aligned); residual and out must be 16-byte aligned.  out may be the residual array
- * itself (bf16), but overlaps no other input (INKATTN_ERR_INVALID_ARG). */
+/* Runs the linear layer.  x and w, which TMA may read, lie in device memory of the current
+ * device, 16-byte aligned; residual and out must be 16-byte aligned.  out may be the residual
+ * array itself (bf16), but overlaps no other input (INKATTN_ERR_INVALID_ARG). */
 INKATTN_API inkattn_status inkattn_linear(const inkattn_linear_params *p, void *stream);
 
 /* Products grouped by expert: the rows i in [expert_offsets[e], expert_offsets[e+1]) of out are
  *   out[i][f] = act( sum_k x[s][k] w[e][f][k] + bias[e][f] ),   s = row_token ? row_token[i] : i.
  * expert_offsets lies on the device, so the same call (or captured graph) serves any split of
  * the rows among the experts; an expert without rows costs nothing.  Rows at and behind
- * expert_offsets[E] are neither read nor written.  An expert whose offsets are negative,
+ * expert_offsets[E] are not written, and nothing depends on them.  An expert whose offsets are negative,
  * decrease, pass M or reach back behind an earlier expert's end is flagged
  * (INKATTN_ERR_DEVICE_BOUNDS) and its rows left as they were, and so is a row whose row_token
  * lies outside [0, N_x). */
@@ -517,7 +521,9 @@ INKATTN_API inkattn_status inkattn_grouped_linear(const inkattn_grouped_linear_p
  * order, equal logits by the lower index first (a NaN counts as -infinity).  With
  *   s(l) = 1 / (1 + exp(-l))  (INKATTN_SCORE_SIGMOID)   or   exp(l)  (INKATTN_SCORE_SOFTMAX)
  * the weights of the chosen and the shared experts are scale * s(l) / (sum of their s(l)), in
- * fp32 (all zero where that sum is zero, as when every logit is -infinity).  The N_tok * top_k
+ * fp32 (all zero where that sum is zero, as when every logit is -infinity), within
+ * (16 + |l - m|) 2^-23 of the value, m the largest of their logits (sigmoid: or 0, if that is
+ * less), and possibly 0 below 2^-125 |scale|.  The N_tok * top_k
  * (token, choice) pairs are then sorted by expert, stably in (token, choice) order:
  *   expert_offsets[e] = first row of expert e, row_token[i] = the token of row i (the row_token
  *   of inkattn_grouped_linear), token_rows[t][j] = the row of token t's j-th choice (the
