@@ -173,7 +173,7 @@ k_prefill_2q(const Tc2Args A, const __grid_constant__ CUtensorMap qmap,
             for (int half = 0; half < 2; ++half) {
                 const int lb = 2 * t + half;                 // logical cache block
                 blk[half] = (long long)lb * kBlock >= T ? -2
-                          : lb < p.max_blocks_per_seq ? __ldg(p.block_table + (size_t)b * p.max_blocks_per_seq + lb)
+                          : lb < p.max_blocks_per_seq ? load_i32(p.block_table + (size_t)b * p.max_blocks_per_seq + lb)
                           : -1;
             }
             if (L >= kSlots && !wwait(bar(B_KV_EMPTY + slot), ((L / kSlots) - 1) & 1)) {

@@ -265,7 +265,7 @@ k_prefill_tc(const TcArgs A, const __grid_constant__ CUtensorMap qmap,
             for (int hh = 0; hh < kHalves; ++hh) {
                 const int lb = 2 * t + (kCluster > 1 ? (int)crank : hh);   // logical cache block
                 blk[hh] = (long long)lb * kBlock >= T ? -2
-                        : lb < p.max_blocks_per_seq ? __ldg(p.block_table + (size_t)b * p.max_blocks_per_seq + lb)
+                        : lb < p.max_blocks_per_seq ? load_i32(p.block_table + (size_t)b * p.max_blocks_per_seq + lb)
                         : -1;
             }
             if (L >= kSlots && !wwait(bar(B_KV_EMPTY + slot), ((L / kSlots) - 1) & 1)) {

@@ -21,7 +21,9 @@ def test_no_non_coherent_loads(name):
     ("output_conv.cu", ["y"]),                       # of inkattn_linear or inkattn_expert_combine
     ("prologue.cu", [r"reinterpret_cast<const uint4 \*>\(\s*qb", r"reinterpret_cast<const uint4 \*>\(p\.[kv] ",
                      r"reinterpret_cast<const uint4 \*>\(src"]),   # q, k and v, of inkattn_linear
-    ("prefill_tc.cu", [r"src \+ j\);\s*\}\s*float n2"]),           # r, of inkattn_qkvr_prologue
+    ("prefill_tc.cu", [r"src \+ j\);\s*\}\s*float n2",             # r, of inkattn_qkvr_prologue
+                       r"p\.block_table"]),                          # (the expansion of an E4M3 cache writes one)
+    ("prefill_2q.cu", [r"p\.block_table"]),
     ("decode_tc.cu", [r"reinterpret_cast<const uint32_t \*>\(rh"]),
     ("dequant.cu", [r"\(stream == 0 \? p\.k_scale", r"reinterpret_cast<const uint4 \*>\(codes"])])   # of the prologue
 def test_outputs_of_early_kernels_are_read_coherently(name, arrays):
