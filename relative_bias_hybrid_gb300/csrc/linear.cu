@@ -39,18 +39,19 @@
 //   warps 2-9   epilogue: a warp owns 32 TMEM lanes (weight rows) and every second block of 32
 //               columns (tokens); bias and activation per lane, and each value leaves from the lane
 //               that has it, a token's 32 features together.  (Turned through shared memory first, so
-//               that they left as 16-byte pieces: 24.5 us where this takes 24.9 for 8192 x 512 x 4096, 46
-//               against 45 with a residual.  What the stores do cost is a predicate each: blocks
-//               whose tokens are all there go without, 54 -> 30 us for 8192 x 512 x 4095.)
+//               that they left as 16-byte pieces: 31 us as well for 8192 x 512 x 4096, and 50 where this
+//               takes 46 with a residual.  What the stores do cost is a predicate each: blocks
+//               whose tokens are all there go without, 53 -> 29 us for 8192 x 512 x 4095.)
 // Both CTAs' copies of a stage complete on the even CTA's barrier, and the pair's commits
 // release it in both, as in the qkvr kernel.
 //
 // fp32 outputs (kFine).  The tensor cores add each K = 16 step to the accumulator without rounding
 // to nearest; over K = 8192 the error grows to about 1e-5 of the result, nothing next to a bf16
 // rounding but much for an fp32 one.  An fp32 output is therefore summed in parts of K = 512,
-// which the epilogue warps add up in TMEM, rounding to nearest (K = 1000: 4.6e-7 of the result
+// which the epilogue warps add up in TMEM, rounding to nearest (K = 1000: 4.7e-7 of the result
 // instead of 9.8e-7, and the same at K = 8192).  The two accumulators and the sums share the 512
-// TMEM columns, so the tiles have 160 tokens at most: 8192 x 8192 x 8192 takes 0.79 ms instead of 0.57.
+// TMEM columns, so the tiles have 160 tokens at most: 8192 x 8192 x 8192 takes 0.64 ms instead of
+// 0.57 (0.72 against 0.64 under the power cap).
 //
 // Few items (a decode batch): the K range is split over the S pairs of one cluster.  Each CTA
 // writes its fp32 partial tile, a share of the tokens to each pair, into the other CTAs' shared
@@ -58,12 +59,13 @@
 // workspace, no atomics, one launch.  (Reading the partials from the other CTAs instead took
 // 11000 cycles for 256 tokens and S = 4: 12 bytes a cycle.)
 //
-// Measured (back to back on one GB300): 8192 x 8192 x 8192 0.56 ms, 1950 TFLOP/s in a burst with
-// the tensor pipe 89.5% active, 1710 under the power cap; 4 x 8192 x 8192 23.3 us, the weights at 7.2
-// TB/s for 18.5 of them; 288 x 8192 x 8192 34 us, bound by the 64 bytes a cycle into an SM; 256
-// experts 8192 -> 2 x 1024 for 1728 gathered rows 1.03 ms, 8.3 TB/s of weights; 64 experts 4096 ->
-// 2 x 2048 for 49152 gathered rows 1.02 ms, 1615 TFLOP/s (tensor pipe 75%; 0.98 ms on contiguous
-// rows).
+// Measured (back to back on one GB300): 8192 x 8192 x 8192 0.57 ms, 1920 TFLOP/s in a burst with
+// the tensor pipe 89.5% active, 0.64 to 0.67 (1650 to 1720) under the power cap; 4 x 8192 x 8192 23.3
+// us, the weights at 7.2 TB/s for 18.5 of them; 288 x 8192 x 8192 33.5 us, 37 with a residual (two
+// tiles: 26 KB a K step at the 64 bytes a cycle into an SM); 256 experts 8192 -> 2 x 1024 for 1728
+// gathered rows 1.01 to 1.07 ms, 8.0 to 8.5 TB/s of weights; 64 experts 4096 -> 2 x 2048 for 49152
+// gathered rows 1.03 ms in a burst (1600 TFLOP/s, tensor pipe 75%; 0.98 ms on contiguous rows), 1.14
+// to 1.19 under the power cap (1390 to 1450).
 #include <climits>
 #include <cmath>
 #include <type_traits>
