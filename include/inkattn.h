@@ -446,13 +446,14 @@ INKATTN_API inkattn_status inkattn_qkvr_prologue(const inkattn_qkvr_params *p, v
  * once to the output type.  They run on the tensor cores, except linear layers of few tokens or
  * of a small size, which are summed by fp32 multiply-adds.  The tensor cores do not round their
  * sums to nearest: fp32 outputs are therefore summed in parts of K = 512 (5e-7 of the result at
- * any K), bf16 outputs in one (1e-5 at K = 8192, before a rounding of up to 4e-3).  With
+ * K = 8192), bf16 outputs in one (1e-5 at K = 8192, before a rounding of up to 4e-3).  With
  * v = x w^T + bias:
  *   NONE v   RELU max(v, 0)   GELU v (1 + erf(v / sqrt 2)) / 2   SILU v / (1 + exp(-v))
  *   (a NaN stays a NaN; an infinite v as in the formula, so that GELU and SILU of -infinity are
  *   NaN.  fp32 outputs: SILU within 11 units of 2^-24 of the value, GELU within 18, and 1.25 v^2
- *   more for negative v.  bf16 outputs, before their rounding: GELU within 1.5e-7 |v| / 2, SILU
- *   within (4 + 1.2 |v|) 2^-23 of the value and 0 below 2^-126)
+ *   more for negative v; values below 2^-126 within 2^-141.  bf16 outputs, before their
+ *   rounding: GELU within 1.5e-7 |v| / 2, SILU within (4 + 1.2 |v|) 2^-23 of the value and 0
+ *   below 2^-126)
  *   SWIGLU   w (and bias) hold 2 F rows, F gate rows first, then F up rows:
  *            SILU(gate) * up, F values.
  * Results do not depend on the GPU's scheduling: every sum is added in a fixed order.
