@@ -8,7 +8,7 @@ form, elementary torch operations, or, where ``own`` is true, by the library's e
 
 The 4-bit cache: a row of 128 values is four groups of 32.  A group's scale s is the smallest
 8-bit float (5 exponent and 3 mantissa bits, the upper byte of an fp16 without its sign) with
-7 s >= max|x|, at most 9216; its values are n s with n = x / s rounded to nearest, ties to even, and at
+7 s >= max|x|, at most 896; its values are n s with n = x / s rounded to nearest, ties to even, and at
 most 7 in magnitude.  A 32-bit word holds eight values as n + 8: value 2 i in bits 4 i and value
 2 i + 1 in bits 16 + 4 i.
 """
@@ -160,7 +160,7 @@ def _quantise(x):
     g = x.double().unflatten(-1, (-1, 32))
     t = g.abs().amax(-1) / 7.0
     step = torch.exp2((torch.frexp(t).exponent - 1).clamp(min=-14).double() - 3.0)
-    s = (torch.ceil(t / step) * step).clamp(max=9216.0)
+    s = (torch.ceil(t / step) * step).clamp(max=896.0)
     n = torch.round(g / torch.where(s > 0, s, torch.ones_like(s))[..., None]).clamp(-7, 7)
     return n, s
 
@@ -511,14 +511,14 @@ def _rollback(s):
 
 def _grid():
     """Every scale in order, from the bits of the 8-bit floats."""
-    return torch.arange(226, device="cuda").to(torch.int16).mul(128).view(torch.float16).double()
+    return torch.arange(199, device="cuda").to(torch.int16).mul(128).view(torch.float16).double()
 
 
 def _four_bit(x):
     """x [..., 128] as the cache holds it: the first scale of the grid that is not below max / 7."""
     grid = _grid()
     parts = x.double().reshape(*x.shape[:-1], 4, 32)
-    s = grid[torch.searchsorted(grid, parts.abs().amax(-1) / 7.0).clamp(max=225)][..., None]
+    s = grid[torch.searchsorted(grid, parts.abs().amax(-1) / 7.0).clamp(max=198)][..., None]
     return torch.nan_to_num(parts / s, 0.0).round().clamp(-7.0, 7.0).mul(s).reshape(x.shape)
 
 
