@@ -87,9 +87,23 @@ typedef uint16_t inkattn_bf16;
  *   down to 2^-15; below, values under 2^-24 flush) and requires every scale to lie in
  *   [2^-24, 2^7], which the prologue's scales do for rows whose magnitudes stay below
  *   57344; a scale outside that range is flagged as INKATTN_ERR_DEVICE_BOUNDS and its
- *   row read as zeros. */
+ *   row read as zeros.
+ * INKATTN_KV_I4: they hold 4-bit whole numbers, [num_blocks][Hkv][64] rows of 64 bytes (128
+ *   values), and k_scale / v_scale, passed through the same pointers, hold 4 scale bytes per
+ *   row ([num_blocks][Hkv][64][4] uint8), one per group of 32 values.  A scale byte b stands
+ *   for s = the fp16 of bits b << 7 (5 exponent and 3 mantissa bits), 0 .. 896 (b <= 0xC6).
+ *   Little-endian 32-bit word w of a row holds its values 8 w .. 8 w + 7 as u = n + 8, n in
+ *   [-7, 7], value 8 w + 2 i in bits 4 i .. 4 i + 3 and value 8 w + 2 i + 1 in bits 16 + 4 i
+ *   .. 19 + 4 i; a value reads back as n * s, exact in bf16.  The prologue writes the smallest
+ *   s with 7 s >= the group's largest magnitude (0 for a zero group, 896 at most, beyond which
+ *   values saturate at 7 * 896 = 6272), and n = x / s rounded to nearest, ties to even, where x is the
+ *   bf16 value the bf16 cache would hold (a NaN is stored as 0).  Its caches are read by
+ *   inkattn_decode and inkattn_prefill_i4 (inkattn_prefill returns INKATTN_ERR_UNSUPPORTED).  A
+ *   scale byte above 0xC6 inside a sequence is flagged as INKATTN_ERR_DEVICE_BOUNDS and its group
+ *   read as zeros; u = 0 is no code of the prologue's (it reads as -8 s). */
 #define INKATTN_KV_BF16 0
 #define INKATTN_KV_E4M3 1
+#define INKATTN_KV_I4 4
 
 typedef enum inkattn_status {
     INKATTN_OK = 0,
@@ -123,7 +137,7 @@ INKATTN_API int inkattn_abi_version(void);
  *   kn    = kc / sqrt(mean(kc^2) + eps) * k_norm_w
  * [SG §Inkling のモデルアーキテクチャ: ShortConv on K and V before the Q/K normalisation].
  * Then, with slot = slot_mapping[t]: k_cache[slot/64][hk][slot%64][:] = kn,
- * v_cache[...] = vc (with kv_dtype = INKATTN_KV_E4M3: their E4M3 codes, and the row
+ * v_cache[...] = vc (with kv_dtype = INKATTN_KV_E4M3 or INKATTN_KV_I4: their codes, and the
  * scales to k_scale / v_scale[slot/64][hk][slot%64]).  V is not normalised and Q is not
  * convolved.
  * ------------------------------------------------------------------------------ */
@@ -151,11 +165,11 @@ typedef struct inkattn_prologue_params {
     inkattn_bf16 *conv_state_k;    /* [num_state_slots][3][C], read then overwritten     */
     inkattn_bf16 *conv_state_v;    /* [num_state_slots][3][C]                            */
     inkattn_bf16 *q_out;           /* [N_tok][Hq][128]                                   */
-    void *k_cache;                 /* [num_blocks][Hkv][64][128], bf16 or E4M3 (kv_dtype) */
+    void *k_cache;                 /* [num_blocks][Hkv][64][128], bf16, E4M3 or 4 bits (kv_dtype) */
     void *v_cache;                 /* [num_blocks][Hkv][64][128]                         */
-    int32_t kv_dtype;              /* INKATTN_KV_BF16 (0) or INKATTN_KV_E4M3 (1)          */
-    float *k_scale;                /* E4M3 only: [num_blocks][Hkv][64] row scales, 16-byte */
-    float *v_scale;                /* aligned; written for the mapped slots (else NULL)   */
+    int32_t kv_dtype;              /* INKATTN_KV_BF16 (0), INKATTN_KV_E4M3 (1) or INKATTN_KV_I4 (4) */
+    float *k_scale;                /* E4M3: [num_blocks][Hkv][64] row scales; I4: 4 scale bytes a row; */
+    float *v_scale;                /* 16-byte aligned; written for the mapped slots (bf16: NULL) */
     int32_t *dev_status;           /* nullable, see the conventions above                */
 } inkattn_prologue_params;
 
@@ -213,11 +227,11 @@ typedef struct inkattn_attn_params {
     const float *P;            /* [Hq][rel_extent][d_r]: per query head, per distance,   */
                                /* the d_r projection weights; 16-byte aligned (nullable  */
                                /* iff rel_extent == 0)                                   */
-    const void *k_cache;           /* [num_blocks][Hkv][64][128], bf16 or E4M3 (kv_dtype) */
+    const void *k_cache;           /* [num_blocks][Hkv][64][128], bf16, E4M3 or 4 bits (kv_dtype) */
     const void *v_cache;           /* [num_blocks][Hkv][64][128]                         */
-    int32_t kv_dtype;              /* INKATTN_KV_BF16 (0) or INKATTN_KV_E4M3 (1)          */
-    const float *k_scale;          /* E4M3 only: [num_blocks][Hkv][64] row scales, 16-byte */
-    const float *v_scale;          /* aligned (else NULL)                                */
+    int32_t kv_dtype;              /* INKATTN_KV_BF16 (0), INKATTN_KV_E4M3 (1) or INKATTN_KV_I4 (4) */
+    const float *k_scale;          /* E4M3: [num_blocks][Hkv][64] row scales; I4: 4 scale bytes a row; */
+    const float *v_scale;          /* 16-byte aligned (bf16: NULL)                       */
     const int32_t *cu_seqlens_q;   /* [B+1]                                              */
     const int32_t *seqlen_k;       /* [B], q_len[b] <= seqlen_k[b] <= max_seqlen_k       */
     const int32_t *block_table;    /* [B][max_blocks_per_seq]                            */
@@ -227,8 +241,8 @@ typedef struct inkattn_attn_params {
     int32_t *dev_status;           /* nullable                                           */
 } inkattn_attn_params;
 
-/* Prefill (any q_len) over a bf16 cache: writes out (and lse).  An E4M3 cache returns
- * INKATTN_ERR_UNSUPPORTED here; it takes inkattn_prefill_e4m3. */
+/* Prefill (any q_len) over a bf16 cache: writes out (and lse).  An E4M3 or 4-bit cache returns
+ * INKATTN_ERR_UNSUPPORTED here; it takes inkattn_prefill_e4m3 or inkattn_prefill_i4. */
 INKATTN_API inkattn_status inkattn_prefill(const inkattn_attn_params *p, void *stream);
 
 /* Prefill over an E4M3 cache (kv_dtype = INKATTN_KV_E4M3) [SG §Relative Attention と FA4
@@ -245,6 +259,12 @@ INKATTN_API inkattn_status inkattn_prefill(const inkattn_attn_params *p, void *s
 INKATTN_API size_t inkattn_prefill_workspace_bytes(const inkattn_attn_params *p);   /* 0 if invalid or bf16 */
 INKATTN_API inkattn_status inkattn_prefill_e4m3(const inkattn_attn_params *p, void *workspace,
                                                 size_t workspace_bytes, void *stream);
+
+/* The same over a 4-bit cache (kv_dtype = INKATTN_KV_I4; a bf16 or E4M3 one is
+ * INKATTN_ERR_INVALID_ARG): same workspace, its size from inkattn_prefill_workspace_bytes,
+ * n * s exact in the bf16 copy, a group with a scale byte above 0xC6 flagged and read as zeros. */
+INKATTN_API inkattn_status inkattn_prefill_i4(const inkattn_attn_params *p, void *workspace, size_t workspace_bytes,
+                                              void *stream);
 
 /* ------------------------------------------------------------------------------
  * Split-KV decode [VJ §低レイテンシコレクティブとカーネル "FA4 Kernel"; VV §FA4 với
@@ -420,8 +440,8 @@ typedef struct inkattn_qkvr_params {
     inkattn_bf16 *y_out;           /* nullable: [N_tok][F], every projection as rounded  */
     void *k_cache;                 /* as in inkattn_prologue_params                      */
     void *v_cache;
-    int32_t kv_dtype;              /* INKATTN_KV_BF16 or INKATTN_KV_E4M3                  */
-    float *k_scale;                /* E4M3 only (else NULL), as in inkattn_prologue_params */
+    int32_t kv_dtype;              /* INKATTN_KV_BF16, INKATTN_KV_E4M3 or INKATTN_KV_I4   */
+    float *k_scale;                /* scales of a cache of codes (else NULL), as in inkattn_prologue_params */
     float *v_scale;
     int32_t *dev_status;           /* nullable, see the conventions above                */
 } inkattn_qkvr_params;

@@ -332,3 +332,43 @@ def qkvr_prologue(*, x, w, d_r, **prologue_args):
     out = prologue(q=q, k=k, v=v, **prologue_args)
     out.update(r=r, q_proj=q, k_proj=k, v_proj=v)
     return out
+
+
+def i4_scales() -> np.ndarray:
+    """Every scale of the 4-bit cache in order, byte 0 .. 0xC6: 5 exponent bits (bias 15) and 3 mantissa
+    bits, written out from the format's definition."""
+    b = np.arange(0xC7)
+    e, m = b >> 3, b & 7
+    return np.where(e == 0, m * 2.0 ** -17, (1 + m / 8.0) * 2.0 ** (e - 15.0))
+
+
+def quantize_rows_i4(x_bits):
+    """Quantise rows of 128 bf16 values (uint16 bits, [..., 128]) to the 4-bit cache's codes
+    (uint8 [..., 64]) and scale bytes (uint8 [..., 4])."""
+    x = bf16_bits_to_f64(np.ascontiguousarray(x_bits, dtype=np.uint16))
+    lead = x.shape[:-1]
+    g = np.where(np.isnan(x), 0.0, x).reshape(*lead, 4, 32)
+    scales = i4_scales()
+    with np.errstate(divide="ignore", invalid="ignore"):
+        byte = np.minimum(np.searchsorted(scales * 7.0, np.abs(g).max(-1), side="left"), 0xC6)
+        s = scales[byte][..., None]
+        n = np.where(s > 0, np.clip(np.rint(g / s), -7, 7), 0.0)      # (rint: ties to even)
+    u = (n.astype(np.int64) + 8).reshape(*lead, 16, 8)
+    shift = np.array([4 * (e >> 1) + 16 * (e & 1) for e in range(8)])
+    words = (u << shift).sum(-1).astype(np.uint32)
+    codes = np.ascontiguousarray(words).astype("<u4").view(np.uint8).reshape(*lead, 64)
+    return codes, byte.astype(np.uint8)
+
+
+def dequantize_i4(codes, scale_bytes) -> np.ndarray:
+    """n * s of every value of 4-bit rows (codes [..., 64], scale bytes [..., 4]), as float64 [..., 128];
+    a group with a scale byte above 0xC6 reads as zeros."""
+    codes = np.ascontiguousarray(codes, dtype=np.uint8)
+    lead = codes.shape[:-1]
+    words = codes.view("<u4").astype(np.int64)
+    shift = np.array([4 * (e >> 1) + 16 * (e & 1) for e in range(8)])
+    n = ((words[..., None] >> shift) & 15) - 8
+    table = np.zeros(256)
+    table[:0xC7] = i4_scales()
+    s = table[np.asarray(scale_bytes, dtype=np.uint8)]
+    return (n.reshape(*lead, 4, 32) * s[..., None]).reshape(*lead, 128)

@@ -67,6 +67,17 @@ bool aligned(const void *ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>
 
 // ---------------------------------------------------------------- validation
 
+// The cache's element type, and the scales that a cache of codes has.
+bool valid_kv(int32_t kv_dtype, const void *k_scale, const void *v_scale) {
+    if (kv_dtype == INKATTN_KV_BF16) return true;
+    return (kv_dtype == INKATTN_KV_E4M3 || kv_dtype == INKATTN_KV_I4) && k_scale && v_scale && aligned(k_scale, 16) &&
+           aligned(v_scale, 16);
+}
+// Bytes of a cache row of one head.
+size_t kv_row_bytes(int32_t kv_dtype) {
+    return kv_dtype == INKATTN_KV_I4 ? kHeadDim / 2 : kv_dtype == INKATTN_KV_E4M3 ? kHeadDim : kHeadDim * 2;
+}
+
 inkattn_status validate_prologue(const inkattn_prologue_params *p) {
     if (!p || p->struct_size != sizeof(inkattn_prologue_params)) return INKATTN_ERR_INVALID_ARG;
     if (p->B < 1 || p->N_tok < 0 || p->max_seqlen_q < 0 || p->Hq < 1 || p->Hkv < 1 ||
@@ -85,10 +96,7 @@ inkattn_status validate_prologue(const inkattn_prologue_params *p) {
     for (const void *ptr : ptrs4)
         if (!ptr || !aligned(ptr, 4)) return INKATTN_ERR_INVALID_ARG;
     if (p->dev_status && !aligned(p->dev_status, 4)) return INKATTN_ERR_INVALID_ARG;
-    if (p->kv_dtype != INKATTN_KV_BF16 && p->kv_dtype != INKATTN_KV_E4M3) return INKATTN_ERR_INVALID_ARG;
-    if (p->kv_dtype == INKATTN_KV_E4M3 &&
-        (!p->k_scale || !p->v_scale || !aligned(p->k_scale, 16) || !aligned(p->v_scale, 16)))
-        return INKATTN_ERR_INVALID_ARG;
+    if (!valid_kv(p->kv_dtype, p->k_scale, p->v_scale)) return INKATTN_ERR_INVALID_ARG;
     return INKATTN_OK;
 }
 
@@ -140,10 +148,7 @@ inkattn_status validate_qkvr(const inkattn_qkvr_params *p) {
         if (!ptr || !aligned(ptr, 4)) return INKATTN_ERR_INVALID_ARG;
     if (p->dev_status && !aligned(p->dev_status, 4)) return INKATTN_ERR_INVALID_ARG;
     if (p->y_out && !aligned(p->y_out, 16)) return INKATTN_ERR_INVALID_ARG;
-    if (p->kv_dtype != INKATTN_KV_BF16 && p->kv_dtype != INKATTN_KV_E4M3) return INKATTN_ERR_INVALID_ARG;
-    if (p->kv_dtype == INKATTN_KV_E4M3 &&
-        (!p->k_scale || !p->v_scale || !aligned(p->k_scale, 16) || !aligned(p->v_scale, 16)))
-        return INKATTN_ERR_INVALID_ARG;
+    if (!valid_kv(p->kv_dtype, p->k_scale, p->v_scale)) return INKATTN_ERR_INVALID_ARG;
     // the new state is written while a sequence's first tile still reads the old one,
     // unless every sequence fits one tile
     if ((p->conv_state_k_out == p->conv_state_k_in || p->conv_state_v_out == p->conv_state_v_in) &&
@@ -152,7 +157,7 @@ inkattn_status validate_qkvr(const inkattn_qkvr_params *p) {
     // no output overlaps an input or another output (in == out for the states excepted)
     const size_t F = (size_t)(p->Hq + 2 * p->Hkv) * kHeadDim + (size_t)p->Hq * p->d_r;
     const size_t st = (size_t)p->num_state_slots * 3 * p->Hkv * kHeadDim * 2;
-    const size_t cache = (size_t)p->num_blocks * p->Hkv * 64 * kHeadDim * (p->kv_dtype == INKATTN_KV_E4M3 ? 1 : 2);
+    const size_t cache = (size_t)p->num_blocks * p->Hkv * 64 * kv_row_bytes(p->kv_dtype);
     struct Range { const void *a; size_t n; };
     const Range ins[] = {{p->x, (size_t)p->N_tok * p->d_model * 2}, {p->w, F * p->d_model * 2},
                          {p->conv_state_k_in, st}, {p->conv_state_v_in, st}};
@@ -219,10 +224,7 @@ inkattn_status validate_attn(const inkattn_attn_params *p) {
         if (!ptr || !aligned(ptr, 4)) return INKATTN_ERR_INVALID_ARG;
     if (p->lse && !aligned(p->lse, 4)) return INKATTN_ERR_INVALID_ARG;
     if (p->dev_status && !aligned(p->dev_status, 4)) return INKATTN_ERR_INVALID_ARG;
-    if (p->kv_dtype != INKATTN_KV_BF16 && p->kv_dtype != INKATTN_KV_E4M3) return INKATTN_ERR_INVALID_ARG;
-    if (p->kv_dtype == INKATTN_KV_E4M3 &&
-        (!p->k_scale || !p->v_scale || !aligned(p->k_scale, 16) || !aligned(p->v_scale, 16)))
-        return INKATTN_ERR_INVALID_ARG;
+    if (!valid_kv(p->kv_dtype, p->k_scale, p->v_scale)) return INKATTN_ERR_INVALID_ARG;
     if (p->rel_extent > 0) {
         if (p->d_r != 32) return INKATTN_ERR_UNSUPPORTED;
         if (!p->r || !p->P || !aligned(p->r, 16) || !aligned(p->P, 16)) return INKATTN_ERR_INVALID_ARG;
@@ -241,10 +243,10 @@ inkattn_status validate_locations(const inkattn_attn_params *p) {
         (void)cudaGetLastError();
         return INKATTN_ERR_INVALID_ARG;
     }
-    const bool f8 = p->kv_dtype == INKATTN_KV_E4M3;
+    const bool codes = p->kv_dtype != INKATTN_KV_BF16;
     const void *q = p->q;
-    const void *ptrs[] = {q, p->k_cache, p->v_cache, f8 ? static_cast<const void *>(p->k_scale) : q,
-                          f8 ? static_cast<const void *>(p->v_scale) : q};
+    const void *ptrs[] = {q, p->k_cache, p->v_cache, codes ? static_cast<const void *>(p->k_scale) : q,
+                          codes ? static_cast<const void *>(p->v_scale) : q};
     for (const void *ptr : ptrs) {
         cudaPointerAttributes a;
         if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
@@ -523,6 +525,18 @@ bool make_cache_map_e4m3(CUtensorMap *map, const void *base, long long rows) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_cache_map_i4(CUtensorMap *map, const void *base, long long rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)kHeadDim / 2, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)kHeadDim / 2};
+    cuuint32_t box[2] = {(cuuint32_t)kHeadDim / 2, (cuuint32_t)kBlock};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_qkvr_maps(const inkattn_qkvr_params &p, CUtensorMap *xmap, CUtensorMap *wmap) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
     if (!enc) return false;
@@ -727,7 +741,7 @@ inkattn_status run_prefill_bf16(const inkattn_attn_params &p, cudaStream_t strea
     return launch_status(launch_prefill_tc(p, scalars(p), qmap, kmap, vmap, stream));
 }
 
-// Workspace of the prefill over an E4M3 cache: bf16 K and V copies of B * max_blocks_per_seq
+// Workspace of the prefill over a cache of codes: bf16 K and V copies of B * max_blocks_per_seq
 // blocks, then their block table, each piece 256-byte aligned.
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t prefill_copy_bytes(const inkattn_attn_params &p) {
@@ -742,7 +756,7 @@ size_t prefill_ws_bytes(const inkattn_attn_params &p) {
 inkattn_status inkattn_prefill(const inkattn_attn_params *p, void *stream) {
     inkattn_status st = validate_attn(p);
     if (st != INKATTN_OK) return st;
-    if (p->kv_dtype != INKATTN_KV_BF16) return INKATTN_ERR_UNSUPPORTED;   // (inkattn_prefill_e4m3)
+    if (p->kv_dtype != INKATTN_KV_BF16) return INKATTN_ERR_UNSUPPORTED;   // (inkattn_prefill_e4m3, _i4)
     if ((st = validate_locations(p)) != INKATTN_OK) return st;
     if ((st = check_device(nullptr)) != INKATTN_OK) return st;
     if (p->N_tok == 0) return INKATTN_OK;
@@ -750,15 +764,16 @@ inkattn_status inkattn_prefill(const inkattn_attn_params *p, void *stream) {
 }
 
 size_t inkattn_prefill_workspace_bytes(const inkattn_attn_params *p) {
-    if (validate_attn(p) != INKATTN_OK || p->kv_dtype != INKATTN_KV_E4M3) return 0;
+    if (validate_attn(p) != INKATTN_OK || p->kv_dtype == INKATTN_KV_BF16) return 0;
     return prefill_ws_bytes(*p);
 }
 
-inkattn_status inkattn_prefill_e4m3(const inkattn_attn_params *p, void *workspace, size_t workspace_bytes,
-                                    void *stream) {
+// The prefill over a cache of codes of the given type.
+static inkattn_status prefill_codes(const inkattn_attn_params *p, int32_t kv_dtype, void *workspace,
+                                    size_t workspace_bytes, void *stream) {
     inkattn_status st = validate_attn(p);
     if (st != INKATTN_OK) return st;
-    if (p->kv_dtype != INKATTN_KV_E4M3) return INKATTN_ERR_INVALID_ARG;     // (inkattn_prefill)
+    if (p->kv_dtype != kv_dtype) return INKATTN_ERR_INVALID_ARG;
     // the copy's rows are addressed by TMA as 32-bit coordinates
     if ((long long)p->B * p->max_blocks_per_seq * p->Hkv * kBlock >= (1ll << 31)) return INKATTN_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < prefill_ws_bytes(*p))
@@ -781,7 +796,7 @@ inkattn_status inkattn_prefill_e4m3(const inkattn_attn_params *p, void *workspac
     inkattn_bf16 *v16 = reinterpret_cast<inkattn_bf16 *>(ws + copy);
     int32_t *table = reinterpret_cast<int32_t *>(ws + 2 * copy);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((st = launch_status(launch_dequant_e4m3(*p, k16, v16, table, s))) != INKATTN_OK) return st;
+    if ((st = launch_status(launch_dequant(*p, k16, v16, table, s))) != INKATTN_OK) return st;
     inkattn_attn_params q = *p;
     q.k_cache = k16;
     q.v_cache = v16;
@@ -791,6 +806,15 @@ inkattn_status inkattn_prefill_e4m3(const inkattn_attn_params *p, void *workspac
     q.block_table = table;
     q.num_blocks = p->B * p->max_blocks_per_seq;
     return run_prefill_bf16(q, s);
+}
+
+inkattn_status inkattn_prefill_e4m3(const inkattn_attn_params *p, void *workspace, size_t workspace_bytes,
+                                    void *stream) {
+    return prefill_codes(p, INKATTN_KV_E4M3, workspace, workspace_bytes, stream);
+}
+
+inkattn_status inkattn_prefill_i4(const inkattn_attn_params *p, void *workspace, size_t workspace_bytes, void *stream) {
+    return prefill_codes(p, INKATTN_KV_I4, workspace, workspace_bytes, stream);
 }
 
 int inkattn_decode_num_splits(const inkattn_attn_params *p, int num_sms) {
@@ -825,7 +849,9 @@ inkattn_status inkattn_decode(const inkattn_attn_params *p, int num_splits, void
     if (p->N_tok == 0) return INKATTN_OK;
     CUtensorMap qmap, kmap, vmap;
     const long long rows = (long long)p->num_blocks * p->Hkv * kBlock;
-    auto cache_map = p->kv_dtype == INKATTN_KV_E4M3 ? make_cache_map_e4m3 : make_cache_map;
+    auto cache_map = p->kv_dtype == INKATTN_KV_I4     ? make_cache_map_i4
+                     : p->kv_dtype == INKATTN_KV_E4M3 ? make_cache_map_e4m3
+                                                      : make_cache_map;
     if (!cache_map(&kmap, p->k_cache, rows) || !cache_map(&vmap, p->v_cache, rows) ||
         !make_q_group_map(&qmap, p->q, p->N_tok, p->Hq, p->Hq / p->Hkv, p->max_seqlen_q))
         return INKATTN_ERR_CUDA;

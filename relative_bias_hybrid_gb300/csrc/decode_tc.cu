@@ -41,6 +41,7 @@
 // and the natural-log LSE: straight to `out` with one split, else to the split workspace.
 #include "common.cuh"
 #include "fp8.cuh"
+#include "int4.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
 
@@ -53,26 +54,29 @@ constexpr int kKeys = 128;                 // keys per tile (two cache blocks)
 constexpr int kSlotBytes = 32768;          // one MMA operand tile: [d half][128 keys][128 B]
 constexpr int kTabW = 144;                 // distances per table row: 128 keys + up to 16 tokens
 constexpr int kTabRows = kDecodeMaxRows;   // g * ql <= 128
-constexpr int kF8TileBytes = kKeys * kHeadDim;           // one E4M3 tile: [128 keys][128 B]
-constexpr int kF8SlotBytes = kF8TileBytes + kKeys * 4;   // + its 128 row scales
 
-// Two variants.  kF8 = false (bf16 cache): TMA loads K/V tiles straight into the MMAs'
-// 4-slot ring.  kF8 = true (E4M3 cache): TMA loads E4M3 tiles and their row scales into a
-// 3-slot ring, and six converter warps (2-7) convert Q to f16 in place, then expand each
-// tile (code * scale, exactly) to f16 in a 3-slot MMA ring; P is packed as f16, so the MMAs
-// run kind::f16 on f16 operands.  Warps: 0 TMA, 1 MMA, [2, 8) converters (E4M3
-// only), then 8 softmax warps.
-template <bool kF8>
+// Three variants, by the cache's element type.  kKv = INKATTN_KV_BF16: TMA loads K/V tiles
+// straight into the MMAs' 4-slot ring.  INKATTN_KV_E4M3 and INKATTN_KV_I4: TMA loads tiles of
+// codes and their scales into a ring of their own (E4M3 3 slots, 4 bits 6), and six converter
+// warps (2-7) convert Q to f16 in place, then expand each tile (code * scale, exactly) to f16
+// in a 3-slot MMA ring; P is packed as f16, so the MMAs run kind::f16 on f16 operands.  Warps:
+// 0 TMA, 1 MMA, [2, 8) converters (codes only), then 8 softmax warps.
+template <int kKv>
 struct Dec {
-    static constexpr int kThreads = kF8 ? 512 : 320;
-    static constexpr int kWarpSm = kF8 ? 8 : 2;              // first softmax warp
-    static constexpr int kConvThreads = kF8 ? 192 : 0;       // converter warps 2-7
-    static constexpr int kSlots = kF8 ? 3 : 4;               // MMA operand ring
-    static constexpr int kF8Slots = kF8 ? 3 : 0;             // E4M3 ring
+    static constexpr bool kCodes = kKv != INKATTN_KV_BF16;
+    static constexpr bool kI4 = kKv == INKATTN_KV_I4;
+    static constexpr int kThreads = kCodes ? 512 : 320;
+    static constexpr int kWarpSm = kCodes ? 8 : 2;           // first softmax warp
+    static constexpr int kConvThreads = kCodes ? 192 : 0;    // converter warps 2-7
+    static constexpr int kSlots = kCodes ? 3 : 4;            // MMA operand ring
+    static constexpr int kCodeSlots = kI4 ? 6 : kCodes ? 3 : 0;      // ring of codes
+    static constexpr int kCodeRow = kI4 ? kI4RowBytes : kHeadDim;    // bytes of a row's codes
+    static constexpr int kCodeTile = kKeys * kCodeRow;               // one tile: [128 keys][row]
+    static constexpr int kCodeSlotBytes = kCodeTile + kKeys * 4;     // + 4 bytes of scales a row
     static constexpr int kOffQ = 0;
     static constexpr int kOffKV = 32768;
-    static constexpr int kOffF8 = kOffKV + kSlots * kSlotBytes;
-    static constexpr int kOffTab = kOffF8 + kF8Slots * kF8SlotBytes;   // 16-bit fixed point [g][ql][kTabW]
+    static constexpr int kOffCodes = kOffKV + kSlots * kSlotBytes;
+    static constexpr int kOffTab = kOffCodes + kCodeSlots * kCodeSlotBytes;   // 16-bit fixed point [g][ql][kTabW]
     static constexpr int kOffXchg = kOffTab + kTabRows * kTabW * 2;     // row maxima / sums
     static constexpr int kOffTsig = kOffXchg + 3 * 2 * kRows * 4;       // fp32 steps [g][ql][2 rounds]
     static constexpr int kOffBar = kOffTsig + kTabRows * 2 * 4;
@@ -86,13 +90,15 @@ struct Dec {
     static constexpr int B_TAB_FULL = B_PV_DONE + 2;
     static constexpr int B_TAB_FREE = B_TAB_FULL + 1;
     static constexpr int B_DRAIN = B_TAB_FREE + 1;
-    static constexpr int B_QF = B_DRAIN + 1;                 // E4M3: Q converted to f16
-    static constexpr int B_F8_FULL = B_QF + 1;
-    static constexpr int B_F8_EMPTY = B_F8_FULL + kF8Slots;
-    static constexpr int B_COUNT = B_F8_EMPTY + kF8Slots;
+    static constexpr int B_QF = B_DRAIN + 1;                 // codes: Q converted to f16
+    static constexpr int B_C_FULL = B_QF + 1;
+    static constexpr int B_C_EMPTY = B_C_FULL + kCodeSlots;
+    static constexpr int B_COUNT = B_C_EMPTY + kCodeSlots;
     static constexpr int kSmem = kOffBar + B_COUNT * 8 + 16;
     static_assert(kSmem <= 232448, "shared memory budget");
-    static_assert(kOffKV % 1024 == 0 && kOffF8 % 1024 == 0 && kF8SlotBytes % 128 == 0, "alignment of the rings");
+    static_assert(kOffKV % 1024 == 0 && kOffCodes % 1024 == 0 && kCodeSlotBytes % (kI4 ? 512 : 128) == 0,
+                  "alignment of the rings (the 64-byte swizzle of 4-bit tiles repeats every 512 bytes)");
+    static_assert(kOffTab % 16 == 0 && kOffBar % 8 == 0, "alignment of the table and the barriers");
     static_assert(kThreads == 32 * (kWarpSm + 8), "eight softmax warps last");
 };
 
@@ -114,13 +120,14 @@ struct DecTcArgs {
 
 }  // namespace
 
-template <bool kF8>
-__global__ void __launch_bounds__(Dec<kF8>::kThreads, 1)
+template <int kKv>
+__global__ void __launch_bounds__(Dec<kKv>::kThreads, 1)
 k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
             const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(1024) unsigned char smem[];
     grid_dep_wait();                                   // q and the cache: written by the prologue
-    using C = Dec<kF8>;
+    using C = Dec<kKv>;
+    constexpr bool kCodes = C::kCodes;
     const inkattn_attn_params &p = A.p;
     // band split: the CTAs of split 0 (the keys before the band) come first in the grid, so
     // that the short split-1 CTAs run on the SMs the streaming ones leave free
@@ -193,14 +200,14 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
     if (threadIdx.x == 0) {
         mbar_init(bar(C::B_Q), 1);
         for (int s = 0; s < C::kSlots; ++s) {
-            mbar_init(bar(C::B_KV_FULL + s), kF8 ? C::kConvThreads : 1);   // tile converters, or the TMA
+            mbar_init(bar(C::B_KV_FULL + s), kCodes ? C::kConvThreads : 1);   // tile converters, or the TMA
             mbar_init(bar(C::B_KV_EMPTY + s), 1);
         }
-        if constexpr (kF8) {
-            mbar_init(bar(C::B_QF), 192);
-            for (int s = 0; s < C::kF8Slots; ++s) {
-                mbar_init(bar(C::B_F8_FULL + s), 1);
-                mbar_init(bar(C::B_F8_EMPTY + s), C::kConvThreads);
+        if constexpr (kCodes) {
+            mbar_init(bar(C::B_QF), C::kConvThreads);
+            for (int s = 0; s < C::kCodeSlots; ++s) {
+                mbar_init(bar(C::B_C_FULL + s), 1);
+                mbar_init(bar(C::B_C_EMPTY + s), C::kConvThreads);
             }
         }
         for (int s = 0; s < 2; ++s) {
@@ -227,11 +234,11 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
     const float c_qk = lam * A.scale * kLog2e;       // S (with the bias folded in) -> log2 logit
     const float inv_scale = 1.f / A.scale;           // bias in S units
 
-    // E4M3 variant (512 threads, 128 registers each at launch): the warpgroups of the TMA,
+    // Variants with codes (512 threads, 128 registers each at launch): the warpgroups of the TMA,
     // MMA and converter warps give registers to the two softmax warpgroups (80 + 176).
     if (warp == 0) {
         // ================================ producer ================================
-        if constexpr (kF8) tc::reg_dealloc<80>();
+        if constexpr (kCodes) tc::reg_dealloc<80>();
         bool ok = true;
         if (lane == 0) {
             tma_prefetch_desc(&qmap);
@@ -242,10 +249,10 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
             tma_load_3d(s_base + C::kOffQ, &qmap, 0, hk * g, start, bar(C::B_Q));
             tma_load_3d(s_base + C::kOffQ + 16384, &qmap, 64, hk * g, start, bar(C::B_Q));
         }
-        // the ring the TMA fills: the MMAs' own (bf16 cache) or the E4M3 one
-        constexpr int kRing = kF8 ? C::kF8Slots : C::kSlots;
-        constexpr int kRingFull = kF8 ? C::B_F8_FULL : C::B_KV_FULL;
-        constexpr int kRingEmpty = kF8 ? C::B_F8_EMPTY : C::B_KV_EMPTY;
+        // the ring the TMA fills: the MMAs' own (bf16 cache) or that of codes
+        constexpr int kRing = kCodes ? C::kCodeSlots : C::kSlots;
+        constexpr int kRingFull = kCodes ? C::B_C_FULL : C::B_KV_FULL;
+        constexpr int kRingEmpty = kCodes ? C::B_C_EMPTY : C::B_KV_EMPTY;
         int kv_loads = 0;
         auto load_kv = [&](int n, int isv) -> bool {
             const int L = kv_loads++, slot = L % kRing;
@@ -272,7 +279,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                 have[half] = blk[half] >= 0 && blk[half] < p.num_blocks;
                 if (have[half]) row[half] = ((long long)blk[half] * p.Hkv + hk) * kBlock;
             }
-            if constexpr (!kF8) {
+            if constexpr (!kCodes) {
                 if (lane == 0) {
                     const uint32_t dst = s_base + C::kOffKV + slot * kSlotBytes;
                     const uint32_t fb = bar(C::B_KV_FULL + slot);
@@ -285,27 +292,27 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                     }
                 }
             } else {
-                // codes [128 keys][128 B], then the 128 row scales; a half without a loaded
+                // codes of 128 keys, then 4 bytes of scales for each; a half without a loaded
                 // block reads as zero codes (TMA fill) with zero scales (written here)
-                unsigned char *slot_p = smem + C::kOffF8 + slot * kF8SlotBytes;
-                float *sc = reinterpret_cast<float *>(slot_p + kF8TileBytes);
+                unsigned char *slot_p = smem + C::kOffCodes + slot * C::kCodeSlotBytes;
+                uint32_t *sc = reinterpret_cast<uint32_t *>(slot_p + C::kCodeTile);
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
                     if (!have[half]) {
-                        sc[half * 64 + lane] = 0.f;
-                        sc[half * 64 + 32 + lane] = 0.f;
+                        sc[half * 64 + lane] = 0u;
+                        sc[half * 64 + 32 + lane] = 0u;
                     }
                 __syncwarp();
                 if (lane == 0) {
                     const uint32_t dst = smem_u32(slot_p);
-                    const uint32_t fb = bar(C::B_F8_FULL + slot);
-                    mbar_arrive_expect_tx(fb, kF8TileBytes + 256u * (uint32_t)(have[0] + have[1]));
+                    const uint32_t fb = bar(C::B_C_FULL + slot);
+                    mbar_arrive_expect_tx(fb, C::kCodeTile + 256u * (uint32_t)(have[0] + have[1]));
                     const float *scales = isv ? p.v_scale : p.k_scale;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         if (blk[half] != -2 && !have[half]) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
-                        tma_load_2d(dst + half * 8192, map, 0, (int)row[half], fb);
-                        if (have[half]) bulk_load(dst + kF8TileBytes + half * 256, scales + row[half], 256u, fb);
+                        tma_load_2d(dst + half * (C::kCodeTile / 2), map, 0, (int)row[half], fb);
+                        if (have[half]) bulk_load(dst + C::kCodeTile + half * 256, scales + row[half], 256u, fb);
                     }
                 }
             }
@@ -328,8 +335,8 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
         }
     } else if (warp == 1) {
         // ================================ MMA issuer ================================
-        if constexpr (kF8) tc::reg_dealloc<80>();
-        constexpr uint32_t kFmt = kF8 ? tc::kFmtF16 : tc::kFmtBF16;   // both operands alike
+        if constexpr (kCodes) tc::reg_dealloc<80>();
+        constexpr uint32_t kFmt = kCodes ? tc::kFmtF16 : tc::kFmtBF16;   // both operands alike
         const uint32_t id_qk = tc::idesc(128, 128, kFmt, 0, 0);
         const uint32_t id_pv = tc::idesc(128, 128, kFmt, 0, 1);
         // the whole warp runs this loop with the same values in every lane (the MMAs and
@@ -339,7 +346,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
         const uint64_t dk0 = tc::sdesc_sw128(s_base + C::kOffKV, 16, 1024);
         const uint64_t dv0 = tc::sdesc_sw128(s_base + C::kOffKV, 16384, 1024);
         auto slot_off = [](int slot) { return (uint64_t)(slot * (kSlotBytes >> 4)); };
-        bool ok = wwait(bar(kF8 ? C::B_QF : C::B_Q), 0);      // (E4M3: Q once converted to f16)
+        bool ok = wwait(bar(kCodes ? C::B_QF : C::B_Q), 0);   // (codes: Q once converted to f16)
         int kv_used = 0;
         auto next_tile = [&](int &slot, bool &last) -> bool {
             const int L = kv_used++;
@@ -393,9 +400,9 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
         __syncwarp();
         (void)mbar_drain(bar(C::B_DRAIN), 0, p.dev_status, A.wait_ns);
         __syncwarp();
-    } else if (kF8 && warp < C::kWarpSm) {
-        // ================================ converters (E4M3 cache) ================================
-        if constexpr (kF8) tc::reg_dealloc<80>();
+    } else if (kCodes && warp < C::kWarpSm) {
+        // ================================ converters (caches of codes) ================================
+        if constexpr (kCodes) tc::reg_dealloc<80>();
         // warps 2-7 convert Q, then the K/V tiles
         const int ct = threadIdx.x - 64;                      // 0 .. 191
         bool ok = wwait(bar(C::B_Q), 0);
@@ -411,37 +418,74 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
         }
         for (int L = 0; L < 2 * N && ok; ++L) {
             const int n = L == 0 ? 0 : L == 2 * N - 1 ? N - 1 : (L & 1) ? (L + 1) >> 1 : (L >> 1) - 1;
-            const int s8 = L % C::kF8Slots, s16 = L % C::kSlots;
-            if (!(ok = wwait(bar(C::B_F8_FULL + s8), (L / C::kF8Slots) & 1))) break;
+            constexpr int kRing = kCodes ? C::kCodeSlots : 1;    // (the bf16 variant has no such warps)
+            const int s8 = L % kRing, s16 = L % C::kSlots;
+            if (!(ok = wwait(bar(C::B_C_FULL + s8), (L / kRing) & 1))) break;
             if (L >= C::kSlots && !(ok = wwait(bar(C::B_KV_EMPTY + s16), ((L / C::kSlots) - 1) & 1))) break;
-            const unsigned char *src = smem + C::kOffF8 + s8 * kF8SlotBytes;
-            const float *sc = reinterpret_cast<const float *>(src + kF8TileBytes);
+            const unsigned char *src = smem + C::kOffCodes + s8 * C::kCodeSlotBytes;
             unsigned char *dst = smem + C::kOffKV + s16 * kSlotBytes;
             const int key_end = min(T, kr_hi) - (kr_lo + n * kKeys);
             bool bad = false;
-            for (int it = ct; it < kKeys * 8; it += 192) {
-                const int key = it >> 3, j16 = it & 7, sw = key & 7;
-                const uint4 w = *reinterpret_cast<const uint4 *>(src + key * 128 + j16 * 16);
-                float sv = key < key_end ? sc[key] : 0.f;
-                const bool good = sv == 0.f || (sv >= 0x1p-24f && sv <= 128.f);
-                bad |= !good;
-                const __half2 s2 = __float2half2_rn(good ? sv : 0.f);
-                const int base = (j16 >> 2) * 16384 + key * 128;
-                *reinterpret_cast<uint4 *>(dst + base + ((((j16 & 3) * 2) ^ sw) << 4)) =
-                    make_uint4(e4m3x2_to_f16x2_scaled(w.x, s2), e4m3x2_to_f16x2_scaled(w.x >> 16, s2),
-                               e4m3x2_to_f16x2_scaled(w.y, s2), e4m3x2_to_f16x2_scaled(w.y >> 16, s2));
-                *reinterpret_cast<uint4 *>(dst + base + ((((j16 & 3) * 2 + 1) ^ sw) << 4)) =
-                    make_uint4(e4m3x2_to_f16x2_scaled(w.z, s2), e4m3x2_to_f16x2_scaled(w.z >> 16, s2),
-                               e4m3x2_to_f16x2_scaled(w.w, s2), e4m3x2_to_f16x2_scaled(w.w >> 16, s2));
+            if constexpr (C::kI4) {
+                // 16 pieces of 32 keys x one group of 32 values, shared out in turn so that the
+                // odd one falls on another warp with every tile; a lane takes one key's group: its
+                // 16 bytes (the TMA's 64-byte swizzle spreads eight keys over the banks), four
+                // chunks of 16 bytes out (the MMA's 128-byte swizzle does the same).  The loads of
+                // a tile go out before the first expansion.
+                constexpr int kWarps = 6, kPieces = (16 + kWarps - 1) / kWarps;
+                const int first = (warp - 2 + 2 * (L % 3)) % kWarps;
+                const uint32_t *sc = reinterpret_cast<const uint32_t *>(src + C::kCodeTile);
+                uint4 w[kPieces];
+                uint32_t byte[kPieces];
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int piece = first + kWarps * i;
+                    if (piece >= 16) break;
+                    const int key = (piece & 3) * 32 + lane, grp = piece >> 2;
+                    w[i] = *reinterpret_cast<const uint4 *>(src + key * kI4RowBytes + ((grp ^ ((key >> 1) & 3)) << 4));
+                    byte[i] = key < key_end ? (sc[key] >> (8 * grp)) & 0xFFu : 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int piece = first + kWarps * i;
+                    if (piece >= 16) break;
+                    const int key = (piece & 3) * 32 + lane, grp = piece >> 2;
+                    const bool good = byte[i] <= kI4ScaleMax;
+                    bad |= !good;
+                    const I4Scale f = i4_factors(good ? byte[i] : 0u);
+                    unsigned char *row = dst + (grp >> 1) * 16384 + key * 128;
+                    const int c0 = (grp & 1) * 4, sw = key & 7;
+                    *reinterpret_cast<uint4 *>(row + ((c0 ^ sw) << 4)) = i4_decode8(w[i].x, f);
+                    *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ sw) << 4)) = i4_decode8(w[i].y, f);
+                    *reinterpret_cast<uint4 *>(row + (((c0 + 2) ^ sw) << 4)) = i4_decode8(w[i].z, f);
+                    *reinterpret_cast<uint4 *>(row + (((c0 + 3) ^ sw) << 4)) = i4_decode8(w[i].w, f);
+                }
+            } else {
+                const float *sc = reinterpret_cast<const float *>(src + C::kCodeTile);
+                for (int it = ct; it < kKeys * 8; it += 192) {
+                    const int key = it >> 3, j16 = it & 7, sw = key & 7;
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + key * 128 + j16 * 16);
+                    float sv = key < key_end ? sc[key] : 0.f;
+                    const bool good = sv == 0.f || (sv >= 0x1p-24f && sv <= 128.f);
+                    bad |= !good;
+                    const __half2 s2 = __float2half2_rn(good ? sv : 0.f);
+                    const int base = (j16 >> 2) * 16384 + key * 128;
+                    *reinterpret_cast<uint4 *>(dst + base + ((((j16 & 3) * 2) ^ sw) << 4)) =
+                        make_uint4(e4m3x2_to_f16x2_scaled(w.x, s2), e4m3x2_to_f16x2_scaled(w.x >> 16, s2),
+                                   e4m3x2_to_f16x2_scaled(w.y, s2), e4m3x2_to_f16x2_scaled(w.y >> 16, s2));
+                    *reinterpret_cast<uint4 *>(dst + base + ((((j16 & 3) * 2 + 1) ^ sw) << 4)) =
+                        make_uint4(e4m3x2_to_f16x2_scaled(w.z, s2), e4m3x2_to_f16x2_scaled(w.z >> 16, s2),
+                                   e4m3x2_to_f16x2_scaled(w.w, s2), e4m3x2_to_f16x2_scaled(w.w >> 16, s2));
+                }
             }
             if (bad) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
             fence_proxy_async_smem();
-            mbar_arrive(bar(C::B_F8_EMPTY + s8));
+            mbar_arrive(bar(C::B_C_EMPTY + s8));
             mbar_arrive(bar(C::B_KV_FULL + s16));
         }
     } else {
         // ================================ softmax ================================
-        if constexpr (kF8) tc::reg_alloc<176>();
+        if constexpr (kCodes) tc::reg_alloc<176>();
         const int quad = warp & 3;
         const int sw = warp - C::kWarpSm;                     // softmax warp index 0..7
         const int hw = sw >> 2;                               // column half
@@ -686,7 +730,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
             if (hw == 0 && mx_raw != -INFINITY) {
                 // the tile's largest P of this row, computed as its element is, and its bf16 rounding
                 const float pm = fast_exp2(fmaf(mx_raw, c_qk, -ref));
-                if constexpr (kF8) lc_run += __half2float(__float2half_rn(pm)) - pm;
+                if constexpr (kCodes) lc_run += __half2float(__float2half_rn(pm)) - pm;
                 else lc_run += bf16_lo(pack_bf16(pm, 0.f)) - pm;
             }
             float2 l4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
@@ -697,7 +741,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                 const float2 x = ffma2(make_float2(s[2 * e], s[2 * e + 1]), cq, nref);
                 const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                 l4[e & 3] = fadd2(l4[e & 3], y);
-                pk[e] = kF8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+                pk[e] = kCodes ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
             }
             tc::st32(sbuf + 32 * hw, pk);
             const float2 l2 = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
@@ -768,23 +812,23 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
     }
 }
 
-template <bool kF8>
+template <int kKv>
 cudaError_t launch_decode_variant(const DecTcArgs &a, dim3 grid, const CUtensorMap &qmap, const CUtensorMap &kmap,
                                   const CUtensorMap &vmap, cudaStream_t stream) {
-    using C = Dec<kF8>;
-    if constexpr (kF8) {
+    using C = Dec<kKv>;
+    if constexpr (C::kCodes) {
         // the register split (2 warpgroups at 80 + 2 at 176 = 512 x 128) needs exactly 128
         // registers a thread at launch: with fewer, setmaxnreg.inc could never be satisfied
         static const cudaError_t regs_check = [] {
             cudaFuncAttributes fa;
-            if (cudaFuncGetAttributes(&fa, k_decode_tc<true>) != cudaSuccess) return cudaErrorInvalidDeviceFunction;
+            if (cudaFuncGetAttributes(&fa, k_decode_tc<kKv>) != cudaSuccess) return cudaErrorInvalidDeviceFunction;
             return fa.numRegs == 128 ? cudaSuccess : cudaErrorInvalidConfiguration;
         }();
         if (regs_check != cudaSuccess) return regs_check;
     }
-    cudaError_t err = cudaFuncSetAttribute(k_decode_tc<kF8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    cudaError_t err = cudaFuncSetAttribute(k_decode_tc<kKv>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (err != cudaSuccess) return err;
-    return launch_dependent(k_decode_tc<kF8>, grid, dim3(C::kThreads), C::kSmem, stream, 1, a, qmap, kmap, vmap);
+    return launch_dependent(k_decode_tc<kKv>, grid, dim3(C::kThreads), C::kSmem, stream, 1, a, qmap, kmap, vmap);
 }
 
 cudaError_t launch_decode_tc(const inkattn_attn_params &p, const AttnScalars &s, int num_splits,
@@ -802,8 +846,11 @@ cudaError_t launch_decode_tc(const inkattn_attn_params &p, const AttnScalars &s,
     a.wait_ns = kernel_debug().wait_ns;
     a.withhold = kernel_debug().withhold;
     const dim3 grid = a.band_split ? dim3(p.Hkv, p.B, 2) : dim3(num_splits, p.Hkv, p.B);
-    return p.kv_dtype == INKATTN_KV_E4M3 ? launch_decode_variant<true>(a, grid, qmap, kmap, vmap, stream)
-                                         : launch_decode_variant<false>(a, grid, qmap, kmap, vmap, stream);
+    switch (p.kv_dtype) {
+        case INKATTN_KV_E4M3: return launch_decode_variant<INKATTN_KV_E4M3>(a, grid, qmap, kmap, vmap, stream);
+        case INKATTN_KV_I4: return launch_decode_variant<INKATTN_KV_I4>(a, grid, qmap, kmap, vmap, stream);
+        default: return launch_decode_variant<INKATTN_KV_BF16>(a, grid, qmap, kmap, vmap, stream);
+    }
 }
 
 }  // namespace inkattn

@@ -70,10 +70,10 @@ struct AttnScalars {
 
 cudaError_t launch_prologue(const inkattn_prologue_params &p, cudaStream_t stream);
 cudaError_t launch_output_conv(const inkattn_output_conv_params &p, cudaStream_t stream);
-// The E4M3 cache blocks a prefill batch reads, expanded to bf16 copies (k_out, v_out:
+// The E4M3 or 4-bit cache blocks a prefill batch reads, expanded to bf16 copies (k_out, v_out:
 // [B * max_blocks_per_seq][Hkv][64][128]) with their block table (table_out: [B][max_blocks_per_seq]).
-cudaError_t launch_dequant_e4m3(const inkattn_attn_params &p, inkattn_bf16 *k_out, inkattn_bf16 *v_out,
-                                int32_t *table_out, cudaStream_t stream);
+cudaError_t launch_dequant(const inkattn_attn_params &p, inkattn_bf16 *k_out, inkattn_bf16 *v_out,
+                           int32_t *table_out, cudaStream_t stream);
 // qkvr projections with the prologue in their epilogue; xmap / wmap from make_qkvr_maps
 cudaError_t launch_qkvr(const inkattn_qkvr_params &p, const CUtensorMap &xmap, const CUtensorMap &wmap,
                         int num_sms, cudaStream_t stream);
@@ -144,6 +144,9 @@ bool make_cache_map(CUtensorMap *map, const void *base, long long rows);
 // The same rows as E4M3 codes: [num_blocks*Hkv*64 rows][128] bytes, box 64 rows x 128 bytes,
 // no swizzle (the decode's converter warps read it row by row).
 bool make_cache_map_e4m3(CUtensorMap *map, const void *base, long long rows);
+// The same rows as 4-bit codes: [num_blocks*Hkv*64 rows][64 bytes], box 64 rows x 64 bytes, 64-byte
+// swizzle (a converter lane reads 16 bytes of one row; eight rows then lie on all banks).
+bool make_cache_map_i4(CUtensorMap *map, const void *base, long long rows);
 // TMA descriptor for q viewed as [N_tok][Hq][128] bf16, box {64, 1, box_rows}, 128-byte swizzle.
 bool make_q_map(CUtensorMap *map, const void *base, int n_tok, int hq, int box_rows);
 // Q as [N_tok][Hq][128] with a box of {64 dims, `group` heads, `tokens` tokens}: the rows of

@@ -28,6 +28,7 @@
 #include "common.cuh"
 #include "conv4.cuh"
 #include "fp8.cuh"
+#include "int4.cuh"
 #include "internal.h"
 
 namespace inkattn {
@@ -178,7 +179,7 @@ k_prologue(const inkattn_prologue_params p, const int kv_tiles) {
     // conv (rounded to bf16), K RMSNorm, cache write.  Half-warps 0-7 take the K stream and
     // 8-15 the V stream.
     const long long slot_limit = (long long)p.num_blocks * kBlock;
-    const bool f8 = p.kv_dtype == INKATTN_KV_E4M3;
+    const bool f8 = p.kv_dtype == INKATTN_KV_E4M3, i4 = p.kv_dtype == INKATTN_KV_I4;
     const int stream = half >> 3;
     const float *wsm = stream == 0 ? s_wk : s_wv;
 #pragma unroll 1
@@ -235,6 +236,19 @@ k_prologue(const inkattn_prologue_params p, const int kv_tiles) {
             row_scale = pow2f(k);
             codes = e4m3_encode8(r8, pow2f(-k));
         }
+        // 4-bit cache: one scale per 32 values (four lanes), a word of codes a lane
+        uint32_t scale_byte = 0;
+        if (i4) {
+            float r8[8];
+            unpack8(row, r8);
+            float am = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(r8[e]));
+            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+            scale_byte = i4_scale_byte(am);
+            codes.x = i4_encode8(r8, i4_scale(scale_byte));
+        }
         const int sm = __shfl_sync(0xffffffffu, sm_mine, ((half & 1) << 4) + u);
         if (!valid) continue;
         if (sm < 0 || (long long)sm >= slot_limit) {
@@ -244,7 +258,11 @@ k_prologue(const inkattn_prologue_params p, const int kv_tiles) {
         const size_t drow = ((size_t)(sm / kBlock) * p.Hkv + hk) * kBlock + (sm % kBlock);
         const size_t dst = drow * kHeadDim + c0;
         void *cache = stream == 0 ? p.k_cache : p.v_cache;
-        if (!f8) {
+        if (i4) {
+            *reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(cache) + drow * kI4RowBytes + lane16 * 4) = codes.x;
+            unsigned char *sc = reinterpret_cast<unsigned char *>(stream == 0 ? p.k_scale : p.v_scale);
+            if ((lane16 & 3) == 0) sc[drow * kI4RowScales + (lane16 >> 2)] = (unsigned char)scale_byte;
+        } else if (!f8) {
             *reinterpret_cast<uint4 *>(static_cast<inkattn_bf16 *>(cache) + dst) = row;
         } else {
             *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(cache) + dst) = codes;

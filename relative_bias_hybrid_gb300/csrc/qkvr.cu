@@ -8,7 +8,7 @@
 //  シャーディング]: the K/V conv, the Q/K RMSNorm and the cache write fused so that nothing
 //  intermediate goes back to memory; here the projections themselves never do either.
 // The prologue's arithmetic is that of prologue.cu: conv correctly rounded to bf16, RMSNorm
-// in fp32 over the bf16 row, the same E4M3 row quantisation.
+// in fp32 over the bf16 row, the same E4M3 and 4-bit row quantisation.
 //
 // GEMM: y[t][o] = sum_k x[t][k] w[o][k], fp32 accumulation in TMEM, each value rounded once
 // to bf16.  Output features in the order [q heads | k | v | r heads].
@@ -52,6 +52,7 @@
 #include "common.cuh"
 #include "conv4.cuh"
 #include "fp8.cuh"
+#include "int4.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
 #include "cta_pair.cuh"
@@ -348,7 +349,7 @@ k_qkvr(const QkvrArgs A, const __grid_constant__ CUtensorMap xmap, const __grid_
             gk[j] = __ldg(p.k_norm_w + c0 + j);
         }
         const long long slot_limit = (long long)p.num_blocks * kBlock;
-        const bool f8 = p.kv_dtype == INKATTN_KV_E4M3;
+        const bool f8 = p.kv_dtype == INKATTN_KV_E4M3, i4 = p.kv_dtype == INKATTN_KV_I4;
         int i = 0;
         for (int w = cid; w < n_items; w += nclusters, ++i) {
             int mt, cb;
@@ -510,6 +511,18 @@ k_qkvr(const QkvrArgs A, const __grid_constant__ CUtensorMap xmap, const __grid_
                     row_scale = pow2f(kx);
                     codes = e4m3_encode8(r8, pow2f(-kx));
                 }
+                uint32_t scale_byte = 0;
+                if (i4) {
+                    float r8[8];
+                    unpack8(outrow, r8);
+                    float am = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(r8[j]));
+                    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+                    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+                    scale_byte = i4_scale_byte(am);
+                    codes.x = i4_encode8(r8, i4_scale(scale_byte));
+                }
                 if (!valid) continue;
                 const int sm = __ldg(p.slot_mapping + tok);
                 if (sm < 0 || (long long)sm >= slot_limit) {
@@ -519,7 +532,11 @@ k_qkvr(const QkvrArgs A, const __grid_constant__ CUtensorMap xmap, const __grid_
                 const size_t drow = ((size_t)(sm / kBlock) * p.Hkv + hk) * kBlock + (sm % kBlock);
                 const size_t dst = drow * kHeadDim + c0;
                 void *cache = type == 1 ? p.k_cache : p.v_cache;
-                if (!f8) {
+                if (i4) {
+                    *reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(cache) + drow * kI4RowBytes + l16 * 4) = codes.x;
+                    unsigned char *sc = reinterpret_cast<unsigned char *>(type == 1 ? p.k_scale : p.v_scale);
+                    if ((l16 & 3) == 0) sc[drow * kI4RowScales + (l16 >> 2)] = (unsigned char)scale_byte;
+                } else if (!f8) {
                     *reinterpret_cast<uint4 *>(static_cast<inkattn_bf16 *>(cache) + dst) = outrow;
                 } else {
                     *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(cache) + dst) = codes;

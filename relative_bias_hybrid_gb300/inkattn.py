@@ -28,6 +28,7 @@ INKATTN_DTYPE_BF16 = 0
 INKATTN_DTYPE_F32 = 1
 INKATTN_KV_BF16 = 0
 INKATTN_KV_E4M3 = 1
+INKATTN_KV_I4 = 4
 INKATTN_ACT_NONE = 0
 INKATTN_ACT_RELU = 1
 INKATTN_ACT_GELU = 2
@@ -190,6 +191,8 @@ def lib():
             L.inkattn_prefill_workspace_bytes.restype = ctypes.c_size_t
             L.inkattn_prefill_e4m3.argtypes = [P(AttnParams), _c_ptr, ctypes.c_size_t, _c_ptr]
             L.inkattn_prefill_e4m3.restype = ctypes.c_int
+            L.inkattn_prefill_i4.argtypes = [P(AttnParams), _c_ptr, ctypes.c_size_t, _c_ptr]
+            L.inkattn_prefill_i4.restype = ctypes.c_int
             L.inkattn_linear.argtypes = [P(LinearParams), _c_ptr]
             L.inkattn_linear.restype = ctypes.c_int
             L.inkattn_grouped_linear.argtypes = [P(GroupedLinearParams), _c_ptr]
@@ -253,6 +256,12 @@ def inkattn_prefill_e4m3(p: AttnParams, workspace: Optional[torch.Tensor], strea
     ptr, nbytes = _workspace(workspace)
     return _check(lib().inkattn_prefill_e4m3(ctypes.byref(p), ptr, nbytes, _stream(stream)),
                   "inkattn_prefill_e4m3", raise_on_error)
+
+
+def inkattn_prefill_i4(p: AttnParams, workspace: Optional[torch.Tensor], stream=None, raise_on_error=True) -> int:
+    ptr, nbytes = _workspace(workspace)
+    return _check(lib().inkattn_prefill_i4(ctypes.byref(p), ptr, nbytes, _stream(stream)), "inkattn_prefill_i4",
+                  raise_on_error)
 
 
 def inkattn_decode_num_splits(p: AttnParams, num_sms: int) -> int:
@@ -345,13 +354,30 @@ def _workspace(t: Optional[torch.Tensor]):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _kv_dtype(cache):
-    """kv_dtype of a cache tensor: bf16 values, or E4M3 codes held as uint8."""
+def _kv_dtype(cache, head_dim):
+    """kv_dtype of a cache tensor: bf16 values, or codes held as uint8, a byte a value (E4M3) or
+    half of one (4 bits)."""
     if cache.dtype == torch.bfloat16:
         return INKATTN_KV_BF16, torch.bfloat16
     if cache.dtype == torch.uint8:
-        return INKATTN_KV_E4M3, torch.uint8
-    raise TypeError(f"KV cache: expected bfloat16 or uint8 (E4M3 codes), got {cache.dtype}")
+        return (INKATTN_KV_I4 if 2 * cache.shape[-1] == head_dim else INKATTN_KV_E4M3), torch.uint8
+    raise TypeError(f"KV cache: expected bfloat16 or uint8 (E4M3 or 4-bit codes), got {cache.dtype}")
+
+
+def _kv_cache(p, k_cache, v_cache, k_scale, v_scale):
+    """Fill the cache fields of a params struct: the codes' scales are fp32 [num_blocks][Hkv][64]
+    (E4M3) or uint8 [num_blocks][Hkv][64][4] (4 bits)."""
+    p.kv_dtype, dt = _kv_dtype(k_cache, p.head_dim)
+    p.k_cache = _ptr(k_cache, dt, "k_cache"); p.v_cache = _ptr(v_cache, dt, "v_cache")
+    if p.kv_dtype == INKATTN_KV_I4:
+        rows = (p.num_blocks, p.Hkv, p.block_size)
+        _one_device(k_cache, v_cache, k_scale, v_scale)
+        for t, per, name in ((k_cache, 2, "k_cache"), (v_cache, 2, "v_cache"), (k_scale, 32, "k_scale"),
+                             (v_scale, 32, "v_scale")):
+            _shape(t, (*rows, p.head_dim // per), name)
+        p.k_scale = _ptr(k_scale, torch.uint8, "k_scale"); p.v_scale = _ptr(v_scale, torch.uint8, "v_scale")
+    elif p.kv_dtype == INKATTN_KV_E4M3:
+        p.k_scale = _ptr(k_scale, torch.float32, "k_scale"); p.v_scale = _ptr(v_scale, torch.float32, "v_scale")
 
 
 def prologue_params(*, q, k, v, conv_w_k, conv_w_v, q_norm_w, k_norm_w, cu_seqlens_q, state_slot,
@@ -381,10 +407,7 @@ def prologue_params(*, q, k, v, conv_w_k, conv_w_v, q_norm_w, k_norm_w, cu_seqle
     p.conv_state_k = _ptr(conv_state_k, bf, "conv_state_k")
     p.conv_state_v = _ptr(conv_state_v, bf, "conv_state_v")
     p.q_out = _ptr(q_out, bf, "q_out")
-    p.kv_dtype, cache_dt = _kv_dtype(k_cache)
-    p.k_cache = _ptr(k_cache, cache_dt, "k_cache"); p.v_cache = _ptr(v_cache, cache_dt, "v_cache")
-    if p.kv_dtype == INKATTN_KV_E4M3:
-        p.k_scale = _ptr(k_scale, f32, "k_scale"); p.v_scale = _ptr(v_scale, f32, "v_scale")
+    _kv_cache(p, k_cache, v_cache, k_scale, v_scale)
     p.dev_status = _ptr(dev_status, i32, "dev_status")
     return p
 
@@ -414,10 +437,7 @@ def attn_params(*, q, k_cache, v_cache, cu_seqlens_q, seqlen_k, block_table, out
     p.q = _ptr(q, bf, "q")
     p.r = _ptr(r, bf, "r") if rel_extent > 0 else None
     p.P = _ptr(P, f32, "P") if rel_extent > 0 else None
-    p.kv_dtype, cache_dt = _kv_dtype(k_cache)
-    p.k_cache = _ptr(k_cache, cache_dt, "k_cache"); p.v_cache = _ptr(v_cache, cache_dt, "v_cache")
-    if p.kv_dtype == INKATTN_KV_E4M3:
-        p.k_scale = _ptr(k_scale, f32, "k_scale"); p.v_scale = _ptr(v_scale, f32, "v_scale")
+    _kv_cache(p, k_cache, v_cache, k_scale, v_scale)
     p.cu_seqlens_q = _ptr(cu_seqlens_q, i32, "cu_seqlens_q")
     p.seqlen_k = _ptr(seqlen_k, i32, "seqlen_k")
     p.block_table = _ptr(block_table, i32, "block_table")
@@ -491,10 +511,7 @@ def qkvr_params(*, x, w, conv_w_k, conv_w_v, q_norm_w, k_norm_w, cu_seqlens_q, s
     p.conv_state_v_out = _ptr(conv_state_v_out, bf, "conv_state_v_out")
     p.q_out = _ptr(q_out, bf, "q_out"); p.r_out = _ptr(r_out, bf, "r_out")
     p.y_out = _ptr(y_out, bf, "y_out")
-    p.kv_dtype, cache_dt = _kv_dtype(k_cache)
-    p.k_cache = _ptr(k_cache, cache_dt, "k_cache"); p.v_cache = _ptr(v_cache, cache_dt, "v_cache")
-    if p.kv_dtype == INKATTN_KV_E4M3:
-        p.k_scale = _ptr(k_scale, f32, "k_scale"); p.v_scale = _ptr(v_scale, f32, "v_scale")
+    _kv_cache(p, k_cache, v_cache, k_scale, v_scale)
     p.dev_status = _ptr(dev_status, i32, "dev_status")
     return p
 

@@ -115,7 +115,7 @@ _TENSOR_IDS = {"q": 1, "k": 2, "v": 3, "r": 4, "P": 5, "conv_w_k": 6, "conv_w_v"
                "k_cache": 12, "v_cache": 13, "perm": 14, "y": 15, "residual": 16,
                "oc_conv_w": 17, "oc_norm_w": 18, "oc_conv_state": 19, "k_cache_e4m3": 20,
                "v_cache_e4m3": 21, "x": 22, "w_qkvr": 23, "w_o": 24, "w_router": 25, "w_up": 26,
-               "w_down": 27, "w_shared_up": 28, "w_shared_down": 29}
+               "w_down": 27, "w_shared_up": 28, "w_shared_down": 29, "k_cache_i4": 30, "v_cache_i4": 31}
 
 
 def _gen(device, seed: int, tensor: str) -> torch.Generator:
@@ -140,7 +140,8 @@ def make_inputs(w: Workload, seed: int = 0, device="cpu", kv_dtype: str = "bf16"
     conv_state_k, conv_state_v [B,3,C] bf16; state_slot [B]; cu_seqlens_q [B+1];
     seqlen_k [B]; block_table [B,max_blocks] (-1 past each sequence's blocks);
     slot_mapping [N]; k_cache, v_cache [num_blocks,Hkv,64,d] bf16, or with kv_dtype "e4m3"
-    uint8 E4M3 codes plus k_scale, v_scale [num_blocks,Hkv,64] fp32.
+    uint8 E4M3 codes plus k_scale, v_scale [num_blocks,Hkv,64] fp32, or with "i4" uint8
+    [num_blocks,Hkv,64,d/2] 4-bit codes plus k_scale, v_scale [num_blocks,Hkv,64,4] uint8.
     """
     device = torch.device(device)
     d, C, N, B = w.head_dim, w.Hkv * w.head_dim, w.N_tok, w.B
@@ -204,6 +205,14 @@ def make_inputs(w: Workload, seed: int = 0, device="cpu", kv_dtype: str = "bf16"
             x = _normal(shape, 128.0, device, seed, f"{name}_cache_e4m3", torch.float32)
             out[f"{name}_cache"] = x.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
             out[f"{name}_scale"] = torch.full(shape[:3], 2.0 ** -7, dtype=torch.float32, device=device)
+    elif kv_dtype == "i4":
+        # 4-bit codes 1 .. 15 drawn evenly, and scales of 0.25 (byte 0x68): the cached rows read
+        # back as values of about unit size
+        for name in ("k", "v"):
+            g = _gen(device, seed, f"{name}_cache_i4")
+            code = torch.randint(1, 16, (2, *shape[:3], d // 2), generator=g, device=device, dtype=torch.uint8)
+            out[f"{name}_cache"] = code[0] | (code[1] << 4)
+            out[f"{name}_scale"] = torch.full((*shape[:3], d // 32), 0x68, dtype=torch.uint8, device=device)
     else:
         raise ValueError(kv_dtype)
     return out

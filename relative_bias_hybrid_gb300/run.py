@@ -29,7 +29,7 @@ def main(argv=None):
     ap.add_argument("--seqs", type=int, default=0, help="keep only the first N sequences")
     ap.add_argument("--seed", type=int, default=0)
     ap.add_argument("--splits", type=int, default=0, help="decode splits (0 = the library's heuristic)")
-    ap.add_argument("--kv", choices=["bf16", "e4m3"], default="bf16", help="KV-cache element type")
+    ap.add_argument("--kv", choices=["bf16", "e4m3", "i4"], default="bf16", help="KV-cache element type")
     ap.add_argument("--output-conv", action="store_true",
                     help="also run the attention-output conv (hidden width Hq * 128) after each pass")
     ap.add_argument("--qkvr", action="store_true",
