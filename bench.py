@@ -612,7 +612,7 @@ def measure(name, args, peaks, dev, stream, flush):
     if mode == "prefill":
         fl = attention_flops(w)
         tf = fl / (att_ms * 1e-3) / 1e12
-        roof = {"bound": "tensor", "kernel": "k_prefill_tc" if kv == "bf16" else "k_dequant_e4m3+k_prefill_tc",
+        roof = {"bound": "tensor", "kernel": "k_prefill_tc" if kv == "bf16" else "k_dequant<false>+k_prefill_tc",
                 "achieved": tf, "peak": peaks["bf16"],
                 "unit": "TFLOP/s", "frac": tf / peaks["bf16"], "peak_src": peaks["src"] + " (burst bf16)",
                 "frac_of_sustained": tf / peaks["bf16_sustained"], "traffic": ncu_traffic("k_prefill_tc", name),

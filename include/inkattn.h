@@ -605,6 +605,116 @@ typedef struct inkattn_expert_combine_params {
  * device; out overlaps no input. */
 INKATTN_API inkattn_status inkattn_expert_combine(const inkattn_expert_combine_params *p, void *stream);
 
+/* ------------------------------------------------------------------------------
+ * A verification step's end [VJ and VV: 8 chained MTP heads draft tokens, and the next step's decode
+ * runs over a sequence's last token and its drafts].  Behind the decode: the probabilities of
+ * the step's logits, the drafts that stand and the token behind them, and the conv states of
+ * the rows kept.  The rejected rows of the KV cache need no undoing: they lie behind the
+ * sequence's new length and are written again.
+ * ------------------------------------------------------------------------------ */
+#define INKATTN_MAX_VOCAB (1 << 20)
+
+/* Probabilities of rows of logits, with t = temperature[row] (1 where temperature is NULL):
+ *   probs[row][v] = exp((l_v - m) / t) / sum_w exp((l_w - m) / t),  m the row's largest logit;
+ *   t = 0: 1 at the first of the largest logits, 0 elsewhere.
+ * A NaN counts as -infinity; a row of -infinities gives zeros; of a row with infinite logits,
+ * those alone share the 1.  A temperature that is negative, infinite or NaN is flagged
+ * (INKATTN_ERR_DEVICE_BOUNDS) and its row written as zeros.  Relative error at most
+ * (32 + V 2^-13 + 2 (m - l_v) / t) 2^-23 of a value, and possibly 0 below 2^-125. */
+typedef struct inkattn_token_probs_params {
+    size_t struct_size;        /* = sizeof(inkattn_token_probs_params)                   */
+    int32_t N_tok;             /* rows, 0 .. 2^24                                        */
+    int32_t V;                 /* logits of a row, 1 .. INKATTN_MAX_VOCAB                */
+    int32_t logits_dtype;      /* INKATTN_DTYPE_BF16 (0) or INKATTN_DTYPE_F32 (1)        */
+    int64_t logits_stride;     /* elements from row to row, >= V                         */
+    int64_t probs_stride;      /* elements from row to row, >= V                         */
+    const void *logits;        /* [N_tok][logits_stride], bf16 or fp32                   */
+    const float *temperature;  /* nullable, [N_tok]                                      */
+    float *probs;              /* [N_tok][probs_stride]; what lies behind V is not written */
+    int32_t *dev_status;       /* nullable                                               */
+} inkattn_token_probs_params;
+
+/* Runs the softmax.  Arrays aligned to their elements' size, in memory of the current device; probs
+ * may be the logits array itself (fp32, the same stride), but overlaps no input otherwise. */
+INKATTN_API inkattn_status inkattn_token_probs(const inkattn_token_probs_params *p, void *stream);
+
+/* Verification of drafted tokens by rejection sampling.  Sequence b has the rows cu_seqlens_q[b]
+ * .. cu_seqlens_q[b+1] - 1 of the step: its last token and its drafts, token_ids as the step took
+ * them in.  Row i of a sequence holds the target's distribution p_i behind its token and, where
+ * draft_p is given, the distribution q_i that the next row's draft x = token_ids[row + 1] was
+ * drawn from (the last row's is not read).  Drafts are taken in order while
+ *   u_accept[row] * q_i(x) < p_i(x)        (fp32; draft_p NULL: q_i(x) = 1, a draft without choice)
+ * and the token behind them is drawn from max(p_i - q_i, 0) at the first row i whose draft does
+ * not stand (draft_p NULL: from p_i without x), or from the last row's p_i where all do; where that
+ * weight is zero everywhere, from p_i.  A probability outside [0, 1] counts as the nearer bound, a
+ * NaN as 0.
+ *   Drawing: weights w_v are rounded to multiples of 2^-43 (ties to even) and summed as whole
+ *   numbers, W in all; with U = floor(u_sample[b] 2^32) the token is the smallest v with w_0 + ..
+ *   + w_v > floor(W U / 2^32).  The result depends on no order of sums, and is the same on
+ *   every call and device.
+ * n_new[b] = drafts that stand + 1: the step's new tokens, and the rows of the step that keep
+ * their place (the n_keep of inkattn_conv_rollback); 0 for a sequence without rows.  out_tokens at
+ * the sequence's rows: the drafts that stand, the drawn token, then -1.
+ * Flagged (INKATTN_ERR_DEVICE_BOUNDS): a cu_seqlens_q out of range or decreasing (n_new 0, the
+ * tokens not written), a draft outside [0, V) (does not stand, nothing is taken from p_i for it), a
+ * row to draw from whose weights are all zero (token -1, n_new without it).  u values outside
+ * [0, 1) count as the nearer bound (the largest float below 1), a NaN as 0. */
+typedef struct inkattn_verify_drafts_params {
+    size_t struct_size;        /* = sizeof(inkattn_verify_drafts_params)                 */
+    int32_t B;                 /* sequences, 1 .. 2^20                                   */
+    int32_t N_tok;             /* rows = cu_seqlens_q[B], 0 .. 2^24                      */
+    int32_t V;                 /* vocabulary, 1 .. INKATTN_MAX_VOCAB                     */
+    int64_t target_stride;     /* elements from row to row, >= V                         */
+    int64_t draft_stride;      /* the same of draft_p (not read where that is NULL)      */
+    const float *target_p;     /* [N_tok][target_stride]                                 */
+    const float *draft_p;      /* nullable, [N_tok][draft_stride]                        */
+    const int32_t *token_ids;  /* [N_tok]                                                */
+    const int32_t *cu_seqlens_q;   /* [B+1]                                              */
+    const float *u_accept;     /* [N_tok], in [0, 1)                                     */
+    const float *u_sample;     /* [B], in [0, 1)                                         */
+    int32_t *n_new;            /* [B]                                                    */
+    int32_t *out_tokens;       /* [N_tok]                                                */
+    int32_t *dev_status;       /* nullable                                               */
+} inkattn_verify_drafts_params;
+
+/* Runs the verification.  All arrays 4-byte aligned, in memory of the current device; the outputs
+ * overlap neither each other nor an input. */
+INKATTN_API inkattn_status inkattn_verify_drafts(const inkattn_verify_drafts_params *p, void *stream);
+
+/* The conv states behind the first n_keep[b] of a step's rows: with xs = the 3 rows of
+ * state_before[slot], then the rows of x from cu_seqlens_q[b] on,
+ *   state_after[slot][i] = xs[n_keep[b] + i],  i = 0 .. 2,  slot = state_slot[b],
+ * for every conv of `states` (a layer's K, V, attention output and MLP output, say) in one
+ * launch.  state_before is the state from before the step, which a call that updates its state
+ * in place has overwritten: keep a copy, or let inkattn_qkvr_prologue write elsewhere.  Other slots
+ * are not touched.  A cu_seqlens_q, slot or n_keep (0 .. the sequence's rows) out of range is
+ * flagged (INKATTN_ERR_DEVICE_BOUNDS) and its sequence skipped. */
+#define INKATTN_ROLLBACK_MAX_STATES 8
+typedef struct inkattn_conv_rows {
+    int32_t C;                 /* channels: a multiple of 8, 8 .. 2^20                   */
+    int64_t x_stride;          /* elements from row to row of x, >= C, a multiple of 8   */
+    const inkattn_bf16 *x;     /* [N_tok][x_stride], the conv's input rows of the step   */
+    const inkattn_bf16 *state_before;  /* [num_state_slots][3][C]                        */
+    inkattn_bf16 *state_after;         /* [num_state_slots][3][C]; may be state_before   */
+} inkattn_conv_rows;
+typedef struct inkattn_conv_rollback_params {
+    size_t struct_size;        /* = sizeof(inkattn_conv_rollback_params)                 */
+    int32_t B;                 /* sequences, 1 .. 65535                                  */
+    int32_t N_tok;             /* rows = cu_seqlens_q[B], >= 0                           */
+    int32_t num_state_slots;   /* capacity in slots (bounds check), >= 1                 */
+    int32_t n_states;          /* 1 .. INKATTN_ROLLBACK_MAX_STATES                       */
+    const int32_t *cu_seqlens_q;   /* [B+1]                                              */
+    const int32_t *state_slot;     /* [B], distinct values in [0, num_state_slots)       */
+    const int32_t *n_keep;         /* [B]                                                */
+    int32_t *dev_status;           /* nullable                                           */
+    inkattn_conv_rows states[INKATTN_ROLLBACK_MAX_STATES];
+} inkattn_conv_rollback_params;
+
+/* Runs the rollback.  x (nullable where N_tok is 0) and the states 16-byte aligned, all arrays in
+ * memory of the current device; a state_after overlaps no other array, its own state_before either
+ * exactly or not at all. */
+INKATTN_API inkattn_status inkattn_conv_rollback(const inkattn_conv_rollback_params *p, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,7 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libinkattn.so")
 SOURCES = ["api.cu", "prologue.cu", "decode.cu", "decode_tc.cu", "prefill_tc.cu", "prefill_2q.cu", "decode_noalloc.cu",
-           "output_conv.cu", "qkvr.cu", "dequant.cu", "linear.cu", "linear_few.cu", "route.cu"]
+           "output_conv.cu", "qkvr.cu", "dequant.cu", "linear.cu", "linear_few.cu", "route.cu",
+           "verify.cu", "rollback.cu"]
 HEADERS = ["common.cuh", "internal.h", "tcgen05.cuh", "context_cache.h", "conv4.cuh", "fp8.cuh", "int4.cuh", "cta_pair.cuh",
            "activation.cuh", "device_table.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

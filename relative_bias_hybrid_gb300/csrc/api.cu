@@ -2,7 +2,7 @@
 // descriptor setup, the decode split heuristic, and the launches.
 //
 // Nothing here computes on the host: every step of the path runs in the kernels of
-// prologue.cu, qkvr.cu, output_conv.cu, prefill_tc.cu, decode.cu, linear.cu and route.cu.
+// prologue.cu, qkvr.cu, output_conv.cu, prefill_tc.cu, decode.cu, linear.cu, route.cu, verify.cu and rollback.cu.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -383,6 +383,86 @@ inkattn_status validate_expert_combine(const inkattn_expert_combine_params *p) {
     return INKATTN_OK;
 }
 
+// Bytes that `rows` rows of `width` elements of `size` bytes span, `stride` elements apart.
+size_t span(int64_t rows, int64_t stride, int64_t width, size_t size) {
+    return rows > 0 ? ((size_t)(rows - 1) * stride + width) * size : 0;
+}
+constexpr int64_t kMaxRowStride = 1ll << 32;       // (spans stay far below 2^63)
+
+inkattn_status validate_token_probs(const inkattn_token_probs_params *p) {
+    if (!p || p->struct_size != sizeof(inkattn_token_probs_params) || p->N_tok < 0 || p->N_tok > (1 << 24) || p->V < 1 ||
+        p->V > INKATTN_MAX_VOCAB || p->logits_stride < p->V || p->probs_stride < p->V ||
+        p->logits_stride > kMaxRowStride || p->probs_stride > kMaxRowStride)
+        return INKATTN_ERR_INVALID_ARG;
+    if (p->logits_dtype != INKATTN_DTYPE_BF16 && p->logits_dtype != INKATTN_DTYPE_F32) return INKATTN_ERR_INVALID_ARG;
+    const size_t size = p->logits_dtype == INKATTN_DTYPE_F32 ? 4 : 2;
+    if ((p->N_tok > 0 && (!p->logits || !p->probs)) || !aligned(p->logits, size) || !aligned(p->probs, 4) ||
+        !aligned(p->temperature, 4) || !aligned(p->dev_status, 4))
+        return INKATTN_ERR_INVALID_ARG;
+    const Range out = {p->probs, span(p->N_tok, p->probs_stride, p->V, 4)};
+    const bool in_place = p->logits == p->probs && size == 4 && p->logits_stride == p->probs_stride;
+    const Range ins[] = {{in_place ? nullptr : p->logits, span(p->N_tok, p->logits_stride, p->V, size)},
+                         {p->temperature, (size_t)p->N_tok * 4}, {p->dev_status, 4}};
+    for (const Range &in : ins)
+        if (overlap(out, in)) return INKATTN_ERR_INVALID_ARG;
+    return INKATTN_OK;
+}
+
+inkattn_status validate_verify_drafts(const inkattn_verify_drafts_params *p) {
+    if (!p || p->struct_size != sizeof(inkattn_verify_drafts_params) || p->B < 1 || p->B > (1 << 20) || p->N_tok < 0 ||
+        p->N_tok > (1 << 24) || p->V < 1 || p->V > INKATTN_MAX_VOCAB || p->target_stride < p->V ||
+        p->target_stride > kMaxRowStride)
+        return INKATTN_ERR_INVALID_ARG;
+    if (p->draft_p && (p->draft_stride < p->V || p->draft_stride > kMaxRowStride)) return INKATTN_ERR_INVALID_ARG;
+    const bool some = p->N_tok > 0;
+    if (!p->cu_seqlens_q || !p->n_new || !p->u_sample ||
+        (some && (!p->target_p || !p->token_ids || !p->u_accept || !p->out_tokens)))
+        return INKATTN_ERR_INVALID_ARG;
+    const size_t T = (size_t)p->N_tok, B = (size_t)p->B;
+    const Range r[] = {{p->n_new, B * 4}, {p->out_tokens, T * 4}, {p->dev_status, 4}, {p->cu_seqlens_q, (B + 1) * 4},
+                       {p->token_ids, T * 4}, {p->u_accept, T * 4}, {p->u_sample, B * 4},
+                       {p->target_p, span(p->N_tok, p->target_stride, p->V, 4)},
+                       {p->draft_p, p->draft_p ? span(p->N_tok, p->draft_stride, p->V, 4) : 0}};
+    for (const Range &x : r)
+        if (!aligned(x.a, 4)) return INKATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)                    // what is written
+        for (int j = i + 1; j < 9; ++j)
+            if (overlap(r[i], r[j])) return INKATTN_ERR_INVALID_ARG;
+    return INKATTN_OK;
+}
+
+inkattn_status validate_conv_rollback(const inkattn_conv_rollback_params *p) {
+    if (!p || p->struct_size != sizeof(inkattn_conv_rollback_params) || p->B < 1 || p->B > 65535 || p->N_tok < 0 ||
+        p->num_state_slots < 1 || p->n_states < 1 || p->n_states > INKATTN_ROLLBACK_MAX_STATES)
+        return INKATTN_ERR_INVALID_ARG;
+    constexpr int kOthers = 4;
+    Range r[kOthers + 3 * INKATTN_ROLLBACK_MAX_STATES] = {{p->cu_seqlens_q, ((size_t)p->B + 1) * 4},
+                                                          {p->state_slot, (size_t)p->B * 4},
+                                                          {p->n_keep, (size_t)p->B * 4}, {p->dev_status, 4}};
+    for (int i = 0; i < kOthers; ++i)
+        if ((i < 3 && !r[i].a) || !aligned(r[i].a, 4)) return INKATTN_ERR_INVALID_ARG;
+    int n = kOthers;
+    for (int s = 0; s < p->n_states; ++s) {
+        const inkattn_conv_rows &c = p->states[s];
+        if (c.C < 8 || c.C % 8 != 0 || c.C > (1 << 20) || c.x_stride < c.C || c.x_stride % 8 != 0 ||
+            c.x_stride > kMaxRowStride)
+            return INKATTN_ERR_INVALID_ARG;
+        if ((p->N_tok > 0 && !c.x) || !c.state_before || !c.state_after || !aligned(c.x, 16) ||
+            !aligned(c.state_before, 16) || !aligned(c.state_after, 16))
+            return INKATTN_ERR_INVALID_ARG;
+        const size_t bytes = (size_t)p->num_state_slots * 3 * c.C * 2;
+        r[n++] = {c.x, span(p->N_tok, c.x_stride, c.C, 2)};
+        r[n++] = {c.state_before, bytes};
+        r[n++] = {c.state_after, bytes};
+    }
+    for (int o = kOthers + 2; o < n; o += 3)       // every state_after against everything else
+        for (int i = 0; i < n; ++i) {
+            const bool in_place = i == o - 1 && r[i].a == r[o].a;
+            if (i != o && !in_place && overlap(r[o], r[i])) return INKATTN_ERR_INVALID_ARG;
+        }
+    return INKATTN_OK;
+}
+
 AttnScalars scalars(const inkattn_attn_params &p) {
     AttnScalars s;
     s.scale = p.softmax_scale > 0.f ? p.softmax_scale : 1.0f / sqrtf((float)kHeadDim);
@@ -725,6 +805,35 @@ inkattn_status inkattn_expert_combine(const inkattn_expert_combine_params *p, vo
     const void *read[] = {p->out, p->weights};
     if ((st = validate_on_device(read, 2)) != INKATTN_OK) return st;
     return launch_status(launch_expert_combine(*p, static_cast<cudaStream_t>(stream)));
+}
+
+inkattn_status inkattn_token_probs(const inkattn_token_probs_params *p, void *stream) {
+    inkattn_status st = validate_token_probs(p);
+    if (st != INKATTN_OK) return st;
+    int sms = 0;
+    if ((st = check_device(&sms)) != INKATTN_OK) return st;
+    if (p->N_tok == 0) return INKATTN_OK;
+    const void *ptrs[] = {p->logits, p->probs};
+    if ((st = validate_on_device(ptrs, 2)) != INKATTN_OK) return st;
+    return launch_status(launch_token_probs(*p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+inkattn_status inkattn_verify_drafts(const inkattn_verify_drafts_params *p, void *stream) {
+    inkattn_status st = validate_verify_drafts(p);
+    if (st != INKATTN_OK) return st;
+    if ((st = check_device(nullptr)) != INKATTN_OK) return st;
+    const void *ptrs[] = {p->n_new, p->cu_seqlens_q, p->target_p};
+    if ((st = validate_on_device(ptrs, p->N_tok > 0 ? 3 : 2)) != INKATTN_OK) return st;
+    return launch_status(launch_verify_drafts(*p, static_cast<cudaStream_t>(stream)));
+}
+
+inkattn_status inkattn_conv_rollback(const inkattn_conv_rollback_params *p, void *stream) {
+    inkattn_status st = validate_conv_rollback(p);
+    if (st != INKATTN_OK) return st;
+    if ((st = check_device(nullptr)) != INKATTN_OK) return st;
+    const void *ptrs[] = {p->cu_seqlens_q, p->states[0].state_after};
+    if ((st = validate_on_device(ptrs, 2)) != INKATTN_OK) return st;
+    return launch_status(launch_conv_rollback(*p, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

@@ -114,6 +114,10 @@ size_t route_workspace_bytes(const inkattn_route_params &p);
 cudaError_t launch_route(const inkattn_route_params &p, uint32_t *ws, cudaStream_t stream);
 cudaError_t launch_expert_combine(const inkattn_expert_combine_params &p, cudaStream_t stream);
 
+cudaError_t launch_token_probs(const inkattn_token_probs_params &p, int num_sms, cudaStream_t stream);
+cudaError_t launch_verify_drafts(const inkattn_verify_drafts_params &p, cudaStream_t stream);
+cudaError_t launch_conv_rollback(const inkattn_conv_rollback_params &p, cudaStream_t stream);
+
 // TMA descriptors of x as [max(N_tok, 1)][d_model] and w as [F][d_model] bf16, box 64
 // columns x 128 rows, 128-byte swizzle.  Returns false on failure.
 bool make_qkvr_maps(const inkattn_qkvr_params &p, CUtensorMap *xmap, CUtensorMap *wmap);

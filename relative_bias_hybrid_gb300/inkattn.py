@@ -38,6 +38,7 @@ INKATTN_SCORE_SIGMOID = 0
 INKATTN_SCORE_SOFTMAX = 1
 
 _c_i32 = ctypes.c_int32
+_c_i64 = ctypes.c_int64
 _c_ptr = ctypes.c_void_p
 
 
@@ -144,6 +145,45 @@ class ExpertCombineParams(ctypes.Structure):
     ]
 
 
+class TokenProbsParams(ctypes.Structure):
+    """inkattn_token_probs_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("N_tok", _c_i32), ("V", _c_i32), ("logits_dtype", _c_i32),
+        ("logits_stride", _c_i64), ("probs_stride", _c_i64),
+        ("logits", _c_ptr), ("temperature", _c_ptr), ("probs", _c_ptr), ("dev_status", _c_ptr),
+    ]
+
+
+class VerifyDraftsParams(ctypes.Structure):
+    """inkattn_verify_drafts_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("B", _c_i32), ("N_tok", _c_i32), ("V", _c_i32), ("target_stride", _c_i64), ("draft_stride", _c_i64),
+        ("target_p", _c_ptr), ("draft_p", _c_ptr), ("token_ids", _c_ptr), ("cu_seqlens_q", _c_ptr),
+        ("u_accept", _c_ptr), ("u_sample", _c_ptr), ("n_new", _c_ptr), ("out_tokens", _c_ptr),
+        ("dev_status", _c_ptr),
+    ]
+
+
+class ConvRows(ctypes.Structure):
+    """inkattn_conv_rows."""
+    _fields_ = [("C", _c_i32), ("x_stride", _c_i64), ("x", _c_ptr), ("state_before", _c_ptr), ("state_after", _c_ptr)]
+
+
+ROLLBACK_MAX_STATES = 8
+
+
+class ConvRollbackParams(ctypes.Structure):
+    """inkattn_conv_rollback_params."""
+    _fields_ = [
+        ("struct_size", ctypes.c_size_t),
+        ("B", _c_i32), ("N_tok", _c_i32), ("num_state_slots", _c_i32), ("n_states", _c_i32),
+        ("cu_seqlens_q", _c_ptr), ("state_slot", _c_ptr), ("n_keep", _c_ptr), ("dev_status", _c_ptr),
+        ("states", ConvRows * ROLLBACK_MAX_STATES),
+    ]
+
+
 class InkattnError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -203,6 +243,12 @@ def lib():
             L.inkattn_route.restype = ctypes.c_int
             L.inkattn_expert_combine.argtypes = [P(ExpertCombineParams), _c_ptr]
             L.inkattn_expert_combine.restype = ctypes.c_int
+            L.inkattn_token_probs.argtypes = [P(TokenProbsParams), _c_ptr]
+            L.inkattn_token_probs.restype = ctypes.c_int
+            L.inkattn_verify_drafts.argtypes = [P(VerifyDraftsParams), _c_ptr]
+            L.inkattn_verify_drafts.restype = ctypes.c_int
+            L.inkattn_conv_rollback.argtypes = [P(ConvRollbackParams), _c_ptr]
+            L.inkattn_conv_rollback.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -331,6 +377,20 @@ def inkattn_route(p: RouteParams, workspace: Optional[torch.Tensor] = None, stre
 
 def inkattn_expert_combine(p: ExpertCombineParams, stream=None, raise_on_error=True) -> int:
     return _check(lib().inkattn_expert_combine(ctypes.byref(p), _stream(stream)), "inkattn_expert_combine",
+                  raise_on_error)
+
+
+def inkattn_token_probs(p: TokenProbsParams, stream=None, raise_on_error=True) -> int:
+    return _check(lib().inkattn_token_probs(ctypes.byref(p), _stream(stream)), "inkattn_token_probs", raise_on_error)
+
+
+def inkattn_verify_drafts(p: VerifyDraftsParams, stream=None, raise_on_error=True) -> int:
+    return _check(lib().inkattn_verify_drafts(ctypes.byref(p), _stream(stream)), "inkattn_verify_drafts",
+                  raise_on_error)
+
+
+def inkattn_conv_rollback(p: ConvRollbackParams, stream=None, raise_on_error=True) -> int:
+    return _check(lib().inkattn_conv_rollback(ctypes.byref(p), _stream(stream)), "inkattn_conv_rollback",
                   raise_on_error)
 
 
@@ -634,4 +694,86 @@ def expert_combine_params(*, y, weights, token_rows, out, shared=None, dev_statu
     p.token_rows = _ptr(token_rows, i32, "token_rows"); p.out = _ptr(out, bf, "out")
     p.dev_status = _ptr(dev_status, i32, "dev_status")
     p.tensors = (y, weights, token_rows, out, shared, dev_status)     # alive as long as the params
+    return p
+
+
+def _rows(t: Optional[torch.Tensor], dtype, name):
+    """Address and row stride of a matrix whose rows are dense, possibly a part of wider rows."""
+    if t is None:
+        return None, 0
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name}: expected rows of adjacent elements that do not overlap")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def token_probs_params(*, logits, probs, temperature=None, dev_status=None) -> TokenProbsParams:
+    """Fill an inkattn_token_probs_params from torch tensors (see include/inkattn.h): logits [N][V]
+    bf16 or fp32, probs [N][V] fp32 (either may be columns of wider rows; probs may be logits),
+    temperature None or [N] fp32."""
+    N, V = logits.shape
+    _one_device(logits, probs, temperature, dev_status)
+    _shape(probs, (N, V), "probs"); _shape(temperature, (N,), "temperature")
+    p = TokenProbsParams()
+    p.struct_size = ctypes.sizeof(TokenProbsParams)
+    p.N_tok, p.V = N, V
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits: expected bfloat16 or float32, got {logits.dtype}")
+    p.logits_dtype = INKATTN_DTYPE_F32 if logits.dtype == torch.float32 else INKATTN_DTYPE_BF16
+    p.logits, p.logits_stride = _rows(logits, None, "logits")
+    p.probs, p.probs_stride = _rows(probs, torch.float32, "probs")
+    p.temperature = _ptr(temperature, torch.float32, "temperature")
+    p.dev_status = _ptr(dev_status, torch.int32, "dev_status")
+    p.tensors = (logits, probs, temperature, dev_status)     # alive as long as the params
+    return p
+
+
+def verify_drafts_params(*, target_p, token_ids, cu_seqlens_q, u_accept, u_sample, n_new, out_tokens, draft_p=None,
+                         dev_status=None) -> VerifyDraftsParams:
+    """Fill an inkattn_verify_drafts_params from torch tensors (see include/inkattn.h): target_p [N][V]
+    fp32, draft_p None or [N][V] fp32 (either may be columns of wider rows), token_ids [N],
+    cu_seqlens_q [B+1], u_accept [N], u_sample [B], n_new [B], out_tokens [N]."""
+    f32, i32 = torch.float32, torch.int32
+    N, V = target_p.shape
+    B = cu_seqlens_q.numel() - 1
+    _one_device(target_p, draft_p, token_ids, cu_seqlens_q, u_accept, u_sample, n_new, out_tokens, dev_status)
+    _shape(draft_p, (N, V), "draft_p"); _shape(token_ids, (N,), "token_ids"); _shape(u_accept, (N,), "u_accept")
+    _shape(cu_seqlens_q, (B + 1,), "cu_seqlens_q"); _shape(u_sample, (B,), "u_sample"); _shape(n_new, (B,), "n_new")
+    _shape(out_tokens, (N,), "out_tokens")
+    p = VerifyDraftsParams()
+    p.struct_size = ctypes.sizeof(VerifyDraftsParams)
+    p.B, p.N_tok, p.V = B, N, V
+    p.target_p, p.target_stride = _rows(target_p, f32, "target_p")
+    p.draft_p, p.draft_stride = _rows(draft_p, f32, "draft_p")
+    p.token_ids = _ptr(token_ids, i32, "token_ids"); p.cu_seqlens_q = _ptr(cu_seqlens_q, i32, "cu_seqlens_q")
+    p.u_accept = _ptr(u_accept, f32, "u_accept"); p.u_sample = _ptr(u_sample, f32, "u_sample")
+    p.n_new = _ptr(n_new, i32, "n_new"); p.out_tokens = _ptr(out_tokens, i32, "out_tokens")
+    p.dev_status = _ptr(dev_status, i32, "dev_status")
+    p.tensors = (target_p, draft_p, token_ids, cu_seqlens_q, u_accept, u_sample, n_new, out_tokens, dev_status)
+    return p
+
+
+def conv_rollback_params(*, x, state_before, state_after, n_keep, cu_seqlens_q, state_slot,
+                         dev_status=None) -> ConvRollbackParams:
+    """Fill an inkattn_conv_rollback_params from torch tensors (see include/inkattn.h): lists of one to
+    eight convs' tensors, x [N][C] bf16 (possibly columns of wider rows), state_before and state_after
+    [num_state_slots][3][C] bf16; n_keep [B], cu_seqlens_q [B+1], state_slot [B]."""
+    bf, i32 = torch.bfloat16, torch.int32
+    if not 1 <= len(x) <= ROLLBACK_MAX_STATES or len(state_before) != len(x) or len(state_after) != len(x):
+        raise ValueError(f"conv states: expected one to {ROLLBACK_MAX_STATES}, as many of each")
+    B, N, slots = cu_seqlens_q.numel() - 1, x[0].shape[0], state_before[0].shape[0]
+    _one_device(*x, *state_before, *state_after, n_keep, cu_seqlens_q, state_slot, dev_status)
+    _shape(cu_seqlens_q, (B + 1,), "cu_seqlens_q"); _shape(state_slot, (B,), "state_slot"); _shape(n_keep, (B,), "n_keep")
+    p = ConvRollbackParams()
+    p.struct_size = ctypes.sizeof(ConvRollbackParams)
+    p.B, p.N_tok, p.num_state_slots, p.n_states = B, N, slots, len(x)
+    p.cu_seqlens_q = _ptr(cu_seqlens_q, i32, "cu_seqlens_q"); p.state_slot = _ptr(state_slot, i32, "state_slot")
+    p.n_keep = _ptr(n_keep, i32, "n_keep"); p.dev_status = _ptr(dev_status, i32, "dev_status")
+    for c, xs, before, after in zip(p.states, x, state_before, state_after):
+        c.C = before.shape[2]
+        _shape(xs, (N, c.C), "x"); _shape(before, (slots, 3, c.C), "state_before"); _shape(after, (slots, 3, c.C), "state_after")
+        c.x, c.x_stride = _rows(xs, bf, "x")
+        c.state_before = _ptr(before, bf, "state_before"); c.state_after = _ptr(after, bf, "state_after")
+    p.tensors = (*x, *state_before, *state_after, n_keep, cu_seqlens_q, state_slot, dev_status)     # alive as long as the params
     return p

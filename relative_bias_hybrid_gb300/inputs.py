@@ -115,7 +115,8 @@ _TENSOR_IDS = {"q": 1, "k": 2, "v": 3, "r": 4, "P": 5, "conv_w_k": 6, "conv_w_v"
                "k_cache": 12, "v_cache": 13, "perm": 14, "y": 15, "residual": 16,
                "oc_conv_w": 17, "oc_norm_w": 18, "oc_conv_state": 19, "k_cache_e4m3": 20,
                "v_cache_e4m3": 21, "x": 22, "w_qkvr": 23, "w_o": 24, "w_router": 25, "w_up": 26,
-               "w_down": 27, "w_shared_up": 28, "w_shared_down": 29, "k_cache_i4": 30, "v_cache_i4": 31}
+               "w_down": 27, "w_shared_up": 28, "w_shared_down": 29, "k_cache_i4": 30, "v_cache_i4": 31,
+               "token_ids": 32, "draft_p": 33, "temperature": 34, "u_accept": 35, "u_sample": 36, "w_head": 37}
 
 
 def _gen(device, seed: int, tensor: str) -> torch.Generator:
@@ -304,6 +305,41 @@ def make_layer_tail_inputs(w: Workload, seed: int = 0, device="cpu", D: int = 0,
     }
     for i, name in enumerate(("attn", "mlp")):
         out[name] = make_output_conv_inputs(w, seed=2 * seed + i, device=device, D=D)
+    return out
+
+
+def make_verify_inputs(w: Workload, V: int, seed: int = 0, device="cpu", drafter: bool = True,
+                       temperatures: bool = True) -> Dict[str, torch.Tensor]:
+    """Inputs of a verification step's end over the workload's new tokens, vocabulary V: token_ids [N]
+    (a sequence's last token, then its drafts); draft_p [N, V] fp32, softmax of N(0, 1) logits, row i
+    the distribution that the draft of row i + 1 is drawn from (None without a drafter: drafts drawn
+    evenly); temperature [N] fp32 in [0.5, 1.5], zero (greedy) in every fifth row (None: 1
+    everywhere); u_accept [N] and u_sample [B] fp32 in [0, 1); cu_seqlens_q [B+1]; state_slot [B]; and
+    w_head [V, Hq * head_dim] bf16 ~ N(0, 9 / width), a head whose logits spread by about 3 on rows of
+    unit size."""
+    device = torch.device(device)
+    N, B, i32 = w.N_tok, w.B, torch.int32
+    out: Dict[str, torch.Tensor] = {}
+    ids = torch.randint(0, V, (N,), generator=_gen(device, seed, "token_ids"), device=device)
+    out["draft_p"] = None
+    if drafter:
+        out["draft_p"] = torch.softmax(_normal((N, V), 1.0, device, seed, "draft_p", torch.float32), 1)
+        if N > 1:
+            drawn = torch.multinomial(out["draft_p"], 1, generator=_gen(device, seed, "token_ids"))[:, 0]
+            ids = torch.cat([ids[:1], drawn[:-1]])
+    out["token_ids"] = ids.to(i32)
+    out["temperature"] = None
+    if temperatures:
+        t = 0.5 + torch.rand((N,), generator=_gen(device, seed, "temperature"), device=device)
+        out["temperature"] = torch.where(torch.arange(N, device=device) % 5 == 4, torch.zeros_like(t), t)
+    out["u_accept"] = torch.rand((N,), generator=_gen(device, seed, "u_accept"), device=device)
+    out["u_sample"] = torch.rand((B,), generator=_gen(device, seed, "u_sample"), device=device)
+    cu = np.zeros(B + 1, dtype=np.int64)
+    cu[1:] = np.cumsum(w.q_lens)
+    out["cu_seqlens_q"] = torch.tensor(cu, dtype=i32, device=device)
+    out["state_slot"] = torch.arange(B, dtype=i32, device=device)
+    D = w.Hq * w.head_dim
+    out["w_head"] = _normal((V, D), 3.0 * D ** -0.5, device, seed, "w_head", torch.bfloat16)
     return out
 
 

@@ -7,7 +7,9 @@ per-pass device time of each call.  Meant as the target of a profiler command, e
 Every pass is the whole path (prologue, then prefill or decode + combine) on seeded
 synthetic inputs already resident on the device, optionally with the qkvr projections
 (their own inputs and outputs) before it and the attention-output conv, or the whole rest of
-the decoder layer (output projection, convs, router and experts), after it.
+the decoder layer (output projection, convs, router and experts), after it; and, as the end of a
+verification step, the logits of the attention's output (a head of its own), their
+probabilities, the verification of the drafts and the K and V conv states of the rows kept.
 ``--seqs N`` keeps only the first N sequences of a batched workload (a smaller case of the
 same kernel, for captures that must hold less memory).
 """
@@ -19,7 +21,8 @@ import dataclasses
 import torch
 
 from . import inputs as gen
-from .step import AttentionStep, LayerTailStep, OutputConvStep, QkvrStep
+from . import inkattn as ia
+from .step import AttentionStep, LayerTailStep, OutputConvStep, QkvrStep, VerifyStep
 
 
 def main(argv=None):
@@ -39,6 +42,8 @@ def main(argv=None):
                     help="also run the rest of the decoder layer on the attention's output after each pass")
     ap.add_argument("--experts", type=int, default=64, help="routed experts of --layer-tail, six a token")
     ap.add_argument("--expert-width", type=int, default=1024, help="inner width of the experts of --layer-tail")
+    ap.add_argument("--verify", type=int, default=0, metavar="V",
+                    help="also run a verification step's end over a vocabulary of V after each pass")
     args = ap.parse_args(argv)
 
     w = gen.workload(args.workload)
@@ -55,11 +60,18 @@ def main(argv=None):
     tail = (LayerTailStep(w, gen.make_layer_tail_inputs(w, seed=args.seed, device=dev, experts=args.experts,
                                                         ff=args.expert_width),
                           step.out, top_k=min(6, args.experts)) if args.layer_tail else None)
+    end = None
+    if args.verify:
+        xv = gen.make_verify_inputs(w, args.verify, seed=args.seed, device=dev)
+        logits = torch.empty((w.N_tok, args.verify), dtype=torch.float32, device=dev)
+        head = ia.linear_params(x=step.out.view(w.N_tok, -1), w=xv["w_head"], out=logits, dev_status=step.status)
+        before = {n: x[f"conv_state_{n}"].clone() for n in ("k", "v")}
+        end = VerifyStep(w, xv, logits, [(x[n], before[n], torch.empty_like(before[n])) for n in ("k", "v")])
     stream = torch.cuda.Stream(device=dev)
     print(w.describe(), f"num_splits={step.num_splits}" if step.mode == "decode" else "")
     with torch.cuda.stream(stream):
         for it in range(args.iters):
-            e = [torch.cuda.Event(enable_timing=True) for _ in range(6)]
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(8)]
             e[4].record(stream)
             if qk is not None:
                 qk.run(stream)
@@ -74,14 +86,22 @@ def main(argv=None):
             if tail is not None:
                 tail.run(stream)
             e[5].record(stream)
+            if end is not None:
+                ia.inkattn_linear(head, stream)
+                e[6].record(stream)
+                end.run(stream)
+            e[7].record(stream)
             stream.synchronize()
             print(f"pass {it}: " + (f"qkvr {e[4].elapsed_time(e[0]):.4f} ms, " if qk is not None else "")
                   + f"prologue {e[0].elapsed_time(e[1]):.4f} ms, "
                   f"attention {e[1].elapsed_time(e[2]):.4f} ms"
                   + (f", output conv {e[2].elapsed_time(e[3]):.4f} ms" if oc is not None else "")
-                  + (f", rest of the layer {e[3].elapsed_time(e[5]):.4f} ms" if tail is not None else ""))
+                  + (f", rest of the layer {e[3].elapsed_time(e[5]):.4f} ms" if tail is not None else "")
+                  + (f", logits {e[5].elapsed_time(e[6]):.4f} ms, verification {e[6].elapsed_time(e[7]):.4f} ms"
+                     if end is not None else ""))
     status = (step.device_status() | (oc.device_status() if oc is not None else 0)
-              | (qk.device_status() if qk is not None else 0) | (tail.device_status() if tail is not None else 0))
+              | (qk.device_status() if qk is not None else 0) | (tail.device_status() if tail is not None else 0)
+              | (end.device_status() if end is not None else 0))
     print(f"device status {status}")
     if status != 0:
         raise SystemExit(1)

@@ -239,3 +239,46 @@ class LayerTailStep:
 
     def device_status(self) -> int:
         return int(self.status.item())
+
+
+class VerifyStep:
+    """Buffers + calls of a verification step's end: the probabilities of its logits
+    (inkattn_token_probs), the drafts that stand and the token behind them (inkattn_verify_drafts),
+    and the conv states of the rows kept (inkattn_conv_rollback).
+
+    `inputs` comes from inputs.make_verify_inputs; logits [N, V] bf16 or fp32 are the step's.
+    `convs` is a list of (x, state_before, state_after): a conv's input rows [N, C] of the step (a
+    slice of columns will do), its state from before the step and the one to write, for any number
+    of convs of any layers; they go out eight to a launch.  probs, n_new and tokens are buffers
+    of this object.
+    """
+
+    def __init__(self, w: Workload, inputs: Dict[str, torch.Tensor], logits: torch.Tensor, convs=()):
+        dev, i32 = logits.device, torch.int32
+        N, V = logits.shape
+        self.w, self.x = w, inputs
+        self.probs = torch.empty((N, V), dtype=torch.float32, device=dev)
+        self.n_new = torch.empty(w.B, dtype=i32, device=dev)
+        self.tokens = torch.empty(N, dtype=i32, device=dev)
+        self.status = torch.zeros(1, dtype=i32, device=dev)
+        self.p_probs = ia.token_probs_params(logits=logits, probs=self.probs, temperature=inputs["temperature"],
+                                             dev_status=self.status)
+        self.p_verify = ia.verify_drafts_params(
+            target_p=self.probs, draft_p=inputs["draft_p"], token_ids=inputs["token_ids"],
+            cu_seqlens_q=inputs["cu_seqlens_q"], u_accept=inputs["u_accept"], u_sample=inputs["u_sample"],
+            n_new=self.n_new, out_tokens=self.tokens, dev_status=self.status)
+        self.p_rollback = []
+        for i in range(0, len(convs), ia.ROLLBACK_MAX_STATES):
+            x, before, after = zip(*convs[i:i + ia.ROLLBACK_MAX_STATES])
+            self.p_rollback.append(ia.conv_rollback_params(
+                x=x, state_before=before, state_after=after, n_keep=self.n_new, cu_seqlens_q=inputs["cu_seqlens_q"],
+                state_slot=inputs["state_slot"], dev_status=self.status))
+
+    def run(self, stream=None):
+        ia.inkattn_token_probs(self.p_probs, stream)
+        ia.inkattn_verify_drafts(self.p_verify, stream)
+        for p in self.p_rollback:
+            ia.inkattn_conv_rollback(p, stream)
+
+    def device_status(self) -> int:
+        return int(self.status.item())
