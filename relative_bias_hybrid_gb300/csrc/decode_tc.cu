@@ -65,11 +65,16 @@ template <int kKv>
 struct Dec {
     static constexpr bool kCodes = kKv != INKATTN_KV_BF16;
     static constexpr bool kI4 = kKv == INKATTN_KV_I4;
-    static constexpr int kThreads = kCodes ? 512 : 320;
-    static constexpr int kWarpSm = kCodes ? 8 : 2;           // first softmax warp
-    static constexpr int kConvThreads = kCodes ? 192 : 0;    // converter warps 2-7
-    static constexpr int kSlots = kCodes ? 3 : 4;            // MMA operand ring
-    static constexpr int kCodeSlots = kI4 ? 6 : kCodes ? 3 : 0;      // ring of codes
+    static constexpr int kThreads = kI4 ? 640 : kCodes ? 512 : 320;
+    static constexpr int kWarpSm = kI4 ? 12 : kCodes ? 8 : 2;           // first softmax warp
+    static constexpr int kWarpMma = 1;
+    // registers of the first two warpgroups and of the softmax's (512 threads x 128 at launch)
+    static constexpr int kRegsLow = kI4 ? 64 : 80, kRegsHigh = kI4 ? 144 : 176;
+    static constexpr int kConvThreads = kCodes ? (kWarpSm - 2) * 32 : 0;    // converter warps, from 2 on
+    static constexpr int kUnitsMax = 3;                      // units of a 4-bit tile that a warp has
+    static constexpr int kConvArrivals = kI4 ? kConvThreads / 32 : kCodes ? kConvThreads : 1;   // for a tile
+    static constexpr int kSlots = kI4 ? 4 : kCodes ? 3 : 4;            // MMA operand ring
+    static constexpr int kCodeSlots = kCodes ? 3 : 0;      // ring of codes
     static constexpr int kCodeRow = kI4 ? kI4RowBytes : kHeadDim;    // bytes of a row's codes
     static constexpr int kCodeTile = kKeys * kCodeRow;               // one tile: [128 keys][row]
     static constexpr int kCodeSlotBytes = kCodeTile + kKeys * 4;     // + 4 bytes of scales a row
@@ -116,6 +121,7 @@ struct DecTcArgs {
     long long kv_rows;      // rows of the cache tensor maps (OOB row = this)
     uint64_t wait_ns;       // limit of every bounded wait
     int withhold;           // failure-path test: the softmax withholds its first P arrival
+    uint32_t i4_mask, i4_exponent;   // i4_decode8's constants
 };
 
 }  // namespace
@@ -200,14 +206,14 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
     if (threadIdx.x == 0) {
         mbar_init(bar(C::B_Q), 1);
         for (int s = 0; s < C::kSlots; ++s) {
-            mbar_init(bar(C::B_KV_FULL + s), kCodes ? C::kConvThreads : 1);   // tile converters, or the TMA
+            mbar_init(bar(C::B_KV_FULL + s), C::kConvArrivals);        // tile converters, or the TMA
             mbar_init(bar(C::B_KV_EMPTY + s), 1);
         }
         if constexpr (kCodes) {
             mbar_init(bar(C::B_QF), C::kConvThreads);
             for (int s = 0; s < C::kCodeSlots; ++s) {
                 mbar_init(bar(C::B_C_FULL + s), 1);
-                mbar_init(bar(C::B_C_EMPTY + s), C::kConvThreads);
+                mbar_init(bar(C::B_C_EMPTY + s), C::kConvArrivals);
             }
         }
         for (int s = 0; s < 2; ++s) {
@@ -221,7 +227,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == C::kWarpMma) {
         tc::tmem_alloc(smem_u32(tmem_slot), 512);
         tc::tmem_relinquish();
     }
@@ -238,7 +244,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
     // MMA and converter warps give registers to the two softmax warpgroups (80 + 176).
     if (warp == 0) {
         // ================================ producer ================================
-        if constexpr (kCodes) tc::reg_dealloc<80>();
+        if constexpr (kCodes) tc::reg_dealloc<C::kRegsLow>();
         bool ok = true;
         if (lane == 0) {
             tma_prefetch_desc(&qmap);
@@ -333,9 +339,9 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
             for (int L = max(0, kv_loads - kRing); L < kv_loads; ++L)
                 mbar_drain(bar(kRingFull + L % kRing), (L / kRing) & 1, p.dev_status, A.wait_ns);
         }
-    } else if (warp == 1) {
+    } else if (warp == C::kWarpMma) {
         // ================================ MMA issuer ================================
-        if constexpr (kCodes) tc::reg_dealloc<80>();
+        if constexpr (kCodes) tc::reg_dealloc<C::kRegsLow>();
         constexpr uint32_t kFmt = kCodes ? tc::kFmtF16 : tc::kFmtBF16;   // both operands alike
         const uint32_t id_qk = tc::idesc(128, 128, kFmt, 0, 0);
         const uint32_t id_pv = tc::idesc(128, 128, kFmt, 0, 1);
@@ -402,22 +408,87 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
         __syncwarp();
     } else if (kCodes && warp < C::kWarpSm) {
         // ================================ converters (caches of codes) ================================
-        if constexpr (kCodes) tc::reg_dealloc<80>();
+        if constexpr (kCodes) tc::reg_dealloc<C::kRegsLow>();
         // warps 2-7 convert Q, then the K/V tiles
-        const int ct = threadIdx.x - 64;                      // 0 .. 191
+        const int ct = threadIdx.x - 32 - (warp > C::kWarpMma ? 32 : 0);   // 0 .. kConvThreads - 1
         bool ok = wwait(bar(C::B_Q), 0);
         if (ok) {
             uint4 *qw = reinterpret_cast<uint4 *>(smem + C::kOffQ);
-            for (int i = ct; i < 32768 / 16; i += 192) {
-                const uint4 w = qw[i];
+            for (int i = ct; i < 32768 / 16; i += C::kConvThreads) {
+                // rows without a query are zeros, and so are their logits: they then need no mask
+                // (16-byte pieces of a row, 8 in each half of the head dimension)
+                const uint4 w = ((i >> 3) & (kRows - 1)) < n_rows ? qw[i] : make_uint4(0, 0, 0, 0);
                 qw[i] = make_uint4(pack_f16(bf16_lo(w.x), bf16_hi(w.x)), pack_f16(bf16_lo(w.y), bf16_hi(w.y)),
                                    pack_f16(bf16_lo(w.z), bf16_hi(w.z)), pack_f16(bf16_lo(w.w), bf16_hi(w.w)));
             }
             fence_proxy_async_smem();
             mbar_arrive(bar(C::B_QF));
         }
-        for (int L = 0; L < 2 * N && ok; ++L) {
-            const int n = L == 0 ? 0 : L == 2 * N - 1 ? N - 1 : (L & 1) ? (L + 1) >> 1 : (L >> 1) - 1;
+        auto tile_of = [&](int L) { return L == 0 ? 0 : L == 2 * N - 1 ? N - 1 : (L & 1) ? (L + 1) >> 1 : (L >> 1) - 1; };
+        if constexpr (C::kI4) {
+            // A tile is 16 units of 16 keys x two groups of 32 values (a half of the head dimension): a
+            // lane takes one key's group, its 16 bytes (the TMA's 64-byte swizzle spreads eight keys
+            // over the banks) to four chunks of 16 bytes (the MMA's 128-byte swizzle does the same).
+            // Both swizzles depend on the lane alone, so a unit's addresses are the lane's plus the
+            // unit's.
+            // A warp has the same units of every tile, more of them where its scheduler (warp % 4) has
+            // softmax warps without rows: units of each warp, a hexadecimal digit, by the live lane
+            // quarters.
+            const uint64_t share = n_rows <= 32 ? 0x121122212200ull : n_rows <= 64 ? 0x221122112200ull : n_rows <= 96 ? 0x211222122100ull : 0x111221222200ull;
+            int u0 = 0;
+            for (int i = 0; i < warp; ++i) u0 += (int)(share >> (4 * i)) & 15;
+            const int units = (int)(share >> (4 * warp)) & 15;
+            const int k16 = lane & 15, grp = lane >> 4;
+            const uint32_t src_lane = (uint32_t)(k16 * kI4RowBytes + ((grp ^ ((k16 >> 1) & 3)) << 4));
+            const uint32_t byte_lane = (uint32_t)(C::kCodeTile + k16 * kI4RowScales + grp);
+            uint32_t dst_lane[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) dst_lane[c] = (uint32_t)(k16 * 128 + (((grp * 4 + c) ^ (k16 & 7)) << 4));
+            int s4 = 0, s16 = 0;
+            uint32_t turn4 = 0, turn16 = 0;                   // of the rings: parity of the waits
+            bool bad = false;
+            for (int L = 0; L < 2 * N; ++L) {
+                if (!(ok = wwait(bar(C::B_C_FULL + s4), turn4))) break;
+                if (L >= C::kSlots && !(ok = wwait(bar(C::B_KV_EMPTY + s16), turn16 ^ 1u))) break;
+                const uint32_t src = s_base + C::kOffCodes + s4 * C::kCodeSlotBytes;
+                const uint32_t dst = s_base + C::kOffKV + s16 * kSlotBytes;
+                const int key_end = min(T, kr_hi) - (kr_lo + tile_of(L) * kKeys);
+                uint4 w[C::kUnitsMax];
+                uint32_t byte[C::kUnitsMax];
+#pragma unroll
+                for (int i = 0; i < C::kUnitsMax; ++i) {      // (the loads of a tile go out together)
+                    if (i >= units) break;
+                    const int kb = (u0 + i) & 7, half = (u0 + i) >> 3;
+                    w[i] = lds_u32x4(src + kb * (16 * kI4RowBytes) + (src_lane ^ (half << 5)));
+                    byte[i] = lds_u8(src + kb * (16 * kI4RowScales) + 2 * half + byte_lane);
+                    if (kb * 16 + k16 >= key_end) byte[i] = 0;
+                }
+#pragma unroll
+                for (int i = 0; i < C::kUnitsMax; ++i) {
+                    if (i >= units) break;
+                    const int kb = (u0 + i) & 7, half = (u0 + i) >> 3;
+                    const bool over = byte[i] > kI4ScaleMax;
+                    bad |= over;
+                    const I4Scale f = i4_factors(over ? 0u : byte[i]);
+                    const uint32_t to = dst + half * 16384 + kb * 2048;
+                    sts_u32x4(to + dst_lane[0], i4_decode8(w[i].x, f, A.i4_mask, A.i4_exponent));
+                    sts_u32x4(to + dst_lane[1], i4_decode8(w[i].y, f, A.i4_mask, A.i4_exponent));
+                    sts_u32x4(to + dst_lane[2], i4_decode8(w[i].z, f, A.i4_mask, A.i4_exponent));
+                    sts_u32x4(to + dst_lane[3], i4_decode8(w[i].w, f, A.i4_mask, A.i4_exponent));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(C::B_C_EMPTY + s4));
+                    mbar_arrive(bar(C::B_KV_FULL + s16));
+                }
+                if (++s4 == C::kCodeSlots) s4 = 0, turn4 ^= 1u;
+                if (++s16 == C::kSlots) s16 = 0, turn16 ^= 1u;
+            }
+            if (bad) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+        }
+        for (int L = 0; !C::kI4 && L < 2 * N && ok; ++L) {
+            const int n = tile_of(L);
             constexpr int kRing = kCodes ? C::kCodeSlots : 1;    // (the bf16 variant has no such warps)
             const int s8 = L % kRing, s16 = L % C::kSlots;
             if (!(ok = wwait(bar(C::B_C_FULL + s8), (L / kRing) & 1))) break;
@@ -426,57 +497,21 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
             unsigned char *dst = smem + C::kOffKV + s16 * kSlotBytes;
             const int key_end = min(T, kr_hi) - (kr_lo + n * kKeys);
             bool bad = false;
-            if constexpr (C::kI4) {
-                // 16 pieces of 32 keys x one group of 32 values, shared out in turn so that the
-                // odd one falls on another warp with every tile; a lane takes one key's group: its
-                // 16 bytes (the TMA's 64-byte swizzle spreads eight keys over the banks), four
-                // chunks of 16 bytes out (the MMA's 128-byte swizzle does the same).  The loads of
-                // a tile go out before the first expansion.
-                constexpr int kWarps = 6, kPieces = (16 + kWarps - 1) / kWarps;
-                const int first = (warp - 2 + 2 * (L % 3)) % kWarps;
-                const uint32_t *sc = reinterpret_cast<const uint32_t *>(src + C::kCodeTile);
-                uint4 w[kPieces];
-                uint32_t byte[kPieces];
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const int piece = first + kWarps * i;
-                    if (piece >= 16) break;
-                    const int key = (piece & 3) * 32 + lane, grp = piece >> 2;
-                    w[i] = *reinterpret_cast<const uint4 *>(src + key * kI4RowBytes + ((grp ^ ((key >> 1) & 3)) << 4));
-                    byte[i] = key < key_end ? (sc[key] >> (8 * grp)) & 0xFFu : 0u;
-                }
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const int piece = first + kWarps * i;
-                    if (piece >= 16) break;
-                    const int key = (piece & 3) * 32 + lane, grp = piece >> 2;
-                    const bool good = byte[i] <= kI4ScaleMax;
-                    bad |= !good;
-                    const I4Scale f = i4_factors(good ? byte[i] : 0u);
-                    unsigned char *row = dst + (grp >> 1) * 16384 + key * 128;
-                    const int c0 = (grp & 1) * 4, sw = key & 7;
-                    *reinterpret_cast<uint4 *>(row + ((c0 ^ sw) << 4)) = i4_decode8(w[i].x, f);
-                    *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ sw) << 4)) = i4_decode8(w[i].y, f);
-                    *reinterpret_cast<uint4 *>(row + (((c0 + 2) ^ sw) << 4)) = i4_decode8(w[i].z, f);
-                    *reinterpret_cast<uint4 *>(row + (((c0 + 3) ^ sw) << 4)) = i4_decode8(w[i].w, f);
-                }
-            } else {
-                const float *sc = reinterpret_cast<const float *>(src + C::kCodeTile);
-                for (int it = ct; it < kKeys * 8; it += 192) {
-                    const int key = it >> 3, j16 = it & 7, sw = key & 7;
-                    const uint4 w = *reinterpret_cast<const uint4 *>(src + key * 128 + j16 * 16);
-                    float sv = key < key_end ? sc[key] : 0.f;
-                    const bool good = sv == 0.f || (sv >= 0x1p-24f && sv <= 128.f);
-                    bad |= !good;
-                    const __half2 s2 = __float2half2_rn(good ? sv : 0.f);
-                    const int base = (j16 >> 2) * 16384 + key * 128;
-                    *reinterpret_cast<uint4 *>(dst + base + ((((j16 & 3) * 2) ^ sw) << 4)) =
-                        make_uint4(e4m3x2_to_f16x2_scaled(w.x, s2), e4m3x2_to_f16x2_scaled(w.x >> 16, s2),
-                                   e4m3x2_to_f16x2_scaled(w.y, s2), e4m3x2_to_f16x2_scaled(w.y >> 16, s2));
-                    *reinterpret_cast<uint4 *>(dst + base + ((((j16 & 3) * 2 + 1) ^ sw) << 4)) =
-                        make_uint4(e4m3x2_to_f16x2_scaled(w.z, s2), e4m3x2_to_f16x2_scaled(w.z >> 16, s2),
-                                   e4m3x2_to_f16x2_scaled(w.w, s2), e4m3x2_to_f16x2_scaled(w.w >> 16, s2));
-                }
+            const float *sc = reinterpret_cast<const float *>(src + C::kCodeTile);
+            for (int it = ct; it < kKeys * 8; it += 192) {
+                const int key = it >> 3, j16 = it & 7, sw = key & 7;
+                const uint4 w = *reinterpret_cast<const uint4 *>(src + key * 128 + j16 * 16);
+                float sv = key < key_end ? sc[key] : 0.f;
+                const bool good = sv == 0.f || (sv >= 0x1p-24f && sv <= 128.f);
+                bad |= !good;
+                const __half2 s2 = __float2half2_rn(good ? sv : 0.f);
+                const int base = (j16 >> 2) * 16384 + key * 128;
+                *reinterpret_cast<uint4 *>(dst + base + ((((j16 & 3) * 2) ^ sw) << 4)) =
+                    make_uint4(e4m3x2_to_f16x2_scaled(w.x, s2), e4m3x2_to_f16x2_scaled(w.x >> 16, s2),
+                               e4m3x2_to_f16x2_scaled(w.y, s2), e4m3x2_to_f16x2_scaled(w.y >> 16, s2));
+                *reinterpret_cast<uint4 *>(dst + base + ((((j16 & 3) * 2 + 1) ^ sw) << 4)) =
+                    make_uint4(e4m3x2_to_f16x2_scaled(w.z, s2), e4m3x2_to_f16x2_scaled(w.z >> 16, s2),
+                               e4m3x2_to_f16x2_scaled(w.w, s2), e4m3x2_to_f16x2_scaled(w.w >> 16, s2));
             }
             if (bad) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
             fence_proxy_async_smem();
@@ -485,7 +520,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
         }
     } else {
         // ================================ softmax ================================
-        if constexpr (kCodes) tc::reg_alloc<176>();
+        if constexpr (kCodes) tc::reg_alloc<C::kRegsHigh>();
         const int quad = warp & 3;
         const int sw = warp - C::kWarpSm;                     // softmax warp index 0..7
         const int hw = sw >> 2;                               // column half
@@ -680,7 +715,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                 b_lo = any ? jv_lo - j0 - cb : (1 << 20);
                 span = any ? jv_hi - jv_lo : 0;
             }
-            const bool need_mask = !valid_row || (j0 + kKeys - 1 > pos0) || (j0 + kKeys > kr_hi) ||
+            const bool need_mask = (!kCodes && !valid_row) || (j0 + kKeys - 1 > pos0) || (j0 + kKeys > kr_hi) ||
                                    (p.window > 0 && pos0 + q_len - 1 - j0 >= p.window);
             if (need_mask) {
 #pragma unroll
@@ -806,7 +841,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
 
     tc::fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == C::kWarpMma) {
         tc::fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
@@ -822,7 +857,7 @@ cudaError_t launch_decode_variant(const DecTcArgs &a, dim3 grid, const CUtensorM
         static const cudaError_t regs_check = [] {
             cudaFuncAttributes fa;
             if (cudaFuncGetAttributes(&fa, k_decode_tc<kKv>) != cudaSuccess) return cudaErrorInvalidDeviceFunction;
-            return fa.numRegs == 128 ? cudaSuccess : cudaErrorInvalidConfiguration;
+            return fa.numRegs == (C::kI4 ? 96 : 128) ? cudaSuccess : cudaErrorInvalidConfiguration;
         }();
         if (regs_check != cudaSuccess) return regs_check;
     }
@@ -845,6 +880,8 @@ cudaError_t launch_decode_tc(const inkattn_attn_params &p, const AttnScalars &s,
     a.kv_rows = (long long)p.num_blocks * p.Hkv * kBlock;
     a.wait_ns = kernel_debug().wait_ns;
     a.withhold = kernel_debug().withhold;
+    a.i4_mask = kI4Mask;
+    a.i4_exponent = kI4Exponent;
     const dim3 grid = a.band_split ? dim3(p.Hkv, p.B, 2) : dim3(num_splits, p.Hkv, p.B);
     switch (p.kv_dtype) {
         case INKATTN_KV_E4M3: return launch_decode_variant<INKATTN_KV_E4M3>(a, grid, qmap, kmap, vmap, stream);

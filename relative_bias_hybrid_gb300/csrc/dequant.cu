@@ -86,7 +86,7 @@ k_dequant(const inkattn_attn_params p, inkattn_bf16 *k_out, inkattn_bf16 *v_out,
                 const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint4 h = i4_decode8(words[i], f);
+                    const uint4 h = i4_decode8(words[i], f, kI4Mask, kI4Exponent);
                     o[i] = make_uint4(f16x2_to_bf16x2(h.x), f16x2_to_bf16x2(h.y), f16x2_to_bf16x2(h.z),
                                       f16x2_to_bf16x2(h.w));
                 }

@@ -68,16 +68,20 @@ __device__ __forceinline__ I4Scale i4_factors(uint32_t byte) {
     f.off = __hmul2(f.s, __float2half2_rn(-72.f));
     return f;
 }
-// Eight values of a word as four fp16x2 in order.  A code u placed at bits 4 .. 7 under the exponent of
-// 64 (0x5400; 16 units of the last place are 1) is 64 + u; (64 + u) s - 72 s = n s in one fused step,
-// exact: 72 s = 9 s * 8 has at most 8 significant bits.  3 shifts, 4 masks and 4 multiply-adds a
-// word.
-__device__ __forceinline__ uint4 i4_decode8(uint32_t w, const I4Scale &f) {
+// Eight values of a word as four fp16x2 in order.  A code u placed in bits 4 .. 7 under the exponent of 64
+// (16 units of the last place are 1) is 64 + u; (64 + u) s - 72 s = n s in one fused step, exact:
+// 72 s = 9 s * 8 has at most 8 significant bits.  3 shifts, 4 masks and 4 multiply-adds a word, and
+// the SM has 4096 words to expand for every 128 keys: with `mask` and `exponent` (kI4Mask, kI4Exponent)
+// in registers or a kernel's parameters a mask is one instruction, with literals it is two (10 cycles a word
+// of a scheduler against 15).
+constexpr uint32_t kI4Mask = 0x00F000F0u, kI4Exponent = 0x54005400u;
+__device__ __forceinline__ uint4 i4_decode8(uint32_t w, const I4Scale &f, uint32_t mask, uint32_t exponent) {
     const uint32_t at[4] = {w << 4, w, w >> 4, w >> 8};
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t m = (at[i] & 0x00F000F0u) | 0x54005400u;
+        uint32_t m;                                // (at & mask) | exponent
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(m) : "r"(at[i]), "r"(mask), "r"(exponent));
         const __half2 v = __hfma2(*reinterpret_cast<const __half2 *>(&m), f.s, f.off);
         r[i] = *reinterpret_cast<const uint32_t *>(&v);
     }
