@@ -140,7 +140,10 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
     const int split = A.band_split ? (int)blockIdx.z : (int)blockIdx.x;
     const int hk = A.band_split ? (int)blockIdx.x : (int)blockIdx.y;
     const int b = A.band_split ? (int)blockIdx.y : (int)blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (broadcast, so that the compiler knows the roles' branches to be uniform over a warp and keeps the MMA
+    // warp's descriptors in uniform registers: without it an MMA of the variants with codes takes
+    // 100 cycles to issue instead of 40)
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int g = p.Hq / p.Hkv;
 
     // ---- sequence geometry and this split's key range (uniform over the CTA)
@@ -434,7 +437,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
             // A warp has the same units of every tile, more of them where its scheduler (warp % 4) has
             // softmax warps without rows: units of each warp, a hexadecimal digit, by the live lane
             // quarters.
-            const uint64_t share = n_rows <= 32 ? 0x121122212200ull : n_rows <= 64 ? 0x221122112200ull : n_rows <= 96 ? 0x211222122100ull : 0x111221222200ull;
+            const uint64_t share = n_rows <= 32 ? 0x121122212200ull : n_rows <= 64 ? 0x221122112200ull : n_rows <= 96 ? 0x311131122100ull : 0x111221222200ull;
             int u0 = 0;
             for (int i = 0; i < warp; ++i) u0 += (int)(share >> (4 * i)) & 15;
             const int units = (int)(share >> (4 * warp)) & 15;
