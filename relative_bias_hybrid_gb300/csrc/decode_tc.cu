@@ -263,18 +263,27 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
         constexpr int kRingFull = kCodes ? C::B_C_FULL : C::B_KV_FULL;
         constexpr int kRingEmpty = kCodes ? C::B_C_EMPTY : C::B_KV_EMPTY;
         int kv_loads = 0;
-        auto load_kv = [&](int n, int isv) -> bool {
-            const int L = kv_loads++, slot = L % kRing;
-            // the tile's block-table entries are read before the wait for the slot, so that
-            // their round trip to memory overlaps it instead of delaying the copy
-            int blk[2];                                      // -2: past this split's range
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int lb = my_lo + 2 * n + half;         // logical cache block
-                blk[half] = lb >= my_hi ? -2
-                          : lb < p.max_blocks_per_seq ? __ldg(p.block_table + (size_t)b * p.max_blocks_per_seq + lb)
-                          : -1;
+        // Block-table entries, 32 at a time, one a lane, and the next 32 already asked for: the tiles of
+        // a 4-bit cache come faster than a round trip to memory for each.  -2: past this split's range.
+        auto entries = [&](int first) -> int {
+            const int lb = first + lane;                     // logical cache block
+            return lb >= my_hi ? -2
+                 : lb < p.max_blocks_per_seq ? load_i32(p.block_table + (size_t)b * p.max_blocks_per_seq + lb) : -1;
+        };
+        int tab_first = my_lo, tab = entries(my_lo), tab_next = entries(my_lo + 32);
+        auto tile_blocks = [&](int n) -> int2 {              // of tile n, in ascending order
+            const int at = my_lo + 2 * n;
+            if (at >= tab_first + 32) {
+                tab_first += 32;
+                tab = tab_next;
+                tab_next = entries(tab_first + 32);
             }
+            return make_int2(__shfl_sync(0xffffffffu, tab, at - tab_first),
+                             __shfl_sync(0xffffffffu, tab, at - tab_first + 1));
+        };
+        auto load_kv = [&](int2 blocks, int isv) -> bool {
+            const int L = kv_loads++, slot = L % kRing;
+            const int blk[2] = {blocks.x, blocks.y};
             if (L >= kRing && !wwait(bar(kRingEmpty + slot), ((L / kRing) - 1) & 1)) {
                 --kv_loads;                                  // not issued
                 return false;
@@ -329,12 +338,15 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
             return true;
         };
         // consumption order of the MMA warp: K_0, then per tile n >= 1: K_n, V_{n-1}; then V_{N-1}
-        ok = load_kv(0, 0);
+        int2 behind = tile_blocks(0);
+        ok = load_kv(behind, 0);
         for (int n = 1; n < N && ok; ++n) {
-            ok = load_kv(n, 0);
-            if (ok) ok = load_kv(n - 1, 1);
+            const int2 blocks = tile_blocks(n);
+            ok = load_kv(blocks, 0);
+            if (ok) ok = load_kv(behind, 1);
+            behind = blocks;
         }
-        if (ok) ok = load_kv(N - 1, 1);
+        if (ok) ok = load_kv(behind, 1);
         // nothing may still be landing in shared memory when the CTA tears down, also when a
         // role gave up: the copies issued and not yet consumed are the last kRing
         if (lane == 0) {
