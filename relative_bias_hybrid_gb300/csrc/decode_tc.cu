@@ -73,8 +73,8 @@ struct Dec {
     static constexpr int kConvThreads = kCodes ? (kWarpSm - 2) * 32 : 0;    // converter warps, from 2 on
     static constexpr int kUnitsMax = 3;                      // units of a 4-bit tile that a warp has
     static constexpr int kConvArrivals = kI4 ? kConvThreads / 32 : kCodes ? kConvThreads : 1;   // for a tile
-    static constexpr int kSlots = kI4 ? 4 : kCodes ? 3 : 4;            // MMA operand ring
-    static constexpr int kCodeSlots = kCodes ? 3 : 0;      // ring of codes
+    static constexpr int kSlots = kCodes ? 3 : 4;            // MMA operand ring
+    static constexpr int kCodeSlots = kI4 ? 6 : kCodes ? 3 : 0;      // ring of codes
     static constexpr int kCodeRow = kI4 ? kI4RowBytes : kHeadDim;    // bytes of a row's codes
     static constexpr int kCodeTile = kKeys * kCodeRow;               // one tile: [128 keys][row]
     static constexpr int kCodeSlotBytes = kCodeTile + kKeys * 4;     // + 4 bytes of scales a row
@@ -321,17 +321,18 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                         sc[half * 64 + 32 + lane] = 0u;
                     }
                 __syncwarp();
-                if (lane == 0) {
+                const uint32_t fb = bar(C::B_C_FULL + slot);
+                if (lane == 0) mbar_arrive_expect_tx(fb, C::kCodeTile + 256u * (uint32_t)(have[0] + have[1]));
+                __syncwarp();
+                if (lane < 2) {                              // a lane for each half: its copies go out beside the other's
+                    const int half = lane;
+                    const bool mine = half == 0 ? have[0] : have[1];
+                    const long long at = half == 0 ? row[0] : row[1];
                     const uint32_t dst = smem_u32(slot_p);
-                    const uint32_t fb = bar(C::B_C_FULL + slot);
-                    mbar_arrive_expect_tx(fb, C::kCodeTile + 256u * (uint32_t)(have[0] + have[1]));
                     const float *scales = isv ? p.v_scale : p.k_scale;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (blk[half] != -2 && !have[half]) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
-                        tma_load_2d(dst + half * (C::kCodeTile / 2), map, 0, (int)row[half], fb);
-                        if (have[half]) bulk_load(dst + C::kCodeTile + half * 256, scales + row[half], 256u, fb);
-                    }
+                    if ((half == 0 ? blk[0] : blk[1]) != -2 && !mine) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+                    tma_load_2d(dst + half * (C::kCodeTile / 2), map, 0, (int)at, fb);
+                    if (mine) bulk_load(dst + C::kCodeTile + half * 256, scales + at, 256u, fb);
                 }
             }
             __syncwarp();
