@@ -6,10 +6,14 @@
 // drawn from q stands with probability min(1, p(x) / q(x)), and the first that does not is
 // replaced by a draw from max(p - q, 0), renormalised.
 //
-// k_token_probs: one row by the CTAs of a cluster.  A CTA's part of the row stays in registers between
-// the maximum, the sum and the store, so the row is read once and written once; the CTAs exchange
-// (maximum, sum) once through shared memory.  Rows of more than 8 x 32768 logits are read twice.
-// Bound: HBM.
+// k_token_probs: one row by the CTAs of a cluster, which exchange (maximum, sum) once through shared
+// memory.  Where all clusters are resident at once, a CTA's part of the row stays in registers
+// between the maximum, the sum and the store (k_token_probs: few rows, bound by the chain of these
+// steps: 9 rows of 50001 bf16 logits 5.9 us, read twice 9.3).  Otherwise the row is read again for the
+// store, from L2 (k_token_probs_twice): a thread then holds nothing over the exchange and
+// four CTAs an SM keep loading, where parts held in registers let two, in step (288 rows of
+// 131072 fp32 logits: 77 us, held in registers 140, and 93 with each thread's next row on its way
+// into shared memory meanwhile).
 //
 // k_verify_drafts: one sequence by the CTAs of a cluster.  Every CTA finds the first draft that does not
 // stand (a few words), then sums its part of that one row; the other rows are never read.  Weights
@@ -28,6 +32,7 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kPer = 8;                    // groups of four that a thread of k_token_probs holds
 
 // The 64-bit word at `local`'s offset in CTA `rank` of the cluster.
 __device__ __forceinline__ void st_cluster_u64(uint32_t local, uint32_t rank, uint64_t v) {
@@ -37,7 +42,7 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t local, uint32_t rank, ui
 
 // A row cut into groups of four elements at multiples of 16 bytes (bf16: 8), whatever its alignment:
 // group g holds the elements 4 g - skew .. 4 g - skew + 3, the first and the last possibly in part.
-__device__ __forceinline__ int row_skew(const void *row, int size) {
+__host__ __device__ __forceinline__ int row_skew(const void *row, int size) {
     return (int)((reinterpret_cast<uintptr_t>(row) / size) & 3);
 }
 template <typename T>
@@ -77,178 +82,270 @@ __device__ __forceinline__ void load_group(const T *row, int e, int V, bool toge
 __device__ __forceinline__ float weight(float l, float m, float k) {
     return l == -INFINITY ? 0.f : l == m ? 1.f : fast_exp2((l - m) * k);
 }
-__device__ __forceinline__ float not_nan(float l) { return l == l ? l : -INFINITY; }
+// The same of a logit, a NaN as -infinity; `below` is m, or 0 where m is -infinity.  (k is finite; an infinite
+// m alone needs the comparisons.)
+__device__ __forceinline__ float weight_of(float l, float m, float below, float k) {
+    const float v = fmaxf(l, -INFINITY);
+    return m < INFINITY ? fast_exp2((v - below) * k) : weight(v, m, k);
+}
+// log2(e) / t, finite also for the smallest t; 1 for a greedy row (t = 0)
+__device__ __forceinline__ float exponent_factor(float t) { return t == 0.f ? 1.f : fminf(kLog2e / t, 0x1.fffffep127f); }
+
+// What the CTAs of a row know of it.
+template <typename T>
+struct RowPart {
+    const T *in;
+    float *out;
+    int skew, g0, g1;                      // this CTA's groups
+    bool same;                             // in and out are aligned alike
+};
+template <typename T>
+__device__ __forceinline__ RowPart<T> row_part(const inkattn_token_probs_params &p, int row, int rank, int ctas) {
+    RowPart<T> r;
+    r.in = static_cast<const T *>(p.logits) + (size_t)row * p.logits_stride;
+    r.out = p.probs + (size_t)row * p.probs_stride;
+    r.skew = row_skew(r.in, sizeof(T));
+    r.same = r.skew == row_skew(r.out, 4);
+    const int groups = (p.V + r.skew + 3) / 4, per = (groups + ctas - 1) / ctas;
+    r.g0 = rank * per;
+    r.g1 = min(groups, r.g0 + per);
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_group(const RowPart<T> &r, int e, int V, const float (&y)[4]) {
+    if (r.same && e >= 0 && e + 4 <= V) {
+        *reinterpret_cast<float4 *>(r.out + e) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if ((unsigned)(e + j) < (unsigned)V) r.out[e + j] = y[j];
+    }
+}
+
+// The maximum of a block's values; the sum of a block's values (in a fixed order).
+__device__ __forceinline__ float block_max(float m, float *s_red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = s_red[threadIdx.x & (kWarps - 1)];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+__device__ __forceinline__ float block_sum(float s, float *s_red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    __syncthreads();                       // (s_red held the maxima)
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = s_red[threadIdx.x & (kWarps - 1)];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+// The row's maximum and sum, CTA by CTA in order, or the place of its first maximum, from every CTA's
+// (maximum, sum or place).
+struct RowTotal {
+    float m, sum;
+    int best;
+};
+__device__ __forceinline__ RowTotal row_total(float m, uint32_t second, bool greedy, float k, int rank, int ctas,
+                                              uint64_t *s_part) {
+    const uint64_t mine = ((uint64_t)__float_as_uint(m) << 32) | second;
+    RowTotal t = {m, 0.f, INT32_MAX};
+    if (ctas > 1) {
+        if ((int)threadIdx.x < ctas) st_cluster_u64(smem_u32(&s_part[rank]), threadIdx.x, mine);
+        cluster_sync();
+        for (int r = 0; r < ctas; ++r) t.m = fmaxf(t.m, __uint_as_float((uint32_t)(s_part[r] >> 32)));
+    }
+    for (int r = 0; r < ctas; ++r) {
+        const uint64_t v = ctas > 1 ? s_part[r] : mine;
+        const float mr = __uint_as_float((uint32_t)(v >> 32));
+        if (greedy) {
+            if (mr == t.m) t.best = min(t.best, (int)(uint32_t)v);
+        } else {
+            t.sum += weight(mr, t.m, k) * __uint_as_float((uint32_t)v);
+        }
+    }
+    return t;
+}
 
 }  // namespace
 
-// kPer = groups that a thread holds (a CTA's part is at most kThreads * kPer groups), 0: the part is
-// read twice.
-template <typename T, int kPer>
-__global__ void __launch_bounds__(kThreads)
+// A CTA's part of a row is at most kThreads * kPer groups.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2)
 k_token_probs(const inkattn_token_probs_params p, int ctas) {
     __shared__ float s_red[kWarps];
     __shared__ int s_best;
-    __shared__ __align__(8) uint64_t s_part[kMaxCluster];          // (maximum, sum or place) of each CTA
+    __shared__ __align__(8) uint64_t s_part[kMaxCluster];
     grid_dep_wait();
     grid_dep_launch();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row = blockIdx.x / ctas, rank = blockIdx.x - row * ctas, V = p.V;
-    const T *in = static_cast<const T *>(p.logits) + (size_t)row * p.logits_stride;
-    float *out = p.probs + (size_t)row * p.probs_stride;
-    const int skew = row_skew(in, sizeof(T));
-    const bool same = skew == row_skew(out, 4);
-    const int groups = (V + skew + 3) / 4, per = (groups + ctas - 1) / ctas;
-    const int g0 = rank * per, g1 = min(groups, g0 + per);
+    const int tid = threadIdx.x, V = p.V;
+    const int row = blockIdx.x / ctas, rank = blockIdx.x - row * ctas;
+    const RowPart<T> r = row_part<T>(p, row, rank, ctas);
     const float t = p.temperature ? load_f32(p.temperature + row) : 1.f;
+    float x[kPer][4], m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int g = r.g0 + i * kThreads + tid;
+        if (g < r.g1) load_group(r.in, 4 * g - r.skew, V, true, -INFINITY, x[i]);
+        else x[i][0] = x[i][1] = x[i][2] = x[i][3] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = fmaxf(m, x[i][j]);         // (a NaN is passed over)
     const bool valid = t >= 0.f && t < INFINITY, greedy = t == 0.f;
     if (!valid && rank == 0 && tid == 0) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
-    const float k = greedy ? 1.f : kLog2e / t;
-
-    constexpr int kHold = kPer > 0 ? kPer : 1;
-    float x[kHold][4];
-    float m = -INFINITY, s = 0.f;
-    if constexpr (kPer > 0) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int g = g0 + i * kThreads + tid;
-            if (g < g1) load_group(in, 4 * g - skew, V, true, -INFINITY, x[i]);
-            else x[i][0] = x[i][1] = x[i][2] = x[i][3] = -INFINITY;
-        }
+    const float k = exponent_factor(t);
+    if (tid == 0) s_best = INT32_MAX;
+    m = block_max(m, s_red);
+    uint32_t second;                                               // this CTA's sum, or its first maximum's place
+    if (greedy) {
+        int best = INT32_MAX;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) m = fmaxf(m, x[i][j]);     // (a NaN is passed over)
+            for (int j = 0; j < 4; ++j) {
+                const int g = r.g0 + i * kThreads + tid, e = 4 * g - r.skew + j;
+                if (x[i][j] == m && g < r.g1 && (unsigned)e < (unsigned)V) best = min(best, e);
+            }
+        if (best != INT32_MAX) atomicMin(&s_best, best);
+        __syncthreads();
+        second = (uint32_t)s_best;
     } else {
-        for (int g = g0 + tid; g < g1; g += kThreads) {
-            load_group(in, 4 * g - skew, V, true, -INFINITY, x[0]);
-            const float gm = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3]));
-            const float m2 = fmaxf(m, gm);
-            s *= weight(m, m2, k);
-            m = m2;
+        const float below = m == -INFINITY ? 0.f : m;
+        float s = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s += weight(not_nan(x[0][j]), m, k);
+        for (int i = 0; i < kPer; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[i][j] = weight_of(x[i][j], m, below, k);
+                s += x[i][j];
+            }
+        second = __float_as_uint(block_sum(s, s_red));
+    }
+    const RowTotal total = row_total(m, second, greedy, k, rank, ctas, s_part);
+    const bool zeros = !valid || total.m == -INFINITY;
+    // of the weights held, which are against this CTA's maximum
+    const float scale = zeros || greedy ? 0.f : weight(m, total.m, k) / total.sum;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int g = r.g0 + i * kThreads + tid, e = 4 * g - r.skew;
+        if (g >= r.g1) break;
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = zeros ? 0.f : greedy ? (e + j == total.best ? 1.f : 0.f) : x[i][j] * scale;
+        store_group(r, e, V, y);
+    }
+}
+
+// Four groups at a time: their loads go out together.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4)
+k_token_probs_twice(const inkattn_token_probs_params p, int ctas) {
+    __shared__ float s_red[kWarps];
+    __shared__ int s_best;
+    __shared__ __align__(8) uint64_t s_part[kMaxCluster];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, V = p.V;
+    const int row = blockIdx.x / ctas, rank = blockIdx.x - row * ctas;
+    const RowPart<T> r = row_part<T>(p, row, rank, ctas);
+    const float t = p.temperature ? load_f32(p.temperature + row) : 1.f;
+    const bool valid = t >= 0.f && t < INFINITY, greedy = t == 0.f;
+    if (!valid && rank == 0 && tid == 0) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+    const float k = exponent_factor(t);
+    constexpr int kAhead = 4;
+    auto load = [&](int g, float (&x)[kAhead][4]) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int gi = g + i * kThreads;
+            if (gi < r.g1) load_group(r.in, 4 * gi - r.skew, V, true, -INFINITY, x[i]);
+            else x[i][0] = x[i][1] = x[i][2] = x[i][3] = -INFINITY;
         }
+    };
+    float m = -INFINITY, s = 0.f;
+    for (int g = r.g0 + tid; g < r.g1; g += kAhead * kThreads) {
+        float x[kAhead][4];
+        load(g, x);
+        float m2 = m;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) m2 = fmaxf(m2, fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])));
+        s *= weight(m, m2, k);
+        m = m2;
+        const float below = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            s += (weight_of(x[i][0], m, below, k) + weight_of(x[i][1], m, below, k)) +
+                 (weight_of(x[i][2], m, below, k) + weight_of(x[i][3], m, below, k));
     }
     const float m_thread = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) s_red[warp] = m;
     if (tid == 0) s_best = INT32_MAX;
-    __syncthreads();
-    m = s_red[lane & (kWarps - 1)];
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    uint32_t second;                                               // this CTA's sum, or its best's place
+    m = block_max(m, s_red);
+    uint32_t second;
     if (greedy) {
         int best = INT32_MAX;
-        auto look = [&](int g, const float (&v)[4]) {
+        if (m_thread == m) {
+            for (int g = r.g0 + tid; g < r.g1; g += kThreads) {
+                float x[4];
+                load_group(r.in, 4 * g - r.skew, V, true, -INFINITY, x);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (v[j] == m && (unsigned)(4 * g - skew + j) < (unsigned)V) best = min(best, 4 * g - skew + j);
-        };
-        if constexpr (kPer > 0) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int g = g0 + i * kThreads + tid;
-                if (g < g1) look(g, x[i]);
-            }
-        } else if (m_thread == m) {
-            for (int g = g0 + tid; g < g1; g += kThreads) {
-                load_group(in, 4 * g - skew, V, true, -INFINITY, x[0]);
-                look(g, x[0]);
+                for (int j = 0; j < 4; ++j)
+                    if (x[j] == m && (unsigned)(4 * g - r.skew + j) < (unsigned)V) best = min(best, 4 * g - r.skew + j);
             }
         }
         if (best != INT32_MAX) atomicMin(&s_best, best);
         __syncthreads();
         second = (uint32_t)s_best;
     } else {
-        if constexpr (kPer > 0) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[i][j] = weight(not_nan(x[i][j]), m, k);
-                    s += x[i][j];
-                }
-        } else {
-            s *= weight(m_thread, m, k);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        __syncthreads();
-        if (lane == 0) s_red[warp] = s;
-        __syncthreads();
-        s = s_red[lane & (kWarps - 1)];
-#pragma unroll
-        for (int o = kWarps / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        second = __float_as_uint(s);
+        second = __float_as_uint(block_sum(s * weight(m_thread, m, k), s_red));
     }
-    const uint64_t mine = ((uint64_t)__float_as_uint(m) << 32) | second;
-    float m_all = m;
-    if (ctas > 1) {
-        if (tid < ctas) st_cluster_u64(smem_u32(&s_part[rank]), tid, mine);
-        cluster_sync();
-        for (int r = 0; r < ctas; ++r) m_all = fmaxf(m_all, __uint_as_float((uint32_t)(s_part[r] >> 32)));
-    }
-    // the row's sum, CTA by CTA in order, or the place of its first maximum
-    int best = INT32_MAX;
-    float sum = 0.f;
-    for (int r = 0; r < ctas; ++r) {
-        const uint64_t v = ctas > 1 ? s_part[r] : mine;
-        const float mr = __uint_as_float((uint32_t)(v >> 32));
-        if (greedy) {
-            if (mr == m_all) best = min(best, (int)(uint32_t)v);
-        } else {
-            sum += weight(mr, m_all, k) * __uint_as_float((uint32_t)v);
-        }
-    }
-    const bool zeros = !valid || m_all == -INFINITY;
-    const float scale = zeros || greedy ? 0.f : 1.f / sum;
-    const float scale_cta = scale * weight(m, m_all, k);           // of the weights held, which are against m
-    auto store = [&](int g, const float (&v)[4]) {
-        const int e = 4 * g - skew;
-        float y[4];
+    const RowTotal total = row_total(m, second, greedy, k, rank, ctas, s_part);
+    const bool zeros = !valid || total.m == -INFINITY;
+    const float scale = zeros || greedy ? 0.f : 1.f / total.sum, below = zeros ? 0.f : total.m;
+    for (int g = r.g0 + tid; g < r.g1; g += kAhead * kThreads) {
+        float x[kAhead][4];
+        if (!greedy && !zeros) load(g, x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            y[j] = zeros ? 0.f : greedy ? (e + j == best ? 1.f : 0.f) : kPer > 0 ? v[j] * scale_cta
-                 : weight(not_nan(v[j]), m_all, k) * scale;
-        if (same && e >= 0 && e + 4 <= V) {
-            *reinterpret_cast<float4 *>(out + e) = make_float4(y[0], y[1], y[2], y[3]);
-        } else {
+        for (int i = 0; i < kAhead; ++i) {
+            const int e = 4 * (g + i * kThreads) - r.skew;
+            if (g + i * kThreads >= r.g1) break;
+            float y[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if ((unsigned)(e + j) < (unsigned)V) out[e + j] = y[j];
-        }
-    };
-    if constexpr (kPer > 0) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int g = g0 + i * kThreads + tid;
-            if (g < g1) store(g, x[i]);
-        }
-    } else {
-        for (int g = g0 + tid; g < g1; g += kThreads) {
-            load_group(in, 4 * g - skew, V, true, -INFINITY, x[0]);
-            store(g, x[0]);
+                y[j] = zeros ? 0.f : greedy ? (e + j == total.best ? 1.f : 0.f) : weight_of(x[i][j], total.m, below, k) * scale;
+            store_group(r, e, V, y);
         }
     }
 }
 
-// CTAs of a row: enough that a CTA's part fits its registers eight groups a thread, more where the rows
-// alone do not fill the GPU (a part then has at least a group for each thread).
-cudaError_t launch_token_probs(const inkattn_token_probs_params &p, int num_sms, cudaStream_t stream) {
-    const int groups = p.V / 4 + 2;
+namespace {
+
+template <typename T>
+cudaError_t launch_token_probs_of(const inkattn_token_probs_params &p, int num_sms, cudaStream_t stream) {
+    // the most groups of a row: those of every row where all are aligned alike
+    const int skew = p.logits_stride % 4 == 0 || p.N_tok == 1 ? row_skew(p.logits, sizeof(T)) : 3;
+    const int groups = (p.V + skew + 3) / 4;
+    // CTAs of a row: enough that a CTA's part fits its threads' registers, more where the rows alone
+    // do not fill the GPU (a part then has at least a group for each thread)
     int ctas = 1;
-    while (ctas < kMaxCluster && (groups > 8 * kThreads * ctas ||
+    while (ctas < kMaxCluster && (groups > kPer * kThreads * ctas ||
                                   ((long long)p.N_tok * ctas < 2 * num_sms && groups > kThreads * ctas)))
         ctas *= 2;
-    const int per = (groups + ctas - 1) / ctas;
-    auto kernel = [&](auto type) {
-        using T = decltype(type);
-        return per <= 8 * kThreads ? k_token_probs<T, 8> : per <= 16 * kThreads ? k_token_probs<T, 16> : k_token_probs<T, 0>;
-    };
-    return launch_dependent(p.logits_dtype == INKATTN_DTYPE_F32 ? kernel(0.f) : kernel(inkattn_bf16{}),
-                            dim3((unsigned)(p.N_tok * ctas)), dim3(kThreads), 0, stream, ctas, p, ctas);
+    const bool few = (long long)p.N_tok * ctas <= 2 * num_sms && (groups + ctas - 1) / ctas <= kPer * kThreads;
+    return launch_dependent(few ? k_token_probs<T> : k_token_probs_twice<T>, dim3((unsigned)(p.N_tok * ctas)),
+                            dim3(kThreads), 0, stream, ctas, p, ctas);
+}
+
+}  // namespace
+
+cudaError_t launch_token_probs(const inkattn_token_probs_params &p, int num_sms, cudaStream_t stream) {
+    return p.logits_dtype == INKATTN_DTYPE_F32 ? launch_token_probs_of<float>(p, num_sms, stream)
+                                               : launch_token_probs_of<inkattn_bf16>(p, num_sms, stream);
 }
 
 // ---------------------------------------------------------------- verification
@@ -343,25 +440,38 @@ k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
     const int groups = (V + skew + 3) / 4, per = (groups + ctas - 1) / ctas, per_warp = (per + kWarps - 1) / kWarps;
     const int g0 = min(groups, rank * per + warp * per_warp);
     const int g1 = min(min(groups, rank * per + per), g0 + per_warp);
-    auto weights = [&](int g, float (&w)[4]) {
-        const int e = 4 * g - skew;
-        load_group(pr, e, V, true, 0.f, w);
-        float q[4] = {0.f, 0.f, 0.f, 0.f};
-        if (qr) load_group(qr, e, V, row_skew(qr, 4) == skew, 0.f, q);
+    // the weights of this lane's groups at g, g + 32, ..., kAhead of them: their loads go out together
+    constexpr int kAhead = 4;
+    auto weights = [&](int g, float (&w)[kAhead][4]) {
+        const bool together = qr && row_skew(qr, 4) == skew;
+        float q[kAhead][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = e + j == without ? 0.f : fmaxf(unit(w[j]) - unit(q[j]), 0.f);
+        for (int i = 0; i < kAhead; ++i) {
+            const int gi = g + 32 * i, e = 4 * gi - skew;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[i][j] = q[i][j] = 0.f;
+            if (gi < g1) {
+                load_group(pr, e, V, true, 0.f, w[i]);
+                if (qr) load_group(qr, e, V, together, 0.f, q[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[i][j] = 4 * (g + 32 * i) - skew + j == without ? 0.f : fmaxf(unit(w[i][j]) - unit(q[i][j]), 0.f);
     };
     uint64_t total = 0;
     int round = 0;
     for (;; ++round) {
         uint32_t hi = 0, lo = 0;                       // (at most 256 weights a thread: below 2^31)
-#pragma unroll 4
-        for (int g = g0 + lane; g < g1; g += 32) {
-            float w[4];
+        for (int g = g0 + lane; g < g1; g += 32 * kAhead) {
+            float w[kAhead][4];
             weights(g, w);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) fixed_add(w[j], hi, lo);
+            for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) fixed_add(w[i][j], hi, lo);
         }
         const uint64_t mine = warp_sum(((uint64_t)hi << 22) + lo);
         if (lane == 0) s_warp[warp] = mine;
@@ -406,38 +516,43 @@ k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
         rest -= s_warp[i];
     }
     if (rest >= s_warp[warp]) return;
-    for (int base = g0; base < g1; base += 32) {       // (one warp of the cluster is left)
-        const int g = base + lane;
-        uint64_t step[4] = {0, 0, 0, 0}, upto = 0;
-        if (g < g1) {
-            float w[4];
-            weights(g, w);
+    for (int base = g0; base < g1; base += 32 * kAhead) {          // (one warp of the cluster is left)
+        float w[kAhead][4];
+        weights(base + lane, w);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            uint64_t step[4], own = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t hi = 0, lo = 0;
-                fixed_add(w[j], hi, lo);
+                fixed_add(w[i][j], hi, lo);
                 step[j] = ((uint64_t)hi << 22) + lo;
-                upto += step[j];
+                own += step[j];
             }
-        }
-        const uint64_t own = upto;
+            uint64_t upto = own;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const uint64_t all = __shfl_sync(0xffffffffu, upto, 31);
+            if (rest >= all) {
+                rest -= all;
+                continue;
+            }
+            if (rest < upto && rest >= upto - own) {               // this lane's group
+                uint64_t left = rest - (upto - own);
+                int j = 0;
+#pragma unroll
+                for (int c = 0; c < 3; ++c)
+                    if (j == c && left >= step[c]) {
+                        left -= step[c];
+                        ++j;
+                    }
+                p.out_tokens[row] = 4 * (base + lane + 32 * i) - skew + j;
+            }
+            return;
         }
-        const uint64_t all = __shfl_sync(0xffffffffu, upto, 31);
-        if (rest >= all) {
-            rest -= all;
-            continue;
-        }
-        if (rest < upto && rest >= upto - own) {       // this lane's group
-            uint64_t left = rest - (upto - own);
-            int j = 0;
-            while (j < 3 && left >= step[j]) left -= step[j++];
-            p.out_tokens[row] = 4 * g - skew + j;
-        }
-        break;
     }
 }
 
