@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -480,7 +481,45 @@ inkattn_status launch_status(cudaError_t e) { return e == cudaSuccess ? INKATTN_
 // `per` blocks at min(its own rate, HBM / active CTAs), so a wave with a CTAs costs
 // per * max(r, a), where r is the number of CTAs that saturate HBM; the split partials add
 // their write + read traffic and the combine launch a fixed cost.
+namespace {
+
+// The same over a 4-bit cache, where a CTA's own steps set its pace and not HBM.  In microseconds, fits to
+// measured times (GB300, nine batches of one to 32 sequences with 1000 to 32768 keys, 1 to 32 parts: the choice
+// is within 13% of the best): a CTA starts and drains in 9, takes 0.5 for a block and kI4BandCost times
+// that for one of the band; the combine of S parts 2 + 0.27 S and its bytes at HBM's rate.
+// S parts of equal cost, one CTA an SM; or two parts cut at the band (csrc/decode_tc.cu), whose CTAs
+// run beside each other.
+int pick_splits_i4(const inkattn_attn_params &p, int num_sms) {
+    constexpr double kStart = 9.0, kBlockUs = 0.5;
+    long long nblk = ((long long)p.max_seqlen_k + kBlock - 1) / kBlock;
+    if (p.window > 0) nblk = std::min(nblk, ((long long)p.window + p.max_seqlen_q + kBlock - 1) / kBlock + 1);
+    nblk = std::max(nblk, 1ll);
+    const long long band = p.rel_extent > 0 ? std::min(nblk, ((long long)p.rel_extent + p.max_seqlen_q + kBlock - 1) / kBlock + 1) : 0;
+    const double before = (double)(nblk - band) * kBlockUs, inside = (double)band * kI4BandCost * kBlockUs;
+    const long long units = (long long)p.B * p.Hkv, slots = num_sms > 0 ? num_sms : 1;
+    int best = 1;
+    double best_us = 1e300;
+    for (int S = 1; S <= kDecodeMaxSplits && S <= (nblk + 1) / 2; ++S) {
+        double us;
+        if (S == 2 && p.rel_extent > 0) {
+            us = fmax(fmax((double)((units + slots - 1) / slots) * (kStart + before), kStart + inside),
+                      (double)units * (2 * kStart + before + inside) / (double)slots);
+        } else {
+            us = (double)((units * S + slots - 1) / slots) * (kStart + (before + inside) / S);
+        }
+        if (S > 1) us += 2.0 + 0.27 * S + 2.0 * 4.0 * (kHeadDim + 1) * p.N_tok * (double)p.Hq * S / 6.7e6;
+        if (us < best_us * (1.0 - 1e-9)) {
+            best_us = us;
+            best = S;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
 int pick_splits(const inkattn_attn_params &p, int num_sms) {
+    if (p.kv_dtype == INKATTN_KV_I4) return pick_splits_i4(p, num_sms);
     const int g = p.Hq / p.Hkv;
     long long nblk = (p.max_seqlen_k + kBlock - 1) / kBlock;
     if (p.window > 0) {

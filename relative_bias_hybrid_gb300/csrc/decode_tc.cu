@@ -170,6 +170,18 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
         const int cut = blk_first + ((max(blk_first, min(blk_end, band_key_lo / kBlock)) - blk_first) & ~1);
         my_lo = split == 0 ? blk_first : cut;
         my_hi = split == 0 ? cut : blk_end;
+    } else if (C::kI4) {
+        // parts of equal cost in whole tiles, a block of the band counting kI4BandCost others: with few
+        // sequences the CTAs of the band would be the last by far
+        const int band = p.rel_extent > 0 ? max(blk_first, min(blk_end, max(0, pos0 - p.rel_extent + 1) / kBlock)) : blk_end;
+        const int before = band - blk_first;
+        const long long cost = before + (long long)kI4BandCost * (blk_end - band);
+        auto cut = [&](int part) {
+            const int at = (int)(part * cost / A.S);
+            return blk_first + min(nblk, ((at <= before ? at : before + (at - before) / kI4BandCost) + 1) & ~1);
+        };
+        my_lo = cut(split);
+        my_hi = split == A.S - 1 ? blk_end : cut(split + 1);
     } else {
         const int per = (nblk + A.S - 1) / A.S;
         my_lo = blk_first + split * per;
