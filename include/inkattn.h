@@ -1,6 +1,7 @@
 /*
  * inkattn.h -- C ABI of libinkattn.so, the GB300 (sm_103a) attention hot path of
- * one Inkling decoder layer, and the layer's products behind it.
+ * one Inkling decoder layer, the layer's products behind it, and the end of a
+ * verification step.
  *
  * Sources, cited by page title and section heading:
  *   [SG] "SGLang と Miles が Inkling を初日からサポート：975Bのマルチモーダル最先端モデルが公開"
@@ -21,8 +22,8 @@
  *   - Kernels are chained by programmatic dependent launch: each may become resident on
  *     the GPU while the kernel before it on the stream finishes, and reads no global
  *     memory before that kernel has completed, so stream order holds as for any launch.
- *     inkattn_prologue, inkattn_output_conv, inkattn_qkvr_prologue and the calls of the
- *     layer's second half let the next kernel be scheduled once all their CTAs have
+ *     inkattn_prologue, inkattn_output_conv, inkattn_qkvr_prologue, the calls of the layer's
+ *     second half and those of a verification step's end let the next kernel be scheduled once all their CTAs have
  *     started; the attention kernels do not.  Every call can be captured
  *     into a CUDA graph.
  *   - Host-side validation runs before any launch; on failure the call returns
@@ -287,7 +288,8 @@ INKATTN_API size_t inkattn_decode_workspace_bytes(const inkattn_attn_params *p, 
  * within rel_extent of the first query, moved down so that the part before it holds
  * whole 128-key tiles): the
  * streaming part and the band part then run in separate CTAs, the streaming ones
- * scheduled first.  With one split the result goes straight to out/lse; otherwise each
+ * scheduled first.  Over a 4-bit cache the other split counts divide the keys into parts of about equal
+ * cost instead, whole 128-key tiles, a tile of the band counting for several others.  With one split the result goes straight to out/lse; otherwise each
  * split's own softmax-normalised partial output and its lse go to the workspace, and
  * inkattn_combine must follow on the same stream with the same num_splits.
  * workspace: device memory of at least inkattn_decode_workspace_bytes bytes,

@@ -234,6 +234,11 @@ __device__ __forceinline__ void cluster_sync() {
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Before a CTA's first access to a peer's shared memory: the peer has to have started.  Every thread arrives
+// once it runs and waits in front of that access.
+__device__ __forceinline__ void cluster_started_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_started_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 // ---------------------------------------------------------------- mma.sync and packing
 
 // D (16x8 fp32) += A (16x16 fp16, row) * B (16x8 fp16, col)

@@ -57,10 +57,22 @@ constexpr int kTabRows = kDecodeMaxRows;   // g * ql <= 128
 
 // Three variants, by the cache's element type.  kKv = INKATTN_KV_BF16: TMA loads K/V tiles
 // straight into the MMAs' 4-slot ring.  INKATTN_KV_E4M3 and INKATTN_KV_I4: TMA loads tiles of
-// codes and their scales into a ring of their own (E4M3 3 slots, 4 bits 6), and six converter
-// warps (2-7) convert Q to f16 in place, then expand each tile (code * scale, exactly) to f16
-// in a 3-slot MMA ring; P is packed as f16, so the MMAs run kind::f16 on f16 operands.  Warps:
-// 0 TMA, 1 MMA, [2, 8) converters (codes only), then 8 softmax warps.
+// codes and their scales into a ring of their own (E4M3 3 slots, 4 bits 6), and converter warps
+// (E4M3 six, 4 bits ten) convert Q to f16 in place, then expand each tile (code * scale, exactly)
+// to f16 in a 3-slot MMA ring; P is packed as f16, so the MMAs run kind::f16 on f16 operands.
+// Warps: 0 TMA, 1 MMA, [2, kWarpSm) converters (codes only), then 8 softmax warps.
+//
+// What bounds the 4-bit variant: a tile of 128 keys is 17 KB from HBM, a quarter of bf16's, and
+// takes about 2100 cycles of an SM (without converting anything 1900), in which the schedulers issue
+// two cycles in three: 32768 values are expanded (about 3000 of its 6300 instructions), 72 rows of
+// softmax run beside them, and the tensor pipe is active for half.  MTP-verify (32 x 9 queries,
+// 32768 keys, band split) 0.60 ms with the combine, bf16 cache 0.67; floor (HBM) 0.17.  Steps: six
+// warps of 512 threads, 16 units shared out evenly 0.88; ten converter warps with shares by their
+// scheduler's load and lane-constant addresses, and rows without a query as zeros instead of masked 0.71;
+// the warp index broadcast (uniform registers for the MMA warp, no spills) 0.68; block-table entries ahead
+// of the tiles 0.64; a lane for each half's copies 0.60.  Pieces taken from a queue in shared memory
+// instead of fixed shares 1.05, the units of a tile in a rolled loop 0.69, 4 operand and 3 code slots
+// the same as 3 and 6.
 template <int kKv>
 struct Dec {
     static constexpr bool kCodes = kKv != INKATTN_KV_BF16;
@@ -68,8 +80,11 @@ struct Dec {
     static constexpr int kThreads = kI4 ? 640 : kCodes ? 512 : 320;
     static constexpr int kWarpSm = kI4 ? 12 : kCodes ? 8 : 2;           // first softmax warp
     static constexpr int kWarpMma = 1;
-    // registers of the first two warpgroups and of the softmax's (512 threads x 128 at launch)
+    // registers a thread at launch, of the warps below kWarpSm, and of the softmax's
+    static constexpr int kRegsLaunch = kI4 ? 96 : 128;
     static constexpr int kRegsLow = kI4 ? 64 : 80, kRegsHigh = kI4 ? 144 : 176;
+    static_assert(!kCodes || kWarpSm * kRegsLow + 8 * kRegsHigh <= (kWarpSm + 8) * kRegsLaunch,
+                  "the split draws on what the block was launched with");
     static constexpr int kConvThreads = kCodes ? (kWarpSm - 2) * 32 : 0;    // converter warps, from 2 on
     static constexpr int kUnitsMax = 3;                      // units of a 4-bit tile that a warp has
     static constexpr int kConvArrivals = kI4 ? kConvThreads / 32 : kCodes ? kConvThreads : 1;   // for a tile
@@ -106,6 +121,25 @@ struct Dec {
     static_assert(kOffTab % 16 == 0 && kOffBar % 8 == 0, "alignment of the table and the barriers");
     static_assert(kThreads == 32 * (kWarpSm + 8), "eight softmax warps last");
 };
+
+// The 4-bit variant's shares: the units of a tile (16) that each warp expands, a hexadecimal digit for warp 0 on,
+// by how many lane quarters have rows; more of them where the warp's scheduler (warp % 4) has
+// softmax warps without rows to work on (MTP-verify, three quarters: 0.60 ms with these shares, 0.64
+// with equal ones).
+constexpr uint64_t kShare1 = 0x121122212200ull, kShare2 = 0x221122112200ull, kShare3 = 0x311131122100ull,
+                   kShare4 = 0x111221222200ull;
+// All warps' units; 0 where a warp has more than three, or one that is no converter any.
+constexpr int share_units(uint64_t share) {
+    int n = 0;
+    for (int w = 0; w < 16; ++w) {
+        const int u = (int)(share >> (4 * w)) & 15;
+        if (u > Dec<INKATTN_KV_I4>::kUnitsMax || (u > 0 && (w < 2 || w >= Dec<INKATTN_KV_I4>::kWarpSm))) return 0;
+        n += u;
+    }
+    return n;
+}
+static_assert(share_units(kShare1) == 16 && share_units(kShare2) == 16 && share_units(kShare3) == 16 &&
+              share_units(kShare4) == 16, "each unit of a tile once");
 
 constexpr uint32_t kTmemO = 0, kTmemS0 = 128;
 constexpr int kBarPair = 8;                // named barriers 8-11: the softmax row pairs, per lane quarter
@@ -255,8 +289,8 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
     const float c_qk = lam * A.scale * kLog2e;       // S (with the bias folded in) -> log2 logit
     const float inv_scale = 1.f / A.scale;           // bias in S units
 
-    // Variants with codes (512 threads, 128 registers each at launch): the warpgroups of the TMA,
-    // MMA and converter warps give registers to the two softmax warpgroups (80 + 176).
+    // Variants with codes: the warpgroups of the TMA, MMA and converter warps give registers to the
+    // two softmax warpgroups.
     if (warp == 0) {
         // ================================ producer ================================
         if constexpr (kCodes) tc::reg_dealloc<C::kRegsLow>();
@@ -459,10 +493,8 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
             // over the banks) to four chunks of 16 bytes (the MMA's 128-byte swizzle does the same).
             // Both swizzles depend on the lane alone, so a unit's addresses are the lane's plus the
             // unit's.
-            // A warp has the same units of every tile, more of them where its scheduler (warp % 4) has
-            // softmax warps without rows: units of each warp, a hexadecimal digit, by the live lane
-            // quarters.
-            const uint64_t share = n_rows <= 32 ? 0x121122212200ull : n_rows <= 64 ? 0x221122112200ull : n_rows <= 96 ? 0x311131122100ull : 0x111221222200ull;
+            // A warp has the same units of every tile.
+            const uint64_t share = n_rows <= 32 ? kShare1 : n_rows <= 64 ? kShare2 : n_rows <= 96 ? kShare3 : kShare4;
             int u0 = 0;
             for (int i = 0; i < warp; ++i) u0 += (int)(share >> (4 * i)) & 15;
             const int units = (int)(share >> (4 * warp)) & 15;
@@ -880,12 +912,12 @@ cudaError_t launch_decode_variant(const DecTcArgs &a, dim3 grid, const CUtensorM
                                   const CUtensorMap &vmap, cudaStream_t stream) {
     using C = Dec<kKv>;
     if constexpr (C::kCodes) {
-        // the register split (2 warpgroups at 80 + 2 at 176 = 512 x 128) needs exactly 128
-        // registers a thread at launch: with fewer, setmaxnreg.inc could never be satisfied
+        // the register split needs exactly kRegsLaunch registers a thread at launch: with fewer,
+        // setmaxnreg.inc could never be satisfied
         static const cudaError_t regs_check = [] {
             cudaFuncAttributes fa;
             if (cudaFuncGetAttributes(&fa, k_decode_tc<kKv>) != cudaSuccess) return cudaErrorInvalidDeviceFunction;
-            return fa.numRegs == (C::kI4 ? 96 : 128) ? cudaSuccess : cudaErrorInvalidConfiguration;
+            return fa.numRegs == C::kRegsLaunch ? cudaSuccess : cudaErrorInvalidConfiguration;
         }();
         if (regs_check != cudaSuccess) return regs_check;
     }

