@@ -26,34 +26,69 @@ constexpr int kI4RowBytes = 64;                    // codes of a row of 128
 constexpr int kI4RowScales = 4;                    // scales of a row of 128
 constexpr uint32_t kI4ScaleMax = 0xC6u;            // 896: 72 * 896, the expansion's offset, is finite in fp16
 
-// The byte of the smallest scale that holds a group of largest magnitude amax (NaN counts as 0;
-// above 7 * 896 the largest, and the values saturate).
-__device__ __forceinline__ uint32_t i4_scale_byte(float amax) {
-    if (!(amax > 0.f)) return 0u;
-    // amax / 7 rounded up: no scale lies between the quotient and its rounding, since every
-    // scale is a float
-    const float t = __fdiv_ru(amax, 7.f);
-    const uint32_t u = __float_as_uint(t);
-    uint32_t b;
-    if (t >= 0x1p-14f) b = ((u + 0xFFFFFu) >> 20) - ((127u - 15u) << 3);   // mantissa up to 3 bits
-    else b = (uint32_t)__float2int_ru(t * 0x1p17f);                        // multiples of 2^-17
-    return b < kI4ScaleMax ? b : kI4ScaleMax;
-}
+constexpr float kI4Max = 7.f * 896.f;              // the largest value
+
 __device__ __forceinline__ float i4_scale(uint32_t byte) {
     return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
 }
-// The word of eight values.  The quotient by division, not by a reciprocal's product: n + 1/2 is
-// reached exactly by bf16 values, and a tie has to be seen as one.  (Any other quotient lies further
-// from a tie than fp32's rounding, x having 8 significant bits and (n + 1/2) s as many.)
-__device__ __forceinline__ uint32_t i4_encode8(const float (&x)[8], float s) {
-    uint32_t w = 0;
+// The byte of the smallest scale s with 7 s >= amax, amax <= kI4Max.
+__device__ __forceinline__ uint32_t i4_scale_byte(float amax) {
+    // amax / 7 from below by at most two units of the last place, up to the next scale; a scale that lies
+    // between the two is told by 7 s, which is exact
+    const float t = __fmul_rd(amax, 0x1.249248p-3f);
+    uint32_t b;
+    if (t >= 0x1p-14f) b = ((__float_as_uint(t) + 0xFFFFFu) >> 20) - ((127u - 15u) << 3);   // mantissa up to 3 bits
+    else b = (uint32_t)__float2int_ru(t * 0x1p17f);                                       // multiples of 2^-17
+    return 7.f * i4_scale(b) < amax ? b + 1 : b;
+}
+// n = x / s to nearest, ties to even, as u = n + 8 in the low four bits; |x| <= 7 s, inv = 1 / s but for
+// rounding.  x / s is a tie or lies 2^-9 of it from one (x has 8 significant bits and so has
+// (n + 1/2) s), so only a tie can come out on the wrong side, and x - n s, which is exact, tells it.
+__device__ __forceinline__ uint32_t i4_code(float x, float s, float half, float inv) {
+    constexpr float kMagic = 12582912.f + 8.f;     // 1.5 * 2^23: the sum's low bits are those of n + 8
+    const float t = fmaf(x, inv, kMagic);
+    const float r = fmaf(kMagic - t, s, x);
+    uint32_t u = __float_as_uint(t);
+    if (fabsf(r) == half && (u & 1u)) u += r > 0.f ? 1u : ~0u;
+    return u & 15u;
+}
+// A lane's eight values of a row (packed bf16, a group in four neighbouring lanes of a converged warp) as a word
+// of codes, and the group's scale byte.
+__device__ __forceinline__ void i4_encode(const uint4 &row, uint32_t &word, uint32_t &byte) {
+    auto larger = [](uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    };
+    const uint32_t mag = 0x7FFF7FFFu;
+    uint32_t m = larger(larger(row.x & mag, row.y & mag), larger(row.z & mag, row.w & mag));
+    m = larger(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = larger(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    float amax = fmaxf(__uint_as_float(m & 0x7FFF0000u), __uint_as_float(m << 16));
+    const uint32_t w[4] = {row.x, row.y, row.z, row.w};
+    float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float n = s > 0.f ? rintf(__fdiv_rn(x[e], s)) : 0.f;
-        n = n == n ? fminf(fmaxf(n, -7.f), 7.f) : 0.f;                     // (a NaN is stored as 0)
-        w |= (uint32_t)((int)n + 8) << (4 * (e >> 1) + 16 * (e & 1));
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(w[i]);
+        x[2 * i + 1] = bf16_hi(w[i]);
     }
-    return w;
+    // rare: a value beyond the largest, an infinity or a NaN (whose bits are larger still) in the group: a NaN
+    // counts as 0, the others saturate
+    if (max(m & 0x7FFFu, m >> 16) > (__float_as_uint(kI4Max) >> 16)) {
+        amax = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = x[e] == x[e] ? fminf(fmaxf(x[e], -kI4Max), kI4Max) : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+        const uint32_t group = 0xFu << ((threadIdx.x & 31) & ~3);          // (the four lanes alike)
+        amax = fmaxf(amax, __shfl_xor_sync(group, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(group, amax, 2));
+    }
+    byte = i4_scale_byte(amax);
+    const float s = i4_scale(byte), inv = byte ? __frcp_rn(s) : 0.f;
+    word = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) word |= i4_code(x[e], s, 0.5f * s, inv) << (4 * (e >> 1) + 16 * (e & 1));
 }
 
 // A group's scale as the two factors of i4_decode8: s and -72 s.

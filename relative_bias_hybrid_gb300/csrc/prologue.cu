@@ -238,17 +238,7 @@ k_prologue(const inkattn_prologue_params p, const int kv_tiles) {
         }
         // 4-bit cache: one scale per 32 values (four lanes), a word of codes a lane
         uint32_t scale_byte = 0;
-        if (i4) {
-            float r8[8];
-            unpack8(row, r8);
-            float am = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(r8[e]));
-            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-            scale_byte = i4_scale_byte(am);
-            codes.x = i4_encode8(r8, i4_scale(scale_byte));
-        }
+        if (i4) i4_encode(row, codes.x, scale_byte);
         const int sm = __shfl_sync(0xffffffffu, sm_mine, ((half & 1) << 4) + u);
         if (!valid) continue;
         if (sm < 0 || (long long)sm >= slot_limit) {

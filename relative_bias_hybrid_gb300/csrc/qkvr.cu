@@ -512,17 +512,7 @@ k_qkvr(const QkvrArgs A, const __grid_constant__ CUtensorMap xmap, const __grid_
                     codes = e4m3_encode8(r8, pow2f(-kx));
                 }
                 uint32_t scale_byte = 0;
-                if (i4) {
-                    float r8[8];
-                    unpack8(outrow, r8);
-                    float am = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) am = fmaxf(am, fabsf(r8[j]));
-                    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-                    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-                    scale_byte = i4_scale_byte(am);
-                    codes.x = i4_encode8(r8, i4_scale(scale_byte));
-                }
+                if (i4) i4_encode(outrow, codes.x, scale_byte);
                 if (!valid) continue;
                 const int sm = __ldg(p.slot_mapping + tok);
                 if (sm < 0 || (long long)sm >= slot_limit) {

@@ -122,6 +122,34 @@ def test_prologue_stores_a_nan_as_zero(env):
     assert (got[:, 5] == 0).all() and np.isfinite(got).all() and (got != 0).mean() > 0.8
 
 
+def test_prologue_ties_at_every_scale(env):
+    """Every scale in a group that reaches 7 s, with each tie (n + 1/2) s and the bf16 values on both sides of it; and
+    groups whose largest value is the bf16 value above 7 s."""
+    gen, AttentionStep, oracle, _ = env
+    groups = []
+    for s in oracle.i4_scales()[1:]:
+        ties = torch.tensor([(n + 0.5) * s for n in range(7)], dtype=torch.float64).to(torch.bfloat16)
+        near = torch.cat([ties, (ties.view(torch.int16) + 1).view(torch.bfloat16), (ties.view(torch.int16) - 1).view(torch.bfloat16)])
+        near = torch.cat([near[:14], -near[14:], -ties])             # 28 values
+        top = torch.tensor([7 * s], dtype=torch.float64).to(torch.bfloat16)
+        above = (top.view(torch.int16) + 1).view(torch.bfloat16)
+        for most in (top, above):
+            groups.append(torch.cat([near, most, -most, torch.zeros(2, dtype=torch.bfloat16)]))
+    groups = torch.stack(groups)
+    rows = groups.reshape(-1, 128)
+    w = gen.custom("ties4", Hq=8, Hkv=1, q_lens=[rows.shape[0]], prefix_lens=[0], rel_extent=16)
+    x = gen.make_inputs(w, seed=4, device="cuda", kv_dtype="i4")
+    x["conv_w_v"][:] = 0.0
+    x["conv_w_v"][:, 3] = 1.0
+    x["v"].copy_(rows)
+    AttentionStep(w, x, mode="prefill").run_prologue()
+    torch.cuda.synchronize()
+    slots = x["slot_mapping"].cpu().numpy()
+    codes, scales = oracle.quantize_rows_i4(gen.bits(rows))
+    assert np.array_equal(x["v_scale"].cpu().numpy()[slots // 64, 0, slots % 64], scales)
+    assert np.array_equal(x["v_cache"].cpu().numpy()[slots // 64, 0, slots % 64], codes)
+
+
 def test_qkvr_writes_the_prologues_rows(env):
     """The fused projections on integer-grid inputs (exact sums): cache rows, scales, queries and states as
     the bf16 run's, quantised."""
