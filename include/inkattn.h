@@ -622,7 +622,8 @@ INKATTN_API inkattn_status inkattn_expert_combine(const inkattn_expert_combine_p
  * A NaN counts as -infinity; a row of -infinities gives zeros; of a row with infinite logits,
  * those alone share the 1.  A temperature that is negative, infinite or NaN is flagged
  * (INKATTN_ERR_DEVICE_BOUNDS) and its row written as zeros.  Relative error at most
- * (32 + V 2^-13 + 2 (m - l_v) / t) 2^-23 of a value, and possibly 0 below 2^-125. */
+ * (32 + V 2^-13 + 2 (m - l_v) / t) 2^-23 of a value, and possibly 0 below 2^-125 (finite logits
+ * further apart than the largest float, and temperatures above 2^126, are less exact). */
 typedef struct inkattn_token_probs_params {
     size_t struct_size;        /* = sizeof(inkattn_token_probs_params)                   */
     int32_t N_tok;             /* rows, 0 .. 2^24                                        */
@@ -658,7 +659,7 @@ INKATTN_API inkattn_status inkattn_token_probs(const inkattn_token_probs_params 
  * their place (the n_keep of inkattn_conv_rollback); 0 for a sequence without rows.  out_tokens at
  * the sequence's rows: the drafts that stand, the drawn token, then -1.
  * Flagged (INKATTN_ERR_DEVICE_BOUNDS): a cu_seqlens_q out of range or decreasing (n_new 0, the
- * tokens not written), a draft outside [0, V) (does not stand, nothing is taken from p_i for it), a
+ * tokens not written), a draft outside [0, V) behind drafts that stand (does not stand, nothing is taken from p_i for it), a
  * row to draw from whose weights are all zero (token -1, n_new without it).  u values outside
  * [0, 1) count as the nearer bound (the largest float below 1), a NaN as 0. */
 typedef struct inkattn_verify_drafts_params {

@@ -99,10 +99,10 @@ k_dequant(const inkattn_attn_params p, inkattn_bf16 *k_out, inkattn_bf16 *v_out,
                 const unsigned char *codes =
                     static_cast<const unsigned char *>(stream == 0 ? p.k_cache : p.v_cache) + src_row * kHeadDim + qd * 32;
                 const uint4 c[2] = {load_u32x4(codes), load_u32x4(codes + 16)};
-    #pragma unroll
+#pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t w[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
-    #pragma unroll
+#pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t lo = w[2 * e], hi = w[2 * e + 1];
                         o[2 * h + e] = make_uint4(e4m3x2_to_bf16x2(lo, s), e4m3x2_to_bf16x2(lo >> 16, s),

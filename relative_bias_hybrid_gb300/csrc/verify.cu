@@ -9,11 +9,13 @@
 // k_token_probs: one row by the CTAs of a cluster, which exchange (maximum, sum) once through shared
 // memory.  Where all clusters are resident at once, a CTA's part of the row stays in registers
 // between the maximum, the sum and the store (k_token_probs: few rows, bound by the chain of these
-// steps: 9 rows of 50001 bf16 logits 5.4 us, read twice 9.3).  Otherwise the row is read again for the
+// steps: 9 rows of 50001 bf16 logits 5.3 us, read twice 9.3).  Otherwise the row is read again for the
 // store, from L2 (k_token_probs_twice): a thread then holds nothing over the exchange and
 // four CTAs an SM keep loading, where parts held in registers let two, in step (288 rows of
-// 131072 fp32 logits: 66 us, 4.6 TB/s to and from HBM; held in registers 140, and 93 with each
-// thread's next row on its way into shared memory meanwhile).
+// 131072 fp32 logits: 58 us, 5.2 TB/s to and from HBM; held in registers 140, and 93 with each
+// thread's next row on its way into shared memory meanwhile).  Steps: 66 us with every element tested for
+// the row's end and for an infinite maximum (49 warp instructions for 32 logits, now 28) 60, and with
+// stores that leave L2 first 58.
 //
 // k_verify_drafts: one sequence by the CTAs of a cluster.  Every CTA finds the first draft that does not
 // stand (a few words), then sums its part of that one row; the other rows are never read.  Weights
@@ -84,11 +86,21 @@ __device__ __forceinline__ void load_group(const T *row, int e, int V, bool toge
 __device__ __forceinline__ float weight(float l, float m, float k) {
     return l == -INFINITY ? 0.f : l == m ? 1.f : fast_exp2((l - m) * k);
 }
-// The same of a logit, a NaN as -infinity; `below` is m, or 0 where m is -infinity.  (k is finite; an infinite
+// Logits to their weights, a NaN as -infinity; m is their maximum or larger.  (k is finite, so an infinite
 // m alone needs the comparisons.)
-__device__ __forceinline__ float weight_of(float l, float m, float below, float k) {
-    const float v = fmaxf(l, -INFINITY);
-    return m < INFINITY ? fast_exp2((v - below) * k) : weight(v, m, k);
+__device__ __forceinline__ void to_weights(float (&x)[4], float m, float k) {
+    if (m < INFINITY) {
+        const float below = m == -INFINITY ? 0.f : -m;
+        const float2 a = fmul2(fadd2(make_float2(x[0], x[1]), make_float2(below, below)), make_float2(k, k));
+        const float2 b = fmul2(fadd2(make_float2(x[2], x[3]), make_float2(below, below)), make_float2(k, k));
+        x[0] = fast_exp2(fmaxf(a.x, -INFINITY));
+        x[1] = fast_exp2(fmaxf(a.y, -INFINITY));
+        x[2] = fast_exp2(fmaxf(b.x, -INFINITY));
+        x[3] = fast_exp2(fmaxf(b.y, -INFINITY));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = weight(fmaxf(x[j], -INFINITY), m, k);
+    }
 }
 // log2(e) / t, finite also for the smallest t; 1 for a greedy row (t = 0)
 __device__ __forceinline__ float exponent_factor(float t) { return t == 0.f ? 1.f : fminf(kLog2e / t, 0x1.fffffep127f); }
@@ -221,15 +233,12 @@ k_token_probs(const inkattn_token_probs_params p, int ctas) {
         __syncthreads();
         second = (uint32_t)s_best;
     } else {
-        const float below = m == -INFINITY ? 0.f : m;
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[i][j] = weight_of(x[i][j], m, below, k);
-                s += x[i][j];
-            }
+        for (int i = 0; i < kPer; ++i) {
+            to_weights(x[i], m, k);
+            s += (x[i][0] + x[i][1]) + (x[i][2] + x[i][3]);
+        }
         second = __float_as_uint(block_sum(s, s_red));
     }
     const RowTotal total = row_total(m, second, greedy, k, rank, ctas, s_part);
@@ -265,7 +274,18 @@ k_token_probs_twice(const inkattn_token_probs_params p, int ctas) {
     if (!valid && rank == 0 && tid == 0) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
     const float k = exponent_factor(t);
     constexpr int kAhead = 4;
+    // whether a thread's next groups, from g on, are all there and whole
+    auto whole = [&](int g) {
+        const int e = 4 * g - r.skew;
+        return g + (kAhead - 1) * kThreads < r.g1 && e >= 0 && e + 4 * (kAhead - 1) * kThreads + 4 <= V;
+    };
     auto load = [&](int g, float (&x)[kAhead][4]) {
+        if (whole(g)) {
+            const T *at = r.in + (4 * g - r.skew);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) load_four(at + 4 * i * kThreads, x[i]);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int gi = g + i * kThreads;
@@ -282,11 +302,11 @@ k_token_probs_twice(const inkattn_token_probs_params p, int ctas) {
         for (int i = 0; i < kAhead; ++i) m2 = fmaxf(m2, fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])));
         s *= weight(m, m2, k);
         m = m2;
-        const float below = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            s += (weight_of(x[i][0], m, below, k) + weight_of(x[i][1], m, below, k)) +
-                 (weight_of(x[i][2], m, below, k) + weight_of(x[i][3], m, below, k));
+        for (int i = 0; i < kAhead; ++i) {
+            to_weights(x[i], m, k);
+            s += (x[i][0] + x[i][1]) + (x[i][2] + x[i][3]);
+        }
     }
     const float m_thread = m;
     if (tid == 0) s_best = INT32_MAX;
@@ -311,19 +331,35 @@ k_token_probs_twice(const inkattn_token_probs_params p, int ctas) {
     }
     const RowTotal total = row_total(m, second, greedy, k, rank, ctas, s_part);
     const bool zeros = !valid || total.m == -INFINITY;
-    const float scale = zeros || greedy ? 0.f : 1.f / total.sum, below = zeros ? 0.f : total.m;
+    const float scale = zeros || greedy ? 0.f : 1.f / total.sum;
     for (int g = r.g0 + tid; g < r.g1; g += kAhead * kThreads) {
         float x[kAhead][4];
-        if (!greedy && !zeros) load(g, x);
+        if (!greedy && !zeros) {
+            load(g, x);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int e = 4 * (g + i * kThreads) - r.skew;
-            if (g + i * kThreads >= r.g1) break;
-            float y[4];
+            for (int i = 0; i < kAhead; ++i) {
+                to_weights(x[i], total.m, k);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                y[j] = zeros ? 0.f : greedy ? (e + j == total.best ? 1.f : 0.f) : weight_of(x[i][j], total.m, below, k) * scale;
-            store_group(r, e, V, y);
+                for (int j = 0; j < 4; ++j) x[i][j] *= scale;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[i][j] = !zeros && 4 * (g + i * kThreads) - r.skew + j == total.best ? 1.f : 0.f;
+        }
+        if (r.same && whole(g)) {
+            float *at = r.out + (4 * g - r.skew);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                __stcs(reinterpret_cast<float4 *>(at + 4 * i * kThreads), make_float4(x[i][0], x[i][1], x[i][2], x[i][3]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (g + i * kThreads >= r.g1) break;
+                store_group(r, 4 * (g + i * kThreads) - r.skew, V, x[i]);
+            }
         }
     }
 }
@@ -335,11 +371,14 @@ cudaError_t launch_token_probs_of(const inkattn_token_probs_params &p, int num_s
     // the most groups of a row: those of every row where all are aligned alike
     const int skew = p.logits_stride % 4 == 0 || p.N_tok == 1 ? row_skew(p.logits, sizeof(T)) : 3;
     const int groups = (p.V + skew + 3) / 4;
-    // CTAs of a row: enough that a CTA's part fits its threads' registers, more where the rows alone
-    // do not fill the GPU (a part then has at least a group for each thread)
+    // CTAs of a row: a part of at most 64 KB (288 rows of 131072 fp32: 58 us, parts of 128 KB 64, of 256 KB
+    // 77; bf16 45, parts of 32 KB 50, and 50001 20, parts of 25 KB 27: a CTA's fixed cost is about 5 us), and
+    // more CTAs as long as all are resident at once and a part has a group for each thread (64 rows of
+    // 50001 bf16 with four 8.0 us, two 9.4, eight 11.4)
+    constexpr int kMost = 65536 / (4 * (int)sizeof(T));
     int ctas = 1;
-    while (ctas < kMaxCluster && (groups > kPer * kThreads * ctas ||
-                                  ((long long)p.N_tok * ctas < 2 * num_sms && groups > kThreads * ctas)))
+    while (ctas < kMaxCluster &&
+           (groups > kMost * ctas || ((long long)p.N_tok * ctas <= num_sms && groups > kThreads * ctas)))
         ctas *= 2;
     const bool few = (long long)p.N_tok * ctas <= 2 * num_sms && (groups + ctas - 1) / ctas <= kPer * kThreads;
     return launch_dependent(few ? k_token_probs<T> : k_token_probs_twice<T>, dim3((unsigned)(p.N_tok * ctas)),

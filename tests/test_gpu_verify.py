@@ -124,6 +124,22 @@ def test_probs_in_place(ia, V):
     assert torch.equal(l, want)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V, wide", [(8192, 8192), (16411, 16417)])
+def test_probs_of_many_rows(ia, dtype, V, wide):
+    """Rows enough to be read twice, whole batches of groups and ragged ends, greedy rows and odd values among
+    them; aligned like their logits or not, and in place."""
+    T = 310
+    l = (3 * torch.randn((T, wide), device=DEV)).to(dtype)[:, :V]
+    t = 0.3 + torch.rand((T,), device=DEV)
+    t[::7] = 0.0
+    l[3], l[5, V // 2], l[6, 1::3], l[14, [9, V - 1]] = -torch.inf, torch.inf, torch.nan, 100.0
+    _check_probs(ia, l, t)
+    _check_probs(ia, l, t, torch.empty((T, wide + 4), device=DEV)[:, 3:V + 3])
+    if dtype == F32:
+        _check_probs(ia, l, t, l)
+
+
 # ---------------------------------------------------------------- verification
 
 def _steps(w):
