@@ -41,16 +41,15 @@ __device__ __forceinline__ uint32_t i4_scale_byte(float amax) {
     else b = (uint32_t)__float2int_ru(t * 0x1p17f);                                       // multiples of 2^-17
     return 7.f * i4_scale(b) < amax ? b + 1 : b;
 }
-// n = x / s to nearest, ties to even, as u = n + 8 in the low four bits; |x| <= 7 s, inv = 1 / s but for
-// rounding.  x / s is a tie or lies 2^-9 of it from one (x has 8 significant bits and so has
-// (n + 1/2) s), so only a tie can come out on the wrong side, and x - n s, which is exact, tells it.
-__device__ __forceinline__ uint32_t i4_code(float x, float s, float half, float inv) {
-    constexpr float kMagic = 12582912.f + 8.f;     // 1.5 * 2^23: the sum's low bits are those of n + 8
-    const float t = fmaf(x, inv, kMagic);
-    const float r = fmaf(kMagic - t, s, x);
-    uint32_t u = __float_as_uint(t);
-    if (fabsf(r) == half && (u & 1u)) u += r > 0.f ? 1u : ~0u;
-    return u & 15u;
+// n = x / s to nearest, ties to even, of two values, as u = n + 8 in the low halves of the results; |x| <= 7 s,
+// inv = 1 / s but for 2^-20 of it.  x / s is a tie or lies 2^-9 of it from one (x has 8 significant bits and so
+// has (n + 1/2) s): rounded to multiples of 2^-11 first, by a sum that ends there, a tie is exact and the
+// others stay on their side.
+__device__ __forceinline__ float2 i4_codes2(float2 x, float inv) {
+    constexpr float kStep = 0x1.8p12f;             // sums with it end at 2^-11
+    constexpr float kMagic = 0x1.8p23f + 8.f;      // and with this at 1: the sum's low bits are those of n + 8
+    const float2 t = ffma2(x, make_float2(inv, inv), make_float2(kStep, kStep));
+    return fadd2(t, make_float2(kMagic - kStep, kMagic - kStep));
 }
 // A lane's eight values of a row (packed bf16, a group in four neighbouring lanes of a converged warp) as a word
 // of codes, and the group's scale byte.
@@ -85,10 +84,15 @@ __device__ __forceinline__ void i4_encode(const uint4 &row, uint32_t &word, uint
         amax = fmaxf(amax, __shfl_xor_sync(group, amax, 2));
     }
     byte = i4_scale_byte(amax);
-    const float s = i4_scale(byte), inv = byte ? __frcp_rn(s) : 0.f;
-    word = 0;
+    float inv = 0.f;
+    if (byte) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(i4_scale(byte)));
+    uint32_t pair[4];                              // of neighbours, a code in each half
 #pragma unroll
-    for (int e = 0; e < 8; ++e) word |= i4_code(x[e], s, 0.5f * s, inv) << (4 * (e >> 1) + 16 * (e & 1));
+    for (int i = 0; i < 4; ++i) {
+        const float2 u = i4_codes2(make_float2(x[2 * i], x[2 * i + 1]), inv);
+        pair[i] = __byte_perm(__float_as_uint(u.x), __float_as_uint(u.y), 0x5410);
+    }
+    word = (pair[0] | pair[1] << 4) | (pair[2] << 8 | pair[3] << 12);
 }
 
 // A group's scale as the two factors of i4_decode8: s and -72 s.
