@@ -63,16 +63,17 @@ constexpr int kTabRows = kDecodeMaxRows;   // g * ql <= 128
 // Warps: 0 TMA, 1 MMA, [2, kWarpSm) converters (codes only), then 8 softmax warps.
 //
 // What bounds the 4-bit variant: a tile of 128 keys is 17 KB from HBM, a quarter of bf16's, and
-// takes about 2100 cycles of an SM (without converting anything 1900), in which the schedulers issue
-// two cycles in three: 32768 values are expanded (about 3000 of its 6300 instructions), 72 rows of
-// softmax run beside them, and the tensor pipe is active for half.  MTP-verify (32 x 9 queries,
-// 32768 keys, band split) 0.60 ms with the combine, bf16 cache 0.67; floor (HBM) 0.17.  Steps: six
-// warps of 512 threads, 16 units shared out evenly 0.88; ten converter warps with shares by their
-// scheduler's load and lane-constant addresses, and rows without a query as zeros instead of masked 0.71;
-// the warp index broadcast (uniform registers for the MMA warp, no spills) 0.68; block-table entries ahead
-// of the tiles 0.64; a lane for each half's copies 0.60.  Pieces taken from a queue in shared memory
-// instead of fixed shares 1.05, the units of a tile in a rolled loop 0.69, 4 operand and 3 code slots
-// the same as 3 and 6.
+// takes about 1950 cycles of an SM, in which the schedulers issue two cycles in three: 32768 values are
+// expanded, 72 rows of softmax run beside them, and the tensor pipe is active for half.  MTP-verify
+// (32 x 9 queries, 32768 keys, band split) 0.56 ms with the combine, bf16 cache 0.67; floor (HBM) 0.17.
+// Steps: six warps of 512 threads, 16 units shared out evenly 0.88; ten converter warps with shares by
+// their scheduler's load and lane-constant addresses, and rows without a query as zeros instead of masked
+// 0.71; the warp index broadcast (uniform registers for the MMA warp, no spills) 0.68; block-table entries
+// ahead of the tiles 0.64; a lane for each half's copies 0.60; the warps in two sets that take the tiles in turn
+// 0.56.  Not kept: pieces taken from a queue in shared memory instead of fixed shares (1.05 for 0.71), the units of a
+// tile in a rolled loop (0.69 for 0.60), 4 operand and 3 code slots (no change), the softmax warpgroups each a tile
+// of their own in turn, with an O each (0.58 for 0.56), Q as an operand in TMEM (no change), the scales by
+// cp.async instead of bulk copies (no change).
 template <int kKv>
 struct Dec {
     static constexpr bool kCodes = kKv != INKATTN_KV_BF16;
@@ -86,8 +87,8 @@ struct Dec {
     static_assert(!kCodes || kWarpSm * kRegsLow + 8 * kRegsHigh <= (kWarpSm + 8) * kRegsLaunch,
                   "the split draws on what the block was launched with");
     static constexpr int kConvThreads = kCodes ? (kWarpSm - 2) * 32 : 0;    // converter warps, from 2 on
-    static constexpr int kUnitsMax = 3;                      // units of a 4-bit tile that a warp has
-    static constexpr int kConvArrivals = kI4 ? kConvThreads / 32 : kCodes ? kConvThreads : 1;   // for a tile
+    static constexpr int kConvArrivals = kI4 ? kConvThreads / 64 : kCodes ? kConvThreads : 1;   // for a tile (4 bits:
+                                                             // the warps take turns, and a lane arrives for each)
     static constexpr int kSlots = kCodes ? 3 : 4;            // MMA operand ring
     static constexpr int kCodeSlots = kI4 ? 6 : kCodes ? 3 : 0;      // ring of codes
     static constexpr int kCodeRow = kI4 ? kI4RowBytes : kHeadDim;    // bytes of a row's codes
@@ -124,22 +125,29 @@ struct Dec {
 
 // The 4-bit variant's shares: the units of a tile (16) that each warp expands, a hexadecimal digit for warp 0 on,
 // by how many lane quarters have rows; more of them where the warp's scheduler (warp % 4) has
-// softmax warps without rows to work on (MTP-verify, three quarters: 0.60 ms with these shares, 0.64
-// with equal ones).
-constexpr uint64_t kShare1 = 0x121122212200ull, kShare2 = 0x221122112200ull, kShare3 = 0x311131122100ull,
-                   kShare4 = 0x111221222200ull;
-// All warps' units; 0 where a warp has more than three, or one that is no converter any.
-constexpr int share_units(uint64_t share) {
-    int n = 0;
-    for (int w = 0; w < 16; ++w) {
-        const int u = (int)(share >> (4 * w)) & 15;
-        if (u > Dec<INKATTN_KV_I4>::kUnitsMax || (u > 0 && (w < 2 || w >= Dec<INKATTN_KV_I4>::kWarpSm))) return 0;
-        n += u;
-    }
-    return n;
+// softmax warps without rows to work on.  Five warps take the tiles 0, 2, ... of the ring, the other five
+// 1, 3, ...: a warp then waits and arrives half as often for the same units (MTP-verify 0.56 ms; all ten for
+// every tile 0.60, of that with equal shares 0.64).
+constexpr int kUnitsMax = 6;               // of a warp
+constexpr uint64_t kEven1 = 0x4040014300ull, kOdd1 = 0x440203300000ull, kEven2 = 0x2040024400ull, kOdd2 = 0x530204200000ull,
+                   kEven3 = 0x3050024200ull, kOdd3 = 0x620203300000ull, kEven4 = 0x3030043300ull, kOdd4 = 0x430302400000ull;
+// Whether each unit of a tile is expanded once, the even tiles' by the warps of ~odd and the odd ones' by those of odd.
+constexpr bool share_holds(uint64_t even_share, uint64_t odd_share, uint32_t odd) {
+    const uint64_t share[2] = {even_share, odd_share};
+    int units[2] = {0, 0}, warps[2] = {0, 0};
+    for (int w = 0; w < 16; ++w)
+        for (int i = 0; i < 2; ++i) {
+            const int u = (int)(share[i] >> (4 * w)) & 15;
+            if (u > kUnitsMax) return false;
+            if (u > 0 && (w < 2 || w >= Dec<INKATTN_KV_I4>::kWarpSm || (int)(odd >> w & 1) != i)) return false;
+            units[i] += u;
+            warps[i] += u > 0;
+        }
+    return units[0] == 16 && units[1] == 16 && warps[0] == Dec<INKATTN_KV_I4>::kConvArrivals && warps[1] == warps[0];
 }
-static_assert(share_units(kShare1) == 16 && share_units(kShare2) == 16 && share_units(kShare3) == 16 &&
-              share_units(kShare4) == 16, "each unit of a tile once");
+constexpr uint32_t kOddWarps = 1u << 5 | 1u << 6 | 1u << 8 | 1u << 10 | 1u << 11;
+static_assert(share_holds(kEven1, kOdd1, kOddWarps) && share_holds(kEven2, kOdd2, kOddWarps) &&
+              share_holds(kEven3, kOdd3, kOddWarps) && share_holds(kEven4, kOdd4, kOddWarps), "each unit of a tile once, by the warps that arrive for it");
 
 constexpr uint32_t kTmemO = 0, kTmemS0 = 128;
 constexpr int kBarPair = 8;                // named barriers 8-11: the softmax row pairs, per lane quarter
@@ -471,7 +479,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
     } else if (kCodes && warp < C::kWarpSm) {
         // ================================ converters (caches of codes) ================================
         if constexpr (kCodes) tc::reg_dealloc<C::kRegsLow>();
-        // warps 2-7 convert Q, then the K/V tiles
+        // Q first, then the K/V tiles
         const int ct = threadIdx.x - 32 - (warp > C::kWarpMma ? 32 : 0);   // 0 .. kConvThreads - 1
         bool ok = wwait(bar(C::B_Q), 0);
         if (ok) {
@@ -493,8 +501,10 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
             // over the banks) to four chunks of 16 bytes (the MMA's 128-byte swizzle does the same).
             // Both swizzles depend on the lane alone, so a unit's addresses are the lane's plus the
             // unit's.
-            // A warp has the same units of every tile.
-            const uint64_t share = n_rows <= 32 ? kShare1 : n_rows <= 64 ? kShare2 : n_rows <= 96 ? kShare3 : kShare4;
+            // A warp has the same units of every other tile.
+            const int odd = (int)(kOddWarps >> warp) & 1;
+            const uint64_t share = odd ? (n_rows <= 32 ? kOdd1 : n_rows <= 64 ? kOdd2 : n_rows <= 96 ? kOdd3 : kOdd4)
+                                       : (n_rows <= 32 ? kEven1 : n_rows <= 64 ? kEven2 : n_rows <= 96 ? kEven3 : kEven4);
             int u0 = 0;
             for (int i = 0; i < warp; ++i) u0 += (int)(share >> (4 * i)) & 15;
             const int units = (int)(share >> (4 * warp)) & 15;
@@ -504,37 +514,42 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
             uint32_t dst_lane[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) dst_lane[c] = (uint32_t)(k16 * 128 + (((grp * 4 + c) ^ (k16 & 7)) << 4));
-            int s4 = 0, s16 = 0;
+            constexpr int kTogether = 3;
+            int s4 = odd, s16 = odd;
             uint32_t turn4 = 0, turn16 = 0;                   // of the rings: parity of the waits
             bool bad = false;
-            for (int L = 0; L < 2 * N; ++L) {
+            for (int L = odd; L < 2 * N; L += 2) {
                 if (!(ok = wwait(bar(C::B_C_FULL + s4), turn4))) break;
                 if (L >= C::kSlots && !(ok = wwait(bar(C::B_KV_EMPTY + s16), turn16 ^ 1u))) break;
                 const uint32_t src = s_base + C::kOffCodes + s4 * C::kCodeSlotBytes;
                 const uint32_t dst = s_base + C::kOffKV + s16 * kSlotBytes;
                 const int key_end = min(T, kr_hi) - (kr_lo + tile_of(L) * kKeys);
-                uint4 w[C::kUnitsMax];
-                uint32_t byte[C::kUnitsMax];
 #pragma unroll
-                for (int i = 0; i < C::kUnitsMax; ++i) {      // (the loads of a tile go out together)
-                    if (i >= units) break;
-                    const int kb = (u0 + i) & 7, half = (u0 + i) >> 3;
-                    w[i] = lds_u32x4(src + kb * (16 * kI4RowBytes) + (src_lane ^ (half << 5)));
-                    byte[i] = lds_u8(src + kb * (16 * kI4RowScales) + 2 * half + byte_lane);
-                    if (kb * 16 + k16 >= key_end) byte[i] = 0;
-                }
+                for (int first = 0; first < kUnitsMax; first += kTogether) {
+                    if (first >= units) break;
+                    uint4 w[kTogether];
+                    uint32_t byte[kTogether];
 #pragma unroll
-                for (int i = 0; i < C::kUnitsMax; ++i) {
-                    if (i >= units) break;
-                    const int kb = (u0 + i) & 7, half = (u0 + i) >> 3;
-                    const bool over = byte[i] > kI4ScaleMax;
-                    bad |= over;
-                    const I4Scale f = i4_factors(over ? 0u : byte[i]);
-                    const uint32_t to = dst + half * 16384 + kb * 2048;
-                    sts_u32x4(to + dst_lane[0], i4_decode8(w[i].x, f, A.i4_mask, A.i4_exponent));
-                    sts_u32x4(to + dst_lane[1], i4_decode8(w[i].y, f, A.i4_mask, A.i4_exponent));
-                    sts_u32x4(to + dst_lane[2], i4_decode8(w[i].z, f, A.i4_mask, A.i4_exponent));
-                    sts_u32x4(to + dst_lane[3], i4_decode8(w[i].w, f, A.i4_mask, A.i4_exponent));
+                    for (int i = 0; i < kTogether; ++i) {     // (their loads go out together)
+                        if (first + i >= units) break;
+                        const int kb = (u0 + first + i) & 7, half = (u0 + first + i) >> 3;
+                        w[i] = lds_u32x4(src + kb * (16 * kI4RowBytes) + (src_lane ^ (half << 5)));
+                        byte[i] = lds_u8(src + kb * (16 * kI4RowScales) + 2 * half + byte_lane);
+                        if (kb * 16 + k16 >= key_end) byte[i] = 0;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kTogether; ++i) {
+                        if (first + i >= units) break;
+                        const int kb = (u0 + first + i) & 7, half = (u0 + first + i) >> 3;
+                        const bool over = byte[i] > kI4ScaleMax;
+                        bad |= over;
+                        const I4Scale f = i4_factors(over ? 0u : byte[i]);
+                        const uint32_t to = dst + half * 16384 + kb * 2048;
+                        sts_u32x4(to + dst_lane[0], i4_decode8(w[i].x, f, A.i4_mask, A.i4_exponent));
+                        sts_u32x4(to + dst_lane[1], i4_decode8(w[i].y, f, A.i4_mask, A.i4_exponent));
+                        sts_u32x4(to + dst_lane[2], i4_decode8(w[i].z, f, A.i4_mask, A.i4_exponent));
+                        sts_u32x4(to + dst_lane[3], i4_decode8(w[i].w, f, A.i4_mask, A.i4_exponent));
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -542,8 +557,8 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                     mbar_arrive(bar(C::B_C_EMPTY + s4));
                     mbar_arrive(bar(C::B_KV_FULL + s16));
                 }
-                if (++s4 == C::kCodeSlots) s4 = 0, turn4 ^= 1u;
-                if (++s16 == C::kSlots) s16 = 0, turn16 ^= 1u;
+                if ((s4 += 2) >= C::kCodeSlots) s4 -= C::kCodeSlots, turn4 ^= 1u;
+                if ((s16 += 2) >= C::kSlots) s16 -= C::kSlots, turn16 ^= 1u;
             }
             if (bad) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
         }
