@@ -363,3 +363,26 @@ def test_decode_winds_down_when_a_wait_runs_out(env):
     assert r.returncode == 0 and line, r.stderr[-2000:]
     got = json.loads(line[0][7:])
     assert got == {"status": env[3].INKATTN_ERR_DEVICE_TIMEOUT, "usable": True}
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+def test_blocks_past_32_bits_of_a_long_cache(env, mode):
+    """The same sequences at the end of a cache whose codes lie past 4 GiB: the same rows and results, bit for bit."""
+    gen, AttentionStep, _, _ = env
+    w = gen.custom("far4", Hq=16, Hkv=8, q_lens=[9, 3], prefix_lens=[300, 70], rel_extent=64)
+    x, step = _run(env, w, seed=15, mode=mode)
+    assert step.device_status() == 0
+    small, far = x["k_cache"].shape[0], 2 ** 32 // (8 * 64 * 64) + 5
+    y = gen.make_inputs(w, seed=15, device="cuda", kv_dtype="i4")
+    for c in ("k_cache", "v_cache", "k_scale", "v_scale"):
+        # only the last blocks are ever read or written
+        big = torch.empty((far + small, *y[c].shape[1:]), dtype=torch.uint8, device="cuda")
+        big[far:] = y[c]
+        y[c] = big
+    y["block_table"] = torch.where(y["block_table"] < 0, y["block_table"], y["block_table"] + far)
+    y["slot_mapping"] = y["slot_mapping"] + far * 64
+    _, again = _run(env, w, seed=15, mode=mode, x=y)
+    assert again.device_status() == 0
+    for c in ("k_cache", "v_cache", "k_scale", "v_scale"):
+        assert torch.equal(y[c][far:], x[c]), c
+    assert torch.equal(again.out, step.out) and torch.equal(again.lse, step.lse)

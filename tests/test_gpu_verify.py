@@ -140,6 +140,62 @@ def test_probs_of_many_rows(ia, dtype, V, wide):
         _check_probs(ia, l, t, l)
 
 
+def test_probs_of_the_most_rows(ia):
+    """2^24 rows of one logit, and of a few logits more rows than a grid's smaller dimensions hold."""
+    probs = torch.zeros((1 << 24, 1), device=DEV)
+    ia.inkattn_token_probs(ia.token_probs_params(logits=torch.randn((1 << 24, 1), device=DEV), probs=probs))
+    assert bool((probs == 1).all())
+    l = torch.randn((70001, 5), device=DEV)
+    probs = torch.empty_like(l)
+    ia.inkattn_token_probs(ia.token_probs_params(logits=l, probs=probs))
+    want = torch.softmax(l.double(), 1)
+    # the bar of _probs_ref at 5 logits less than 12 apart
+    assert float((l.max(1).values - l.min(1).values).max()) < 12
+    assert bool(((probs.double() - want).abs() <= want * (33 + 24) * 2.0 ** -23).all())
+
+
+def test_rows_past_32_bits(ia):
+    """Rows whose elements lie past 2^32 of the arrays' start: the same probabilities and tokens as of a copy."""
+    V, last = 131072, 2 ** 32 // 131072 + 3
+    c = _case(7, [9], V)
+    far = {k: torch.empty((last + 9, V), device=DEV) for k in ("logits", "target_p", "draft_p")}
+    near = 3 * torch.randn((3, V), device=DEV)
+    rows = [i * (last // 2) for i in range(3)]                     # three rows of the array, the last past 2^32
+    for i, r in enumerate(rows):
+        far["logits"][r] = near[i]
+    p = ia.token_probs_params(logits=far["logits"], probs=far["target_p"])
+    p.N_tok, p.logits_stride, p.probs_stride = 3, V * rows[1], V * rows[1]
+    ia.inkattn_token_probs(p)
+    want = torch.empty_like(near)
+    ia.inkattn_token_probs(ia.token_probs_params(logits=near, probs=want))
+    torch.cuda.synchronize()
+    for i, r in enumerate(rows):
+        assert torch.equal(far["target_p"][r], want[i])
+    far["target_p"][last:], far["draft_p"][last:] = c["target_p"], c["draft_p"]
+    ids = torch.zeros(last + 9, dtype=I32, device=DEV)
+    ids[last:] = c["token_ids"]
+    u = torch.zeros(last + 9, device=DEV)
+    u[last:] = c["u_accept"]
+    got = _verify(ia, dict(c, target_p=far["target_p"], draft_p=far["draft_p"], token_ids=ids, u_accept=u,
+                           cu_seqlens_q=torch.tensor([last, last + 9], dtype=I32, device=DEV)))
+    near_got = _verify(ia, c)
+    assert got[0] == near_got[0] and got[1][last:] == near_got[1] and got[1][:last] == [-7] * last
+
+
+def test_verify_of_the_most_sequences(ia):
+    """2^20 sequences of one row each."""
+    B = 1 << 20
+    p = torch.zeros((B, 2), device=DEV)
+    odd = torch.arange(B, device=DEV) % 2
+    p[torch.arange(B, device=DEV), odd] = 1
+    n_new, out = torch.zeros(B, dtype=I32, device=DEV), torch.zeros(B, dtype=I32, device=DEV)
+    st = _status()
+    ia.inkattn_verify_drafts(ia.verify_drafts_params(
+        target_p=p, token_ids=torch.zeros(B, dtype=I32, device=DEV), cu_seqlens_q=torch.arange(B + 1, dtype=I32, device=DEV),
+        u_accept=torch.zeros(B, device=DEV), u_sample=torch.rand(B, device=DEV), n_new=n_new, out_tokens=out, dev_status=st))
+    assert int(st) == 0 and bool((n_new == 1).all()) and torch.equal(out, odd.to(I32))
+
+
 # ---------------------------------------------------------------- verification
 
 def _steps(w):
@@ -499,3 +555,14 @@ def test_two_streams_at_once(ia):
         torch.cuda.synchronize()
         got = [(o["n_new"].tolist(), o["out_tokens"].tolist(), False) for o, _, _ in outs]
         assert got == want
+
+
+def test_rollback_of_the_most_sequences(ia):
+    B, C = 65535, 8
+    x, before = torch.randn((B, C), device=DEV).to(BF16), torch.randn((B, 3, C), device=DEV).to(BF16)
+    n = (torch.arange(B, device=DEV) % 2).to(I32)
+    want = torch.where((n == 1)[:, None, None], torch.cat([before[:, 1:], x[:, None]], 1), before)
+    ia.inkattn_conv_rollback(ia.conv_rollback_params(
+        x=[x], state_before=[before], state_after=[before], n_keep=n, state_slot=torch.arange(B, dtype=I32, device=DEV),
+        cu_seqlens_q=torch.arange(B + 1, dtype=I32, device=DEV)))
+    assert torch.equal(before, want)
