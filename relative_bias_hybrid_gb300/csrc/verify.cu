@@ -22,8 +22,8 @@
 // are whole multiples of 2^-43, so partial sums in 64 bits are exact: thread, warp, CTA and cluster sums
 // nest, and the CTA, then the warp, then the lane in whose range the draw falls finds its token by
 // the same sums.  (Doubles keep the sums as well, but an SM adds two a clock: 32 rows of 200000 would take
-// 11 us, where reading them from HBM takes 8.)  One sequence over 131072 tokens 7.1 us, of which the
-// launch and five dependent round trips to memory are nearly all; 32 over 200019 14.5 us, 3.5 TB/s (19.8
+// 11 us, where reading them from HBM takes 8.)  One sequence over 131072 tokens 7.0 us, of which the
+// launch and four dependent round trips to memory are nearly all; 32 over 200019 14.3 us, 3.6 TB/s (19.8
 // with the loads of one group at a time and the whole of the last warp's part read again).
 #include <type_traits>
 
@@ -423,7 +423,7 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 
 __global__ void __launch_bounds__(kThreads)
 k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
-    __shared__ int s_accepted;
+    __shared__ int s_accepted, s_lost;
     __shared__ uint64_t s_warp[kWarps], s_batch[kWarps][kMaxBatches];
     __shared__ __align__(8) uint64_t s_total[2][kMaxCluster];
     grid_dep_wait();
@@ -431,6 +431,7 @@ k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = blockIdx.x / ctas, rank = blockIdx.x - b * ctas, V = p.V;
     const int start = load_i32(p.cu_seqlens_q + b), end = load_i32(p.cu_seqlens_q + b + 1);
+    const float u_sample = load_f32(p.u_sample + b);   // (needed last, asked for first)
     const bool bad = start < 0 || end < start || end > p.N_tok;
     if (bad || start == end) {                         // (the same in every CTA of the cluster)
         if (rank == 0 && tid == 0) {
@@ -448,9 +449,10 @@ k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
         for (int base = 0; base < drafts; base += 32) {
             const int i = base + lane;
             bool stands = true;
+            int x = 0;
             if (i < drafts) {
                 const size_t row = (size_t)start + i;
-                const int x = load_i32(p.token_ids + row + 1);
+                x = load_i32(p.token_ids + row + 1);
                 stands = false;
                 if (x >= 0 && x < V) {
                     const float u = below_one(load_f32(p.u_accept + row));
@@ -462,6 +464,7 @@ k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
             const uint32_t no = __ballot_sync(0xffffffffu, !stands);
             if (no) {
                 accepted = base + __ffs(no) - 1;
+                if (i == accepted) s_lost = x;
                 break;
             }
         }
@@ -469,6 +472,9 @@ k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
     }
     __syncthreads();
     const int accepted = s_accepted;
+    if (rank == 0)
+        for (int i = tid; i < n; i += kThreads)
+            if (i != accepted) p.out_tokens[start + i] = i < accepted ? load_i32(p.token_ids + start + i + 1) : -1;
 
     // ---- the weights of the row behind the drafts that stand
     const size_t row = (size_t)start + accepted;
@@ -476,7 +482,7 @@ k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
     const float *qr = nullptr;
     int without = -1;                                  // the token left out (a draft without choice)
     if (accepted < drafts) {
-        const int x = load_i32(p.token_ids + row + 1);
+        const int x = s_lost;
         if (x < 0 || x >= V) {
             if (rank == 0 && tid == 0) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
         } else if (p.draft_p) {
@@ -545,18 +551,15 @@ k_verify_drafts(const inkattn_verify_drafts_params p, int ctas) {
     }
 
     // ---- the draw
-    if (rank == 0) {
-        for (int i = tid; i < n; i += kThreads) {
-            if (i < accepted) p.out_tokens[start + i] = load_i32(p.token_ids + start + i + 1);
-            else if (i > accepted || total == 0) p.out_tokens[start + i] = -1;
-        }
-        if (tid == 0) {
-            p.n_new[b] = accepted + (total != 0 ? 1 : 0);
-            if (total == 0) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
+    if (rank == 0 && tid == 0) {
+        p.n_new[b] = accepted + (total != 0 ? 1 : 0);
+        if (total == 0) {
+            p.out_tokens[row] = -1;
+            set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
         }
     }
     if (total == 0) return;
-    const uint64_t u = (uint64_t)(below_one(load_f32(p.u_sample + b)) * 0x1p32f);
+    const uint64_t u = (uint64_t)(below_one(u_sample) * 0x1p32f);
     uint64_t rest = __umul64hi(total, u << 32);        // floor(W U / 2^32) < W
     for (int r = 0; r < rank; ++r) {
         if (rest < s_total[round][r]) return;          // an earlier CTA's
