@@ -53,6 +53,7 @@ constexpr int kRows = 128;                 // MMA M: (token, query head) rows, p
 constexpr int kKeys = 128;                 // keys per tile (two cache blocks)
 constexpr int kSlotBytes = 32768;          // one MMA operand tile: [d half][128 keys][128 B]
 constexpr int kTabW = 144;                 // distances per table row: 128 keys + up to 16 tokens
+constexpr int kTabStride = 146;            // entries from row to row: 73 words, so that a warp's rows spread over the banks
 constexpr int kTabRows = kDecodeMaxRows;   // g * ql <= 128
 
 // Three variants, by the cache's element type.  kKv = INKATTN_KV_BF16: TMA loads K/V tiles
@@ -98,7 +99,7 @@ struct Dec {
     static constexpr int kOffKV = 32768;
     static constexpr int kOffCodes = kOffKV + kSlots * kSlotBytes;
     static constexpr int kOffTab = kOffCodes + kCodeSlots * kCodeSlotBytes;   // 16-bit fixed point [g][ql][kTabW]
-    static constexpr int kOffXchg = kOffTab + kTabRows * kTabW * 2;     // row maxima / sums
+    static constexpr int kOffXchg = kOffTab + kTabRows * kTabStride * 2;     // row maxima / sums
     static constexpr int kOffTsig = kOffXchg + 3 * 2 * kRows * 4;       // fp32 steps [g][ql][2 rounds]
     static constexpr int kOffBar = kOffTsig + kTabRows * 2 * 4;
     // mbarrier indices, laid out from the slot counts
@@ -638,6 +639,25 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                     // d_r = 32 (checked on the host): two k steps of 16.  A fragments: tokens gq
                     // (e even) and gq + 8 (e odd), each lane 8 of a token's 32 features; the four
                     // lanes of a token (tq = 0..3) hold all of them.
+                    // (Which column a k stands for is free as long as r and P agree: a lane has the columns
+                    // 16 kk + 4 tq .. + 3 of a step, 16 bytes of P, so that a row's 128 bytes take two accesses.)
+                    // The first round's P is asked for before r is waited for, the second's before the first is
+                    // stored (bf16, whose softmax has the registers) or right behind.
+                    constexpr int kGrp = 9;
+                    static_assert(kTabW / 8 == 2 * kGrp, "two rounds");
+                    float4 raw[kGrp][2];
+                    auto ask = [&](int rd) {
+#pragma unroll
+                        for (int u = 0; u < kGrp; ++u) {
+                            const int dl = dlo + (rd * kGrp + u) * 8 + gq;
+                            const bool dv = dl >= 0 && dl < p.rel_extent;
+#pragma unroll
+                            for (int kk = 0; kk < 2; ++kk)
+                                raw[u][kk] = dv ? __ldg(reinterpret_cast<const float4 *>(Ph + (size_t)dl * 32 + kk * 16 + 4 * tq))
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                    };
+                    ask(0);
                     float rv[2][4][2];
                     float rm[2] = {0.f, 0.f};
 #pragma unroll
@@ -645,7 +665,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int tt = gq + ((e & 1) << 3);
-                            const int col = kk * 16 + 2 * tq + ((e >> 1) << 3);
+                            const int col = kk * 16 + 4 * tq + (e >> 1) * 2;
                             const uint32_t w2 = tt < q_len
                                 ? load_u32(rh + (size_t)tt * 32 * p.Hq + col)
                                 : 0u;
@@ -672,27 +692,17 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                     // trips (the first also covers r above), not one per group; while K/V
                     // streams saturate the memory system a round trip costs thousands of cycles.
                     // Each round's results set the steps of its part of the rows and are stored.
-                    constexpr int kGrp = 9;
-                    static_assert(kTabW / 8 == 2 * kGrp, "two rounds");
 #pragma unroll
                     for (int rd = 0; rd < 2; ++rd) {
                         float res[kGrp][4];
                         uint32_t pb[kGrp][2][2];
 #pragma unroll
-                        for (int u = 0; u < kGrp; ++u) {
-                            const int dl = dlo + (rd * kGrp + u) * 8 + gq;
-                            const bool dv = dl >= 0 && dl < p.rel_extent;
+                        for (int u = 0; u < kGrp; ++u)
 #pragma unroll
                             for (int kk = 0; kk < 2; ++kk) {
-                                const int e0 = kk * 16 + 2 * tq;
-                                const float2 lo = dv ? __ldg(reinterpret_cast<const float2 *>(Ph + (size_t)dl * 32 + e0))
-                                                     : make_float2(0.f, 0.f);
-                                const float2 hi = dv ? __ldg(reinterpret_cast<const float2 *>(Ph + (size_t)dl * 32 + e0 + 8))
-                                                     : make_float2(0.f, 0.f);
-                                pb[u][kk][0] = pack_f16(lo.x, lo.y);
-                                pb[u][kk][1] = pack_f16(hi.x, hi.y);
+                                pb[u][kk][0] = pack_f16(raw[u][kk].x, raw[u][kk].y);
+                                pb[u][kk][1] = pack_f16(raw[u][kk].z, raw[u][kk].w);
                             }
-                        }
                         bool finite = true;
 #pragma unroll
                         for (int u = 0; u < kGrp; ++u) {
@@ -705,6 +715,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                             res[u][3] = acc[3] * rusc[1];
                             finite = finite && isfinite(acc[0] + acc[1] + acc[2] + acc[3]);
                         }
+                        if (!kCodes && rd == 0) ask(1);
                         // a P beyond fp16's range (|P| >= 65520) leaves an infinite or undefined entry
                         if (!finite) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
                         // each token row's largest |entry| in this round (its four lanes hold all
@@ -735,10 +746,11 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                                 const int tt = gq + 8 * i;
                                 if (tt >= q_len) continue;
                                 const float2 v = fix16_encode2(make_float2(res[u][2 * i], res[u][2 * i + 1]), enc[i]);
-                                *reinterpret_cast<uint32_t *>(tab + ((size_t)hq * A.ql + tt) * kTabW + c) =
+                                *reinterpret_cast<uint32_t *>(tab + ((size_t)hq * A.ql + tt) * kTabStride + c) =
                                     (__float_as_uint(v.x) & 0xFFFFu) | (__float_as_uint(v.y) << 16);
                             }
                         }
+                        if (kCodes && rd == 0) ask(1);
                     }
                 }
                 mbar_arrive(bar(C::B_TAB_FULL));
@@ -770,7 +782,7 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                 if (valid_row) {
                     // column b of the tile is at distance i - j = dlo + (t + 127 - b)
                     const int c0 = t + (kKeys - 1) - cb;             // table column of key column cb
-                    const unsigned short *trow = tab + ((size_t)hh * A.ql + t) * kTabW + c0;
+                    const unsigned short *trow = tab + ((size_t)hh * A.ql + t) * kTabStride + c0;
                     const float sg0 = tsig[(hh * A.ql + t) * 2], sg1 = tsig[(hh * A.ql + t) * 2 + 1];
 #pragma unroll
                     for (int bb = 0; bb < 64; ++bb) {
