@@ -31,7 +31,10 @@
 // undone on the fp32 results).  P must lie inside fp16's range (|P| < 65504); a table entry
 // that comes out infinite or undefined is flagged as INKATTN_ERR_DEVICE_BOUNDS.  The table holds 16-bit fixed point with one
 // step per (head, token) row and round of 72 distances, sigma = (largest |entry| of that
-// part of the row) / 32000; the staged bias is within sigma / 2 of the fp32 value.
+// part of the row) / 32000; the staged bias is within sigma / 2 of the fp32 value.  A tile of the band costs
+// about five others (L2 round trips for P and 64 table entries a thread).  Rows of 73 words instead of
+// 72, P in 16-byte pieces, loads ahead and one step's factor for most of a half: 64 sequences x 4 queries
+// over 4096 keys, 4 bits 315 -> 262 us.
 // Normalisation: O accumulates P V with P rounded to bf16, and each tile's largest P (its
 // row maximum's) is the dominant term whose bf16 rounding matters; that rounding error is
 // added to the row's normaliser, while the LSE uses the sum of the fp32 P.
@@ -53,6 +56,9 @@ constexpr int kRows = 128;                 // MMA M: (token, query head) rows, p
 constexpr int kKeys = 128;                 // keys per tile (two cache blocks)
 constexpr int kSlotBytes = 32768;          // one MMA operand tile: [d half][128 keys][128 B]
 constexpr int kTabW = 144;                 // distances per table row: 128 keys + up to 16 tokens
+// Of the 64 keys of a half, at a token t < 16 of table column t + 127 - bb (t + 63 - bb in the second half), those
+// that lie on one side of column 72 whatever t.
+constexpr int kTabMidLo = 7, kTabMidHi = 54;
 constexpr int kTabStride = 146;            // entries from row to row: 73 words, so that a warp's rows spread over the banks
 constexpr int kTabRows = kDecodeMaxRows;   // g * ql <= 128
 
@@ -66,12 +72,12 @@ constexpr int kTabRows = kDecodeMaxRows;   // g * ql <= 128
 // What bounds the 4-bit variant: a tile of 128 keys is 17 KB from HBM, a quarter of bf16's, and
 // takes about 1950 cycles of an SM, in which the schedulers issue two cycles in three: 32768 values are
 // expanded, 72 rows of softmax run beside them, and the tensor pipe is active for half.  MTP-verify
-// (32 x 9 queries, 32768 keys, band split) 0.56 ms with the combine, bf16 cache 0.67; floor (HBM) 0.17.
+// (32 x 9 queries, 32768 keys, band split) 0.54 ms with the combine, bf16 cache 0.66; floor (HBM) 0.17.
 // Steps: six warps of 512 threads, 16 units shared out evenly 0.88; ten converter warps with shares by
 // their scheduler's load and lane-constant addresses, and rows without a query as zeros instead of masked
 // 0.71; the warp index broadcast (uniform registers for the MMA warp, no spills) 0.68; block-table entries
 // ahead of the tiles 0.64; a lane for each half's copies 0.60; the warps in two sets that take the tiles in turn
-// 0.56.  Not kept: pieces taken from a queue in shared memory instead of fixed shares (1.05 for 0.71), the units of a
+// 0.555; the bias tables' layout and loads below 0.54.  Not kept: pieces taken from a queue in shared memory instead of fixed shares (1.05 for 0.71), the units of a
 // tile in a rolled loop (0.69 for 0.60), 4 operand and 3 code slots (no change), the softmax warpgroups each a tile
 // of their own in turn, with an O each (0.58 for 0.56), Q as an operand in TMEM (no change), the scales by
 // cp.async instead of bulk copies (no change).
@@ -784,10 +790,12 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
                     const int c0 = t + (kKeys - 1) - cb;             // table column of key column cb
                     const unsigned short *trow = tab + ((size_t)hh * A.ql + t) * kTabStride + c0;
                     const float sg0 = tsig[(hh * A.ql + t) * 2], sg1 = tsig[(hh * A.ql + t) * 2 + 1];
+                    const float sgm = hw == 0 ? sg1 : sg0;
 #pragma unroll
                     for (int bb = 0; bb < 64; ++bb) {
                         const float q = __uint_as_float(0x4B000000u | (uint32_t)trow[-bb]) - 8421376.0f;
-                        s[bb] = fmaf(q, c0 - bb < 72 ? sg0 : sg1, s[bb]);   // columns [0, 72): first round
+                        const bool mid = bb >= kTabMidLo && bb <= kTabMidHi;
+                        s[bb] = fmaf(q, mid ? sgm : c0 - bb < 72 ? sg0 : sg1, s[bb]);
                     }
                 }
                 mbar_arrive(bar(C::B_TAB_FREE));
