@@ -284,7 +284,8 @@ struct Range {
 };
 bool overlap(const Range &x, const Range &y) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(x.a), b = reinterpret_cast<uintptr_t>(y.a);
-    return x.a && y.a && x.n && y.n && a < b + y.n && b < a + x.n;
+    // (by distances: rows of a wide stride may claim more than lies behind their address)
+    return x.a && y.a && x.n && y.n && (a <= b ? b - a < x.n : a - b < y.n);
 }
 
 // Sizes, types and alignment that the linear layer and the grouped products share.  Arrays of
@@ -388,7 +389,7 @@ inkattn_status validate_expert_combine(const inkattn_expert_combine_params *p) {
 size_t span(int64_t rows, int64_t stride, int64_t width, size_t size) {
     return rows > 0 ? ((size_t)(rows - 1) * stride + width) * size : 0;
 }
-constexpr int64_t kMaxRowStride = 1ll << 32;       // (spans stay far below 2^63)
+constexpr int64_t kMaxRowStride = 1ll << 32;       // (spans stay below 2^64)
 
 inkattn_status validate_token_probs(const inkattn_token_probs_params *p) {
     if (!p || p->struct_size != sizeof(inkattn_token_probs_params) || p->N_tok < 0 || p->N_tok > (1 << 24) || p->V < 1 ||
