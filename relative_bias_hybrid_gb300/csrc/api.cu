@@ -259,21 +259,51 @@ inkattn_status validate_locations(const inkattn_attn_params *p) {
     return INKATTN_OK;
 }
 
-// Device memory of the current device: what TMA reads, and, where nothing is read by TMA, one or
-// two arrays of a call, so that a call made under another current device is refused.
+// Device memory of the current device: what TMA reads; where nothing is read by TMA, one or two arrays of a
+// call, so that a call made under another current device is refused; every array (dev_status aside) of a
+// verification step's end.
+//
+// Arrays of one allocation are told by its range, so that a call of many arrays asks about few: a rollback of
+// eight convs takes 3.5 us of the host's time, 5.7 with its 27 arrays asked about one by one.
+PFN_cuPointerGetAttributes_v7000 pointer_attributes() {
+    static const PFN_cuPointerGetAttributes_v7000 f = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool found = cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &fn, 7000, cudaEnableDefault, &q) ==
+                               cudaSuccess && q == cudaDriverEntryPointSuccess;
+        return found ? reinterpret_cast<PFN_cuPointerGetAttributes_v7000>(fn) : nullptr;
+    }();
+    return f;
+}
 inkattn_status validate_on_device(const void *const *ptrs, int n) {
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
+    const PFN_cuPointerGetAttributes_v7000 query = pointer_attributes();
+    if (!query || cudaGetDevice(&dev) != cudaSuccess) {
         (void)cudaGetLastError();
         return INKATTN_ERR_INVALID_ARG;
     }
+    constexpr int kKnown = 4;                          // allocations of this device seen in this call
+    CUdeviceptr known[kKnown] = {};
+    size_t known_bytes[kKnown] = {};
+    int next = 0;
     for (int i = 0; i < n; ++i) {
-        cudaPointerAttributes a;
-        if (cudaPointerGetAttributes(&a, ptrs[i]) != cudaSuccess) {
-            (void)cudaGetLastError();
-            return INKATTN_ERR_INVALID_ARG;
-        }
-        if (a.type != cudaMemoryTypeDevice || a.device != dev) return INKATTN_ERR_INVALID_ARG;
+        const CUdeviceptr ptr = reinterpret_cast<CUdeviceptr>(ptrs[i]);
+        bool seen = false;
+        for (int k = 0; k < kKnown; ++k) seen = seen || ptr - known[k] < known_bytes[k];
+        if (seen) continue;
+        unsigned int type = 0, managed = 0;
+        int where = -1;
+        CUdeviceptr start = 0;
+        size_t bytes = 0;
+        CUpointer_attribute names[] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_IS_MANAGED,
+                                       CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL, CU_POINTER_ATTRIBUTE_RANGE_START_ADDR,
+                                       CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+        void *values[] = {&type, &managed, &where, &start, &bytes};
+        if (query(5, names, values, ptr) != CUDA_SUCCESS) return INKATTN_ERR_INVALID_ARG;
+        if (type != CU_MEMORYTYPE_DEVICE || managed || where != dev) return INKATTN_ERR_INVALID_ARG;
+        known[next] = start;                           // (0 bytes where the driver does not say)
+        known_bytes[next] = bytes;
+        next = (next + 1) % kKnown;
     }
     return INKATTN_OK;
 }
@@ -853,8 +883,8 @@ inkattn_status inkattn_token_probs(const inkattn_token_probs_params *p, void *st
     int sms = 0;
     if ((st = check_device(&sms)) != INKATTN_OK) return st;
     if (p->N_tok == 0) return INKATTN_OK;
-    const void *ptrs[] = {p->logits, p->probs};
-    if ((st = validate_on_device(ptrs, 2)) != INKATTN_OK) return st;
+    const void *ptrs[] = {p->logits, p->probs, p->temperature};
+    if ((st = validate_on_device(ptrs, p->temperature ? 3 : 2)) != INKATTN_OK) return st;
     return launch_status(launch_token_probs(*p, sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -862,8 +892,10 @@ inkattn_status inkattn_verify_drafts(const inkattn_verify_drafts_params *p, void
     inkattn_status st = validate_verify_drafts(p);
     if (st != INKATTN_OK) return st;
     if ((st = check_device(nullptr)) != INKATTN_OK) return st;
-    const void *ptrs[] = {p->n_new, p->cu_seqlens_q, p->target_p};
-    if ((st = validate_on_device(ptrs, p->N_tok > 0 ? 3 : 2)) != INKATTN_OK) return st;
+    // (those without rows may be NULL)
+    const void *ptrs[] = {p->n_new, p->cu_seqlens_q, p->u_sample, p->target_p, p->token_ids, p->u_accept,
+                          p->out_tokens, p->draft_p};
+    if ((st = validate_on_device(ptrs, p->N_tok == 0 ? 3 : p->draft_p ? 8 : 7)) != INKATTN_OK) return st;
     return launch_status(launch_verify_drafts(*p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -871,8 +903,15 @@ inkattn_status inkattn_conv_rollback(const inkattn_conv_rollback_params *p, void
     inkattn_status st = validate_conv_rollback(p);
     if (st != INKATTN_OK) return st;
     if ((st = check_device(nullptr)) != INKATTN_OK) return st;
-    const void *ptrs[] = {p->cu_seqlens_q, p->states[0].state_after};
-    if ((st = validate_on_device(ptrs, 2)) != INKATTN_OK) return st;
+    const void *ptrs[3 + 3 * INKATTN_ROLLBACK_MAX_STATES] = {p->cu_seqlens_q, p->state_slot, p->n_keep};
+    int n = 3;
+    for (int s = 0; s < p->n_states; ++s) {
+        const inkattn_conv_rows &c = p->states[s];
+        if (p->N_tok > 0) ptrs[n++] = c.x;             // (may be NULL without rows)
+        ptrs[n++] = c.state_before;
+        if (c.state_after != c.state_before) ptrs[n++] = c.state_after;
+    }
+    if ((st = validate_on_device(ptrs, n)) != INKATTN_OK) return st;
     return launch_status(launch_conv_rollback(*p, static_cast<cudaStream_t>(stream)));
 }
 
