@@ -65,13 +65,16 @@ def main(argv=None):
         xv = gen.make_verify_inputs(w, args.verify, seed=args.seed, device=dev)
         logits = torch.empty((w.N_tok, args.verify), dtype=torch.float32, device=dev)
         head = ia.linear_params(x=step.out.view(w.N_tok, -1), w=xv["w_head"], out=logits, dev_status=step.status)
-        before = {n: x[f"conv_state_{n}"].clone() for n in ("k", "v")}
+        before = {n: torch.empty_like(x[f"conv_state_{n}"]) for n in ("k", "v")}
         end = VerifyStep(w, xv, logits, [(x[n], before[n], torch.empty_like(before[n])) for n in ("k", "v")])
     stream = torch.cuda.Stream(device=dev)
     print(w.describe(), f"num_splits={step.num_splits}" if step.mode == "decode" else "")
     with torch.cuda.stream(stream):
         for it in range(args.iters):
             e = [torch.cuda.Event(enable_timing=True) for _ in range(8)]
+            if end is not None:               # (the prologue updates its conv states in place)
+                for n in before:
+                    before[n].copy_(x[f"conv_state_{n}"])
             e[4].record(stream)
             if qk is not None:
                 qk.run(stream)
