@@ -622,8 +622,8 @@ INKATTN_API inkattn_status inkattn_expert_combine(const inkattn_expert_combine_p
  * A NaN counts as -infinity; a row of -infinities gives zeros; of a row with infinite logits,
  * those alone share the 1.  A temperature that is negative, infinite or NaN is flagged
  * (INKATTN_ERR_DEVICE_BOUNDS) and its row written as zeros.  Relative error at most
- * (32 + V 2^-13 + 2 (m - l_v) / t) 2^-23 of a value, and possibly 0 below 2^-125 (finite logits
- * further apart than the largest float, and temperatures above 2^126, are less exact). */
+ * (64 + V 2^-14 + 2 (m - l_v) / t) 2^-23 of a value, and possibly 0 below 2^-125 (finite logits
+ * further apart than the largest float, and temperatures above 2^126 or below 2^-127, are less exact). */
 typedef struct inkattn_token_probs_params {
     size_t struct_size;        /* = sizeof(inkattn_token_probs_params)                   */
     int32_t N_tok;             /* rows, 0 .. 2^24                                        */
