@@ -257,6 +257,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// the larger of two 16-bit numbers, in each half
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // 2^-k for the k that brings m (>= 0) to at most 2^15, 1 when m is below that: a scale by
 // which values of magnitude <= m convert to fp16 without overflow (exact, being a power of 2)
 __device__ __forceinline__ float fp16_prescale(float m) {

@@ -491,15 +491,20 @@ k_decode_tc(const DecTcArgs A, const __grid_constant__ CUtensorMap qmap,
         bool ok = wwait(bar(C::B_Q), 0);
         if (ok) {
             uint4 *qw = reinterpret_cast<uint4 *>(smem + C::kOffQ);
+            uint32_t most = 0;                                // the largest |q|, as bf16 bits, in each half
             for (int i = ct; i < 32768 / 16; i += C::kConvThreads) {
                 // rows without a query are zeros, and so are their logits: they then need no mask
                 // (16-byte pieces of a row, 8 in each half of the head dimension)
                 const uint4 w = ((i >> 3) & (kRows - 1)) < n_rows ? qw[i] : make_uint4(0, 0, 0, 0);
                 qw[i] = make_uint4(pack_f16(bf16_lo(w.x), bf16_hi(w.x)), pack_f16(bf16_lo(w.y), bf16_hi(w.y)),
                                    pack_f16(bf16_lo(w.z), bf16_hi(w.z)), pack_f16(bf16_lo(w.w), bf16_hi(w.w)));
+                most = max_u16x2(max_u16x2(most, max_u16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu)),
+                                 max_u16x2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
             }
             fence_proxy_async_smem();
             mbar_arrive(bar(C::B_QF));
+            // 65280 is the last bf16 number inside fp16's range
+            if (max(most & 0xFFFFu, most >> 16) > 0x477Fu) set_status(p.dev_status, INKATTN_ERR_DEVICE_BOUNDS);
         }
         auto tile_of = [&](int L) { return L == 0 ? 0 : L == 2 * N - 1 ? N - 1 : (L & 1) ? (L + 1) >> 1 : (L >> 1) - 1; };
         if constexpr (C::kI4) {

@@ -54,15 +54,10 @@ __device__ __forceinline__ float2 i4_codes2(float2 x, float inv) {
 // A lane's eight values of a row (packed bf16, a group in four neighbouring lanes of a converged warp) as a word
 // of codes, and the group's scale byte.
 __device__ __forceinline__ void i4_encode(const uint4 &row, uint32_t &word, uint32_t &byte) {
-    auto larger = [](uint32_t a, uint32_t b) {
-        uint32_t d;
-        asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-        return d;
-    };
     const uint32_t mag = 0x7FFF7FFFu;
-    uint32_t m = larger(larger(row.x & mag, row.y & mag), larger(row.z & mag, row.w & mag));
-    m = larger(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = larger(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    uint32_t m = max_u16x2(max_u16x2(row.x & mag, row.y & mag), max_u16x2(row.z & mag, row.w & mag));
+    m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
     float amax = fmaxf(__uint_as_float(m & 0x7FFF0000u), __uint_as_float(m << 16));
     const uint32_t w[4] = {row.x, row.y, row.z, row.w};
     float x[8];
