@@ -631,8 +631,8 @@ typedef struct inkattn_token_probs_params {
     int32_t N_tok;             /* rows, 0 .. 2^24                                        */
     int32_t V;                 /* logits of a row, 1 .. INKATTN_MAX_VOCAB                */
     int32_t logits_dtype;      /* INKATTN_DTYPE_BF16 (0) or INKATTN_DTYPE_F32 (1)        */
-    int64_t logits_stride;     /* elements from row to row, >= V                         */
-    int64_t probs_stride;      /* elements from row to row, >= V                         */
+    int64_t logits_stride;     /* elements from row to row, V .. 2^32                    */
+    int64_t probs_stride;      /* elements from row to row, V .. 2^32                    */
     const void *logits;        /* [N_tok][logits_stride], bf16 or fp32                   */
     const float *temperature;  /* nullable, [N_tok]                                      */
     float *probs;              /* [N_tok][probs_stride]; what lies behind V is not written */
@@ -640,7 +640,8 @@ typedef struct inkattn_token_probs_params {
 } inkattn_token_probs_params;
 
 /* Runs the softmax.  Arrays aligned to their elements' size, in memory of the current device; probs
- * may be the logits array itself (fp32, the same stride), but overlaps no input otherwise. */
+ * may be the logits array itself (fp32, the same stride), but overlaps no input otherwise (an array
+ * is all from its first element to its last, what lies between its rows included). */
 INKATTN_API inkattn_status inkattn_token_probs(const inkattn_token_probs_params *p, void *stream);
 
 /* Verification of drafted tokens by rejection sampling.  Sequence b has the rows cu_seqlens_q[b]
@@ -652,7 +653,7 @@ INKATTN_API inkattn_status inkattn_token_probs(const inkattn_token_probs_params 
  * and the token behind them is drawn from max(p_i - q_i, 0) at the first row i whose draft does
  * not stand (draft_p NULL: from p_i without x), or from the last row's p_i where all do; where that
  * weight is zero everywhere, from p_i.  A probability outside [0, 1] counts as the nearer bound, a
- * NaN as 0.
+ * NaN as 0, and the difference is one of fp32 numbers, rounded to nearest.
  *   Drawing: weights w_v are rounded to multiples of 2^-43 (ties to even) and summed as whole
  *   numbers, W in all; with U = floor(u_sample[b] 2^32) the token is the smallest v with w_0 + ..
  *   + w_v > floor(W U / 2^32).  The result depends on no order of sums, and is the same on
@@ -669,7 +670,7 @@ typedef struct inkattn_verify_drafts_params {
     int32_t B;                 /* sequences, 1 .. 2^20                                   */
     int32_t N_tok;             /* rows = cu_seqlens_q[B], 0 .. 2^24                      */
     int32_t V;                 /* vocabulary, 1 .. INKATTN_MAX_VOCAB                     */
-    int64_t target_stride;     /* elements from row to row, >= V                         */
+    int64_t target_stride;     /* elements from row to row, V .. 2^32                    */
     int64_t draft_stride;      /* the same of draft_p (not read where that is NULL)      */
     const float *target_p;     /* [N_tok][target_stride]                                 */
     const float *draft_p;      /* nullable, [N_tok][draft_stride]                        */
@@ -683,7 +684,7 @@ typedef struct inkattn_verify_drafts_params {
 } inkattn_verify_drafts_params;
 
 /* Runs the verification.  All arrays 4-byte aligned, in memory of the current device; the outputs
- * overlap neither each other nor an input. */
+ * overlap neither each other nor an input (rows of a stride as for the softmax). */
 INKATTN_API inkattn_status inkattn_verify_drafts(const inkattn_verify_drafts_params *p, void *stream);
 
 /* The conv states behind the first n_keep[b] of a step's rows: with xs = the 3 rows of
@@ -697,7 +698,7 @@ INKATTN_API inkattn_status inkattn_verify_drafts(const inkattn_verify_drafts_par
 #define INKATTN_ROLLBACK_MAX_STATES 8
 typedef struct inkattn_conv_rows {
     int32_t C;                 /* channels: a multiple of 8, 8 .. 2^20                   */
-    int64_t x_stride;          /* elements from row to row of x, >= C, a multiple of 8   */
+    int64_t x_stride;          /* elements from row to row of x, C .. 2^32, a multiple of 8 */
     const inkattn_bf16 *x;     /* [N_tok][x_stride], the conv's input rows of the step   */
     const inkattn_bf16 *state_before;  /* [num_state_slots][3][C]                        */
     inkattn_bf16 *state_after;         /* [num_state_slots][3][C]; may be state_before   */
