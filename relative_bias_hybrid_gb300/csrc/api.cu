@@ -506,20 +506,16 @@ inkattn_status launch_status(cudaError_t e) { return e == cudaSuccess ? INKATTN_
 
 }  // namespace
 
-// Decode split heuristic ([vLLM TML Inkling サポート, §低レイテンシコレクティブとカーネル
-// "FA4 Kernel"]: num_splits from batch size, TP size and KV length; TP = 1 here).
-// Cost model in units of one 64-key K+V block moved at the full HBM rate: a CTA streams
-// `per` blocks at min(its own rate, HBM / active CTAs), so a wave with a CTAs costs
-// per * max(r, a), where r is the number of CTAs that saturate HBM; the split partials add
-// their write + read traffic and the combine launch a fixed cost.
 namespace {
 
-// The same over a 4-bit cache, where a CTA's own steps set its pace and not HBM.  In microseconds, fits to
-// measured times (GB300, nine batches of one to 32 sequences with 1000 to 32768 keys, 1 to 32 parts: the choice
-// is within 13% of the best): a CTA starts and drains in 9, takes 0.5 for a block and kI4BandCost times
-// that for one of the band; the combine of S parts 2 + 0.27 S and its bytes at HBM's rate.
-// S parts of equal cost, one CTA an SM; or two parts cut at the band (csrc/decode_tc.cu), whose CTAs
-// run beside each other.
+// Decode split heuristic over a 4-bit cache, where a CTA's own steps set its pace and not HBM.  S parts of equal
+// cost, one CTA an SM; or two parts cut at the band (csrc/decode_tc.cu), whose CTAs run beside each other.
+// In microseconds: a CTA starts and drains in 9, takes 0.5 for a block and kI4BandCost times that for one of the
+// band; the combine of S parts takes 2 + 0.27 S and its bytes at HBM's rate.  Fitted to a slower kernel: the
+// present one starts and drains in 5, takes 0.5 for a block and 4.5 times that in the band, so that times come
+// out too long, but the choice mostly stands.  GB300, 1 to 32 parts: in nine batches of one to 64 sequences with
+// 1000 to 32768 keys it is the best or within 2% of it; in sixteen drawn ones within 11%, but for two of
+// lengths far apart (28 us for 24, 89 for 39): every sequence is taken to be as long as the longest.
 int pick_splits_i4(const inkattn_attn_params &p, int num_sms) {
     constexpr double kStart = 9.0, kBlockUs = 0.5;
     long long nblk = ((long long)p.max_seqlen_k + kBlock - 1) / kBlock;
@@ -549,6 +545,12 @@ int pick_splits_i4(const inkattn_attn_params &p, int num_sms) {
 
 }  // namespace
 
+// Decode split heuristic ([vLLM TML Inkling サポート, §低レイテンシコレクティブとカーネル
+// "FA4 Kernel"]: num_splits from batch size, TP size and KV length; TP = 1 here), over bf16 and E4M3 caches.
+// Cost model in units of one 64-key K+V block moved at the full HBM rate: a CTA streams
+// `per` blocks at min(its own rate, HBM / active CTAs), so a wave with a CTAs costs
+// per * max(r, a), where r is the number of CTAs that saturate HBM; the split partials add
+// their write + read traffic and the combine launch a fixed cost.
 int pick_splits(const inkattn_attn_params &p, int num_sms) {
     if (p.kv_dtype == INKATTN_KV_I4) return pick_splits_i4(p, num_sms);
     const int g = p.Hq / p.Hkv;

@@ -32,9 +32,10 @@
 // that comes out infinite or undefined is flagged as INKATTN_ERR_DEVICE_BOUNDS.  The table holds 16-bit fixed point with one
 // step per (head, token) row and round of 72 distances, sigma = (largest |entry| of that
 // part of the row) / 32000; the staged bias is within sigma / 2 of the fp32 value.  A tile of the band costs
-// about five others (L2 round trips for P and 64 table entries a thread).  Rows of 73 words instead of
-// 72, P in 16-byte pieces, loads ahead and one step's factor for most of a half: 64 sequences x 4 queries
-// over 4096 keys, 4 bits 315 -> 262 us.
+// four others over a bf16 cache, three over E4M3, 4.5 over 4 bits (L2 round trips for P and 64 table entries a
+// thread; 8 sequences x 9 queries, with a bias and without).  Rows of 73 words instead of 72, P in 16-byte
+// pieces, loads ahead and one step's factor for most of a half: 64 sequences x 4 queries over 4096 keys, 4
+// bits 315 -> 262 us.
 // Normalisation: O accumulates P V with P rounded to bf16, and each tile's largest P (its
 // row maximum's) is the dominant term whose bf16 rounding matters; that rounding error is
 // added to the row's normaliser, while the LSE uses the sum of the fp32 P.
@@ -70,8 +71,8 @@ constexpr int kTabRows = kDecodeMaxRows;   // g * ql <= 128
 // Warps: 0 TMA, 1 MMA, [2, kWarpSm) converters (codes only), then 8 softmax warps.
 //
 // What bounds the 4-bit variant: a tile of 128 keys is 17 KB from HBM, a quarter of bf16's, and
-// takes about 1950 cycles of an SM, in which the schedulers issue two cycles in three: 32768 values are
-// expanded, 72 rows of softmax run beside them, and the tensor pipe is active for half.  MTP-verify
+// takes about 1950 cycles of an SM, in which the schedulers issue two cycles in three (63%, the busiest
+// 65%): 32768 values are expanded, 72 rows of softmax run beside them, and the tensor pipe is active for half.  MTP-verify
 // (32 x 9 queries, 32768 keys, band split) 0.54 ms with the combine, bf16 cache 0.66; floor (HBM) 0.17.
 // Steps: six warps of 512 threads, 16 units shared out evenly 0.88; ten converter warps with shares by
 // their scheduler's load and lane-constant addresses, and rows without a query as zeros instead of masked
@@ -104,7 +105,7 @@ struct Dec {
     static constexpr int kOffQ = 0;
     static constexpr int kOffKV = 32768;
     static constexpr int kOffCodes = kOffKV + kSlots * kSlotBytes;
-    static constexpr int kOffTab = kOffCodes + kCodeSlots * kCodeSlotBytes;   // 16-bit fixed point [g][ql][kTabW]
+    static constexpr int kOffTab = kOffCodes + kCodeSlots * kCodeSlotBytes;   // 16-bit fixed point [g][ql][kTabStride]
     static constexpr int kOffXchg = kOffTab + kTabRows * kTabStride * 2;     // row maxima / sums
     static constexpr int kOffTsig = kOffXchg + 3 * 2 * kRows * 4;       // fp32 steps [g][ql][2 rounds]
     static constexpr int kOffBar = kOffTsig + kTabRows * 2 * 4;

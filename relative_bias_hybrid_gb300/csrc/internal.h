@@ -131,7 +131,8 @@ constexpr int kDecodeMinSplitBlocks = 8; // a split streams at least 8 cache blo
 // 40 B/clk (its MMAs take ~1600 cycles per 64 KB tile), HBM gives ~23 B/clk per SM.
 constexpr double kDecodeHbmSmFrac = 0.6;
 constexpr double kCombineCostBlocks = 600.0; // fixed cost of the combine launch (~3 us), in block loads
-// The decode over a 4-bit cache: what a cache block of the bias band costs a CTA, in other blocks.
+// The decode over a 4-bit cache: what a cache block of the bias band counts, in other blocks, where keys are
+// divided into parts of equal cost and in the split rule (measured: 4.5; api.cu says what the choice loses).
 constexpr int kI4BandCost = 6;
 cudaError_t launch_combine(const inkattn_attn_params &p, int num_splits, const float *ws_o,
                            const float *ws_lse, cudaStream_t stream);
