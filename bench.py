@@ -504,6 +504,7 @@ def time_output_conv(w, args, dev, stream, flush, peaks, name):
     D = w.Hq * w.head_dim
     x = gen.make_output_conv_inputs(w, seed=0, D=D, device=dev)
     oc = OutputConvStep(w, x)
+    torch.cuda.synchronize()        # the inputs are made on another stream
     with torch.cuda.stream(stream):
         for _ in range(args.warmup):
             flush.zero_()
@@ -539,6 +540,7 @@ def time_qkvr(w, args, dev, stream, flush, peaks, name):
     from relative_bias_hybrid_gb300.step import QkvrStep
     x = gen.make_qkvr_inputs(w, QKVR_D_MODEL, seed=0, device=dev)
     qk = QkvrStep(w, x)
+    torch.cuda.synchronize()        # the inputs are made on another stream
     with torch.cuda.stream(stream):
         for _ in range(args.warmup):
             flush.zero_()
@@ -579,6 +581,7 @@ def measure(name, args, peaks, dev, stream, flush):
     mode = "decode" if name.startswith("decode") else "prefill"
     x = gen.make_inputs(w, seed=0, device=dev, kv_dtype=kv)
     step = AttentionStep(w, x, mode=mode)
+    torch.cuda.synchronize()        # the inputs are made on another stream
     tot, att, pro = timed_steps(step, args.steps, args.warmup, flush, stream)
     if step.device_status() != 0:
         raise RuntimeError(f"{name}: device status {step.device_status()} during the timed steps")
@@ -591,6 +594,7 @@ def measure(name, args, peaks, dev, stream, flush):
     for n in ("q", "k", "v", "r"):
         x2[n] = torch.empty_like(x[n])
     step2 = AttentionStep(w, x2, mode=mode, num_splits=step.num_splits)
+    torch.cuda.synchronize()
     e2e_ms, h2d, d2h = e2e_steps((step, step2), x_host, args.steps, args.warmup, stream)
     if step.device_status() | step2.device_status():
         raise RuntimeError(f"{name}: device status set during the end-to-end steps")

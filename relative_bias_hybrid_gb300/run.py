@@ -68,6 +68,7 @@ def main(argv=None):
         before = {n: torch.empty_like(x[f"conv_state_{n}"]) for n in ("k", "v")}
         end = VerifyStep(w, xv, logits, [(x[n], before[n], torch.empty_like(before[n])) for n in ("k", "v")])
     stream = torch.cuda.Stream(device=dev)
+    stream.wait_stream(torch.cuda.current_stream(dev))      # (which makes the inputs)
     print(w.describe(), f"num_splits={step.num_splits}" if step.mode == "decode" else "")
     with torch.cuda.stream(stream):
         for it in range(args.iters):
