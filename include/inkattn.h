@@ -102,8 +102,8 @@ typedef uint16_t inkattn_bf16;
  *   inkattn_decode and inkattn_prefill_i4 (inkattn_prefill returns INKATTN_ERR_UNSUPPORTED).  A
  *   scale byte above 0xC6 inside a sequence is flagged as INKATTN_ERR_DEVICE_BOUNDS and its group
  *   read as zeros; u = 0 is no code of the prologue's (it reads as -8 s).
- * Over a cache of codes (E4M3, I4) the decode holds q as fp16: |q| <= 65280, beyond which a value is flagged as
- *   INKATTN_ERR_DEVICE_BOUNDS and its row's result undefined; values below 2^-14 count in steps of 2^-24. */
+ * Over a cache of codes (E4M3, I4) the decode holds q as fp16: |q| <= 65280; a value beyond that, or a NaN, is
+ *   flagged as INKATTN_ERR_DEVICE_BOUNDS and its row's result undefined; below 2^-14 values count in steps of 2^-24. */
 #define INKATTN_KV_BF16 0
 #define INKATTN_KV_E4M3 1
 #define INKATTN_KV_I4 4
